@@ -105,11 +105,13 @@ enum {
                               shared-memory pipelined ones apply (same output
                               bits; for A/B checks). The backward's weight-grad
                               sums may differ in rounding. */
-  QKVP_NORM_OFF = 16       /* GQA layouts: no RMSNorm of q and k (split ->
+  QKVP_NORM_OFF = 16,      /* GQA layouts: no RMSNorm of q and k (split ->
                               RoPE only, the GQAttention variant of Llama 3 and
                               GPT-OSS). w_q / w_k may be NULL; the backward
                               reads neither q_pre nor k_pre and has no weight
                               gradients (dw_q / dw_k may be NULL, untouched). */
+  QKVP_ZERO_REST = 32      /* attention over packed sequences: rows of no
+                              sequence are set to zero instead of left alone  */
 };
 
 /* Options of the GQAttention variant (the *_ex entry points; NULL = none).
@@ -140,6 +142,13 @@ typedef struct {
  * *dev_status when a token's page or offset is out of range; that token's
  * pool store is skipped, nothing traps. */
 enum { QKVP_DEV_BAD_PAGE = 1, QKVP_DEV_BAD_OFFSET = 2 };
+
+/* Device-side status bits of the attention calls. BAD_SEQUENCE: sequence
+ * offsets that do not ascend inside [0, T]; the call then computes no row.
+ * BAD_LENGTH: a decode length outside [0, max_pages * page_size]; it is
+ * clamped. (A decode page out of range sets QKVP_DEV_BAD_PAGE; its tokens are
+ * not attended.) */
+enum { QKVP_DEV_BAD_LENGTH = 4, QKVP_DEV_BAD_SEQUENCE = 8 };
 
 /* ---------------------------------------------------------------------------
  * qkv_prologue_fwd -- split + per-head RMSNorm + RoPE, contiguous outputs.
@@ -424,6 +433,39 @@ QKVP_API int qkv_newton_schulz_workspace(const qkvp_layout* layout, int64_t coun
  * these arguments (host only, nothing is launched; count 0 gives 0, 0). */
 QKVP_API int qkv_newton_schulz_plan(const qkvp_layout* layout, int64_t count, int64_t cols, int32_t split,
                                     int32_t* split_out, int32_t* grid_out);
+
+/* ---------------------------------------------------------------------------
+ * qkv_attention_fwd -- causal attention over packed sequences, the reader of
+ * the q, k and v that qkv_prologue_fwd writes.
+ *
+ * Sequence s is the rows [cu_seqlens[s], cu_seqlens[s + 1]); its row i attends
+ * the rows j <= i of the same sequence, query head h the key/value head
+ * h / (n_q / n_kv):
+ *     out_i = sum_j softmax_j(scale q_i . k_j) v_j.
+ * Products on the tensor cores with fp32 accumulation; the softmax weights are
+ * rounded to bf16 before they multiply v, maxima and sums are fp32; one
+ * rounding of the result to bf16.
+ *
+ * layout      GQA layout; n_q, n_kv, head_dim are used, the packing is not.
+ * T           rows of q, k, v and out (at most 2^31 - 257).
+ * batch       sequences (>= 0; empty ones are allowed).
+ * cu_seqlens  int32 [batch + 1], ascending within [0, T]. Where they do not
+ *             ascend, no row is computed and QKVP_DEV_BAD_SEQUENCE is set.
+ * q, k, v     bf16 [T, n_q | n_kv, head_dim], memory of the current device.
+ *             Rows of no sequence are never used, whatever they hold.
+ * scale       > 0 and finite; 0 means head_dim^-0.5.
+ * flags       QKVP_ZERO_REST.
+ * out         bf16 [T, n_q, head_dim]. Rows of no sequence are left as they
+ *             are (with QKVP_ZERO_REST: set to zero).
+ * lse         float32 [n_q, T] or NULL: log sum_j exp(scale q_i . k_j), which
+ *             the backward needs. Rows of no sequence: as out (-inf for zero).
+ * dev_status  int32 or NULL, bits OR-ed in.
+ * A NaN or infinity in a row of k or v reaches the rows that attend it, and may
+ * reach the other rows of its sequence in the same block of 128.
+ * ------------------------------------------------------------------------- */
+QKVP_API int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const int32_t* cu_seqlens,
+                               const void* q, const void* k, const void* v, float scale, uint32_t flags, void* out,
+                               float* lse, int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------
  * qkv_prologue_device_error -- read (and with clear != 0, reset) the

@@ -43,9 +43,12 @@ QKVP_SAVE_PRE = 2
 QKVP_ACCUMULATE_DW = 4
 QKVP_FORCE_GENERIC = 8
 QKVP_NORM_OFF = 16
+QKVP_ZERO_REST = 32
 
 QKVP_DEV_BAD_PAGE = 1
 QKVP_DEV_BAD_OFFSET = 2
+QKVP_DEV_BAD_LENGTH = 4
+QKVP_DEV_BAD_SEQUENCE = 8
 
 
 class qkvp_layout(ctypes.Structure):
@@ -107,6 +110,7 @@ _SIGS = {
     "qkv_newton_schulz_workspace": ([_LP, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "qkv_newton_schulz_plan": ([_LP, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_int32),
                                 ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
+    "qkv_attention_fwd": ([_LP, _i64, _i32, _vp, _vp, _vp, _vp, _f32, _u32, _vp, _vp, _vp, _vp], ctypes.c_int),
     "qkv_prologue_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "qkv_prologue_version": ([], ctypes.c_int),
     "qkv_prologue_device_error": ([ctypes.c_int, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
@@ -311,3 +315,10 @@ def qkv_newton_schulz_plan(L, cols, split=0, count=1):
                                      ctypes.byref(g))
     _ret(st, "qkv_newton_schulz_plan", True)
     return c.value, g.value
+
+
+def qkv_attention_fwd(L, T, batch, cu_seqlens, q, k, v, scale, flags, out, lse=None, dev_status=None, stream=None,
+                      check=True):
+    st = _lib.qkv_attention_fwd(ctypes.byref(L), int(T), int(batch), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
+                                float(scale), int(flags), _ptr(out), _ptr(lse), _ptr(dev_status), _stream(stream))
+    return _ret(st, "qkv_attention_fwd", check)

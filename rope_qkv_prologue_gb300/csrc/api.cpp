@@ -527,6 +527,18 @@ int check_ns(const qkvp_layout* layout, int64_t count, int64_t cols, int32_t spl
   return QKVP_OK;
 }
 
+// -------------------------------------------------------- attention ----
+
+// Argument checks shared by the attention entry points.
+int check_attention(const qkvp_layout* layout, int32_t batch, float scale, float* scale_out) {
+  Gqa g;
+  QKVP_TRY(check_gqa(layout, 0, &g));
+  if (batch < 0) return QKVP_ERR_SHAPE;
+  if (!std::isfinite(scale) || scale < 0.f) return QKVP_ERR_VALUE;
+  *scale_out = scale == 0.f ? (float)(1.0 / std::sqrt((double)layout->head_dim)) : scale;
+  return QKVP_OK;
+}
+
 bool overlaps(const void* p, size_t pn, const void* q, size_t qn) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
   return a < b + qn && b < a + pn;
@@ -1195,6 +1207,55 @@ int qkv_newton_schulz_plan(const qkvp_layout* layout, int64_t count, int64_t col
   *split_out = sp;
   *grid_out = (int32_t)(units * sp);
   return QKVP_OK;
+}
+
+// ----------------------------------------------------------- attention ----
+
+int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const int32_t* cu_seqlens, const void* q,
+                      const void* k, const void* v, float scale, uint32_t flags, void* out, float* lse,
+                      int32_t* dev_status, void* stream) {
+  AttnFwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  QKVP_TRY(check_attention(layout, batch, scale, &a.scale));
+  if (T < 0 || T > INT32_MAX - 256) return QKVP_ERR_SHAPE;
+  if (flags & ~(uint32_t)QKVP_ZERO_REST) return QKVP_ERR_FLAGS;
+  if (!cu_seqlens || !q || !k || !v || !out) return QKVP_ERR_NULL;
+  for (const void* p : {q, k, v, (const void*)out})
+    if (!aligned16(p)) return QKVP_ERR_ALIGN;
+  if (!aligned4(cu_seqlens) || (lse && !aligned4(lse)) || (dev_status && !aligned4(dev_status))) return QKVP_ERR_ALIGN;
+  if (T == 0) return QKVP_OK;
+  int sms = 0;
+  QKVP_TRY(current_device(&sms));
+  for (const void* p : {q, k, v})  // tensor maps cover this GPU's own memory
+    if (!on_current_device(p)) return QKVP_ERR_VALUE;
+  const int hd = layout->head_dim;
+  CUtensorMap tq, tk, tv;
+  if (!bf16_tile_map(&tq, q, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
+      !bf16_tile_map(&tk, k, T, (int64_t)layout->n_kv * hd, kAttnBlock) ||
+      !bf16_tile_map(&tv, v, T, (int64_t)layout->n_kv * hd, kAttnBlock))
+    return QKVP_ERR_LAUNCH;
+  a.n_q = layout->n_q;
+  a.n_kv = layout->n_kv;
+  a.group = layout->n_q / layout->n_kv;
+  a.batch = batch;
+  a.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  a.dev_status = dev_status;
+  a.T = T;
+  a.cu = cu_seqlens;
+  a.pair_heads = a.group % 2 == 0;
+  a.units = a.pair_heads ? a.n_q / 2 : a.n_q;
+  a.zero_rest = (flags & QKVP_ZERO_REST) != 0;
+  a.out = static_cast<uint4*>(out);
+  a.lse = lse;
+  if ((a.err = device_error_word()) == nullptr) return QKVP_ERR_LAUNCH;
+  const void* kern = attention_fwd_kernel(hd, false);
+  const size_t smem = (size_t)attention_fwd_smem_bytes(hd, false);
+  if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
+  const int64_t unit_rows = a.pair_heads ? kAttnBlock : 2 * kAttnBlock;
+  const int64_t most = (T / unit_rows + std::max(batch, 1)) * a.units;  // at least the number of work items
+  void* args[] = {&tq, &tk, &tv, &a};
+  return launch_args(kern, most < sms ? most : sms, attention_fwd_threads(), smem, static_cast<cudaStream_t>(stream),
+                     args);
 }
 
 int qkv_prologue_wait_selftest(void* stream) {

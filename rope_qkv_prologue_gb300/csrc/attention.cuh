@@ -1,0 +1,224 @@
+// Shared pieces of the attention kernels on the tensor cores (sm_103a): waits
+// that give up together, tensor-memory operands, tensor-map loads of three
+// dimensions, and the order in which the persistent kernels take the blocks of
+// packed sequences.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "pipeline.cuh"
+#include "tcgen05.cuh"
+
+namespace qkvp {
+
+constexpr int kAttnRows = kAttnBlock;            // rows of a block (queries or keys)
+constexpr int kAttnBox = kAttnRows * 128;        // bytes of 128 rows x 64 bf16, 128B-swizzled
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Byte offset of 16-byte chunk `chunk` (0..7) of row `row` in a swizzled box.
+__device__ __forceinline__ int attn_swz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+// Bounded wait that gives up at once when another thread of the CTA already
+// gave up (*fail): after one timeout the rest of the kernel runs through
+// without waiting, and every loop still ends.
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* fail) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*fail) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *fail = 1;
+      atomicOr(err, kErrWaitTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A is M = 128 lanes x 16 bf16 per K step, two
+// consecutive K values per 32-bit column. Issued by one lane of the warp.
+__device__ __forceinline__ void umma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Whole warp: 32 consecutive 32-bit columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_after_wait(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31]));
+}
+
+// Whole warp: 128 consecutive fp32 columns of this warp's 32 TMEM lanes, four
+// loads in flight and one wait. The empty asm keeps the uses of the later
+// loads' registers behind the wait.
+__device__ __forceinline__ void tmem_ld128(uint32_t addr, float (&v)[128]) {
+  uint32_t r0[32], r1[32], r2[32], r3[32];
+  tmem_ld32_issue(addr, r0);
+  tmem_ld32_issue(addr + 32, r1);
+  tmem_ld32_issue(addr + 64, r2);
+  tmem_ld32_issue(addr + 96, r3);
+  tmem_wait_ld32(r0);
+  tmem_after_wait(r1);
+  tmem_after_wait(r2);
+  tmem_after_wait(r3);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = __uint_as_float(r0[i]);
+    v[32 + i] = __uint_as_float(r1[i]);
+    v[64 + i] = __uint_as_float(r2[i]);
+    v[96 + i] = __uint_as_float(r3[i]);
+  }
+}
+
+// 3-D tensor-map load (c0: the contiguous coordinate).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// D (+)= A B^T over K = HD, both operands K-major boxes of 64 columns.
+template <int HD>
+__device__ __forceinline__ void attn_mma_ss(uint32_t d, const unsigned char* a, const unsigned char* b, uint32_t id) {
+#pragma unroll
+  for (int k = 0; k < HD / 16; ++k) {
+    const int box = (k >> 2) * kAttnBox;
+    umma_bf16_warp(d, umma_desc_sw128(a + box) + 2 * (k & 3), umma_desc_sw128(b + box) + 2 * (k & 3), id, k != 0);
+  }
+}
+
+// The blocks of packed sequences, taken from the most expensive to the
+// cheapest. Sequence s has n_s = ceil(len_s / unit) blocks, one of each cost
+// 1 .. n_s (with the causal mask the block at distance c from the sequence's
+// beginning, or end, has c times the work of the first). F(c) = sum over s of
+// max(0, n_s - c) blocks cost more than c, so rank r has the smallest cost c
+// with F(c) <= r, and is the (r - F(c))-th sequence with n_s >= c. Evaluated by
+// one warp from the sequence offsets alone: no list in memory, no launch before
+// the kernel that uses it.
+struct AttnOrder {
+  static constexpr int kCached = 128;  // sequences whose block counts are kept in shared memory
+  const int32_t* cu;
+  int batch;
+  int unit;
+  int* cache;      // [kCached]
+  int most;        // largest n_s
+  uint32_t total;  // sum of n_s
+
+  __device__ __forceinline__ int blocks(int s) const {
+    if (s < kCached) return cache[s];
+    return (int)(((int64_t)cu[s + 1] - cu[s] + unit - 1) / unit);
+  }
+
+  // Whole warp. False (and no blocks) when the offsets do not ascend in [0, T].
+  __device__ __forceinline__ bool init(int64_t T, int lane) {
+    bool bad = false;
+    uint32_t sum = 0, top = 0;
+    for (int s = lane; s < batch; s += 32) {
+      const int64_t a = cu[s], b = cu[s + 1];
+      const bool ok = a >= 0 && b >= a && b <= T;
+      bad |= !ok;
+      const uint32_t n = ok ? (uint32_t)((b - a + unit - 1) / unit) : 0u;
+      if (s < kCached) cache[s] = (int)n;
+      sum += n;
+      top = n > top ? n : top;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    total = bad ? 0u : __reduce_add_sync(0xffffffffu, sum);
+    most = bad ? 0 : (int)__reduce_max_sync(0xffffffffu, top);
+    __syncwarp();
+    return !bad;
+  }
+
+  // Whole warp: the sequence and cost of rank r < total.
+  __device__ __forceinline__ void find(uint32_t r, int lane, int& seq, int& cost) const {
+    int lo = 0, hi = most;  // F(hi) <= r, and F(lo - 1) > r or lo == 0
+    uint32_t f_hi = 0;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      uint32_t f = 0;
+      for (int s = lane; s < batch; s += 32) {
+        const int n = blocks(s) - mid;
+        f += n > 0 ? (uint32_t)n : 0u;
+      }
+      f = __reduce_add_sync(0xffffffffu, f);
+      if (f <= r) {
+        hi = mid;
+        f_hi = f;
+      } else {
+        lo = mid + 1;
+      }
+    }
+    cost = hi;
+    uint32_t idx = r - f_hi;
+    seq = 0;
+    for (int s0 = 0; s0 < batch; s0 += 32) {
+      const int s = s0 + lane;
+      uint32_t m = __ballot_sync(0xffffffffu, s < batch && blocks(s) >= cost);
+      const uint32_t n = __popc(m);
+      if (idx < n) {
+        for (; idx; --idx) m &= m - 1;
+        seq = s0 + __ffs(m) - 1;
+        break;
+      }
+      idx -= n;
+    }
+  }
+};
+
+// Work item of round k for CTA b of g: the items descend in cost, and every
+// other round is dealt backwards, so that the sums stay even.
+__device__ __forceinline__ int64_t attn_deal(int64_t k, int64_t b, int64_t g) {
+  return k * g + ((k & 1) ? g - 1 - b : b);
+}
+
+// Rows of no sequence ([0, cu[0]) and [cu[batch], T), or all of them when the
+// offsets are refused): `chunks` 16-byte pieces per row set to zero, one warp
+// of each CTA.
+__device__ __forceinline__ void attn_zero_rest(uint4* out, int64_t T, int64_t chunks, int64_t first, int64_t last,
+                                               int lane) {
+  const int64_t head = first * chunks, n = head + (T - last) * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < n; i += (int64_t)gridDim.x * 32)
+    out[i < head ? i : last * chunks + (i - head)] = make_uint4(0, 0, 0, 0);
+}
+
+}  // namespace qkvp

@@ -1,0 +1,503 @@
+// Attention forward on the tensor cores (sm_103a), for two callers:
+//
+//   prompt   causal attention over packed sequences: q [T, n_q, D], k and v
+//            [T, n_kv, D], offsets cu[batch + 1]; writes out (bf16) and, for
+//            training, the log-sum-exp of each row;
+//   prefix   the query rows of a decode batch (sequence b, head g of the group
+//            of key/value head h) against a prefix that all sequences share,
+//            read from the paged pool; writes float32 partial results of key
+//            ranges that the decode's last kernel joins.
+//
+// With s_ij = scale q_i . k_j over the keys row i may see,
+//   m_i = max_j s_ij,  l_i = sum_j e^(s_ij - m_i),  o_i = sum_j e^(s_ij - m_i) v_j / l_i,
+// in one pass over the keys, m and l running: a block of 128 keys gives S = Q K^T
+// (fp32 in tensor memory), each row's maximum, P = e^(S - m) rounded to bf16 (the
+// rounding of an operand of the second product; l sums P before it), and
+// O += P V. When a row's maximum grows, what O and l hold has the factor
+// e^(m_old - m_new). O is only rescaled when that maximum grew by more than 8
+// powers of two: up to there P stays below 2^8, where bf16 has the same relative
+// precision and the fp32 sums have room, and the division by l makes the
+// reference point drop out.
+//
+// One CTA per SM holds two blocks of 128 query rows ("slots") that share every
+// key block: two heads of the same group at the same rows where the group is
+// even, else two consecutive row blocks of a head. Sharing halves what K and V
+// cost to fetch (64 KiB per 2 x 8.4 MFLOP at head_dim 128), and while one slot's
+// softmax runs, the tensor cores work on the other's products:
+//   warp 0      loads Q, K, V tiles with TMA into 128B-swizzled shared memory;
+//   warp 1      issues the MMAs: PV(i) then S(i + 1) of slot 0, the same of slot 1.
+//               P lives in the tensor-memory columns of the S it came from; MMAs
+//               execute in order, so S(i + 1) overwrites P(i) after PV(i) read it;
+//   warp 2      finds the next work item (AttnOrder), one ahead;
+//   warp 3      zeroes the rows of no sequence where the caller asked for it;
+//   warps 4-7   softmax, rescaling and epilogue of slot 0, thread i owning row i,
+//   warps 8-11  the same of slot 1.
+// Keys behind the end of a sequence may hold anything (another sequence, unused
+// memory): their scores are replaced, not added to, and their V rows are zeroed
+// in shared memory, since 0 times a NaN is not 0.
+#include "attention.cuh"
+
+namespace qkvp {
+namespace {
+
+constexpr int kFwdThreads = 384;
+constexpr int kFwdSched = 2;  // work items in flight between the finder and the others
+constexpr float kRescale = 8.f;  // powers of two a row's maximum may grow before O is rescaled
+constexpr int kStageBytes = 32 * 128;  // an epilogue warp's buffer: 32 rows x 64 bf16
+
+template <int HD>
+struct FwdSmem {
+  static constexpr int kTile = (HD / 64) * kAttnBox;  // 128 rows x HD bf16
+  static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kOut = kRing + kStages * kTile;
+};
+
+struct FwdItem {
+  int n0, n1;        // key blocks of each slot (0: the slot is idle)
+  int row0, row1;    // first query row of each slot (prompt: of T; prefix: row tile)
+  int head0, head1;  // query head of each slot
+  int kvh;           // key/value head
+  int kv0;           // first key row (prompt)
+  int len;           // keys (of the sequence, or of this key range of the prefix)
+  int valid;
+};
+
+}  // namespace
+
+template <int HD, bool PREFIX>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    qkvp_attention_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                              const __grid_constant__ CUtensorMap tmap_v, const AttnFwdArgs a) {
+  using SM = FwdSmem<HD>;
+  constexpr int ST = SM::kStages;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], tail_bar, mma_done, q_full[2], q_empty[2], s_full[2], p_full[2],
+      o_done[2], o_free[2], it_full[kFwdSched], it_empty[kFwdSched];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_fail;
+  __shared__ FwdItem s_item[kFwdSched];
+  __shared__ int s_cache[PREFIX ? 1 : AttnOrder::kCached];
+  __shared__ int s_slot[PREFIX ? kAttnMaxChunk / 8 : 1];  // pool row of each page box of the key range, or -1
+  __shared__ uint32_t s_whole;                            // prefix: bit i set when all 128 keys of block i are valid
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&tail_bar, 1);
+    mbar_init(&mma_done, 1);
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(&q_full[j], 1);
+      mbar_init(&q_empty[j], 1);
+      mbar_init(&s_full[j], 1);
+      mbar_init(&p_full[j], 4);
+      mbar_init(&o_done[j], 1);
+      mbar_init(&o_free[j], 4);
+    }
+    for (int j = 0; j < kFwdSched; ++j) {
+      mbar_init(&it_full[j], 1);
+      mbar_init(&it_empty[j], 10);  // loader, issuer, 8 softmax warps
+    }
+    s_fail = 0;
+    s_whole = 0xffffffffu;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(&s_tmem, 512);
+  griddep_wait();
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile int* fail = &s_fail;
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    int ok = 1;
+    if (lane == 0) ok = attn_wait(bar, parity, a.err, fail) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  };
+
+  int px_len = 0, px_first = 0, px_chunk = 0;  // prefix: this CTA's key range
+  if constexpr (PREFIX) {
+    const int per = a.n_kv * a.pairs;
+    px_chunk = (int)blockIdx.x / per;
+    px_first = px_chunk * a.chunk;
+    px_len = min(a.chunk, a.prefix_len - px_first);
+    const int boxes = (px_len + a.box_rows - 1) / a.box_rows;
+    for (int g = threadIdx.x; g < boxes; g += kFwdThreads) {
+      const int key = px_first + g * a.box_rows;
+      const int page = a.prefix_pages[key / a.page_size];
+      const bool ok = page >= 0 && page < a.num_pages;
+      s_slot[g] = ok ? page * a.page_size + key % a.page_size : -1;
+      if (!ok) {
+        atomicAnd(&s_whole, ~(1u << (g * a.box_rows / kAttnRows)));
+        if (a.dev_status) atomicOr(a.dev_status, kDevBadPage);
+      }
+    }
+    if (threadIdx.x == 0 && px_len % kAttnRows) atomicAnd(&s_whole, ~(1u << (px_len / kAttnRows)));
+    __syncthreads();
+  }
+
+  // The next work item, in order: read from the finder's ring, or (prefix) the
+  // CTA's only one. Every role sees the same items.
+  uint32_t it_pos = 0;
+  auto next_item = [&](FwdItem& t) -> bool {
+    if constexpr (PREFIX) {
+      if (it_pos++) return false;
+      const int r = (int)blockIdx.x % (a.n_kv * a.pairs);
+      t.kvh = r % a.n_kv;
+      const int n = (px_len + kAttnRows - 1) / kAttnRows;
+      t.row0 = 2 * (r / a.n_kv);
+      t.row1 = t.row0 + 1;
+      t.n0 = n;
+      t.n1 = t.row1 < a.row_tiles ? n : 0;
+      t.head0 = t.head1 = 0;
+      t.kv0 = 0;
+      t.len = px_len;
+      return true;
+    } else {
+      const uint32_t s = it_pos % kFwdSched, ph = (it_pos / kFwdSched) & 1;
+      ++it_pos;
+      if (!warp_wait(&it_full[s], ph)) return false;
+      t = s_item[s];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[s]);
+      return t.valid != 0;
+    }
+  };
+
+  if (warp == 0) {
+    // ---- loader
+    uint32_t it = 0, tails = 0, qc[2] = {0, 0};
+    FwdItem t;
+    while (next_item(t)) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if ((j ? t.n1 : t.n0) == 0) continue;
+        if (qc[j] > 0) warp_wait(&q_empty[j], (qc[j] - 1) & 1);
+        ++qc[j];
+        if (lane == 0) {
+          unsigned char* dst = base + SM::kQ + j * SM::kTile;
+          const int row = j ? t.row1 : t.row0;
+          if constexpr (PREFIX) {
+            mbar_arrive_expect_tx(&q_full[j], (uint32_t)(a.bpt * a.group * HD * 2));
+            for (int x = 0; x < HD / 64; ++x)
+              tma_load_3d(dst + x * kAttnBox, &tmap_q, 64 * x, t.kvh * a.group, row * a.bpt, &q_full[j]);
+          } else {
+            mbar_arrive_expect_tx(&q_full[j], SM::kTile);
+            for (int x = 0; x < HD / 64; ++x)
+              tma_load_2d(dst + x * kAttnBox, &tmap_q, (j ? t.head1 : t.head0) * HD + 64 * x, row, &q_full[j]);
+          }
+        }
+      }
+      const int n = max(t.n0, t.n1);
+      for (int i = 0; i < n; ++i) {
+#pragma unroll
+        for (int which = 0; which < 2; ++which, ++it) {
+          const uint32_t s = it % ST;
+          if (it >= ST) warp_wait(&empty[s], ((it / ST) - 1) & 1);
+          unsigned char* dst = base + SM::kRing + s * SM::kTile;
+          const CUtensorMap* map = which ? &tmap_v : &tmap_k;
+          const bool part = PREFIX ? ((s_whole >> i) & 1) == 0 : kAttnRows * (i + 1) > t.len;
+          const bool patch = which && part;  // rows of V to zero once they are here
+          uint64_t* bar = patch ? &tail_bar : &full[s];
+          if constexpr (PREFIX) {
+            // one box per page piece (box_rows keys); lanes take them in turn
+            const int per = kAttnRows / a.box_rows;
+            int mine = 0;
+            for (int g = lane; g < per; g += 32) {
+              const int gg = i * per + g;
+              if (gg * a.box_rows < px_len && s_slot[gg] >= 0) ++mine;
+            }
+            const int boxes = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * a.box_rows * HD * 2));
+            __syncwarp();
+            for (int g = lane; g < per; g += 32) {
+              const int gg = i * per + g;
+              if (gg * a.box_rows < px_len && s_slot[gg] >= 0)
+                for (int x = 0; x < HD / 64; ++x)
+                  tma_load_3d(dst + x * kAttnBox + g * a.box_rows * 128, map, 64 * x, t.kvh, s_slot[gg], bar);
+            }
+          } else if (lane == 0) {
+            mbar_arrive_expect_tx(bar, SM::kTile);
+            for (int x = 0; x < HD / 64; ++x)
+              tma_load_2d(dst + x * kAttnBox, map, t.kvh * HD + 64 * x, t.kv0 + kAttnRows * i, bar);
+          }
+          if (patch) {
+            warp_wait(&tail_bar, tails++ & 1);
+            for (int r = lane >> 3; r < kAttnRows; r += 4) {
+              const int key = kAttnRows * i + r;
+              const bool in = key < t.len && (!PREFIX || s_slot[key / a.box_rows] >= 0);
+              if (!in)
+                for (int x = 0; x < HD / 64; ++x)
+                  *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_cta();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+          }
+        }
+      }
+    }
+    // every copy has landed before the CTA may exit (phases already consumed return at once)
+    if (lane == 0) {
+      for (uint32_t k = it > ST ? it - ST : 0; k < it; ++k) mbar_wait(&full[k % ST], (k / ST) & 1, a.err);
+      for (int j = 0; j < 2; ++j)
+        if (qc[j]) mbar_wait(&q_full[j], (qc[j] - 1) & 1, a.err);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer
+    constexpr uint32_t id_s = umma_idesc_bf16(kAttnRows, kAttnRows), id_o = umma_idesc_bf16_bmn(kAttnRows, HD);
+    uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, tiles[2] = {0, 0};
+    FwdItem t;
+    while (next_item(t)) {
+      const int n = max(t.n0, t.n1);
+      if (n == 0) continue;
+      auto tile_at = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
+      auto scores = [&](int j, uint32_t k, bool last) {
+        attn_mma_ss<HD>(tmem + kAttnRows * j, base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
+        umma_commit_warp(&s_full[j]);
+        if (last) umma_commit_warp(&q_empty[j]);
+      };
+      warp_wait(&full[it % ST], (it / ST) & 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int nj = j ? t.n1 : t.n0;
+        if (nj == 0) continue;
+        warp_wait(&q_full[j], qc[j]++ & 1);
+        tc_fence_after();
+        scores(j, it, nj == 1);
+      }
+      umma_commit_warp(&empty[it % ST]);
+      for (int i = 0; i < n; ++i, it += 2) {
+        const uint32_t kv = it + 1, kn = it + 2;
+        warp_wait(&full[kv % ST], (kv / ST) & 1);
+        if (i + 1 < n) warp_wait(&full[kn % ST], (kn / ST) & 1);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int nj = j ? t.n1 : t.n0;
+          if (i >= nj) continue;
+          warp_wait(&p_full[j], pc[j]++ & 1);
+          if (i == 0) {
+            if (tiles[j] > 0) warp_wait(&o_free[j], (tiles[j] - 1) & 1);
+            ++tiles[j];
+          }
+          tc_fence_after();
+          const unsigned char* v = tile_at(kv);
+#pragma unroll
+          for (int k = 0; k < kAttnRows / 16; ++k)
+            umma_bf16_ts_warp(tmem + 2 * kAttnRows + HD * j, tmem + kAttnRows * j + 8 * k,
+                              umma_desc_sw128_mn(v, kAttnBox) + 128 * k, id_o, (i | k) != 0);
+          umma_commit_warp(&o_done[j]);
+          if (i + 1 < nj) scores(j, kn, i + 2 == nj);
+        }
+        umma_commit_warp(&empty[kv % ST]);
+        if (i + 1 < n) umma_commit_warp(&empty[kn % ST]);
+      }
+    }
+    umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
+    if (lane == 0) mbar_wait(&mma_done, 0, a.err);
+  } else if (warp == 2) {
+    // ---- finder
+    if constexpr (!PREFIX) {
+      AttnOrder ord{a.cu, a.batch, a.pair_heads ? kAttnRows : 2 * kAttnRows, s_cache, 0, 0};
+      const bool ok = ord.init(a.T, lane);
+      if (!ok && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
+      const int64_t work = (int64_t)ord.total * a.units;
+      for (uint32_t k = 0;; ++k) {
+        const uint32_t s = k % kFwdSched;
+        if (k >= kFwdSched && !warp_wait(&it_empty[s], ((k / kFwdSched) - 1) & 1)) break;
+        const int64_t w = attn_deal(k, blockIdx.x, gridDim.x);
+        const bool done = (int64_t)k * gridDim.x >= work;
+        FwdItem t = {};
+        if (w < work) {
+          int seq, cost;
+          ord.find((uint32_t)(w / a.units), lane, seq, cost);
+          const int hu = (int)(w % a.units);
+          const int start = a.cu[seq], len = a.cu[seq + 1] - start;
+          if (a.pair_heads) {
+            t.head0 = 2 * hu;
+            t.head1 = t.head0 + 1;
+            t.row0 = t.row1 = start + kAttnRows * (cost - 1);
+            t.n0 = t.n1 = cost;
+          } else {
+            t.head0 = t.head1 = hu;
+            t.row0 = start + 2 * kAttnRows * (cost - 1);
+            t.row1 = t.row0 + kAttnRows;
+            t.n0 = 2 * cost - 1;
+            t.n1 = t.row1 < start + len ? 2 * cost : 0;
+          }
+          t.kvh = t.head0 / a.group;
+          t.kv0 = start;
+          t.len = len;
+          t.valid = 1;
+        } else if (!done) {
+          t.valid = 1;  // an empty item: this CTA has none in the last round
+        }
+        if (lane == 0) {
+          s_item[s] = t;
+          mbar_arrive(&it_full[s]);
+        }
+        __syncwarp();
+        if (done) break;
+      }
+    }
+  } else if (warp == 3) {
+    if constexpr (!PREFIX) {
+      if (a.zero_rest) {
+        bool bad = false;
+        for (int s = lane; s < a.batch; s += 32) bad |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T;
+        bad = __any_sync(0xffffffffu, bad) || a.batch == 0;
+        const int64_t first = bad ? 0 : a.cu[0], last = bad ? 0 : a.cu[a.batch];
+        attn_zero_rest(a.out, a.T, (int64_t)a.n_q * (HD / 8), first, last, lane);
+        if (a.lse)
+          for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < (first + a.T - last) * a.n_q; i += (int64_t)gridDim.x * 32) {
+            const int64_t r = i / a.n_q;
+            a.lse[(i % a.n_q) * a.T + (r < first ? r : last + (r - first))] = -INFINITY;
+          }
+      }
+    }
+  } else {
+    // ---- softmax, rescaling, epilogue
+    const int j = (warp - 4) >> 2, qtr = warp & 3, row = 32 * qtr + lane;
+    const uint32_t lanes = (uint32_t)(32 * qtr) << 16;
+    const uint32_t t_s = tmem + lanes + kAttnRows * j, t_o = tmem + lanes + 2 * kAttnRows + HD * j;
+    const float c = a.scale_log2;
+    uint32_t done = 0;  // blocks of this slot so far
+    FwdItem t;
+    while (next_item(t)) {
+      const int n = j ? t.n1 : t.n0;
+      if (n == 0) continue;
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < n; ++i, ++done) {
+        warp_wait(&s_full[j], done & 1);
+        tc_fence_after();
+        float s[kAttnRows];
+        tmem_ld128(t_s, s);
+        if constexpr (PREFIX) {
+          if (!((s_whole >> i) & 1)) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = kAttnRows * i + 32 * x + lane;
+              const uint32_t in = __ballot_sync(0xffffffffu, key < px_len && s_slot[min(key, px_len - 1) / a.box_rows] >= 0);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((in >> e) & 1)) s[32 * x + e] = -INFINITY;
+            }
+          }
+        } else if (i == n - 1) {  // the diagonal block: keys after the row (and so behind the sequence) are not seen
+#pragma unroll
+          for (int e = 0; e < kAttnRows; ++e)
+            if (e > row) s[e] = -INFINITY;
+        }
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < kAttnRows; ++e) top = fmaxf(top, s[e]);
+        if (i == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, (top - m) * c > kRescale)) {  // also where m is -inf and top is not
+          const float m_new = fmaxf(m, top);
+          const float f = m_new == m ? 1.f : ex2((m - m_new) * c);
+          m = m_new;
+          l *= f;
+          warp_wait(&o_done[j], (done - 1) & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < HD / 32; ++x) {
+            float o[32];
+            tmem_ld32(t_o + 32 * x, o);
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+            tmem_st32(t_o + 32 * x, w);
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m * c;
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = ex2(fmaf(s[32 * x + 2 * e], c, off)), p1 = ex2(fmaf(s[32 * x + 2 * e + 1], c, off));
+            sum0 += p0;
+            sum1 += p1;
+            w[e] = pack2(p0, p1);
+          }
+          tmem_st16(t_s + 16 * x, w);
+        }
+        l += sum0 + sum1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[j]);
+      }
+      warp_wait(&o_done[j], (done - 1) & 1);
+      tc_fence_after();
+      float o[HD];
+#pragma unroll
+      for (int x = 0; x < HD / 32; ++x) tmem_ld32(t_o + 32 * x, o + 32 * x);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[j]);
+      if constexpr (PREFIX) {
+        const int b = (j ? t.row1 : t.row0) * a.bpt + row / a.group, g = row % a.group;
+        if (row < a.bpt * a.group && b < a.batch) {
+          const int64_t r = (int64_t)px_chunk * a.batch * a.n_q + (int64_t)b * a.n_q + t.kvh * a.group + g;
+          a.part_ml[r] = make_float2(m * c, l);
+          float4* dst = reinterpret_cast<float4*>(a.part_o + r * HD);
+#pragma unroll
+          for (int e = 0; e < HD / 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      } else {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
+        unsigned char* buf = base + SM::kOut + (warp - 4) * kStageBytes;
+        const int row0 = (j ? t.row1 : t.row0) + 32 * qtr, head = j ? t.head1 : t.head0;
+        const int rows = t.kv0 + t.len - row0;  // rows of this warp that belong to the sequence
+        if (a.lse && lane < rows) a.lse[(int64_t)head * a.T + row0 + lane] = m * a.scale + logf(l);
+#pragma unroll
+        for (int x = 0; x < HD / 64; ++x) {
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            const float* v = o + 64 * x + 8 * ch;
+            *reinterpret_cast<uint4*>(buf + attn_swz(lane, ch)) =
+                make_uint4(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv), pack2(v[4] * inv, v[5] * inv),
+                           pack2(v[6] * inv, v[7] * inv));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r4 = 0; r4 < 8; ++r4) {
+            const int r = 4 * r4 + (lane >> 3);
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + attn_swz(r, lane & 7));
+            if (r < rows) a.out[((int64_t)(row0 + r) * a.n_q + head) * (HD / 8) + 8 * x + (lane & 7)] = v;
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+const void* attention_fwd_kernel(int head_dim, bool prefix) {
+  if (head_dim == 64)
+    return prefix ? reinterpret_cast<const void*>(&qkvp_attention_fwd_kernel<64, true>)
+                  : reinterpret_cast<const void*>(&qkvp_attention_fwd_kernel<64, false>);
+  return prefix ? reinterpret_cast<const void*>(&qkvp_attention_fwd_kernel<128, true>)
+                : reinterpret_cast<const void*>(&qkvp_attention_fwd_kernel<128, false>);
+}
+
+int attention_fwd_smem_bytes(int head_dim, bool prefix) {
+  const int out = prefix ? 0 : 8 * kStageBytes;
+  return (head_dim == 64 ? FwdSmem<64>::kOut : FwdSmem<128>::kOut) + out + 1024;
+}
+int attention_fwd_threads() { return kFwdThreads; }
+
+}  // namespace qkvp

@@ -333,6 +333,40 @@ int ns_gram_threads();
 int ns_poly_threads();
 int ns_apply_threads();
 
+// Attention over the prologue's outputs. Device status bits, as in the C header.
+constexpr int kDevBadPage = 1, kDevBadLength = 4, kDevBadSequence = 8;
+constexpr int kAttnBlock = 128;      // rows of a block of queries or keys
+constexpr int kAttnMaxChunk = 4096;  // keys of the shared prefix per CTA of its kernel (at most)
+struct AttnFwdArgs {
+  int32_t n_q, n_kv, group;
+  int32_t batch;           // sequences
+  float scale;             // of q . k
+  float scale_log2;        // scale * log2(e)
+  int* err;
+  int32_t* dev_status;
+  // whole prompts
+  int64_t T;
+  const int32_t* cu;       // [batch + 1] row offsets of the sequences
+  int32_t pair_heads;      // a CTA's two slots: two heads at the same rows, else two row blocks of a head
+  int32_t units;           // head units: n_q / 2 or n_q
+  int32_t zero_rest;       // zero the rows of no sequence
+  uint4* out;              // bf16 [T, n_q, head_dim]
+  float* lse;              // [n_q, T], or null
+  // shared prefix
+  const int32_t* prefix_pages;
+  int32_t prefix_len;
+  int32_t num_pages, page_size;
+  int32_t box_rows;        // keys per copy: the largest power of two that divides page_size, at most 128
+  int32_t bpt;             // sequences per tile of 128 query rows
+  int32_t row_tiles, pairs;  // tiles of query rows per key/value head, and CTAs (two tiles each) for them
+  int32_t chunk;           // keys per CTA
+  float* part_o;           // [chunks][batch * n_q][head_dim] sums of e^(s - m) v
+  float2* part_ml;         // [chunks][batch * n_q] (m log2(e), sum of e^(s - m))
+};
+const void* attention_fwd_kernel(int head_dim, bool prefix);
+int attention_fwd_smem_bytes(int head_dim, bool prefix);
+int attention_fwd_threads();
+
 // One thread whose only wait never completes (the bounded-wait self-test).
 const void* wait_selftest_kernel();
 

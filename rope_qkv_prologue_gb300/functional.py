@@ -252,6 +252,58 @@ def mla_kv_path_beside(side, pos, w, page, offset, pool, kv_rows=None, kv_proj=N
     return on_side_stream(side, kv_path)
 
 
+def _attention_layout(q, k, v):
+    """The layout of q [rows, n_q, D] over k, v [rows, n_kv, D], all contiguous bf16 on one device."""
+    _check_dev(q, k, v)
+    for t in (q, k, v):
+        if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError("q, k and v must be contiguous bf16 [T, heads, head_dim] tensors")
+    if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("k and v must have one shape, and q's rows and head_dim")
+    if k.device != q.device or v.device != q.device:
+        raise ValueError("q, k and v must live on one device")
+    return C.layout("sectioned", q.shape[1], k.shape[1], q.shape[2])
+
+
+def _check_like(t, shape, dtype, device, name):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
+
+
+def _check_offsets(cu_seqlens, device):
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    _check_like(cu_seqlens, cu_seqlens.shape, torch.int32, device, "cu_seqlens")
+    return cu_seqlens.numel() - 1
+
+
+def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None, dev_status=None, stream=None):
+    """Causal attention over packed sequences: q [T, n_q, D], k, v [T, n_kv, D]
+    bf16 as prologue_forward returns them, cu_seqlens int32 [batch + 1] on the
+    device (sequence s is the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1).
+    Returns out [T, n_q, D], or (out, lse [n_q, T] float32) with save_lse.
+    scale defaults to D ** -0.5. Rows of no sequence are zero in an out made
+    here, and left as they are in one given (lse: -inf, in both)."""
+    L = _attention_layout(q, k, v)
+    batch = _check_offsets(cu_seqlens, q.device)
+    flags = 0
+    if out is None:
+        out, flags = torch.empty_like(q), C.QKVP_ZERO_REST
+    else:
+        _check_like(out, q.shape, torch.bfloat16, q.device, "out")
+    lse = None
+    if save_lse:
+        fill = torch.empty if flags else _neg_inf
+        lse = fill((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    C.qkv_attention_fwd(L, q.shape[0], batch, cu_seqlens, q, k, v, 0.0 if scale is None else scale, flags, out, lse,
+                        dev_status, stream)
+    return (out, lse) if save_lse else out
+
+
+def _neg_inf(shape, dtype, device):
+    return torch.full(shape, float("-inf"), dtype=dtype, device=device)
+
+
 class QKVPrologue(torch.autograd.Function):
     """packed [T, row] -> (q, k, v); backward writes d(packed) in one pass.
 
