@@ -468,6 +468,52 @@ QKVP_API int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t bat
                                float* lse, int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * qkv_attention_decode -- attention of one new token per sequence over the
+ * paged pool that qkv_prologue_pool_write fills, with a prefix that the whole
+ * batch may share.
+ *
+ * Sequence b attends the prefix_len tokens of prefix_pages, then its own
+ * lengths[b] tokens in the pages page_table[b]: token t of a page list is at
+ * pool slot [list[t / page_size], t % page_size]. (The new token's own k and v
+ * are written into the pool before this call and counted in lengths[b].)
+ *     out[b, h] = sum_t softmax_t(scale q[b, h] . k_t[g]) v_t[g],
+ * g = h / (n_q / n_kv). A sequence without any token gives zeros (lse -inf).
+ * Arithmetic as qkv_attention_fwd; partial results of key ranges are fp32 and
+ * are joined in a fixed order (which depends on the lengths of the batch).
+ *
+ * layout       GQA layout; n_q, n_kv, head_dim are used.
+ * batch        sequences (0 .. 2^20).
+ * q            bf16 [batch, n_q, head_dim].
+ * k_pool, v_pool  bf16 [num_pages, page_size, n_kv, head_dim]. Slots that no
+ *              sequence names are never used, whatever they hold.
+ * page_table   int32 [batch, max_pages] with table_stride (>= max_pages)
+ *              elements between rows; only the pages that lengths[b] tokens
+ *              need are read. A page outside [0, num_pages) sets
+ *              QKVP_DEV_BAD_PAGE; its tokens are not attended.
+ * lengths      int32 [batch], device memory: a captured call follows lengths
+ *              that change. A length outside [0, max_pages * page_size] is
+ *              clamped and sets QKVP_DEV_BAD_LENGTH.
+ * prefix_pages int32 [ceil(prefix_len / page_size)] or NULL (prefix_len 0).
+ * scale        > 0 and finite; 0 means head_dim^-0.5.
+ * out          bf16 [batch, n_q, head_dim].
+ * lse          float32 [batch, n_q] or NULL.
+ * dev_status   int32 or NULL, bits OR-ed in.
+ * workspace    at least qkv_attention_decode_workspace() bytes, 16-byte
+ *              aligned, any contents. Two calls whose work can overlap on the
+ *              GPU must not share a workspace.
+ * ------------------------------------------------------------------------- */
+QKVP_API int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q, const void* k_pool,
+                                  const void* v_pool, int32_t num_pages, int32_t page_size, const int32_t* page_table,
+                                  int32_t max_pages, int64_t table_stride, const int32_t* lengths,
+                                  const int32_t* prefix_pages, int32_t prefix_len, float scale, void* out, float* lse,
+                                  int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of qkv_attention_decode for these arguments on the current
+ * device (host only; batch 0: 0). */
+QKVP_API int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size,
+                                            int32_t max_pages, int32_t prefix_len, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
  * qkv_prologue_device_error -- read (and with clear != 0, reset) the
  * library's device error word on the current device. Bit 1 means a
  * pipelined kernel's bounded wait on its shared-memory pipeline gave up

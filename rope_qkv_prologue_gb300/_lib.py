@@ -111,6 +111,9 @@ _SIGS = {
     "qkv_newton_schulz_plan": ([_LP, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_int32),
                                 ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "qkv_attention_fwd": ([_LP, _i64, _i32, _vp, _vp, _vp, _vp, _f32, _u32, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "qkv_attention_decode": ([_LP, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _i32, _f32, _vp, _vp,
+                              _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+    "qkv_attention_decode_workspace": ([_LP, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "qkv_prologue_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "qkv_prologue_version": ([], ctypes.c_int),
     "qkv_prologue_device_error": ([ctypes.c_int, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
@@ -322,3 +325,25 @@ def qkv_attention_fwd(L, T, batch, cu_seqlens, q, k, v, scale, flags, out, lse=N
     st = _lib.qkv_attention_fwd(ctypes.byref(L), int(T), int(batch), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
                                 float(scale), int(flags), _ptr(out), _ptr(lse), _ptr(dev_status), _stream(stream))
     return _ret(st, "qkv_attention_fwd", check)
+
+
+def qkv_attention_decode(L, batch, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages, table_stride,
+                         lengths, prefix_pages, prefix_len, scale, out, lse=None, dev_status=None, workspace=None,
+                         workspace_bytes=0, stream=None, check=True):
+    st = _lib.qkv_attention_decode(ctypes.byref(L), int(batch), _ptr(q), _ptr(k_pool), _ptr(v_pool), int(num_pages),
+                                   int(page_size), _ptr(page_table), int(max_pages), int(table_stride), _ptr(lengths),
+                                   _ptr(prefix_pages), int(prefix_len), float(scale), _ptr(out), _ptr(lse),
+                                   _ptr(dev_status), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _ret(st, "qkv_attention_decode", check)
+
+
+def qkv_attention_decode_workspace(L, batch, page_size, max_pages, prefix_len, check=True):
+    """Workspace bytes of qkv_attention_decode for these arguments (a status
+    code instead when check is False and the call fails)."""
+    n = ctypes.c_size_t(0)
+    st = _lib.qkv_attention_decode_workspace(ctypes.byref(L), int(batch), int(page_size), int(max_pages),
+                                             int(prefix_len), ctypes.byref(n))
+    if not check and st != QKVP_OK:
+        return st
+    _ret(st, "qkv_attention_decode_workspace", True)
+    return n.value

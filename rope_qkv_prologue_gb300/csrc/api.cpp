@@ -539,6 +539,78 @@ int check_attention(const qkvp_layout* layout, int32_t batch, float scale, float
   return QKVP_OK;
 }
 
+// Launch shape and workspace of a decode call. Partial results: one row of
+// head_dim floats and (maximum, sum) per query head for every sequence, every
+// part, and every (key range of the shared prefix, sequence).
+struct DecodePlan {
+  bool apart = false;         // the prefix has its own kernel (tensor cores, all sequences' rows at once)
+  int box_rows = 0, bpt = 0, row_tiles = 0, pairs = 0, chunk = 0, chunks = 0;
+  int head_blocks = 1, ranges = 0, grid = 0;
+  int64_t rows = 0;           // partial results, each of n_q rows
+};
+
+// The prefix is computed apart when several sequences share it: the tensor-core
+// kernel then reads it once for all their rows. It copies pieces of pages of a
+// power of two of at least 8 keys (whole 8-row groups of the swizzled layout)
+// and holds whole groups of heads in a tile of 128 rows; otherwise every
+// sequence walks the prefix itself.
+constexpr int kDecApartKeys = 128;
+
+void plan_decode(const qkvp_layout* L, int32_t batch, int32_t page_size, int32_t max_pages, int32_t prefix_len, int sms,
+                 DecodePlan* p) {
+  const int group = L->n_q / L->n_kv;
+  p->box_rows = std::min(page_size & -page_size, kAttnBlock);
+  p->apart = batch >= 2 && prefix_len >= kDecApartKeys && p->box_rows >= 8 && group <= kAttnBlock;
+  if (p->apart) {
+    p->bpt = kAttnBlock / group;
+    p->row_tiles = (batch + p->bpt - 1) / p->bpt;
+    p->pairs = (p->row_tiles + 1) / 2;
+    const int per = p->pairs * L->n_kv;
+    const int64_t want = std::max(1, sms / per);
+    int64_t chunk = (prefix_len + want - 1) / want;
+    chunk = (chunk + kAttnBlock - 1) / kAttnBlock * kAttnBlock;
+    p->chunk = (int)std::min<int64_t>(std::max<int64_t>(chunk, 2 * kAttnBlock), kAttnMaxChunk);
+    p->chunks = (prefix_len + p->chunk - 1) / p->chunk;
+  }
+  p->head_blocks = (group + 15) / 16;
+  const int64_t heads = (int64_t)L->n_kv * p->head_blocks;
+  const int64_t warps = (int64_t)sms * attention_decode_warps();
+  const int64_t keys = (int64_t)max_pages * page_size + (p->apart ? 0 : prefix_len);
+  const int64_t most = (int64_t)batch * ((keys + 15) / 16);  // tiles, at most
+  p->ranges = (int)std::max<int64_t>(1, std::min<int64_t>(warps / heads, (most + kDecMinTiles - 1) / kDecMinTiles));
+  const int64_t ctas = (p->ranges * heads + attention_decode_warps() - 1) / attention_decode_warps();
+  p->grid = (int)std::min<int64_t>(ctas, sms);
+  p->rows = (int64_t)batch + p->ranges + (int64_t)p->chunks * batch;
+}
+
+size_t decode_workspace(const qkvp_layout* L, const DecodePlan& p) {
+  return (size_t)p.rows * L->n_q * ((size_t)L->head_dim + 2) * sizeof(float);
+}
+
+int check_decode(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages, int32_t prefix_len) {
+  float unused;
+  QKVP_TRY(check_attention(layout, batch, 0.f, &unused));
+  if (page_size <= 0) return QKVP_ERR_VALUE;
+  if (max_pages < 0 || (int64_t)max_pages * page_size > INT32_MAX || prefix_len < 0 || prefix_len > INT32_MAX - 4096 ||
+      batch > (1 << 20))
+    return QKVP_ERR_SHAPE;
+  return QKVP_OK;
+}
+
+// Tensor map of bf16 [n2, n1, cols] (cols contiguous) read in boxes of 64 x
+// box1 x box2 with the 128-byte swizzle; outside it a box reads 0.
+bool bf16_box_map(CUtensorMap* map, const void* ptr, int64_t n2, int64_t n1, int64_t cols, int box2, int box1) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)n1, (cuuint64_t)n2};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(cols * n1) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool overlaps(const void* p, size_t pn, const void* q, size_t qn) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
   return a < b + qn && b < a + pn;
@@ -1256,6 +1328,124 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   void* args[] = {&tq, &tk, &tv, &a};
   return launch_args(kern, most < sms ? most : sms, attention_fwd_threads(), smem, static_cast<cudaStream_t>(stream),
                      args);
+}
+
+int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,
+                                   int32_t prefix_len, size_t* bytes) {
+  QKVP_TRY(check_decode(layout, batch, page_size, max_pages, prefix_len));
+  if (!bytes) return QKVP_ERR_NULL;
+  *bytes = 0;
+  if (batch == 0) return QKVP_OK;
+  int sms = 0;
+  QKVP_TRY(current_device(&sms));
+  DecodePlan p;
+  plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, &p);
+  *bytes = decode_workspace(layout, p);
+  return QKVP_OK;
+}
+
+int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q, const void* k_pool,
+                         const void* v_pool, int32_t num_pages, int32_t page_size, const int32_t* page_table,
+                         int32_t max_pages, int64_t table_stride, const int32_t* lengths, const int32_t* prefix_pages,
+                         int32_t prefix_len, float scale, void* out, float* lse, int32_t* dev_status, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  QKVP_TRY(check_decode(layout, batch, page_size, max_pages, prefix_len));
+  QKVP_TRY(check_pool(num_pages, page_size));
+  float sc = 0.f;
+  QKVP_TRY(check_attention(layout, batch, scale, &sc));
+  if (table_stride < max_pages) return QKVP_ERR_SHAPE;
+  if (!q || !k_pool || !v_pool || !lengths || !out || (max_pages > 0 && !page_table) || (prefix_len > 0 && !prefix_pages))
+    return QKVP_ERR_NULL;
+  for (const void* p : {q, k_pool, v_pool, (const void*)out})
+    if (!aligned16(p)) return QKVP_ERR_ALIGN;
+  for (const void* p : {(const void*)lengths, (const void*)page_table, (const void*)prefix_pages, (const void*)lse,
+                        (const void*)dev_status})
+    if (p && !aligned4(p)) return QKVP_ERR_ALIGN;
+  if (batch == 0) return QKVP_OK;
+  int sms = 0;
+  QKVP_TRY(current_device(&sms));
+  DecodePlan p;
+  plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, &p);
+  if (!workspace || workspace_bytes < decode_workspace(layout, p)) return QKVP_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int hd = layout->head_dim;
+  float* part_o = static_cast<float*>(workspace);
+  float2* part_ml = reinterpret_cast<float2*>(part_o + p.rows * layout->n_q * hd);
+  const int group = layout->n_q / layout->n_kv;
+  const float scale_log2 = (float)((double)sc * 1.4426950408889634);
+  if (p.apart) {
+    for (const void* x : {q, k_pool, v_pool})  // tensor maps cover this GPU's own memory
+      if (!on_current_device(x)) return QKVP_ERR_VALUE;
+    CUtensorMap tq, tk, tv;
+    const int64_t slots = (int64_t)num_pages * page_size;
+    if (!bf16_box_map(&tq, q, batch, layout->n_q, hd, p.bpt, group) ||
+        !bf16_box_map(&tk, k_pool, slots, layout->n_kv, hd, p.box_rows, 1) ||
+        !bf16_box_map(&tv, v_pool, slots, layout->n_kv, hd, p.box_rows, 1))
+      return QKVP_ERR_LAUNCH;
+    AttnFwdArgs f;
+    std::memset(&f, 0, sizeof(f));
+    f.n_q = layout->n_q;
+    f.n_kv = layout->n_kv;
+    f.group = group;
+    f.batch = batch;
+    f.scale = sc;
+    f.scale_log2 = scale_log2;
+    f.dev_status = dev_status;
+    f.prefix_pages = prefix_pages;
+    f.prefix_len = prefix_len;
+    f.num_pages = num_pages;
+    f.page_size = page_size;
+    f.box_rows = p.box_rows;
+    f.bpt = p.bpt;
+    f.row_tiles = p.row_tiles;
+    f.pairs = p.pairs;
+    f.chunk = p.chunk;
+    const int64_t first = (int64_t)(batch + p.ranges) * layout->n_q;
+    f.part_o = part_o + first * hd;
+    f.part_ml = part_ml + first;
+    if ((f.err = device_error_word()) == nullptr) return QKVP_ERR_LAUNCH;
+    const void* kern = attention_fwd_kernel(hd, true);
+    const size_t smem = (size_t)attention_fwd_smem_bytes(hd, true);
+    if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
+    void* args[] = {&tq, &tk, &tv, &f};
+    QKVP_TRY(launch_args(kern, (int64_t)p.chunks * p.pairs * layout->n_kv, attention_fwd_threads(), smem, st, args));
+  }
+  AttnDecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.n_q = layout->n_q;
+  a.n_kv = layout->n_kv;
+  a.group = group;
+  a.head_blocks = p.head_blocks;
+  a.batch = batch;
+  a.scale_log2 = scale_log2;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_pool = static_cast<const uint4*>(k_pool);
+  a.v_pool = static_cast<const uint4*>(v_pool);
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.lengths = lengths;
+  a.prefix_pages = prefix_pages;
+  a.joint_len = p.apart ? 0 : prefix_len;
+  a.prefix_chunks = p.chunks;
+  a.ranges = p.ranges;
+  a.part_o = part_o;
+  a.part_ml = part_ml;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.dev_status = dev_status;
+  // warps per head of the join: about four partial results each
+  const int64_t parts = p.ranges / batch + 2 + p.chunks;
+  a.wph = parts > 16 ? 8 : (parts > 8 ? 4 : (parts > 4 ? 2 : 1));
+  const void* kern = attention_decode_kernel(hd);
+  const size_t smem = (size_t)attention_decode_smem_bytes(hd);
+  if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
+  QKVP_TRY(launch(kern, p.grid, attention_decode_threads(), smem, st, &a));
+  const int per = kJoinWarps / a.wph;
+  return launch(attention_join_kernel(hd), (int64_t)batch * ((layout->n_q + per - 1) / per), 32 * kJoinWarps, 0, st, &a);
 }
 
 int qkv_prologue_wait_selftest(void* stream) {

@@ -367,6 +367,39 @@ const void* attention_fwd_kernel(int head_dim, bool prefix);
 int attention_fwd_smem_bytes(int head_dim, bool prefix);
 int attention_fwd_threads();
 
+// One query row per sequence over the paged pool.
+constexpr int kDecMinTiles = 4;   // tiles of 16 keys of a part (at least)
+constexpr int kJoinWarps = 8;     // warps per CTA of the kernel that joins the partial results
+struct AttnDecodeArgs {
+  int32_t n_q, n_kv, group;
+  int32_t head_blocks;     // blocks of 16 query heads per key/value head
+  int32_t batch;
+  float scale_log2;
+  const uint16_t* q;       // bf16 [batch, n_q, head_dim]
+  const uint4* k_pool;
+  const uint4* v_pool;
+  int32_t num_pages, page_size;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int32_t max_pages;
+  const int32_t* lengths;
+  const int32_t* prefix_pages;
+  int64_t joint_len;       // prefix keys that every sequence walks itself (0: none, or computed apart)
+  int32_t prefix_chunks;   // key ranges of the prefix kernel's partial results (0: none)
+  int32_t ranges;          // parts that the tiles of all sequences are cut into
+  int32_t wph;             // join: warps per head
+  float* part_o;           // [batch + ranges + prefix_chunks * batch][n_q][head_dim]
+  float2* part_ml;         // the same rows: (maximum in powers of two, sum)
+  uint16_t* out;           // bf16 [batch, n_q, head_dim]
+  float* lse;              // [batch, n_q], or null
+  int32_t* dev_status;
+};
+const void* attention_decode_kernel(int head_dim);
+const void* attention_join_kernel(int head_dim);
+int attention_decode_smem_bytes(int head_dim);
+int attention_decode_threads();
+int attention_decode_warps();
+
 // One thread whose only wait never completes (the bounded-wait self-test).
 const void* wait_selftest_kernel();
 

@@ -300,6 +300,68 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
     return (out, lse) if save_lse else out
 
 
+def _check_pages(pages, name, device, dim):
+    if pages.dim() != dim or pages.dtype != torch.int32 or pages.device != device:
+        raise ValueError(f"{name} must be a {dim}-dimensional int32 tensor on {device}")
+    if pages.shape[-1] > 1 and pages.stride(-1) != 1:
+        raise ValueError(f"the entries of a row of {name} must be contiguous")
+
+
+def attention_decode_workspace_bytes(n_q, n_kv, head_dim, batch, page_size, max_pages, prefix_len=0):
+    """Workspace bytes attention_decode needs for these sizes on the current device."""
+    return C.qkv_attention_decode_workspace(C.layout("sectioned", n_q, n_kv, head_dim), batch, page_size, max_pages,
+                                            prefix_len)
+
+
+def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, prefix_len=0, scale=None,
+                     save_lse=False, out=None, workspace=None, dev_status=None, stream=None):
+    """Attention of one new token per sequence over a paged pool: q [B, n_q, D]
+    bf16; k_pool, v_pool [num_pages, page_size, n_kv, D] as prologue_pool_write
+    fills them; page_table int32 [B, max_pages] (rows may be a slice of a wider
+    table) and lengths int32 [B] name each sequence's own tokens, the new one
+    among them. The first prefix_len tokens of prefix_pages (int32 [n]) precede
+    them in every sequence: stored once, and read once for the whole batch.
+    Returns out [B, n_q, D], or (out, lse [B, n_q] float32) with save_lse.
+    `workspace` (a device tensor of attention_decode_workspace_bytes bytes) is
+    allocated here when not given."""
+    _check_dev(q, k_pool, v_pool, page_table, lengths, prefix_pages)
+    for t, n in ((q, 3), (k_pool, 4), (v_pool, 4)):
+        if t.dim() != n or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError("q must be a contiguous bf16 [B, n_q, D] and the pools contiguous bf16 "
+                             "[num_pages, page_size, n_kv, D] tensors")
+    dev, (B, n_q, D) = q.device, q.shape
+    if k_pool.shape != v_pool.shape or k_pool.shape[3] != D or k_pool.device != dev or v_pool.device != dev:
+        raise ValueError("k_pool and v_pool must have one shape, q's head_dim and q's device")
+    _check_pages(page_table, "page_table", dev, 2)
+    max_pages = page_table.shape[1]
+    if page_table.shape[0] != B or (B > 1 and page_table.stride(0) < max_pages):
+        raise ValueError("page_table must have a row per sequence, and the rows must not overlap")
+    _check_like(lengths, (B,), torch.int32, dev, "lengths")
+    num_pages, page_size = k_pool.shape[:2]
+    if prefix_len:
+        if prefix_pages is None or prefix_len < 0:
+            raise ValueError("a prefix needs prefix_len >= 0 and its pages")
+        _check_pages(prefix_pages, "prefix_pages", dev, 1)
+        if prefix_pages.numel() * page_size < prefix_len:
+            raise ValueError("prefix_pages must hold prefix_len tokens")
+    else:
+        prefix_pages = None
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_like(out, q.shape, torch.bfloat16, dev, "out")
+    lse = torch.empty((B, n_q), dtype=torch.float32, device=dev) if save_lse else None
+    L = C.layout("sectioned", n_q, k_pool.shape[2], D)
+    need = C.qkv_attention_decode_workspace(L, B, page_size, max_pages, prefix_len)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    C.qkv_attention_decode(L, B, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages,
+                           page_table.stride(0) if B > 1 else max_pages, lengths, prefix_pages,
+                           prefix_len, 0.0 if scale is None else scale, out, lse, dev_status, workspace,
+                           workspace.numel() * workspace.element_size(), stream)
+    return (out, lse) if save_lse else out
+
+
 def _neg_inf(shape, dtype, device):
     return torch.full(shape, float("-inf"), dtype=dtype, device=device)
 
