@@ -468,6 +468,34 @@ QKVP_API int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t bat
                                float* lse, int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * qkv_attention_bwd -- the gradients of qkv_attention_fwd.
+ *
+ * With p_ij = exp(scale q_i . k_j - lse_i), delta_i = dout_i . out_i and
+ * ds_ij = p_ij (dout_i . v_j - delta_i):
+ *     dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,
+ *     dv_j = sum_i p_ij dout_i,
+ * dk and dv summed over the n_q / n_kv query heads of their group. p and ds are
+ * rounded to bf16 as operands of products with fp32 accumulation; one rounding
+ * of each gradient to bf16. Deterministic (no atomics).
+ *
+ * T, batch, cu_seqlens, q, k, v, scale: as the forward's.
+ * dout, out   bf16 [T, n_q, head_dim]; lse float32 [n_q, T]: the forward's.
+ * flags       QKVP_ZERO_REST: rows of no sequence of dq, dk and dv become zero
+ *             instead of being left as they are.
+ * dq          bf16 [T, n_q, head_dim] out; dk, dv bf16 [T, n_kv, head_dim] out.
+ * workspace   at least qkv_attention_bwd_workspace() bytes (float32 [n_q, T]),
+ *             16-byte aligned, any contents. Two calls whose work can overlap on
+ *             the GPU must not share a workspace.
+ * ------------------------------------------------------------------------- */
+QKVP_API int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const int32_t* cu_seqlens,
+                               const void* dout, const void* q, const void* k, const void* v, const void* out,
+                               const float* lse, float scale, uint32_t flags, void* dq, void* dk, void* dv,
+                               int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of qkv_attention_bwd (host only; needs no device). */
+QKVP_API int qkv_attention_bwd_workspace(const qkvp_layout* layout, int64_t T, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
  * qkv_attention_decode -- attention of one new token per sequence over the
  * paged pool that qkv_prologue_pool_write fills, with a prefix that the whole
  * batch may share.

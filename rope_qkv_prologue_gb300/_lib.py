@@ -111,6 +111,9 @@ _SIGS = {
     "qkv_newton_schulz_plan": ([_LP, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_int32),
                                 ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "qkv_attention_fwd": ([_LP, _i64, _i32, _vp, _vp, _vp, _vp, _f32, _u32, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "qkv_attention_bwd": ([_LP, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _u32, _vp, _vp, _vp, _vp, _vp,
+                           ctypes.c_size_t, _vp], ctypes.c_int),
+    "qkv_attention_bwd_workspace": ([_LP, _i64, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "qkv_attention_decode": ([_LP, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _i32, _f32, _vp, _vp,
                               _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
     "qkv_attention_decode_workspace": ([_LP, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
@@ -325,6 +328,25 @@ def qkv_attention_fwd(L, T, batch, cu_seqlens, q, k, v, scale, flags, out, lse=N
     st = _lib.qkv_attention_fwd(ctypes.byref(L), int(T), int(batch), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
                                 float(scale), int(flags), _ptr(out), _ptr(lse), _ptr(dev_status), _stream(stream))
     return _ret(st, "qkv_attention_fwd", check)
+
+
+def qkv_attention_bwd(L, T, batch, cu_seqlens, dout, q, k, v, out, lse, scale, flags, dq, dk, dv, dev_status=None,
+                      workspace=None, workspace_bytes=0, stream=None, check=True):
+    st = _lib.qkv_attention_bwd(ctypes.byref(L), int(T), int(batch), _ptr(cu_seqlens), _ptr(dout), _ptr(q), _ptr(k),
+                                _ptr(v), _ptr(out), _ptr(lse), float(scale), int(flags), _ptr(dq), _ptr(dk), _ptr(dv),
+                                _ptr(dev_status), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    return _ret(st, "qkv_attention_bwd", check)
+
+
+def qkv_attention_bwd_workspace(L, T, check=True):
+    """Workspace bytes of qkv_attention_bwd (a status code instead when check is
+    False and the call fails)."""
+    n = ctypes.c_size_t(0)
+    st = _lib.qkv_attention_bwd_workspace(ctypes.byref(L), int(T), ctypes.byref(n))
+    if not check and st != QKVP_OK:
+        return st
+    _ret(st, "qkv_attention_bwd_workspace", True)
+    return n.value
 
 
 def qkv_attention_decode(L, batch, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages, table_stride,

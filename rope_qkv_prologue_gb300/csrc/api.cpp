@@ -1330,6 +1330,77 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
                      args);
 }
 
+int qkv_attention_bwd_workspace(const qkvp_layout* layout, int64_t T, size_t* bytes) {
+  float unused;
+  QKVP_TRY(check_attention(layout, 0, 0.f, &unused));
+  if (T < 0 || T > INT32_MAX - 256) return QKVP_ERR_SHAPE;
+  if (!bytes) return QKVP_ERR_NULL;
+  *bytes = (size_t)T * layout->n_q * sizeof(float);
+  return QKVP_OK;
+}
+
+int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const int32_t* cu_seqlens, const void* dout,
+                      const void* q, const void* k, const void* v, const void* out, const float* lse, float scale,
+                      uint32_t flags, void* dq, void* dk, void* dv, int32_t* dev_status, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  AttnBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  QKVP_TRY(check_attention(layout, batch, scale, &a.scale));
+  size_t need = 0;
+  QKVP_TRY(qkv_attention_bwd_workspace(layout, T, &need));
+  if (flags & ~(uint32_t)QKVP_ZERO_REST) return QKVP_ERR_FLAGS;
+  const void* vec[] = {dout, q, k, v, out, dq, dk, dv};
+  for (const void* p : vec)
+    if (!p) return QKVP_ERR_NULL;
+  if (!cu_seqlens || !lse) return QKVP_ERR_NULL;
+  for (const void* p : vec)
+    if (!aligned16(p)) return QKVP_ERR_ALIGN;
+  if (!aligned4(cu_seqlens) || !aligned4(lse) || (dev_status && !aligned4(dev_status))) return QKVP_ERR_ALIGN;
+  if (T == 0) return QKVP_OK;
+  if (!workspace || workspace_bytes < need) return QKVP_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
+  int sms = 0;
+  QKVP_TRY(current_device(&sms));
+  for (const void* p : {dout, q, k, v})  // tensor maps cover this GPU's own memory
+    if (!on_current_device(p)) return QKVP_ERR_VALUE;
+  const int hd = layout->head_dim;
+  CUtensorMap tq, td, tk, tv;
+  if (!bf16_tile_map(&tq, q, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
+      !bf16_tile_map(&td, dout, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
+      !bf16_tile_map(&tk, k, T, (int64_t)layout->n_kv * hd, kAttnBlock) ||
+      !bf16_tile_map(&tv, v, T, (int64_t)layout->n_kv * hd, kAttnBlock))
+    return QKVP_ERR_LAUNCH;
+  a.T = T;
+  a.n_q = layout->n_q;
+  a.n_kv = layout->n_kv;
+  a.group = layout->n_q / layout->n_kv;
+  a.batch = batch;
+  a.cu = cu_seqlens;
+  a.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  a.out = static_cast<const uint4*>(out);
+  a.dout = static_cast<const uint4*>(dout);
+  a.lse = lse;
+  a.delta = static_cast<float*>(workspace);
+  a.zero_rest = (flags & QKVP_ZERO_REST) != 0;
+  a.dq = static_cast<uint4*>(dq);
+  a.dk = static_cast<uint4*>(dk);
+  a.dv = static_cast<uint4*>(dv);
+  a.dev_status = dev_status;
+  if ((a.err = device_error_word()) == nullptr) return QKVP_ERR_LAUNCH;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t smem = (size_t)attention_bwd_smem_bytes(hd);
+  const void* kkv = attention_bwd_kernel(hd, true);
+  const void* kq = attention_bwd_kernel(hd, false);
+  if (!allow_smem(kkv, smem) || !allow_smem(kq, smem)) return QKVP_ERR_LAUNCH;
+  const int64_t rows_per_cta = 8 * 32 / (hd / 8);
+  const int64_t dgrid = (T * a.n_q + rows_per_cta - 1) / rows_per_cta;
+  QKVP_TRY(launch(attention_delta_kernel(hd), std::min<int64_t>(dgrid, 16 * (int64_t)sms), 256, 0, st, &a));
+  const int64_t blocks = T / kAttnBlock + std::max(batch, 1);  // at least the number of blocks
+  void* args[] = {&tq, &td, &tk, &tv, &a};
+  QKVP_TRY(launch_args(kkv, std::min<int64_t>(blocks * a.n_kv, sms), attention_bwd_threads(), smem, st, args));
+  return launch_args(kq, std::min<int64_t>(blocks * a.n_q, sms), attention_bwd_threads(), smem, st, args);
+}
+
 int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,
                                    int32_t prefix_len, size_t* bytes) {
   QKVP_TRY(check_decode(layout, batch, page_size, max_pages, prefix_len));

@@ -367,6 +367,29 @@ const void* attention_fwd_kernel(int head_dim, bool prefix);
 int attention_fwd_smem_bytes(int head_dim, bool prefix);
 int attention_fwd_threads();
 
+// Backward over whole prompts: delta, then the key/value and the query kernel.
+struct AttnBwdArgs {
+  int64_t T;
+  int32_t n_q, n_kv, group;
+  int32_t batch;
+  const int32_t* cu;
+  float scale, scale_log2;
+  const uint4* out;        // bf16 [T, n_q, head_dim]: the forward's result
+  const uint4* dout;
+  const float* lse;        // [n_q, T]
+  float* delta;            // [n_q, T]: workspace
+  int32_t zero_rest;
+  uint4* dq;
+  uint4* dk;
+  uint4* dv;
+  int32_t* dev_status;
+  int* err;
+};
+const void* attention_bwd_kernel(int head_dim, bool kv);
+const void* attention_delta_kernel(int head_dim);
+int attention_bwd_smem_bytes(int head_dim);
+int attention_bwd_threads();
+
 // One query row per sequence over the paged pool.
 constexpr int kDecMinTiles = 4;   // tiles of 16 keys of a part (at least)
 constexpr int kJoinWarps = 8;     // warps per CTA of the kernel that joins the partial results

@@ -300,6 +300,45 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
     return (out, lse) if save_lse else out
 
 
+def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspace=None, dev_status=None, stream=None):
+    """Gradients (dq, dk, dv) of attention_forward(q, k, v, cu_seqlens, scale) for
+    the upstream gradient dout [T, n_q, D] bf16, from the forward's out and lse.
+    Rows of no sequence get zero gradients. `workspace` (a device tensor of at
+    least 4 * n_q * T bytes) is allocated here when not given."""
+    L = _attention_layout(q, k, v)
+    T, n_q, _ = q.shape
+    batch = _check_offsets(cu_seqlens, q.device)
+    _check_like(dout, q.shape, torch.bfloat16, q.device, "dout")
+    _check_like(out, q.shape, torch.bfloat16, q.device, "out")
+    _check_like(lse, (n_q, T), torch.float32, q.device, "lse")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    if workspace is None:
+        workspace = torch.empty(max(4 * n_q * T, 16), dtype=torch.uint8, device=q.device)
+    C.qkv_attention_bwd(L, T, batch, cu_seqlens, dout, q, k, v, out, lse, 0.0 if scale is None else scale,
+                        C.QKVP_ZERO_REST, dq, dk, dv, dev_status, workspace,
+                        workspace.numel() * workspace.element_size(), stream)
+    return dq, dk, dv
+
+
+class PackedAttention(torch.autograd.Function):
+    """apply(q, k, v, cu_seqlens, scale=None) -> out: causal attention over packed
+    sequences with its gradients, the step after QKVPrologue.apply. The offsets
+    receive no gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale=None):
+        out, lse = attention_forward(q, k, v, cu_seqlens, scale, save_lse=True)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
+        ctx.scale = scale
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
+        dq, dk, dv = attention_backward(dout.contiguous(), q, k, v, out, lse, cu_seqlens, ctx.scale)
+        return dq, dk, dv, None, None
+
+
 def _check_pages(pages, name, device, dim):
     if pages.dim() != dim or pages.dtype != torch.int32 or pages.device != device:
         raise ValueError(f"{name} must be a {dim}-dimensional int32 tensor on {device}")

@@ -64,3 +64,21 @@ def test_forward(lib, cuda, lengths, before, after, n_q, n_kv, D):
     ref = A.attention_fwd(f64(q), f64(k), f64(v), cu)
     assert_within(f64(out), ref["out"], out_bound(ref), "out")
     assert_lse(lse.cpu().numpy(), ref, max(lengths), D, "lse")
+
+
+@pytest.mark.parametrize("lengths,before,after", PACKED)
+@pytest.mark.parametrize("n_q,n_kv,D", HEADS)
+def test_backward(lib, cuda, lengths, before, after, n_q, n_kv, D):
+    F = lib.functional
+    cu = offsets(lengths, before)
+    T = int(cu[-1]) + after
+    q, k, v, do = inputs(T, n_q, n_kv, D, 200 + T)
+    dev = [t.to(cuda) for t in (q, k, v, do)]
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    out, lse = F.attention_forward(*dev[:3], cu_dev, save_lse=True)
+    grads = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev)
+    no_error(lib)
+    fwd = A.attention_fwd(f64(q), f64(k), f64(v), cu)
+    ref = A.attention_bwd(f64(do), f64(q), f64(k), f64(v), cu, out_err=out_bound(fwd))
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        assert_within(f64(got), ref[name], ref["e_" + name] + U * np.abs(ref[name]), name)
