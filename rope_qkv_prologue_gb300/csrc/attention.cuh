@@ -46,12 +46,12 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]: A is M = 128 lanes x 16 bf16 per K step, two
-// consecutive K values per 32-bit column. Issued by one lane of the warp.
-__device__ __forceinline__ void umma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// consecutive K values per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                   uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -117,14 +117,28 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// D (+)= A B^T over K = HD, both operands K-major boxes of 64 columns.
+// D = A B^T over K = HD, both operands K-major boxes of 64 columns. Issued, like
+// every MMA of the attention kernels, by one lane that runs the issuer's whole
+// loop: electing a lane for each MMA measured 0.67 of this (16384 tokens, 32 over
+// 8 heads of 128: 650 against 960 TFLOP/s).
 template <int HD>
 __device__ __forceinline__ void attn_mma_ss(uint32_t d, const unsigned char* a, const unsigned char* b, uint32_t id) {
+  const uint64_t ad = umma_desc_sw128(a), bd = umma_desc_sw128(b);
 #pragma unroll
   for (int k = 0; k < HD / 16; ++k) {
-    const int box = (k >> 2) * kAttnBox;
-    umma_bf16_warp(d, umma_desc_sw128(a + box) + 2 * (k & 3), umma_desc_sw128(b + box) + 2 * (k & 3), id, k != 0);
+    const int off = (k >> 2) * (kAttnBox >> 4) + 2 * (k & 3);
+    umma_bf16(d, ad + off, bd + off, id, k != 0);
   }
+}
+
+// D (+)= W B over the 128 keys or queries of a block: W bf16 in tensor memory, the
+// K steps of its second half `half` columns behind the first's; B read MN-major.
+__device__ __forceinline__ void attn_mma_ts(uint32_t d, uint32_t w, int half, const unsigned char* b, uint32_t id,
+                                            bool more) {
+  const uint64_t bd = umma_desc_sw128_mn(b, kAttnBox);
+#pragma unroll
+  for (int k = 0; k < kAttnRows / 16; ++k)
+    umma_bf16_ts(d, w + half * (k >> 2) + 8 * (k & 3), bd + 128 * k, id, more || k != 0);
 }
 
 // The blocks of packed sequences, taken from the most expensive to the

@@ -121,18 +121,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* fail = &s_fail;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_wait(bar, parity, a.err, fail); };  // one lane
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     int ok = 1;
     if (lane == 0) ok = attn_wait(bar, parity, a.err, fail) ? 1 : 0;
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
   };
   uint32_t it_pos = 0;
-  auto next_item = [&](BwdItem& t) -> bool {
+  auto next_item = [&](BwdItem& t, bool solo = false) -> bool {  // solo: called by one lane
     const uint32_t s = it_pos % kBwdSched, ph = (it_pos / kBwdSched) & 1;
     ++it_pos;
-    if (!warp_wait(&it_full[s], ph)) return false;
+    if (!(solo ? wait(&it_full[s], ph) : warp_wait(&it_full[s], ph))) return false;
     t = s_item[s];
-    __syncwarp();
+    if (!solo) __syncwarp();
     if (lane == 0) mbar_arrive(&it_empty[s]);
     return t.valid != 0;
   };
@@ -205,72 +206,67 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 1) {
     // ---- MMA issuer
-    constexpr uint32_t id_x = umma_idesc_bf16(kAttnRows, kAttnRows), id_acc = umma_idesc_bf16_bmn(kAttnRows, HD);
-    uint32_t it = 0, items = 0;
-    BwdItem t;
-    auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % ST) * SM::kTile; };
-    auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % ST) * SM::kTile; };
-    auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
-      warp_wait(&b1_full[k % ST], (k / ST) & 1);
-      tc_fence_after();
-      const uint32_t buf = KV ? 0 : k & 1;
-      attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
-      umma_commit_warp(&x_full[buf]);
-    };
-    auto product_y = [&](uint32_t k) {
-      warp_wait(&b2_full[k % ST], (k / ST) & 1);
-      tc_fence_after();
-      attn_mma_ss<HD>(tmem + tY, base + SM::kA + SM::kTile, b2(k), id_x);
-      umma_commit_warp(&y_full);
-    };
-    // acc (+)= W B: W bf16 in tensor memory, the K steps of each half of the block in that half's columns
-    auto accumulate = [&](uint32_t acc, uint32_t w, const unsigned char* b, bool more) {
-#pragma unroll
-      for (int k = 0; k < kAttnRows / 16; ++k)
-        umma_bf16_ts_warp(tmem + acc, tmem + w + 64 * (k >> 2) + 8 * (k & 3), umma_desc_sw128_mn(b, kAttnBox) + 128 * k,
-                          id_acc, more || k != 0);
-    };
-    while (next_item(t)) {
-      if (t.n == 0) continue;
-      warp_wait(&a_full, items & 1);
-      tc_fence_after();
-      product_x(it);
-      product_y(it);
-      if constexpr (!KV) umma_commit_warp(&b2_empty[it % ST]);
-      if (t.n == 1) umma_commit_warp(&a_empty);
-      for (int i = 0; i < t.n; ++i, ++it) {
-        const bool more = i + 1 < t.n;
-        if constexpr (KV) {
-          warp_wait(&p_full, it & 1);
-          if (i == 0 && items > 0) warp_wait(&acc_free, (items - 1) & 1);
-          tc_fence_after();
-          accumulate(tAcc1, tX, b2(it), i > 0);
-          umma_commit_warp(&b2_empty[it % ST]);
-          if (more) product_x(it + 1);
-          warp_wait(&ds_full, it & 1);
-          tc_fence_after();
-          accumulate(tAcc2, tY, b1(it), i > 0);
-          umma_commit_warp(&b1_empty[it % ST]);
-          if (more) product_y(it + 1);
-        } else {
-          if (more) product_x(it + 1);
-          warp_wait(&ds_full, it & 1);
-          if (i == 0 && items > 0) warp_wait(&acc_free, (items - 1) & 1);
-          tc_fence_after();
-          accumulate(tAcc1, tX + 128 * (it & 1), b1(it), i > 0);
-          umma_commit_warp(&b1_empty[it % ST]);
-          if (more) {
-            product_y(it + 1);
-            umma_commit_warp(&b2_empty[(it + 1) % ST]);
+    if (lane == 0) {
+      constexpr uint32_t id_x = umma_idesc_bf16(kAttnRows, kAttnRows), id_acc = umma_idesc_bf16_bmn(kAttnRows, HD);
+      uint32_t it = 0, items = 0;
+      BwdItem t;
+      auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % ST) * SM::kTile; };
+      auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % ST) * SM::kTile; };
+      auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
+        wait(&b1_full[k % ST], (k / ST) & 1);
+        tc_fence_after();
+        const uint32_t buf = KV ? 0 : k & 1;
+        attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
+        umma_commit(&x_full[buf]);
+      };
+      auto product_y = [&](uint32_t k) {
+        wait(&b2_full[k % ST], (k / ST) & 1);
+        tc_fence_after();
+        attn_mma_ss<HD>(tmem + tY, base + SM::kA + SM::kTile, b2(k), id_x);
+        umma_commit(&y_full);
+      };
+      while (next_item(t, true)) {
+        if (t.n == 0) continue;
+        wait(&a_full, items & 1);
+        tc_fence_after();
+        product_x(it);
+        product_y(it);
+        if constexpr (!KV) umma_commit(&b2_empty[it % ST]);
+        if (t.n == 1) umma_commit(&a_empty);
+        for (int i = 0; i < t.n; ++i, ++it) {
+          const bool more = i + 1 < t.n;
+          if constexpr (KV) {
+            wait(&p_full, it & 1);
+            if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
+            tc_fence_after();
+            attn_mma_ts(tmem + tAcc1, tmem + tX, 64, b2(it), id_acc, i > 0);
+            umma_commit(&b2_empty[it % ST]);
+            if (more) product_x(it + 1);
+            wait(&ds_full, it & 1);
+            tc_fence_after();
+            attn_mma_ts(tmem + tAcc2, tmem + tY, 64, b1(it), id_acc, i > 0);
+            umma_commit(&b1_empty[it % ST]);
+            if (more) product_y(it + 1);
+          } else {
+            if (more) product_x(it + 1);
+            wait(&ds_full, it & 1);
+            if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
+            tc_fence_after();
+            attn_mma_ts(tmem + tAcc1, tmem + tX + 128 * (it & 1), 64, b1(it), id_acc, i > 0);
+            umma_commit(&b1_empty[it % ST]);
+            if (more) {
+              product_y(it + 1);
+              umma_commit(&b2_empty[(it + 1) % ST]);
+            }
           }
+          if (i + 2 == t.n) umma_commit(&a_empty);  // the last X and Y are issued
         }
-        if (i + 2 == t.n) umma_commit_warp(&a_empty);  // the last X and Y are issued
+        umma_commit(&acc_done);
+        ++items;
       }
-      umma_commit_warp(&acc_done);
-      ++items;
+      umma_commit(&mma_done);  // nothing it issued may still run when the CTA exits
+      mbar_wait(&mma_done, 0, a.err);
     }
-    umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
-    if (lane == 0) mbar_wait(&mma_done, 0, a.err);
   } else if (warp == 2) {
     // ---- finder
     AttnOrder ord{a.cu, a.batch, kAttnRows, s_cache, 0, 0};

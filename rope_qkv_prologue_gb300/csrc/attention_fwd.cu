@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* fail = &s_fail;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_wait(bar, parity, a.err, fail); };  // one lane
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     int ok = 1;
     if (lane == 0) ok = attn_wait(bar, parity, a.err, fail) ? 1 : 0;
@@ -143,9 +144,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 
   // The next work item, in order: read from the finder's ring, or (prefix) the
-  // CTA's only one. Every role sees the same items.
+  // CTA's only one. Every role sees the same items. solo: called by one lane.
   uint32_t it_pos = 0;
-  auto next_item = [&](FwdItem& t) -> bool {
+  auto next_item = [&](FwdItem& t, bool solo = false) -> bool {
     if constexpr (PREFIX) {
       if (it_pos++) return false;
       const int r = (int)blockIdx.x % (a.n_kv * a.pairs);
@@ -162,9 +163,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     } else {
       const uint32_t s = it_pos % kFwdSched, ph = (it_pos / kFwdSched) & 1;
       ++it_pos;
-      if (!warp_wait(&it_full[s], ph)) return false;
+      if (!(solo ? wait(&it_full[s], ph) : warp_wait(&it_full[s], ph))) return false;
       t = s_item[s];
-      __syncwarp();
+      if (!solo) __syncwarp();
       if (lane == 0) mbar_arrive(&it_empty[s]);
       return t.valid != 0;
     }
@@ -251,56 +252,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
   } else if (warp == 1) {
     // ---- MMA issuer
-    constexpr uint32_t id_s = umma_idesc_bf16(kAttnRows, kAttnRows), id_o = umma_idesc_bf16_bmn(kAttnRows, HD);
-    uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, tiles[2] = {0, 0};
-    FwdItem t;
-    while (next_item(t)) {
-      const int n = max(t.n0, t.n1);
-      if (n == 0) continue;
-      auto tile_at = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
-      auto scores = [&](int j, uint32_t k, bool last) {
-        attn_mma_ss<HD>(tmem + kAttnRows * j, base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
-        umma_commit_warp(&s_full[j]);
-        if (last) umma_commit_warp(&q_empty[j]);
-      };
-      warp_wait(&full[it % ST], (it / ST) & 1);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int nj = j ? t.n1 : t.n0;
-        if (nj == 0) continue;
-        warp_wait(&q_full[j], qc[j]++ & 1);
-        tc_fence_after();
-        scores(j, it, nj == 1);
-      }
-      umma_commit_warp(&empty[it % ST]);
-      for (int i = 0; i < n; ++i, it += 2) {
-        const uint32_t kv = it + 1, kn = it + 2;
-        warp_wait(&full[kv % ST], (kv / ST) & 1);
-        if (i + 1 < n) warp_wait(&full[kn % ST], (kn / ST) & 1);
+    if (lane == 0) {
+      constexpr uint32_t id_s = umma_idesc_bf16(kAttnRows, kAttnRows), id_o = umma_idesc_bf16_bmn(kAttnRows, HD);
+      uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, tiles[2] = {0, 0};
+      FwdItem t;
+      while (next_item(t, true)) {
+        const int n = max(t.n0, t.n1);
+        if (n == 0) continue;
+        auto tile_at = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
+        auto scores = [&](int j, uint32_t k, bool last) {
+          attn_mma_ss<HD>(tmem + kAttnRows * j, base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
+          umma_commit(&s_full[j]);
+          if (last) umma_commit(&q_empty[j]);
+        };
+        wait(&full[it % ST], (it / ST) & 1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int nj = j ? t.n1 : t.n0;
-          if (i >= nj) continue;
-          warp_wait(&p_full[j], pc[j]++ & 1);
-          if (i == 0) {
-            if (tiles[j] > 0) warp_wait(&o_free[j], (tiles[j] - 1) & 1);
-            ++tiles[j];
-          }
+          if (nj == 0) continue;
+          wait(&q_full[j], qc[j]++ & 1);
           tc_fence_after();
-          const unsigned char* v = tile_at(kv);
-#pragma unroll
-          for (int k = 0; k < kAttnRows / 16; ++k)
-            umma_bf16_ts_warp(tmem + 2 * kAttnRows + HD * j, tmem + kAttnRows * j + 8 * k,
-                              umma_desc_sw128_mn(v, kAttnBox) + 128 * k, id_o, (i | k) != 0);
-          umma_commit_warp(&o_done[j]);
-          if (i + 1 < nj) scores(j, kn, i + 2 == nj);
+          scores(j, it, nj == 1);
         }
-        umma_commit_warp(&empty[kv % ST]);
-        if (i + 1 < n) umma_commit_warp(&empty[kn % ST]);
+        umma_commit(&empty[it % ST]);
+        for (int i = 0; i < n; ++i, it += 2) {
+          const uint32_t kv = it + 1, kn = it + 2;
+          wait(&full[kv % ST], (kv / ST) & 1);
+          if (i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int nj = j ? t.n1 : t.n0;
+            if (i >= nj) continue;
+            wait(&p_full[j], pc[j]++ & 1);
+            if (i == 0) {
+              if (tiles[j] > 0) wait(&o_free[j], (tiles[j] - 1) & 1);
+              ++tiles[j];
+            }
+            tc_fence_after();
+            attn_mma_ts(tmem + 2 * kAttnRows + HD * j, tmem + kAttnRows * j, 32, tile_at(kv), id_o, i > 0);
+            umma_commit(&o_done[j]);
+            if (i + 1 < nj) scores(j, kn, i + 2 == nj);
+          }
+          umma_commit(&empty[kv % ST]);
+          if (i + 1 < n) umma_commit(&empty[kn % ST]);
+        }
       }
+      umma_commit(&mma_done);  // nothing it issued may still run when the CTA exits
+      mbar_wait(&mma_done, 0, a.err);
     }
-    umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
-    if (lane == 0) mbar_wait(&mma_done, 0, a.err);
   } else if (warp == 2) {
     // ---- finder
     if constexpr (!PREFIX) {
