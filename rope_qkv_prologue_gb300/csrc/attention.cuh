@@ -39,6 +39,26 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, int* e
   return true;
 }
 
+// The same by every lane of a warp. All lanes poll: with one lane polling and the
+// others waiting for it, the kernels below measured up to half slower (16384
+// tokens, 32 over 8 heads of 128, the MMA issuer's waits alone: 3200 against
+// 2070 us).
+__device__ __forceinline__ bool attn_warp_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* fail) {
+  return __all_sync(0xffffffffu, attn_wait(bar, parity, err, fail));
+}
+
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.b32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// A value that every lane holds, in a form the compiler knows to be uniform: the
+// operands of an MMA are then computed in uniform registers, not moved there one
+// by one for each MMA.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -117,17 +137,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// D = A B^T over K = HD, both operands K-major boxes of 64 columns. Issued, like
-// every MMA of the attention kernels, by one lane that runs the issuer's whole
-// loop: electing a lane for each MMA measured 0.67 of this (16384 tokens, 32 over
-// 8 heads of 128: 650 against 960 TFLOP/s).
+// D = A B^T over K = HD, both operands K-major boxes of 64 columns. The whole warp
+// calls it (and attn_mma_ts) with uniform operands; one elected lane issues.
 template <int HD>
 __device__ __forceinline__ void attn_mma_ss(uint32_t d, const unsigned char* a, const unsigned char* b, uint32_t id) {
   const uint64_t ad = umma_desc_sw128(a), bd = umma_desc_sw128(b);
+  if (elect_one()) {
 #pragma unroll
-  for (int k = 0; k < HD / 16; ++k) {
-    const int off = (k >> 2) * (kAttnBox >> 4) + 2 * (k & 3);
-    umma_bf16(d, ad + off, bd + off, id, k != 0);
+    for (int k = 0; k < HD / 16; ++k) {
+      const int off = (k >> 2) * (kAttnBox >> 4) + 2 * (k & 3);
+      umma_bf16(d, ad + off, bd + off, id, k != 0);
+    }
   }
 }
 
@@ -136,9 +156,11 @@ __device__ __forceinline__ void attn_mma_ss(uint32_t d, const unsigned char* a, 
 __device__ __forceinline__ void attn_mma_ts(uint32_t d, uint32_t w, int half, const unsigned char* b, uint32_t id,
                                             bool more) {
   const uint64_t bd = umma_desc_sw128_mn(b, kAttnBox);
+  if (elect_one()) {
 #pragma unroll
-  for (int k = 0; k < kAttnRows / 16; ++k)
-    umma_bf16_ts(d, w + half * (k >> 2) + 8 * (k & 3), bd + 128 * k, id, more || k != 0);
+    for (int k = 0; k < kAttnRows / 16; ++k)
+      umma_bf16_ts(d, w + half * (k >> 2) + 8 * (k & 3), bd + 128 * k, id, more || k != 0);
+  }
 }
 
 // The blocks of packed sequences, taken from the most expensive to the

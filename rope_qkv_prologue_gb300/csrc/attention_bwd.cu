@@ -121,19 +121,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* fail = &s_fail;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_wait(bar, parity, a.err, fail); };  // one lane
-  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-    int ok = 1;
-    if (lane == 0) ok = attn_wait(bar, parity, a.err, fail) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_warp_wait(bar, parity, a.err, fail); };
   uint32_t it_pos = 0;
-  auto next_item = [&](BwdItem& t, bool solo = false) -> bool {  // solo: called by one lane
+  auto next_item = [&](BwdItem& t) -> bool {
     const uint32_t s = it_pos % kBwdSched, ph = (it_pos / kBwdSched) & 1;
     ++it_pos;
-    if (!(solo ? wait(&it_full[s], ph) : warp_wait(&it_full[s], ph))) return false;
+    if (!wait(&it_full[s], ph)) return false;
     t = s_item[s];
-    if (!solo) __syncwarp();
+    __syncwarp();
     if (lane == 0) mbar_arrive(&it_empty[s]);
     return t.valid != 0;
   };
@@ -156,7 +151,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     BwdItem t;
     while (next_item(t)) {
       if (t.n == 0) continue;
-      if (items > 0) warp_wait(&a_empty, (items - 1) & 1);
+      if (items > 0) wait(&a_empty, (items - 1) & 1);
       ++items;
       if (lane == 0) {
         mbar_arrive_expect_tx(&a_full, 2 * SM::kTile);
@@ -174,7 +169,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           uint64_t* full = which ? &b2_full[s] : &b1_full[s];
-          if (it >= ST) warp_wait(which ? &b2_empty[s] : &b1_empty[s], ((it / ST) - 1) & 1);
+          if (it >= ST) wait(which ? &b2_empty[s] : &b1_empty[s], ((it / ST) - 1) & 1);
           unsigned char* dst = base + (which ? SM::kB2 : SM::kB1) + s * SM::kTile;
           const CUtensorMap* map = KV ? (which ? &tmap_do : &tmap_q) : (which ? &tmap_v : &tmap_k);
           const bool patch = rows < kAttnRows && (KV || which == 0);
@@ -185,7 +180,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               tma_load_2d(dst + x * kAttnBox, map, head * HD + 64 * x, t.first + kAttnRows * blk, bar);
           }
           if (patch) {
-            warp_wait(&tail_bar, tails++ & 1);
+            wait(&tail_bar, tails++ & 1);
             for (int r = rows + (lane >> 3); r < kAttnRows; r += 4)
               for (int x = 0; x < HD / 64; ++x)
                 *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -206,67 +201,67 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 1) {
     // ---- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_x = umma_idesc_bf16(kAttnRows, kAttnRows), id_acc = umma_idesc_bf16_bmn(kAttnRows, HD);
-      uint32_t it = 0, items = 0;
-      BwdItem t;
-      auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % ST) * SM::kTile; };
-      auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % ST) * SM::kTile; };
-      auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
-        wait(&b1_full[k % ST], (k / ST) & 1);
-        tc_fence_after();
-        const uint32_t buf = KV ? 0 : k & 1;
-        attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
-        umma_commit(&x_full[buf]);
-      };
-      auto product_y = [&](uint32_t k) {
-        wait(&b2_full[k % ST], (k / ST) & 1);
-        tc_fence_after();
-        attn_mma_ss<HD>(tmem + tY, base + SM::kA + SM::kTile, b2(k), id_x);
-        umma_commit(&y_full);
-      };
-      while (next_item(t, true)) {
-        if (t.n == 0) continue;
-        wait(&a_full, items & 1);
-        tc_fence_after();
-        product_x(it);
-        product_y(it);
-        if constexpr (!KV) umma_commit(&b2_empty[it % ST]);
-        if (t.n == 1) umma_commit(&a_empty);
-        for (int i = 0; i < t.n; ++i, ++it) {
-          const bool more = i + 1 < t.n;
-          if constexpr (KV) {
-            wait(&p_full, it & 1);
-            if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
-            tc_fence_after();
-            attn_mma_ts(tmem + tAcc1, tmem + tX, 64, b2(it), id_acc, i > 0);
-            umma_commit(&b2_empty[it % ST]);
-            if (more) product_x(it + 1);
-            wait(&ds_full, it & 1);
-            tc_fence_after();
-            attn_mma_ts(tmem + tAcc2, tmem + tY, 64, b1(it), id_acc, i > 0);
-            umma_commit(&b1_empty[it % ST]);
-            if (more) product_y(it + 1);
-          } else {
-            if (more) product_x(it + 1);
-            wait(&ds_full, it & 1);
-            if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
-            tc_fence_after();
-            attn_mma_ts(tmem + tAcc1, tmem + tX + 128 * (it & 1), 64, b1(it), id_acc, i > 0);
-            umma_commit(&b1_empty[it % ST]);
-            if (more) {
-              product_y(it + 1);
-              umma_commit(&b2_empty[(it + 1) % ST]);
-            }
+    constexpr uint32_t id_x = umma_idesc_bf16(kAttnRows, kAttnRows), id_acc = umma_idesc_bf16_bmn(kAttnRows, HD);
+    uint32_t it = 0, items = 0;
+    const uint32_t tmem = uniform(s_tmem);
+    BwdItem t;
+    auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % ST) * SM::kTile; };
+    auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % ST) * SM::kTile; };
+    auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
+      wait(&b1_full[k % ST], (k / ST) & 1);
+      tc_fence_after();
+      const uint32_t buf = KV ? 0 : k & 1;
+      attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
+      umma_commit_warp(&x_full[buf]);
+    };
+    auto product_y = [&](uint32_t k) {
+      wait(&b2_full[k % ST], (k / ST) & 1);
+      tc_fence_after();
+      attn_mma_ss<HD>(tmem + tY, base + SM::kA + SM::kTile, b2(k), id_x);
+      umma_commit_warp(&y_full);
+    };
+    while (next_item(t)) {
+      t.n = (int)uniform(t.n);
+      if (t.n == 0) continue;
+      wait(&a_full, items & 1);
+      tc_fence_after();
+      product_x(it);
+      product_y(it);
+      if constexpr (!KV) umma_commit_warp(&b2_empty[it % ST]);
+      if (t.n == 1) umma_commit_warp(&a_empty);
+      for (int i = 0; i < t.n; ++i, ++it) {
+        const bool more = i + 1 < t.n;
+        if constexpr (KV) {
+          wait(&p_full, it & 1);
+          if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
+          tc_fence_after();
+          attn_mma_ts(tmem + tAcc1, tmem + tX, 64, b2(it), id_acc, i > 0);
+          umma_commit_warp(&b2_empty[it % ST]);
+          if (more) product_x(it + 1);
+          wait(&ds_full, it & 1);
+          tc_fence_after();
+          attn_mma_ts(tmem + tAcc2, tmem + tY, 64, b1(it), id_acc, i > 0);
+          umma_commit_warp(&b1_empty[it % ST]);
+          if (more) product_y(it + 1);
+        } else {
+          if (more) product_x(it + 1);
+          wait(&ds_full, it & 1);
+          if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
+          tc_fence_after();
+          attn_mma_ts(tmem + tAcc1, tmem + tX + 128 * (it & 1), 64, b1(it), id_acc, i > 0);
+          umma_commit_warp(&b1_empty[it % ST]);
+          if (more) {
+            product_y(it + 1);
+            umma_commit_warp(&b2_empty[(it + 1) % ST]);
           }
-          if (i + 2 == t.n) umma_commit(&a_empty);  // the last X and Y are issued
         }
-        umma_commit(&acc_done);
-        ++items;
+        if (i + 2 == t.n) umma_commit_warp(&a_empty);  // the last X and Y are issued
       }
-      umma_commit(&mma_done);  // nothing it issued may still run when the CTA exits
-      mbar_wait(&mma_done, 0, a.err);
+      umma_commit_warp(&acc_done);
+      ++items;
     }
+    umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
+    if (lane == 0) mbar_wait(&mma_done, 0, a.err);
   } else if (warp == 2) {
     // ---- finder
     AttnOrder ord{a.cu, a.batch, kAttnRows, s_cache, 0, 0};
@@ -276,7 +271,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int64_t work = (int64_t)ord.total * units;
     for (uint32_t k = 0;; ++k) {
       const uint32_t s = k % kBwdSched;
-      if (k >= kBwdSched && !warp_wait(&it_empty[s], ((k / kBwdSched) - 1) & 1)) break;
+      if (k >= kBwdSched && !wait(&it_empty[s], ((k / kBwdSched) - 1) & 1)) break;
       const int64_t w = attn_deal(k, blockIdx.x, gridDim.x);
       const bool done = (int64_t)k * gridDim.x >= work;
       BwdItem t = {};
@@ -318,7 +313,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             de[x] = in ? a.delta[at] : 0.f;
             if (ls[x] == -INFINITY) ls[x] = INFINITY;
           }
-          if (it >= kStatStages) warp_wait(&st_empty[s], ((it / kStatStages) - 1) & 1);
+          if (it >= kStatStages) wait(&st_empty[s], ((it / kStatStages) - 1) & 1);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             s_stat[s][0][32 * x + lane] = ls[x];
@@ -351,14 +346,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool diagonal = block_of(t, i, head) == t.blk;
         const uint32_t buf = KV ? 0 : it & 1;
         const uint32_t t_x = tmem + lanes + tX + 128 * buf + 64 * wg, t_y = tmem + lanes + tY + 64 * wg;
-        warp_wait(&x_full[buf], KV ? it & 1 : (it >> 1) & 1);
+        wait(&x_full[buf], KV ? it & 1 : (it >> 1) & 1);
         tc_fence_after();
         float p[64];
         tmem_ld32(t_x, p);
         tmem_ld32(t_x + 32, p + 32);
         const float* st = s_stat[KV ? it % kStatStages : 0][0] + 64 * wg;
         if constexpr (KV) {
-          warp_wait(&st_full[it % kStatStages], (it / kStatStages) & 1);
+          wait(&st_full[it % kStatStages], (it / kStatStages) & 1);
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float4 v = *reinterpret_cast<const float4*>(st + e);
@@ -386,7 +381,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; ++e) p[e] = ex2(fmaf(p[e], c, -r_lse));
         }
-        warp_wait(&y_full, it & 1);
+        wait(&y_full, it & 1);
         tc_fence_after();
         float y[64];
         tmem_ld32(t_y, y);
@@ -423,7 +418,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ds_full);
       }
-      warp_wait(&acc_done, items & 1);
+      wait(&acc_done, items & 1);
       ++items;
       tc_fence_after();
       // key/value kernel: warps 4-7 store dv, 8-11 dk; query kernel: each half of dq's columns

@@ -115,12 +115,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* fail = &s_fail;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_wait(bar, parity, a.err, fail); };  // one lane
-  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-    int ok = 1;
-    if (lane == 0) ok = attn_wait(bar, parity, a.err, fail) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_warp_wait(bar, parity, a.err, fail); };
 
   int px_len = 0, px_first = 0, px_chunk = 0;  // prefix: this CTA's key range
   if constexpr (PREFIX) {
@@ -144,9 +139,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 
   // The next work item, in order: read from the finder's ring, or (prefix) the
-  // CTA's only one. Every role sees the same items. solo: called by one lane.
+  // CTA's only one. Every role sees the same items.
   uint32_t it_pos = 0;
-  auto next_item = [&](FwdItem& t, bool solo = false) -> bool {
+  auto next_item = [&](FwdItem& t) -> bool {
     if constexpr (PREFIX) {
       if (it_pos++) return false;
       const int r = (int)blockIdx.x % (a.n_kv * a.pairs);
@@ -163,9 +158,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     } else {
       const uint32_t s = it_pos % kFwdSched, ph = (it_pos / kFwdSched) & 1;
       ++it_pos;
-      if (!(solo ? wait(&it_full[s], ph) : warp_wait(&it_full[s], ph))) return false;
+      if (!wait(&it_full[s], ph)) return false;
       t = s_item[s];
-      if (!solo) __syncwarp();
+      __syncwarp();
       if (lane == 0) mbar_arrive(&it_empty[s]);
       return t.valid != 0;
     }
@@ -179,7 +174,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if ((j ? t.n1 : t.n0) == 0) continue;
-        if (qc[j] > 0) warp_wait(&q_empty[j], (qc[j] - 1) & 1);
+        if (qc[j] > 0) wait(&q_empty[j], (qc[j] - 1) & 1);
         ++qc[j];
         if (lane == 0) {
           unsigned char* dst = base + SM::kQ + j * SM::kTile;
@@ -200,7 +195,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
         for (int which = 0; which < 2; ++which, ++it) {
           const uint32_t s = it % ST;
-          if (it >= ST) warp_wait(&empty[s], ((it / ST) - 1) & 1);
+          if (it >= ST) wait(&empty[s], ((it / ST) - 1) & 1);
           unsigned char* dst = base + SM::kRing + s * SM::kTile;
           const CUtensorMap* map = which ? &tmap_v : &tmap_k;
           const bool part = PREFIX ? ((s_whole >> i) & 1) == 0 : kAttnRows * (i + 1) > t.len;
@@ -229,7 +224,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               tma_load_2d(dst + x * kAttnBox, map, t.kvh * HD + 64 * x, t.kv0 + kAttnRows * i, bar);
           }
           if (patch) {
-            warp_wait(&tail_bar, tails++ & 1);
+            wait(&tail_bar, tails++ & 1);
             for (int r = lane >> 3; r < kAttnRows; r += 4) {
               const int key = kAttnRows * i + r;
               const bool in = key < t.len && (!PREFIX || s_slot[key / a.box_rows] >= 0);
@@ -252,54 +247,55 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
   } else if (warp == 1) {
     // ---- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = umma_idesc_bf16(kAttnRows, kAttnRows), id_o = umma_idesc_bf16_bmn(kAttnRows, HD);
-      uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, tiles[2] = {0, 0};
-      FwdItem t;
-      while (next_item(t, true)) {
-        const int n = max(t.n0, t.n1);
-        if (n == 0) continue;
-        auto tile_at = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
-        auto scores = [&](int j, uint32_t k, bool last) {
-          attn_mma_ss<HD>(tmem + kAttnRows * j, base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
-          umma_commit(&s_full[j]);
-          if (last) umma_commit(&q_empty[j]);
-        };
-        wait(&full[it % ST], (it / ST) & 1);
+    constexpr uint32_t id_s = umma_idesc_bf16(kAttnRows, kAttnRows), id_o = umma_idesc_bf16_bmn(kAttnRows, HD);
+    uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, tiles[2] = {0, 0};
+    const uint32_t tmem = uniform(s_tmem);
+    FwdItem t;
+    while (next_item(t)) {
+      t.n0 = (int)uniform(t.n0);
+      t.n1 = (int)uniform(t.n1);
+      const int n = max(t.n0, t.n1);
+      if (n == 0) continue;
+      auto tile_at = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
+      auto scores = [&](int j, uint32_t k, bool last) {
+        attn_mma_ss<HD>(tmem + kAttnRows * j, base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
+        umma_commit_warp(&s_full[j]);
+        if (last) umma_commit_warp(&q_empty[j]);
+      };
+      wait(&full[it % ST], (it / ST) & 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int nj = j ? t.n1 : t.n0;
+        if (nj == 0) continue;
+        wait(&q_full[j], qc[j]++ & 1);
+        tc_fence_after();
+        scores(j, it, nj == 1);
+      }
+      umma_commit_warp(&empty[it % ST]);
+      for (int i = 0; i < n; ++i, it += 2) {
+        const uint32_t kv = it + 1, kn = it + 2;
+        wait(&full[kv % ST], (kv / ST) & 1);
+        if (i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int nj = j ? t.n1 : t.n0;
-          if (nj == 0) continue;
-          wait(&q_full[j], qc[j]++ & 1);
-          tc_fence_after();
-          scores(j, it, nj == 1);
-        }
-        umma_commit(&empty[it % ST]);
-        for (int i = 0; i < n; ++i, it += 2) {
-          const uint32_t kv = it + 1, kn = it + 2;
-          wait(&full[kv % ST], (kv / ST) & 1);
-          if (i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int nj = j ? t.n1 : t.n0;
-            if (i >= nj) continue;
-            wait(&p_full[j], pc[j]++ & 1);
-            if (i == 0) {
-              if (tiles[j] > 0) wait(&o_free[j], (tiles[j] - 1) & 1);
-              ++tiles[j];
-            }
-            tc_fence_after();
-            attn_mma_ts(tmem + 2 * kAttnRows + HD * j, tmem + kAttnRows * j, 32, tile_at(kv), id_o, i > 0);
-            umma_commit(&o_done[j]);
-            if (i + 1 < nj) scores(j, kn, i + 2 == nj);
+          if (i >= nj) continue;
+          wait(&p_full[j], pc[j]++ & 1);
+          if (i == 0) {
+            if (tiles[j] > 0) wait(&o_free[j], (tiles[j] - 1) & 1);
+            ++tiles[j];
           }
-          umma_commit(&empty[kv % ST]);
-          if (i + 1 < n) umma_commit(&empty[kn % ST]);
+          tc_fence_after();
+          attn_mma_ts(tmem + 2 * kAttnRows + HD * j, tmem + kAttnRows * j, 32, tile_at(kv), id_o, i > 0);
+          umma_commit_warp(&o_done[j]);
+          if (i + 1 < nj) scores(j, kn, i + 2 == nj);
         }
+        umma_commit_warp(&empty[kv % ST]);
+        if (i + 1 < n) umma_commit_warp(&empty[kn % ST]);
       }
-      umma_commit(&mma_done);  // nothing it issued may still run when the CTA exits
-      mbar_wait(&mma_done, 0, a.err);
     }
+    umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
+    if (lane == 0) mbar_wait(&mma_done, 0, a.err);
   } else if (warp == 2) {
     // ---- finder
     if constexpr (!PREFIX) {
@@ -309,7 +305,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int64_t work = (int64_t)ord.total * a.units;
       for (uint32_t k = 0;; ++k) {
         const uint32_t s = k % kFwdSched;
-        if (k >= kFwdSched && !warp_wait(&it_empty[s], ((k / kFwdSched) - 1) & 1)) break;
+        if (k >= kFwdSched && !wait(&it_empty[s], ((k / kFwdSched) - 1) & 1)) break;
         const int64_t w = attn_deal(k, blockIdx.x, gridDim.x);
         const bool done = (int64_t)k * gridDim.x >= work;
         FwdItem t = {};
@@ -373,7 +369,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (n == 0) continue;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i, ++done) {
-        warp_wait(&s_full[j], done & 1);
+        wait(&s_full[j], done & 1);
         tc_fence_after();
         float s[kAttnRows];
         tmem_ld128(t_s, s);
@@ -403,7 +399,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const float f = m_new == m ? 1.f : ex2((m - m_new) * c);
           m = m_new;
           l *= f;
-          warp_wait(&o_done[j], (done - 1) & 1);
+          wait(&o_done[j], (done - 1) & 1);
           tc_fence_after();
 #pragma unroll
           for (int x = 0; x < HD / 32; ++x) {
@@ -435,7 +431,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[j]);
       }
-      warp_wait(&o_done[j], (done - 1) & 1);
+      wait(&o_done[j], (done - 1) & 1);
       tc_fence_after();
       float o[HD];
 #pragma unroll
