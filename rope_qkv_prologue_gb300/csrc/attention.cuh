@@ -54,6 +54,17 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Registers per thread of this warp's group of four warps, which calls it together.
+// The shares of a CTA's groups add up to no more than what it was launched with.
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // A value that every lane holds, in a form the compiler knows to be uniform: the
 // operands of an MMA are then computed in uniform registers, not moved there one
 // by one for each MMA.
@@ -63,6 +74,37 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two fp32 values in a register pair, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]: A is M = 128 lanes x 16 bf16 per K step, two
@@ -97,35 +139,42 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_after_wait(uint32_t (&r)[32]) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31]));
+// The maximum of 32 values, in two chains of three-input maxima.
+__device__ __forceinline__ float max32(const float* v) {
+  float a = max3(v[0], v[1], v[2]), b = max3(v[3], v[4], v[5]);
+#pragma unroll
+  for (int i = 6; i < 30; i += 4) {
+    a = max3(a, v[i], v[i + 1]);
+    b = max3(b, v[i + 2], v[i + 3]);
+  }
+  a = max3(a, v[30], v[31]);
+  return fmaxf(a, b);
 }
 
-// Whole warp: 128 consecutive fp32 columns of this warp's 32 TMEM lanes, four
-// loads in flight and one wait. The empty asm keeps the uses of the later
-// loads' registers behind the wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t addr, float (&v)[128]) {
+// Whole warp: 128 consecutive fp32 columns of this warp's 32 TMEM lanes into v, and
+// their maximum: a quarter's maximum is taken while the next quarter loads.
+__device__ __forceinline__ float tmem_ld128_max(uint32_t addr, float (&v)[128]) {
   uint32_t r0[32], r1[32], r2[32], r3[32];
-  tmem_ld32_issue(addr, r0);
-  tmem_ld32_issue(addr + 32, r1);
-  tmem_ld32_issue(addr + 64, r2);
-  tmem_ld32_issue(addr + 96, r3);
-  tmem_wait_ld32(r0);
-  tmem_after_wait(r1);
-  tmem_after_wait(r2);
-  tmem_after_wait(r3);
+  auto keep = [&](const uint32_t (&r)[32], int x) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = __uint_as_float(r0[i]);
-    v[32 + i] = __uint_as_float(r1[i]);
-    v[64 + i] = __uint_as_float(r2[i]);
-    v[96 + i] = __uint_as_float(r3[i]);
-  }
+    for (int i = 0; i < 32; ++i) v[32 * x + i] = __uint_as_float(r[i]);
+  };
+  tmem_ld32_issue(addr, r0);
+  tmem_wait_ld32(r0);
+  tmem_ld32_issue(addr + 32, r1);
+  keep(r0, 0);
+  const float m0 = max32(v);
+  tmem_wait_ld32(r1);
+  tmem_ld32_issue(addr + 64, r2);
+  keep(r1, 1);
+  const float m1 = max32(v + 32);
+  tmem_wait_ld32(r2);
+  tmem_ld32_issue(addr + 96, r3);
+  keep(r2, 2);
+  const float m2 = max32(v + 64);
+  tmem_wait_ld32(r3);
+  keep(r3, 3);
+  return fmaxf(max3(m0, m1, m2), max32(v + 96));
 }
 
 // 3-D tensor-map load (c0: the contiguous coordinate).

@@ -52,6 +52,11 @@ struct FwdSmem {
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kOut = kRing + kStages * kTile;
+  // tensor memory of slot j: scores, weights, result
+  static constexpr bool kApart = HD == 64;  // P has its own columns
+  __host__ __device__ static constexpr uint32_t tS(int j) { return kApart ? 256 * j : 128 * j; }
+  __host__ __device__ static constexpr uint32_t tP(int j) { return kApart ? 256 * j + 128 : tS(j); }
+  __host__ __device__ static constexpr uint32_t tO(int j) { return kApart ? 256 * j + 192 : 256 + 128 * j; }
 };
 
 struct FwdItem {
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   constexpr int ST = SM::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], tail_bar, mma_done, q_full[2], q_empty[2], s_full[2], p_full[2],
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], tail_bar, mma_done, q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2],
       o_done[2], o_free[2], it_full[kFwdSched], it_empty[kFwdSched];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
@@ -95,6 +100,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&q_full[j], 1);
       mbar_init(&q_empty[j], 1);
       mbar_init(&s_full[j], 1);
+      mbar_init(&s_read[j], 4);
       mbar_init(&p_full[j], 4);
       mbar_init(&o_done[j], 1);
       mbar_init(&o_free[j], 4);
@@ -166,6 +172,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
   };
 
+  // 12 warps launched with 168 registers a thread (the launch bounds' share of 65536):
+  // 4 warps x 88 + 8 x 208 = 12 x 168. A softmax thread holds its row's 128 scores.
+  if (warp < 4) {
+  regs_less<88>();
   if (warp == 0) {
     // ---- loader
     uint32_t it = 0, tails = 0, qc[2] = {0, 0};
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (n == 0) continue;
       auto tile_at = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
       auto scores = [&](int j, uint32_t k, bool last) {
-        attn_mma_ss<HD>(tmem + kAttnRows * j, base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
+        attn_mma_ss<HD>(tmem + SM::tS(j), base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
         umma_commit_warp(&s_full[j]);
         if (last) umma_commit_warp(&q_empty[j]);
       };
@@ -274,8 +284,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       umma_commit_warp(&empty[it % ST]);
       for (int i = 0; i < n; ++i, it += 2) {
         const uint32_t kv = it + 1, kn = it + 2;
+        if constexpr (SM::kApart) {  // the next scores as soon as the last ones have been read
+          if (i + 1 < n) {
+            wait(&full[kn % ST], (kn / ST) & 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int nj = j ? t.n1 : t.n0;
+              if (i + 1 >= nj) continue;
+              wait(&s_read[j], pc[j] & 1);
+              tc_fence_after();
+              scores(j, kn, i + 2 == nj);
+            }
+            umma_commit_warp(&empty[kn % ST]);
+          }
+        }
         wait(&full[kv % ST], (kv / ST) & 1);
-        if (i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
+        if (!SM::kApart && i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int nj = j ? t.n1 : t.n0;
@@ -286,12 +310,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             ++tiles[j];
           }
           tc_fence_after();
-          attn_mma_ts(tmem + 2 * kAttnRows + HD * j, tmem + kAttnRows * j, 32, tile_at(kv), id_o, i > 0);
+          attn_mma_ts(tmem + SM::tO(j), tmem + SM::tP(j), 32, tile_at(kv), id_o, i > 0);
           umma_commit_warp(&o_done[j]);
-          if (i + 1 < nj) scores(j, kn, i + 2 == nj);
+          if (!SM::kApart && i + 1 < nj) scores(j, kn, i + 2 == nj);
         }
         umma_commit_warp(&empty[kv % ST]);
-        if (i + 1 < n) umma_commit_warp(&empty[kn % ST]);
+        if (!SM::kApart && i + 1 < n) umma_commit_warp(&empty[kn % ST]);
       }
     }
     umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
@@ -356,11 +380,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
       }
     }
+  }
   } else {
+    regs_more<208>();
     // ---- softmax, rescaling, epilogue
     const int j = (warp - 4) >> 2, qtr = warp & 3, row = 32 * qtr + lane;
     const uint32_t lanes = (uint32_t)(32 * qtr) << 16;
-    const uint32_t t_s = tmem + lanes + kAttnRows * j, t_o = tmem + lanes + 2 * kAttnRows + HD * j;
+    const uint32_t t_s = tmem + lanes + SM::tS(j), t_p = tmem + lanes + SM::tP(j), t_o = tmem + lanes + SM::tO(j);
     const float c = a.scale_log2;
     uint32_t done = 0;  // blocks of this slot so far
     FwdItem t;
@@ -372,9 +398,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         wait(&s_full[j], done & 1);
         tc_fence_after();
         float s[kAttnRows];
-        tmem_ld128(t_s, s);
+        float top = tmem_ld128_max(t_s, s);
+        if constexpr (SM::kApart) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_read[j]);
+        }
+        bool masked = false;
         if constexpr (PREFIX) {
           if (!((s_whole >> i) & 1)) {
+            masked = true;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int key = kAttnRows * i + 32 * x + lane;
@@ -385,13 +418,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
           }
         } else if (i == n - 1) {  // the diagonal block: keys after the row (and so behind the sequence) are not seen
+          masked = true;
 #pragma unroll
           for (int e = 0; e < kAttnRows; ++e)
             if (e > row) s[e] = -INFINITY;
         }
-        float top = s[0];
-#pragma unroll
-        for (int e = 1; e < kAttnRows; ++e) top = fmaxf(top, s[e]);
+        if (masked) top = fmaxf(fmaxf(max32(s), max32(s + 32)), fmaxf(max32(s + 64), max32(s + 96)));
         if (i == 0) {
           m = top;
         } else if (__any_sync(0xffffffffu, (top - m) * c > kRescale)) {  // also where m is -inf and top is not
@@ -412,19 +444,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m * c;
-        float sum0 = 0.f, sum1 = 0.f;
+        if constexpr (SM::kApart) {  // PV of the block before has read the columns that P goes to
+          if (i > 0) wait(&o_done[j], (done - 1) & 1);
+        }
+        const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+        uint64_t sum_a = 0, sum_b = 0;  // pairs of zeros
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float p0 = ex2(fmaf(s[32 * x + 2 * e], c, off)), p1 = ex2(fmaf(s[32 * x + 2 * e + 1], c, off));
-            sum0 += p0;
-            sum1 += p1;
+            float p0, p1;
+            unpair(fma2(pair(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), c2, off2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            if (e & 1)
+              sum_b = add2(sum_b, pair(p0, p1));
+            else
+              sum_a = add2(sum_a, pair(p0, p1));
             w[e] = pack2(p0, p1);
           }
-          tmem_st16(t_s + 16 * x, w);
+          tmem_st16(t_p + 16 * x, w);
         }
+        float sum0, sum1;
+        unpair(add2(sum_a, sum_b), sum0, sum1);
         l += sum0 + sum1;
         tmem_wait_st();
         tc_fence_before();
