@@ -145,6 +145,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   };
 
+  // 12 warps launched with 168 registers a thread: 4 warps x 88 + 8 x 208 = 12 x 168
+  if (warp < 4) {
+  regs_less<88>();
   if (warp == 0) {
     // ---- loader
     uint32_t it = 0, tails = 0, items = 0;
@@ -324,7 +327,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
     }
+  }
   } else {
+    regs_more<208>();
     // ---- P and dS, and the results
     const int wg = (warp - 4) >> 2, qtr = warp & 3, row = 32 * qtr + lane;
     const uint32_t lanes = (uint32_t)(32 * qtr) << 16;
