@@ -54,6 +54,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to global memory.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)),
+               "r"(bytes)
+               : "memory");
+}
+
 // Registers per thread of this warp's group of four warps, which calls it together.
 // The shares of a CTA's groups add up to no more than what it was launched with.
 template <int N>
@@ -278,11 +285,11 @@ struct AttnOrder {
     seq = 0;
     for (int s0 = 0; s0 < batch; s0 += 32) {
       const int s = s0 + lane;
-      uint32_t m = __ballot_sync(0xffffffffu, s < batch && blocks(s) >= cost);
-      const uint32_t n = __popc(m);
+      const bool in = s < batch && blocks(s) >= cost;
+      const uint32_t m = __ballot_sync(0xffffffffu, in), n = __popc(m);
       if (idx < n) {
-        for (; idx; --idx) m &= m - 1;
-        seq = s0 + __ffs(m) - 1;
+        const bool it = in && __popc(m & ((1u << lane) - 1u)) == idx;
+        seq = s0 + __ffs(__ballot_sync(0xffffffffu, it)) - 1;
         break;
       }
       idx -= n;

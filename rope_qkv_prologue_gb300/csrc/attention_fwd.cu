@@ -25,11 +25,15 @@
 // cost to fetch (64 KiB per 2 x 8.4 MFLOP at head_dim 128), and while one slot's
 // softmax runs, the tensor cores work on the other's products:
 //   warp 0      loads Q, K, V tiles with TMA into 128B-swizzled shared memory;
-//   warp 1      issues the MMAs: PV(i) then S(i + 1) of slot 0, the same of slot 1.
-//               P lives in the tensor-memory columns of the S it came from; MMAs
-//               execute in order, so S(i + 1) overwrites P(i) after PV(i) read it;
-//   warp 2      finds the next work item (AttnOrder), one ahead;
-//   warp 3      zeroes the rows of no sequence where the caller asked for it;
+//   warp 1      issues the MMAs: PV(i) then S(i + 1) of slot 0, the same of slot 1. At
+//               head_dim 128 P lives in the tensor-memory columns of the S it came
+//               from; MMAs execute in order, so S(i + 1) overwrites P(i) after PV(i)
+//               read it. At head_dim 64 there is room for P apart, and S(i + 1) is
+//               issued as soon as the softmax has S(i) in registers. (One issuer per
+//               slot measured slower, 1279 -> 1434 us at 16384 tokens and head_dim
+//               128: the slots fall into step and their products collide.);
+//   warp 2      finds the next work item (AttnOrder), one ahead, and at last zeroes the
+//               rows of no sequence where the caller asked for it;
 //   warps 4-7   softmax, rescaling and epilogue of slot 0, thread i owning row i,
 //   warps 8-11  the same of slot 1.
 // Keys behind the end of a sequence may hold anything (another sequence, unused
@@ -42,13 +46,13 @@ namespace {
 
 constexpr int kFwdThreads = 384;
 constexpr int kFwdSched = 2;  // work items in flight between the finder and the others
-constexpr float kRescale = 8.f;  // powers of two a row's maximum may grow before O is rescaled
 constexpr int kStageBytes = 32 * 128;  // an epilogue warp's buffer: 32 rows x 64 bf16
+constexpr float kRescale = 8.f;  // powers of two a row's maximum may grow before O is rescaled
 
 template <int HD>
 struct FwdSmem {
   static constexpr int kTile = (HD / 64) * kAttnBox;  // 128 rows x HD bf16
-  static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr int kStages = HD == 128 ? 4 : 8;  // K and V tiles in flight
   static constexpr int kQ = 0;
   static constexpr int kRing = 2 * kTile;
   static constexpr int kOut = kRing + kStages * kTile;
@@ -335,8 +339,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         FwdItem t = {};
         if (w < work) {
           int seq, cost;
-          ord.find((uint32_t)(w / a.units), lane, seq, cost);
-          const int hu = (int)(w % a.units);
+          const uint32_t rank = work <= UINT32_MAX ? (uint32_t)w / (uint32_t)a.units : (uint32_t)(w / a.units);
+          ord.find(rank, lane, seq, cost);
+          const int hu = (int)(w - (int64_t)rank * a.units);
           const int start = a.cu[seq], len = a.cu[seq + 1] - start;
           if (a.pair_heads) {
             t.head0 = 2 * hu;
@@ -364,14 +369,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
         if (done) break;
       }
-    }
-  } else if (warp == 3) {
-    if constexpr (!PREFIX) {
+      // ---- then the rows of no sequence
       if (a.zero_rest) {
-        bool bad = false;
-        for (int s = lane; s < a.batch; s += 32) bad |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T;
-        bad = __any_sync(0xffffffffu, bad) || a.batch == 0;
-        const int64_t first = bad ? 0 : a.cu[0], last = bad ? 0 : a.cu[a.batch];
+        const bool none = !ok || a.batch == 0;
+        const int64_t first = none ? 0 : a.cu[0], last = none ? 0 : a.cu[a.batch];
         attn_zero_rest(a.out, a.T, (int64_t)a.n_q * (HD / 8), first, last, lane);
         if (a.lse)
           for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < (first + a.T - last) * a.n_q; i += (int64_t)gridDim.x * 32) {
@@ -404,10 +405,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_read[j]);
         }
-        bool masked = false;
+        int quarters = 4;  // 32-key quarters of the block that any row of this warp sees
         if constexpr (PREFIX) {
           if (!((s_whole >> i) & 1)) {
-            masked = true;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int key = kAttnRows * i + 32 * x + lane;
@@ -416,14 +416,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               for (int e = 0; e < 32; ++e)
                 if (!((in >> e) & 1)) s[32 * x + e] = -INFINITY;
             }
+            top = fmaxf(fmaxf(max32(s), max32(s + 32)), fmaxf(max32(s + 64), max32(s + 96)));
           }
-        } else if (i == n - 1) {  // the diagonal block: keys after the row (and so behind the sequence) are not seen
-          masked = true;
+        } else if (i == n - 1) {
+          // the diagonal block: keys after the row (and so behind the sequence) are not
+          // seen. The warp's rows see the quarters before their own whole, their own up
+          // to the lane, and none after it.
+          quarters = qtr + 1;
+          top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < kAttnRows; ++e)
-            if (e > row) s[e] = -INFINITY;
+          for (int x = 0; x < 4; ++x) {
+            if (x == qtr)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e > lane) s[32 * x + e] = -INFINITY;
+            if (x <= qtr) top = fmaxf(top, max32(s + 32 * x));
+          }
         }
-        if (masked) top = fmaxf(fmaxf(max32(s), max32(s + 32)), fmaxf(max32(s + 64), max32(s + 96)));
         if (i == 0) {
           m = top;
         } else if (__any_sync(0xffffffffu, (top - m) * c > kRescale)) {  // also where m is -inf and top is not
@@ -452,6 +461,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t w[16];
+          if (!PREFIX && x >= quarters) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = 0;
+            tmem_st16(t_p + 16 * x, w);
+            continue;
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float p0, p1;
@@ -493,27 +508,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
       } else {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
-        unsigned char* buf = base + SM::kOut + (warp - 4) * kStageBytes;
         const int row0 = (j ? t.row1 : t.row0) + 32 * qtr, head = j ? t.head1 : t.head0;
         const int rows = t.kv0 + t.len - row0;  // rows of this warp that belong to the sequence
         if (a.lse && lane < rows) a.lse[(int64_t)head * a.T + row0 + lane] = m * a.scale + logf(l);
+        // through shared memory, 64 columns at a time, so that whole 128-byte lines leave:
+        // eight lanes per row, four rows per store
+        if (rows > 0) {
+          unsigned char* buf = base + SM::kOut + (warp - 4) * kStageBytes;
+          const int r0 = lane >> 3, ch0 = lane & 7;
+          const int64_t stride = (int64_t)a.n_q * (HD / 8);
+          uint4* dst = a.out + (row0 + r0) * stride + head * (HD / 8) + ch0;
 #pragma unroll
-        for (int x = 0; x < HD / 64; ++x) {
+          for (int x = 0; x < HD / 64; ++x) {
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            const float* v = o + 64 * x + 8 * ch;
-            *reinterpret_cast<uint4*>(buf + attn_swz(lane, ch)) =
-                make_uint4(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv), pack2(v[4] * inv, v[5] * inv),
-                           pack2(v[6] * inv, v[7] * inv));
+            for (int ch = 0; ch < 8; ++ch) {
+              const float* v = o + 64 * x + 8 * ch;
+              *reinterpret_cast<uint4*>(buf + attn_swz(lane, ch)) =
+                  make_uint4(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv), pack2(v[4] * inv, v[5] * inv),
+                             pack2(v[6] * inv, v[7] * inv));
+            }
+            __syncwarp();
+            uint4 w[8];
+#pragma unroll
+            for (int r4 = 0; r4 < 8; ++r4) w[r4] = *reinterpret_cast<const uint4*>(buf + attn_swz(4 * r4 + r0, ch0));
+            __syncwarp();
+#pragma unroll
+            for (int r4 = 0; r4 < 8; ++r4)
+              if (4 * r4 + r0 < rows) dst[4 * r4 * stride + 8 * x] = w[r4];
           }
-          __syncwarp();
-#pragma unroll
-          for (int r4 = 0; r4 < 8; ++r4) {
-            const int r = 4 * r4 + (lane >> 3);
-            const uint4 v = *reinterpret_cast<const uint4*>(buf + attn_swz(r, lane & 7));
-            if (r < rows) a.out[((int64_t)(row0 + r) * a.n_q + head) * (HD / 8) + 8 * x + (lane & 7)] = v;
-          }
-          __syncwarp();
         }
       }
     }
@@ -533,8 +555,8 @@ const void* attention_fwd_kernel(int head_dim, bool prefix) {
 }
 
 int attention_fwd_smem_bytes(int head_dim, bool prefix) {
-  const int out = prefix ? 0 : 8 * kStageBytes;
-  return (head_dim == 64 ? FwdSmem<64>::kOut : FwdSmem<128>::kOut) + out + 1024;
+  const int rows = prefix ? 0 : 256;  // the prefix kernel's results go straight to memory
+  return 1024 + (head_dim == 64 ? FwdSmem<64>::kOut : FwdSmem<128>::kOut) + rows * 128;
 }
 int attention_fwd_threads() { return kFwdThreads; }
 
