@@ -1325,6 +1325,7 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
   const int64_t unit_rows = a.pair_heads ? kAttnBlock : 2 * kAttnBlock;
   const int64_t most = (T / unit_rows + std::max(batch, 1)) * a.units;  // at least the number of work items
+  if (most > INT32_MAX / 2) return QKVP_ERR_SHAPE;
   void* args[] = {&tq, &tk, &tv, &a};
   return launch_args(kern, most < sms ? most : sms, attention_fwd_threads(), smem, static_cast<cudaStream_t>(stream),
                      args);
@@ -1370,6 +1371,8 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
       !bf16_tile_map(&tk, k, T, (int64_t)layout->n_kv * hd, kAttnBlock) ||
       !bf16_tile_map(&tv, v, T, (int64_t)layout->n_kv * hd, kAttnBlock))
     return QKVP_ERR_LAUNCH;
+  const int64_t blocks = T / kAttnBlock + std::max(batch, 1);  // at least the number of blocks
+  if (blocks * layout->n_q > INT32_MAX / 2) return QKVP_ERR_SHAPE;
   a.T = T;
   a.n_q = layout->n_q;
   a.n_kv = layout->n_kv;
@@ -1395,7 +1398,6 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   const int64_t rows_per_cta = 8 * 32 / (hd / 8);
   const int64_t dgrid = (T * a.n_q + rows_per_cta - 1) / rows_per_cta;
   QKVP_TRY(launch(attention_delta_kernel(hd), std::min<int64_t>(dgrid, 16 * (int64_t)sms), 256, 0, st, &a));
-  const int64_t blocks = T / kAttnBlock + std::max(batch, 1);  // at least the number of blocks
   void* args[] = {&tq, &td, &tk, &tv, &a};
   QKVP_TRY(launch_args(kkv, std::min<int64_t>(blocks * a.n_kv, sms), attention_bwd_threads(), smem, st, args));
   return launch_args(kq, std::min<int64_t>(blocks * a.n_q, sms), attention_bwd_threads(), smem, st, args);

@@ -22,29 +22,36 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` in a swizzled box.
 __device__ __forceinline__ int attn_swz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 
-// Bounded wait that gives up at once when another thread of the CTA already
-// gave up (*fail): after one timeout the rest of the kernel runs through
-// without waiting, and every loop still ends.
-__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* fail) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*fail) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
-      *fail = 1;
-      atomicOr(err, kErrWaitTimeout);
-      return false;
-    }
-  }
-  return true;
-}
+// The kernels run long straight code in several roles at once, and at short
+// sequences each role goes through all of its code for a few blocks: instruction
+// fetches were a quarter of the stalls (60 sequences of 67 rows). So what is in
+// many places, like a wait, is kept short.
 
-// The same by every lane of a warp. All lanes poll: with one lane polling and the
-// others waiting for it, the kernels below measured up to half slower (16384
-// tokens, 32 over 8 heads of 128, the MMA issuer's waits alone: 3200 against
-// 2070 us).
-__device__ __forceinline__ bool attn_warp_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* fail) {
-  return __all_sync(0xffffffffu, attn_wait(bar, parity, err, fail));
+// Bounded wait, every lane of the calling warp: with one lane polling and the
+// others waiting for it, the kernels measured up to half slower. Gives up after
+// kWaitLimitNs, and at once when another warp already gave up (*fail): after one
+// timeout the rest of the kernel runs through without waiting, every loop still
+// ends, and attn_report tells the host.
+__device__ __forceinline__ uint32_t global_ns_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = global_ns_lo();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*fail) return false;
+  } while (global_ns_lo() - t0 < (uint32_t)kWaitLimitNs);
+  *fail = 1;
+  return false;
+}
+static_assert(kWaitLimitNs < (1ull << 31), "the waits count nanoseconds in 32 bits");
+
+// At the kernel's end, behind a barrier.
+__device__ __forceinline__ void attn_report(volatile int* fail, int* err) {
+  if (threadIdx.x == 0 && *fail) atomicOr(err, kErrWaitTimeout);
 }
 
 // True in one lane of the (converged) warp, always the same one.
@@ -143,6 +150,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// 16 consecutive fp32 columns of this warp's 32 TMEM lanes, in place: times f.
+__device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  tmem_st16(addr, r);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -299,18 +320,17 @@ struct AttnOrder {
 
 // Work item of round k for CTA b of g: the items descend in cost, and every
 // other round is dealt backwards, so that the sums stay even.
-__device__ __forceinline__ int64_t attn_deal(int64_t k, int64_t b, int64_t g) {
+__device__ __forceinline__ uint32_t attn_deal(uint32_t k, uint32_t b, uint32_t g) {
   return k * g + ((k & 1) ? g - 1 - b : b);
 }
 
-// Rows of no sequence ([0, cu[0]) and [cu[batch], T), or all of them when the
-// offsets are refused): `chunks` 16-byte pieces per row set to zero, one warp
-// of each CTA.
-__device__ __forceinline__ void attn_zero_rest(uint4* out, int64_t T, int64_t chunks, int64_t first, int64_t last,
-                                               int lane) {
-  const int64_t head = first * chunks, n = head + (T - last) * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < n; i += (int64_t)gridDim.x * 32)
-    out[i < head ? i : last * chunks + (i - head)] = make_uint4(0, 0, 0, 0);
+// Rows of no sequence ([0, first) and [last, T)): `chunks` 16-byte pieces per row
+// set to zero, one warp of each CTA.
+__device__ __forceinline__ void attn_zero_rows(uint4* out, int64_t T, int chunks, int64_t first, int64_t last, int lane) {
+  for (int64_t r = blockIdx.x; r < first + T - last; r += gridDim.x) {
+    uint4* row = out + (r < first ? r : last + (r - first)) * chunks;
+    for (int c = lane; c < chunks; c += 32) row[c] = make_uint4(0, 0, 0, 0);
+  }
 }
 
 }  // namespace qkvp

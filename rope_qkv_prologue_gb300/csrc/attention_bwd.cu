@@ -121,12 +121,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* fail = &s_fail;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_warp_wait(bar, parity, a.err, fail); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = attn_wait(bar, parity, fail);
+    __syncwarp();
+    return ok;
+  };
   uint32_t it_pos = 0;
   auto next_item = [&](BwdItem& t) -> bool {
     const uint32_t s = it_pos % kBwdSched, ph = (it_pos / kBwdSched) & 1;
     ++it_pos;
-    if (!wait(&it_full[s], ph)) return false;
+    if (!__all_sync(0xffffffffu, wait(&it_full[s], ph))) return false;
     t = s_item[s];
     __syncwarp();
     if (lane == 0) mbar_arrive(&it_empty[s]);
@@ -271,18 +275,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool ok = ord.init(a.T, lane);
     if (!ok && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
     const int units = KV ? a.n_kv : a.n_q;
-    const int64_t work = (int64_t)ord.total * units;
+    const uint32_t work = ord.total * (uint32_t)units;  // below 2^31: the host checks
     for (uint32_t k = 0;; ++k) {
       const uint32_t s = k % kBwdSched;
-      if (k >= kBwdSched && !wait(&it_empty[s], ((k / kBwdSched) - 1) & 1)) break;
-      const int64_t w = attn_deal(k, blockIdx.x, gridDim.x);
-      const bool done = (int64_t)k * gridDim.x >= work;
+      if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kBwdSched) & 1) ^ 1))) break;
+      const uint32_t w = attn_deal(k, blockIdx.x, gridDim.x);
       BwdItem t = {};
-      t.valid = !done;
-      if (w < work) {
+      t.valid = k * gridDim.x < work;  // else no CTA has any left
+      if (w < work) {                  // (an empty item: this CTA has none in the last round)
         int seq, cost;
-        ord.find((uint32_t)(w / units), lane, seq, cost);
-        t.head = (int)(w % units);
+        const uint32_t rank = w / (uint32_t)units;
+        ord.find(rank, lane, seq, cost);
+        t.head = (int)(w - rank * (uint32_t)units);
         t.first = a.cu[seq];
         t.len = a.cu[seq + 1] - t.first;
         t.blk = KV ? (t.len + kAttnRows - 1) / kAttnRows - cost : cost - 1;
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_arrive(&it_full[s]);
       }
       __syncwarp();
-      if (done) break;
+      if (!t.valid) break;
     }
   } else if (warp == 3) {
     if constexpr (KV) {
@@ -466,6 +470,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  attn_report(fail, a.err);
 }
 
 // delta[h, t] = dout[t, h] . out[t, h] in fp32, and (where asked for) zeros in the
@@ -497,9 +502,9 @@ __global__ void __launch_bounds__(256) qkvp_attention_delta_kernel(const AttnBwd
     for (int s = lane; s < a.batch; s += 32) bad |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T;
     bad = __any_sync(0xffffffffu, bad) || a.batch == 0;
     const int64_t first = bad ? 0 : a.cu[0], last = bad ? 0 : a.cu[a.batch];
-    attn_zero_rest(a.dq, a.T, (int64_t)a.n_q * L, first, last, lane);
-    attn_zero_rest(a.dk, a.T, (int64_t)a.n_kv * L, first, last, lane);
-    attn_zero_rest(a.dv, a.T, (int64_t)a.n_kv * L, first, last, lane);
+    attn_zero_rows(a.dq, a.T, a.n_q * L, first, last, lane);
+    attn_zero_rows(a.dk, a.T, a.n_kv * L, first, last, lane);
+    attn_zero_rows(a.dv, a.T, a.n_kv * L, first, last, lane);
   }
 }
 

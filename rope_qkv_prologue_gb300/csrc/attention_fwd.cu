@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   constexpr int ST = SM::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], tail_bar, mma_done, q_full[2], q_empty[2], s_full[2], s_read[2], p_full[2],
-      o_done[2], o_free[2], it_full[kFwdSched], it_empty[kFwdSched];
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], tail_bar, mma_done, q_full[2], q_empty[2], s_full[2],
+      s_read[2], p_full[2], o_done[2], o_free[2], it_full[kFwdSched], it_empty[kFwdSched];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   __shared__ FwdItem s_item[kFwdSched];
@@ -125,7 +125,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* fail = &s_fail;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn_warp_wait(bar, parity, a.err, fail); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = attn_wait(bar, parity, fail);
+    __syncwarp();
+    return ok;
+  };
 
   int px_len = 0, px_first = 0, px_chunk = 0;  // prefix: this CTA's key range
   if constexpr (PREFIX) {
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     } else {
       const uint32_t s = it_pos % kFwdSched, ph = (it_pos / kFwdSched) & 1;
       ++it_pos;
-      if (!wait(&it_full[s], ph)) return false;
+      if (!__all_sync(0xffffffffu, wait(&it_full[s], ph))) return false;
       t = s_item[s];
       __syncwarp();
       if (lane == 0) mbar_arrive(&it_empty[s]);
@@ -179,37 +183,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   // 12 warps launched with 168 registers a thread (the launch bounds' share of 65536):
   // 4 warps x 88 + 8 x 208 = 12 x 168. A softmax thread holds its row's 128 scores.
   if (warp < 4) {
-  regs_less<88>();
-  if (warp == 0) {
-    // ---- loader
-    uint32_t it = 0, tails = 0, qc[2] = {0, 0};
-    FwdItem t;
-    while (next_item(t)) {
+    regs_less<88>();
+    if (warp == 0) {
+      // ---- loader. A wait for a buffer that was never used passes: the phase before a
+      // barrier's first counts as complete.
+      uint32_t it = 0, tails = 0, q_ph = 0;  // ring position; bit j: phase of slot j's query tile
+      FwdItem t;
+      while (next_item(t)) {
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          if ((j ? t.n1 : t.n0) == 0) continue;
+          wait(&q_empty[j], ((q_ph >> j) & 1) ^ 1);
+          q_ph ^= 1u << j;
+          if (lane == 0) {
+            unsigned char* dst = base + SM::kQ + j * SM::kTile;
+            const int row = j ? t.row1 : t.row0, head = j ? t.head1 : t.head0;
+            mbar_arrive_expect_tx(&q_full[j], PREFIX ? (uint32_t)(a.bpt * a.group * HD * 2) : (uint32_t)SM::kTile);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if ((j ? t.n1 : t.n0) == 0) continue;
-        if (qc[j] > 0) wait(&q_empty[j], (qc[j] - 1) & 1);
-        ++qc[j];
-        if (lane == 0) {
-          unsigned char* dst = base + SM::kQ + j * SM::kTile;
-          const int row = j ? t.row1 : t.row0;
-          if constexpr (PREFIX) {
-            mbar_arrive_expect_tx(&q_full[j], (uint32_t)(a.bpt * a.group * HD * 2));
-            for (int x = 0; x < HD / 64; ++x)
-              tma_load_3d(dst + x * kAttnBox, &tmap_q, 64 * x, t.kvh * a.group, row * a.bpt, &q_full[j]);
-          } else {
-            mbar_arrive_expect_tx(&q_full[j], SM::kTile);
-            for (int x = 0; x < HD / 64; ++x)
-              tma_load_2d(dst + x * kAttnBox, &tmap_q, (j ? t.head1 : t.head0) * HD + 64 * x, row, &q_full[j]);
+            for (int x = 0; x < HD / 64; ++x) {
+              if constexpr (PREFIX)
+                tma_load_3d(dst + x * kAttnBox, &tmap_q, 64 * x, t.kvh * a.group, row * a.bpt, &q_full[j]);
+              else
+                tma_load_2d(dst + x * kAttnBox, &tmap_q, head * HD + 64 * x, row, &q_full[j]);
+            }
           }
         }
-      }
-      const int n = max(t.n0, t.n1);
-      for (int i = 0; i < n; ++i) {
-#pragma unroll
-        for (int which = 0; which < 2; ++which, ++it) {
+        const int n = max(t.n0, t.n1);
+#pragma unroll 1
+        for (int i2 = 0; i2 < 2 * n; ++i2, ++it) {  // K and V of block 0, of block 1, ...
+          const int i = i2 >> 1, which = i2 & 1;
           const uint32_t s = it % ST;
-          if (it >= ST) wait(&empty[s], ((it / ST) - 1) & 1);
+          wait(&empty[s], ((it / ST) & 1) ^ 1);
           unsigned char* dst = base + SM::kRing + s * SM::kTile;
           const CUtensorMap* map = which ? &tmap_v : &tmap_k;
           const bool part = PREFIX ? ((s_whole >> i) & 1) == 0 : kAttnRows * (i + 1) > t.len;
@@ -218,33 +222,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if constexpr (PREFIX) {
             // one box per page piece (box_rows keys); lanes take them in turn
             const int per = kAttnRows / a.box_rows;
-            int mine = 0;
-            for (int g = lane; g < per; g += 32) {
-              const int gg = i * per + g;
-              if (gg * a.box_rows < px_len && s_slot[gg] >= 0) ++mine;
-            }
-            const int boxes = __reduce_add_sync(0xffffffffu, mine);
+            const int gg = i * per + lane;  // box_rows >= 8: at most 16 pieces
+            const bool mine = lane < per && gg * a.box_rows < px_len && s_slot[gg] >= 0;
+            const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * a.box_rows * HD * 2));
             __syncwarp();
-            for (int g = lane; g < per; g += 32) {
-              const int gg = i * per + g;
-              if (gg * a.box_rows < px_len && s_slot[gg] >= 0)
-                for (int x = 0; x < HD / 64; ++x)
-                  tma_load_3d(dst + x * kAttnBox + g * a.box_rows * 128, map, 64 * x, t.kvh, s_slot[gg], bar);
-            }
+            if (mine)
+#pragma unroll
+              for (int x = 0; x < HD / 64; ++x)
+                tma_load_3d(dst + x * kAttnBox + lane * a.box_rows * 128, map, 64 * x, t.kvh, s_slot[gg], bar);
           } else if (lane == 0) {
             mbar_arrive_expect_tx(bar, SM::kTile);
+#pragma unroll
             for (int x = 0; x < HD / 64; ++x)
               tma_load_2d(dst + x * kAttnBox, map, t.kvh * HD + 64 * x, t.kv0 + kAttnRows * i, bar);
           }
           if (patch) {
             wait(&tail_bar, tails++ & 1);
+#pragma unroll 1
             for (int r = lane >> 3; r < kAttnRows; r += 4) {
               const int key = kAttnRows * i + r;
-              const bool in = key < t.len && (!PREFIX || s_slot[key / a.box_rows] >= 0);
-              if (!in)
-                for (int x = 0; x < HD / 64; ++x)
-                  *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+              if (key < t.len && (!PREFIX || s_slot[key / a.box_rows] >= 0)) continue;
+#pragma unroll
+              for (int x = 0; x < HD / 64; ++x)
+                *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_cta();
             __syncwarp();
@@ -252,96 +253,88 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
       }
-    }
-    // every copy has landed before the CTA may exit (phases already consumed return at once)
-    if (lane == 0) {
-      for (uint32_t k = it > ST ? it - ST : 0; k < it; ++k) mbar_wait(&full[k % ST], (k / ST) & 1, a.err);
-      for (int j = 0; j < 2; ++j)
-        if (qc[j]) mbar_wait(&q_full[j], (qc[j] - 1) & 1, a.err);
-    }
-  } else if (warp == 1) {
-    // ---- MMA issuer
-    constexpr uint32_t id_s = umma_idesc_bf16(kAttnRows, kAttnRows), id_o = umma_idesc_bf16_bmn(kAttnRows, HD);
-    uint32_t it = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, tiles[2] = {0, 0};
-    const uint32_t tmem = uniform(s_tmem);
-    FwdItem t;
-    while (next_item(t)) {
-      t.n0 = (int)uniform(t.n0);
-      t.n1 = (int)uniform(t.n1);
-      const int n = max(t.n0, t.n1);
-      if (n == 0) continue;
-      auto tile_at = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
-      auto scores = [&](int j, uint32_t k, bool last) {
-        attn_mma_ss<HD>(tmem + SM::tS(j), base + SM::kQ + j * SM::kTile, tile_at(k), id_s);
-        umma_commit_warp(&s_full[j]);
-        if (last) umma_commit_warp(&q_empty[j]);
-      };
-      wait(&full[it % ST], (it / ST) & 1);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int nj = j ? t.n1 : t.n0;
-        if (nj == 0) continue;
-        wait(&q_full[j], qc[j]++ & 1);
-        tc_fence_after();
-        scores(j, it, nj == 1);
+      // every copy has landed before the CTA may exit (phases already consumed return at once)
+      if (lane == 0) {
+#pragma unroll 1
+        for (uint32_t k = it > ST ? it - ST : 0; k < it; ++k) mbar_wait(&full[k % ST], (k / ST) & 1, a.err);
+        // slot j's last query tile: its phase is the one before the next
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) mbar_wait(&q_full[j], ((q_ph >> j) & 1) ^ 1, a.err);
       }
-      umma_commit_warp(&empty[it % ST]);
-      for (int i = 0; i < n; ++i, it += 2) {
-        const uint32_t kv = it + 1, kn = it + 2;
-        if constexpr (SM::kApart) {  // the next scores as soon as the last ones have been read
-          if (i + 1 < n) {
-            wait(&full[kn % ST], (kn / ST) & 1);
-#pragma unroll
+    } else if (warp == 1) {
+      // ---- MMA issuer. Step i: P V of block i and the scores of block i + 1.
+      constexpr uint32_t id_s = umma_idesc_bf16(kAttnRows, kAttnRows), id_o = umma_idesc_bf16_bmn(kAttnRows, HD);
+      uint32_t it = 0, q_ph = 0, p_ph = 0, o_ph = 0;  // bit j: phases of slot j
+      const uint32_t tmem = uniform(s_tmem);
+      FwdItem t;
+      while (next_item(t)) {
+        const int n0 = (int)uniform(t.n0), n1 = (int)uniform(t.n1), n = max(n0, n1);
+        auto tile = [&](uint32_t k) { return base + SM::kRing + (k % ST) * SM::kTile; };
+        auto scores = [&](int j, int i, int nj) {
+          if (i == 0) {
+            wait(&q_full[j], (q_ph >> j) & 1);
+            q_ph ^= 1u << j;
+          }
+          tc_fence_after();
+          attn_mma_ss<HD>(tmem + SM::tS(j), base + SM::kQ + j * SM::kTile, tile(it + 2 * i), id_s);
+          umma_commit_warp(&s_full[j]);
+          if (i + 1 == nj) umma_commit_warp(&q_empty[j]);
+        };
+#pragma unroll 1
+        for (int i = -1; i < n; ++i) {
+          const uint32_t kv = it + 2 * i + 1, kn = it + 2 * i + 2;
+          if (i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
+          if (SM::kApart && i + 1 < n) {  // the next scores as soon as the last ones have been read
+#pragma unroll 1
             for (int j = 0; j < 2; ++j) {
-              const int nj = j ? t.n1 : t.n0;
+              const int nj = j ? n1 : n0;
               if (i + 1 >= nj) continue;
-              wait(&s_read[j], pc[j] & 1);
-              tc_fence_after();
-              scores(j, kn, i + 2 == nj);
+              if (i >= 0) wait(&s_read[j], (p_ph >> j) & 1);
+              scores(j, i + 1, nj);
             }
             umma_commit_warp(&empty[kn % ST]);
           }
-        }
-        wait(&full[kv % ST], (kv / ST) & 1);
-        if (!SM::kApart && i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int nj = j ? t.n1 : t.n0;
-          if (i >= nj) continue;
-          wait(&p_full[j], pc[j]++ & 1);
-          if (i == 0) {
-            if (tiles[j] > 0) wait(&o_free[j], (tiles[j] - 1) & 1);
-            ++tiles[j];
+          if (i >= 0) wait(&full[kv % ST], (kv / ST) & 1);
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {
+            const int nj = j ? n1 : n0;
+            if (i >= 0 && i < nj) {
+              wait(&p_full[j], (p_ph >> j) & 1);
+              p_ph ^= 1u << j;
+              if (i == 0) {
+                wait(&o_free[j], ((o_ph >> j) & 1) ^ 1);
+                o_ph ^= 1u << j;
+              }
+              tc_fence_after();
+              attn_mma_ts(tmem + SM::tO(j), tmem + SM::tP(j), 32, tile(kv), id_o, i > 0);
+              umma_commit_warp(&o_done[j]);
+            }
+            if (!SM::kApart && i + 1 < nj) scores(j, i + 1, nj);
           }
-          tc_fence_after();
-          attn_mma_ts(tmem + SM::tO(j), tmem + SM::tP(j), 32, tile_at(kv), id_o, i > 0);
-          umma_commit_warp(&o_done[j]);
-          if (!SM::kApart && i + 1 < nj) scores(j, kn, i + 2 == nj);
+          if (i >= 0) umma_commit_warp(&empty[kv % ST]);
+          if (!SM::kApart && i + 1 < n) umma_commit_warp(&empty[kn % ST]);
         }
-        umma_commit_warp(&empty[kv % ST]);
-        if (!SM::kApart && i + 1 < n) umma_commit_warp(&empty[kn % ST]);
+        it += 2 * n;
       }
-    }
-    umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
-    if (lane == 0) mbar_wait(&mma_done, 0, a.err);
-  } else if (warp == 2) {
-    // ---- finder
-    if constexpr (!PREFIX) {
+      umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
+      if (lane == 0) mbar_wait(&mma_done, 0, a.err);
+    } else if (warp == 2 && !PREFIX) {
+      // ---- finder
       AttnOrder ord{a.cu, a.batch, a.pair_heads ? kAttnRows : 2 * kAttnRows, s_cache, 0, 0};
-      const bool ok = ord.init(a.T, lane);
-      if (!ok && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
-      const int64_t work = (int64_t)ord.total * a.units;
+      const bool good = ord.init(a.T, lane);
+      if (!good && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
+      const uint32_t work = ord.total * (uint32_t)a.units;  // below 2^31: the host checks
       for (uint32_t k = 0;; ++k) {
         const uint32_t s = k % kFwdSched;
-        if (k >= kFwdSched && !wait(&it_empty[s], ((k / kFwdSched) - 1) & 1)) break;
-        const int64_t w = attn_deal(k, blockIdx.x, gridDim.x);
-        const bool done = (int64_t)k * gridDim.x >= work;
+        if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kFwdSched) & 1) ^ 1))) break;
+        const uint32_t w = attn_deal(k, blockIdx.x, gridDim.x);
         FwdItem t = {};
-        if (w < work) {
+        t.valid = k * gridDim.x < work;  // else no CTA has any left
+        if (w < work) {                  // (an empty item: this CTA has none in the last round)
           int seq, cost;
-          const uint32_t rank = work <= UINT32_MAX ? (uint32_t)w / (uint32_t)a.units : (uint32_t)(w / a.units);
+          const uint32_t rank = w / (uint32_t)a.units;
           ord.find(rank, lane, seq, cost);
-          const int hu = (int)(w - (int64_t)rank * a.units);
+          const int hu = (int)(w - rank * (uint32_t)a.units);
           const int start = a.cu[seq], len = a.cu[seq + 1] - start;
           if (a.pair_heads) {
             t.head0 = 2 * hu;
@@ -358,33 +351,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           t.kvh = t.head0 / a.group;
           t.kv0 = start;
           t.len = len;
-          t.valid = 1;
-        } else if (!done) {
-          t.valid = 1;  // an empty item: this CTA has none in the last round
         }
         if (lane == 0) {
           s_item[s] = t;
           mbar_arrive(&it_full[s]);
         }
         __syncwarp();
-        if (done) break;
+        if (!t.valid) break;
       }
       // ---- then the rows of no sequence
       if (a.zero_rest) {
-        const bool none = !ok || a.batch == 0;
+        const bool none = !good || a.batch == 0;
         const int64_t first = none ? 0 : a.cu[0], last = none ? 0 : a.cu[a.batch];
-        attn_zero_rest(a.out, a.T, (int64_t)a.n_q * (HD / 8), first, last, lane);
+        attn_zero_rows(a.out, a.T, a.n_q * (HD / 8), first, last, lane);
         if (a.lse)
-          for (int64_t i = (int64_t)blockIdx.x * 32 + lane; i < (first + a.T - last) * a.n_q; i += (int64_t)gridDim.x * 32) {
-            const int64_t r = i / a.n_q;
-            a.lse[(i % a.n_q) * a.T + (r < first ? r : last + (r - first))] = -INFINITY;
-          }
+          for (int h = blockIdx.x; h < a.n_q; h += gridDim.x)
+            for (int64_t r = lane; r < first + a.T - last; r += 32)
+              a.lse[h * a.T + (r < first ? r : last + (r - first))] = -INFINITY;
       }
     }
-  }
   } else {
     regs_more<208>();
-    // ---- softmax, rescaling, epilogue
+    // ---- softmax, rescaling, results
     const int j = (warp - 4) >> 2, qtr = warp & 3, row = 32 * qtr + lane;
     const uint32_t lanes = (uint32_t)(32 * qtr) << 16;
     const uint32_t t_s = tmem + lanes + SM::tS(j), t_p = tmem + lanes + SM::tP(j), t_o = tmem + lanes + SM::tO(j);
@@ -394,10 +382,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     while (next_item(t)) {
       const int n = j ? t.n1 : t.n0;
       if (n == 0) continue;
+      const int row0 = (j ? t.row1 : t.row0) + 32 * qtr;
+      const int rows = t.kv0 + t.len - row0;  // prompt: rows of this warp that belong to the sequence
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int i = 0; i < n; ++i, ++done) {
         wait(&s_full[j], done & 1);
         tc_fence_after();
+        if (!PREFIX && rows <= 0) {  // whatever P holds for rows of no sequence stays in those rows
+          if (SM::kApart) {
+            if (lane == 0) mbar_arrive(&s_read[j]);
+            if (i > 0) wait(&o_done[j], (done - 1) & 1);  // not two blocks' arrivals in one phase of p_full
+          }
+          if (lane == 0) mbar_arrive(&p_full[j]);
+          continue;
+        }
         float s[kAttnRows];
         float top = tmem_ld128_max(t_s, s);
         if constexpr (SM::kApart) {
@@ -411,7 +410,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int key = kAttnRows * i + 32 * x + lane;
-              const uint32_t in = __ballot_sync(0xffffffffu, key < px_len && s_slot[min(key, px_len - 1) / a.box_rows] >= 0);
+              const uint32_t in =
+                  __ballot_sync(0xffffffffu, key < px_len && s_slot[min(key, px_len - 1) / a.box_rows] >= 0);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!((in >> e) & 1)) s[32 * x + e] = -INFINITY;
@@ -421,16 +421,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         } else if (i == n - 1) {
           // the diagonal block: keys after the row (and so behind the sequence) are not
           // seen. The warp's rows see the quarters before their own whole, their own up
-          // to the lane, and none after it.
+          // to the lane, and none after it. (The empty asm makes a branch of each quarter:
+          // selects run at half rate, and all 128 of them took longer than the exponentials.)
           quarters = qtr + 1;
           top = -INFINITY;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            if (x == qtr)
+            if (x == qtr) {
+              asm volatile("");
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (e > lane) s[32 * x + e] = -INFINITY;
-            if (x <= qtr) top = fmaxf(top, max32(s + 32 * x));
+            }
+            if (x <= qtr) {
+              asm volatile("");
+              top = fmaxf(top, max32(s + 32 * x));
+            }
           }
         }
         if (i == 0) {
@@ -442,20 +448,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           l *= f;
           wait(&o_done[j], (done - 1) & 1);
           tc_fence_after();
-#pragma unroll
-          for (int x = 0; x < HD / 32; ++x) {
-            float o[32];
-            tmem_ld32(t_o + 32 * x, o);
-            uint32_t w[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-            tmem_st32(t_o + 32 * x, w);
-          }
+#pragma unroll 1
+          for (int x = 0; x < HD; x += 16) tmem_scale16(t_o + x, f);
         }
         const float off = m == -INFINITY ? 0.f : -m * c;
-        if constexpr (SM::kApart) {  // PV of the block before has read the columns that P goes to
-          if (i > 0) wait(&o_done[j], (done - 1) & 1);
-        }
+        if (SM::kApart && i > 0) wait(&o_done[j], (done - 1) & 1);  // PV before has read the columns that P goes to
         const uint64_t c2 = pair(c, c), off2 = pair(off, off);
         uint64_t sum_a = 0, sum_b = 0;  // pairs of zeros
 #pragma unroll
@@ -464,20 +461,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (!PREFIX && x >= quarters) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[e] = 0;
-            tmem_st16(t_p + 16 * x, w);
-            continue;
-          }
+          } else {
+            asm volatile("");
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float p0, p1;
-            unpair(fma2(pair(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), c2, off2), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            if (e & 1)
-              sum_b = add2(sum_b, pair(p0, p1));
-            else
-              sum_a = add2(sum_a, pair(p0, p1));
-            w[e] = pack2(p0, p1);
+            for (int e = 0; e < 16; ++e) {
+              float p0, p1;
+              unpair(fma2(pair(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), c2, off2), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              if (e & 1)
+                sum_b = add2(sum_b, pair(p0, p1));
+              else
+                sum_a = add2(sum_a, pair(p0, p1));
+              w[e] = pack2(p0, p1);
+            }
           }
           tmem_st16(t_p + 16 * x, w);
         }
@@ -491,52 +488,60 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       wait(&o_done[j], (done - 1) & 1);
       tc_fence_after();
-      float o[HD];
-#pragma unroll
-      for (int x = 0; x < HD / 32; ++x) tmem_ld32(t_o + 32 * x, o + 32 * x);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free[j]);
       if constexpr (PREFIX) {
         const int b = (j ? t.row1 : t.row0) * a.bpt + row / a.group, g = row % a.group;
-        if (row < a.bpt * a.group && b < a.batch) {
-          const int64_t r = (int64_t)px_chunk * a.batch * a.n_q + (int64_t)b * a.n_q + t.kvh * a.group + g;
-          a.part_ml[r] = make_float2(m * c, l);
-          float4* dst = reinterpret_cast<float4*>(a.part_o + r * HD);
+        const bool in = row < a.bpt * a.group && b < a.batch;
+        const int64_t r = (int64_t)px_chunk * a.batch * a.n_q + (int64_t)b * a.n_q + t.kvh * a.group + g;
+        if (in) a.part_ml[r] = make_float2(m * c, l);
+        float4* dst = reinterpret_cast<float4*>(a.part_o + r * HD);
+#pragma unroll 1
+        for (int x = 0; x < HD / 32; ++x) {
+          float o[32];
+          tmem_ld32(t_o + 32 * x, o);
+          if (in)
 #pragma unroll
-          for (int e = 0; e < HD / 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) dst[8 * x + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[j]);
+      } else if (rows <= 0) {
+        if (lane == 0) mbar_arrive(&o_free[j]);
       } else {
+        // O / l through shared memory, 64 columns at a time, so that whole 128-byte lines
+        // leave: eight lanes per row, four rows per store
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
-        const int row0 = (j ? t.row1 : t.row0) + 32 * qtr, head = j ? t.head1 : t.head0;
-        const int rows = t.kv0 + t.len - row0;  // rows of this warp that belong to the sequence
-        if (a.lse && lane < rows) a.lse[(int64_t)head * a.T + row0 + lane] = m * a.scale + logf(l);
-        // through shared memory, 64 columns at a time, so that whole 128-byte lines leave:
-        // eight lanes per row, four rows per store
-        if (rows > 0) {
-          unsigned char* buf = base + SM::kOut + (warp - 4) * kStageBytes;
-          const int r0 = lane >> 3, ch0 = lane & 7;
-          const int64_t stride = (int64_t)a.n_q * (HD / 8);
-          uint4* dst = a.out + (row0 + r0) * stride + head * (HD / 8) + ch0;
-#pragma unroll
-          for (int x = 0; x < HD / 64; ++x) {
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-              const float* v = o + 64 * x + 8 * ch;
-              *reinterpret_cast<uint4*>(buf + attn_swz(lane, ch)) =
-                  make_uint4(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv), pack2(v[4] * inv, v[5] * inv),
-                             pack2(v[6] * inv, v[7] * inv));
-            }
+        const int head = j ? t.head1 : t.head0, r0 = lane >> 3, ch0 = lane & 7;
+        unsigned char* buf = base + SM::kOut + (warp - 4) * kStageBytes;
+        const int64_t stride = (int64_t)a.n_q * (HD / 8);
+        uint4* dst = a.out + (row0 + r0) * stride + head * (HD / 8) + ch0;
+#pragma unroll 1
+        for (int x = 0; x < HD / 64; ++x) {
+          float o[64];
+          tmem_ld32(t_o + 64 * x, o);
+          tmem_ld32(t_o + 64 * x + 32, o + 32);
+          if (x + 1 == HD / 64) {
+            tc_fence_before();
             __syncwarp();
-            uint4 w[8];
-#pragma unroll
-            for (int r4 = 0; r4 < 8; ++r4) w[r4] = *reinterpret_cast<const uint4*>(buf + attn_swz(4 * r4 + r0, ch0));
-            __syncwarp();
-#pragma unroll
-            for (int r4 = 0; r4 < 8; ++r4)
-              if (4 * r4 + r0 < rows) dst[4 * r4 * stride + 8 * x] = w[r4];
+            if (lane == 0) mbar_arrive(&o_free[j]);
           }
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            const float* v = o + 8 * ch;
+            *reinterpret_cast<uint4*>(buf + attn_swz(lane, ch)) =
+                make_uint4(pack2(v[0] * inv, v[1] * inv), pack2(v[2] * inv, v[3] * inv), pack2(v[4] * inv, v[5] * inv),
+                           pack2(v[6] * inv, v[7] * inv));
+          }
+          __syncwarp();
+          uint4 w[8];
+#pragma unroll
+          for (int r4 = 0; r4 < 8; ++r4) w[r4] = *reinterpret_cast<const uint4*>(buf + attn_swz(4 * r4 + r0, ch0));
+          __syncwarp();
+#pragma unroll
+          for (int r4 = 0; r4 < 8; ++r4)
+            if (4 * r4 + r0 < rows) dst[4 * r4 * stride + 8 * x] = w[r4];
         }
+        if (a.lse && lane < rows) a.lse[(int64_t)head * a.T + row0 + lane] = m * a.scale + logf(l);
       }
     }
   }
@@ -544,6 +549,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  attn_report(fail, a.err);
 }
 
 const void* attention_fwd_kernel(int head_dim, bool prefix) {
