@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const uint32_t kv = it + 2 * i + 1, kn = it + 2 * i + 2;
           if (i + 1 < n) wait(&full[kn % ST], (kn / ST) & 1);
           if (SM::kApart && i + 1 < n) {  // the next scores as soon as the last ones have been read
-#pragma unroll 1
+#pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int nj = j ? n1 : n0;
               if (i + 1 >= nj) continue;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             umma_commit_warp(&empty[kn % ST]);
           }
           if (i >= 0) wait(&full[kv % ST], (kv / ST) & 1);
-#pragma unroll 1
+#pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int nj = j ? n1 : n0;
             if (i >= 0 && i < nj) {
