@@ -576,8 +576,8 @@ void plan_decode(const qkvp_layout* L, int32_t batch, int32_t page_size, int32_t
   const int64_t heads = (int64_t)L->n_kv * p->head_blocks;
   const int64_t warps = (int64_t)sms * attention_decode_warps();
   const int64_t keys = (int64_t)max_pages * page_size + (p->apart ? 0 : prefix_len);
-  const int64_t most = (int64_t)batch * ((keys + 15) / 16);  // tiles, at most
-  p->ranges = (int)std::max<int64_t>(1, std::min<int64_t>(warps / heads, (most + kDecMinTiles - 1) / kDecMinTiles));
+  const int64_t parts = (int64_t)batch * ((keys + kDecMinKeys - 1) / kDecMinKeys);  // of the least length, at most
+  p->ranges = (int)std::max<int64_t>(1, std::min<int64_t>(warps / heads, parts));
   const int64_t ctas = (p->ranges * heads + attention_decode_warps() - 1) / attention_decode_warps();
   p->grid = (int)std::min<int64_t>(ctas, sms);
   p->rows = (int64_t)batch + p->ranges + (int64_t)p->chunks * batch;
@@ -591,7 +591,8 @@ int check_decode(const qkvp_layout* layout, int32_t batch, int32_t page_size, in
   float unused;
   QKVP_TRY(check_attention(layout, batch, 0.f, &unused));
   if (page_size <= 0) return QKVP_ERR_VALUE;
-  if (max_pages < 0 || (int64_t)max_pages * page_size > INT32_MAX || prefix_len < 0 || prefix_len > INT32_MAX - 4096 ||
+  if (max_pages < 0 || (int64_t)max_pages * page_size > INT32_MAX || prefix_len < 0 ||
+      (int64_t)max_pages * page_size + prefix_len > INT32_MAX - 4096 ||
       batch > (1 << 20))
     return QKVP_ERR_SHAPE;
   return QKVP_OK;
@@ -1502,6 +1503,8 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   a.max_pages = max_pages;
   a.lengths = lengths;
   a.prefix_pages = prefix_pages;
+  a.tile_keys = dec_tile_keys(hd);
+  a.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
   a.joint_len = p.apart ? 0 : prefix_len;
   a.prefix_chunks = p.chunks;
   a.ranges = p.ranges;

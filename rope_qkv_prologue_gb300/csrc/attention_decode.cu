@@ -5,9 +5,9 @@
 // heads of the group: with G of 4 to 16 that is far below what the tensor cores
 // could do, so the kernel is bound by reading the pool once, and its work is to
 // keep enough of it in flight. Every warp is a worker of its own: it streams
-// tiles of 16 keys of one key/value head through its own ring of shared memory
+// tiles of 16 or 32 keys of one key/value head through its own ring of shared memory
 // (16-byte asynchronous copies, no barrier with other warps), with
-//     S [16 heads x 16 keys] = Q K^T,  P = 2^(c S - m),  O += P V
+//     S = Q K^T,  P = 2^(c S - m),  O += P V
 // on m16n8k16 matrix instructions, the group's heads being the rows (rows past
 // the group are zero). Running maxima and sums are fp32; P is rounded to bf16 as
 // an operand.
@@ -27,12 +27,13 @@ namespace {
 
 constexpr int kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kTileKeys = 16;
 
+// Keys per tile and tiles in flight per warp: 8 KiB a tile, 192 KiB an SM.
 template <int HD>
-struct DecSmem {
-  static constexpr int kTileBytes = 2 * kTileKeys * HD * 2;  // k rows, then v rows
-  static constexpr int kStages = HD == 128 ? 3 : 6;
+struct DecShape {
+  static constexpr int kKeys = dec_tile_keys(HD);
+  static constexpr int kStages = 3;
+  static constexpr int kTileBytes = 2 * kKeys * HD * 2;  // k rows, then v rows
   static constexpr int kWarpBytes = kStages * kTileBytes;
 };
 
@@ -63,13 +64,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Keys of sequence b: the prefix (when it is not computed apart), then its own.
-__device__ __forceinline__ int64_t dec_own(const AttnDecodeArgs& a, int b) {
-  const int64_t n = a.lengths[b], most = (int64_t)a.max_pages * a.page_size;
+// Own keys of sequence b, within what its row of the page table can name.
+__device__ __forceinline__ int dec_own(const AttnDecodeArgs& a, int b) {
+  const int n = a.lengths[b], most = a.max_pages * a.page_size;
   return n < 0 ? 0 : (n > most ? most : n);
 }
+// Tiles of sequence b: the prefix's keys (when it is not computed apart), then its own.
 __device__ __forceinline__ int dec_tiles(const AttnDecodeArgs& a, int b) {
-  return (int)((a.joint_len + dec_own(a, b) + kTileKeys - 1) / kTileKeys);
+  return (int)(((uint32_t)a.joint_len + (uint32_t)dec_own(a, b) + (uint32_t)a.tile_keys - 1) / (uint32_t)a.tile_keys);
 }
 
 // Whole warp: all tiles of the batch, and those of the sequences before `b`.
@@ -90,8 +92,8 @@ __device__ __forceinline__ int64_t dec_total(const AttnDecodeArgs& a, int b, int
 }
 
 __device__ __forceinline__ int64_t dec_quota(const AttnDecodeArgs& a, int64_t total) {
-  const int64_t q = (total + a.ranges - 1) / a.ranges;
-  return q < kDecMinTiles ? kDecMinTiles : q;
+  const int64_t q = (total + a.ranges - 1) / a.ranges, least = kDecMinKeys / a.tile_keys;
+  return q < least ? least : q;
 }
 
 // A position in the concatenated tiles.
@@ -109,32 +111,35 @@ struct DecCursor {
 };
 
 // Pool row of key `key` of sequence b, or -1 (behind its end, or a bad page).
-__device__ __forceinline__ int64_t dec_slot(const AttnDecodeArgs& a, int b, int64_t keys, int64_t key) {
+__device__ __forceinline__ int dec_slot(const AttnDecodeArgs& a, int b, uint32_t keys, uint32_t key) {
   if (key >= keys) return -1;
   const int32_t* pages = a.prefix_pages;
-  if (key >= a.joint_len) {
-    key -= a.joint_len;
+  if (key >= (uint32_t)a.joint_len) {
+    key -= (uint32_t)a.joint_len;
     pages = a.page_table + (int64_t)b * a.table_stride;
   }
-  const int64_t p = key / a.page_size;
+  const uint32_t p = a.page_shift >= 0 ? key >> a.page_shift : key / (uint32_t)a.page_size;
   const int page = pages[p];
   if (page < 0 || page >= a.num_pages) {
     if (a.dev_status) atomicOr(a.dev_status, kDevBadPage);
     return -1;
   }
-  return (int64_t)page * a.page_size + (key - p * a.page_size);
+  return page * a.page_size + (int)(key - p * (uint32_t)a.page_size);
 }
 
 }  // namespace
 
 template <int HD>
 __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(const AttnDecodeArgs a) {
-  using SM = DecSmem<HD>;
-  constexpr int ST = SM::kStages, CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks per row, rows per copy instruction
+  using SH = DecShape<HD>;
+  constexpr int ST = SH::kStages, KT = SH::kKeys, NT = KT / 8;
+  constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks per row, rows per copy instruction
+  constexpr uint32_t kAll = KT == 32 ? 0xffffffffu : (1u << KT) - 1u;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ uint32_t s_in[kDecWarps][ST];  // bit i: key i of the stage's tile is attended
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = smem_addr(smem_raw) + warp * SM::kWarpBytes;
+  const uint32_t ring = smem_addr(smem_raw) + warp * SH::kWarpBytes;
+  const float c = a.scale_log2;
   griddep_wait();
   griddep_launch_dependents();
 
@@ -142,15 +147,17 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
   const int64_t total = dec_total(a, 0, lane, &before);
   const int64_t quota = dec_quota(a, total);
   const int heads = a.n_kv * a.head_blocks;
-  const int64_t items = (int64_t)a.ranges * heads;
-  for (int64_t w = (int64_t)blockIdx.x * kDecWarps + warp; w < items; w += (int64_t)gridDim.x * kDecWarps) {
-    const int64_t range = w / heads, t0 = range * quota, t1 = min(total, t0 + quota);
-    if (t0 >= t1) break;
-    const int hv = (int)(w % heads), kvh = hv / a.head_blocks, hb = hv % a.head_blocks;
-    const int head0 = kvh * a.group + hb * kTileKeys, n_heads = min(kTileKeys, a.group - hb * kTileKeys);
+  const int items = a.ranges * heads;
+  for (int w = blockIdx.x * kDecWarps + warp; w < items; w += gridDim.x * kDecWarps) {
+    const int range = w / heads;
+    const int64_t t0 = range * quota;
+    if (t0 >= total) break;
+    const int n_tiles = (int)min(quota, total - t0);
+    const int hv = w % heads, kvh = hv / a.head_blocks, hb = hv % a.head_blocks;
+    const int head0 = kvh * a.group + hb * 16, n_heads = min(16, a.group - hb * 16);
 
     // where the range begins
-    DecCursor c{0, 0, 0};
+    DecCursor cu{0, 0, 0};
     {
       int64_t left = t0;
       for (int s0 = 0; s0 < a.batch; s0 += 32) {
@@ -164,9 +171,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
         const uint32_t past = __ballot_sync(0xffffffffu, sum > left);
         if (past) {
           const int src = __ffs(past) - 1;
-          c.b = s0 + src;
-          c.tiles = __shfl_sync(0xffffffffu, n, src);
-          c.tile = (int)(left - (__shfl_sync(0xffffffffu, sum, src) - c.tiles));
+          cu.b = s0 + src;
+          cu.tiles = __shfl_sync(0xffffffffu, n, src);
+          cu.tile = (int)(left - (__shfl_sync(0xffffffffu, sum, src) - cu.tiles));
           break;
         }
         left -= __shfl_sync(0xffffffffu, sum, 31);
@@ -175,33 +182,34 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
 
     // Loads run ST - 1 tiles ahead of the arithmetic, and the page lookup of a
     // tile one step ahead of its loads.
-    DecCursor ld = c;
-    int64_t ld_keys = a.joint_len + dec_own(a, ld.b), slot = -1;
+    DecCursor ld = cu;
+    uint32_t ld_keys = (uint32_t)(a.joint_len + dec_own(a, ld.b));
+    int slot = -1;
     auto look_up = [&]() {
-      if (lane < kTileKeys) slot = dec_slot(a, ld.b, ld_keys, (int64_t)ld.tile * kTileKeys + lane);
+      if (lane < KT) slot = dec_slot(a, ld.b, ld_keys, (uint32_t)(ld.tile * KT + lane));
     };
     auto advance = [&]() {
-      const int b = ld.b;
-      ++ld.tile;
+      if (++ld.tile < ld.tiles) return;
       ld.settle(a);
-      if (ld.b != b) ld_keys = a.joint_len + dec_own(a, ld.b);
+      ld_keys = (uint32_t)(a.joint_len + dec_own(a, ld.b));
     };
+    const int ch = lane % CH, row_ch = a.n_kv * CH;
+    const uint4* k_src = a.k_pool + kvh * CH + ch;
+    const uint4* v_src = a.v_pool + kvh * CH + ch;
     auto issue = [&](uint32_t st) {
-      const uint32_t in = __ballot_sync(0xffffffffu, lane < kTileKeys && slot >= 0);
+      const uint32_t in = __ballot_sync(0xffffffffu, lane < KT && slot >= 0);
       if (lane == 0) s_in[warp][st] = in;
-      const uint32_t dst = ring + st * SM::kTileBytes;
-      const int ch = lane % CH;
+      const uint32_t dst = ring + st * SH::kTileBytes;
 #pragma unroll
-      for (int i = 0; i < kTileKeys / RPI; ++i) {
+      for (int i = 0; i < KT / RPI; ++i) {
         const int r = i * RPI + lane / CH;
-        const int64_t row = __shfl_sync(0xffffffffu, slot, r);
-        const int64_t off = ((row < 0 ? 0 : row) * a.n_kv + kvh) * CH + ch;
+        const int row = __shfl_sync(0xffffffffu, slot, r);
+        const int64_t off = (int64_t)max(row, 0) * row_ch;
         const uint32_t to = dst + r * (HD * 2) + ((ch ^ (r & 7)) << 4);
-        cp_async16(to, a.k_pool + off, row >= 0);
-        cp_async16(to + kTileKeys * HD * 2, a.v_pool + off, row >= 0);
+        cp_async16(to, k_src + off, row >= 0);
+        cp_async16(to + KT * HD * 2, v_src + off, row >= 0);
       }
     };
-    const int64_t n_tiles = t1 - t0;
     look_up();
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) {
@@ -216,31 +224,30 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
     }
 
     uint32_t qf[HD / 16][4];
-    float o[HD / 8][4], m[2], l[2];
-    auto begin = [&]() {  // a sequence's first tile here
+    float o[HD / 8][4], m[2], l[2];  // m in powers of two (the scores times scale log2(e))
+    auto begin = [&]() {             // a sequence's first tile here
 #pragma unroll
       for (int ks = 0; ks < HD / 16; ++ks)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int r = (lane >> 2) + 8 * (x & 1), d = 16 * ks + 8 * (x >> 1) + 2 * (lane & 3);
-          qf[ks][x] = r < n_heads ? *reinterpret_cast<const uint32_t*>(
-                                        a.q + ((int64_t)c.b * a.n_q + head0 + r) * HD + d)
-                                  : 0u;
+          qf[ks][x] =
+              r < n_heads ? *reinterpret_cast<const uint32_t*>(a.q + ((int64_t)cu.b * a.n_q + head0 + r) * HD + d) : 0u;
         }
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
     };
-    bool first = c.tile == 0;  // of the sequence: else the segment continues one of the range before
-    auto end = [&]() {         // its last tile here: the partial result
+    bool first = cu.tile == 0;  // of the sequence: else the segment continues one of the range before
+    auto end = [&]() {          // its last tile here: the partial result
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
         const int r = (lane >> 2) + 8 * x;
         if (r < n_heads) {
-          const int64_t row = (first ? (int64_t)c.b : a.batch + range) * a.n_q + head0 + r;
+          const int64_t row = (int64_t)(first ? cu.b : a.batch + range) * a.n_q + head0 + r;
           if ((lane & 3) == 0) a.part_ml[row] = make_float2(m[x], l[x]);
           float2* dst = reinterpret_cast<float2*>(a.part_o + row * HD) + (lane & 3);
 #pragma unroll
@@ -250,53 +257,58 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
     };
     begin();
     uint32_t st = 0;
-    for (int64_t t = 0; t < n_tiles; ++t) {
+#pragma unroll 1
+    for (int t = 0; t < n_tiles; ++t) {
       cp_wait<ST - 2>();
       __syncwarp();  // this tile is here, and every lane is done with the one before
-      {
-        const uint32_t nst = st == 0 ? ST - 1 : st - 1;
-        if (t + ST - 1 < n_tiles) {
-          issue(nst);
-          if (t + ST < n_tiles) {
-            advance();
-            look_up();
-          }
+      if (t + ST - 1 < n_tiles) {
+        issue(st == 0 ? ST - 1 : st - 1);
+        if (t + ST < n_tiles) {
+          advance();
+          look_up();
         }
-        cp_commit();
       }
-      const uint32_t kt = ring + st * SM::kTileBytes, vt = kt + kTileKeys * HD * 2;
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      cp_commit();
+      const uint32_t kt = ring + st * SH::kTileBytes, vt = kt + KT * HD * 2;
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
       {
         const int key = ((lane >> 4) << 3) + (lane & 7), hi = (lane >> 3) & 1;
-        const uint32_t row = kt + key * (HD * 2);
 #pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks) {
-          uint32_t b[4];
-          ldsm4(row + (((2 * ks + hi) ^ (key & 7)) << 4), b);
-          mma16816(s[0], qf[ks], b[0], b[1]);
-          mma16816(s[1], qf[ks], b[2], b[3]);
-        }
+        for (int ks = 0; ks < HD / 16; ++ks)
+#pragma unroll
+          for (int n = 0; n < NT; n += 2) {
+            uint32_t b[4];
+            ldsm4(kt + (8 * n + key) * (HD * 2) + (((2 * ks + hi) ^ (key & 7)) << 4), b);
+            mma16816(s[n], qf[ks], b[0], b[1]);
+            mma16816(s[n + 1], qf[ks], b[2], b[3]);
+          }
       }
       const uint32_t in = s_in[warp][st];
+      if (in != kAll) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = 8 * n + 2 * (lane & 3) + (x & 1);
-          s[n][x] = (in >> key) & 1 ? s[n][x] * a.scale_log2 : -INFINITY;
-        }
+          for (int x = 0; x < 4; ++x)
+            if (!((in >> (8 * n + 2 * (lane & 3) + (x & 1))) & 1)) s[n][x] = -INFINITY;
+      }
+      // A row's reference m only moves where a score passes it by more than 8 powers of
+      // two (see the prompt kernel); until then no lane has to know the others' maxima.
       float top[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float v = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        top[x] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        top[x] = fmaxf(s[0][2 * x], s[0][2 * x + 1]);
+#pragma unroll
+        for (int n = 1; n < NT; ++n) top[x] = max3(top[x], s[n][2 * x], s[n][2 * x + 1]);
       }
-      // rescale only where a maximum grew by more than 8 powers of two (see the prompt kernel)
-      if (__any_sync(0xffffffffu, top[0] - m[0] > 8.f || top[1] - m[1] > 8.f)) {
+      if (__any_sync(0xffffffffu, fmaf(top[0], c, -m[0]) > 8.f || fmaf(top[1], c, -m[1]) > 8.f)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float m_new = fmaxf(m[x], top[x]);
+          float v = top[x] * c;
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+          const float m_new = fmaxf(m[x], v);
           const float f = m_new == m[x] ? 1.f : ex2(m[x] - m_new);
           m[x] = m_new;
           l[x] *= f;
@@ -307,37 +319,35 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
           }
         }
       }
-      uint32_t pf[4];
+      uint32_t pf[NT / 2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float off = m[x] == -INFINITY ? 0.f : m[x];
+        const float off = m[x] == -INFINITY ? 0.f : -m[x];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float p0 = ex2(s[n][2 * x] - off), p1 = ex2(s[n][2 * x + 1] - off);
+        for (int n = 0; n < NT; ++n) {
+          const float p0 = ex2(fmaf(s[n][2 * x], c, off)), p1 = ex2(fmaf(s[n][2 * x + 1], c, off));
           l[x] += p0 + p1;
-          pf[2 * n + x] = pack2(p0, p1);
+          pf[n >> 1][2 * (n & 1) + x] = pack2(p0, p1);
         }
       }
       {
         const int key = (((lane >> 3) & 1) << 3) + (lane & 7), hi = lane >> 4;
-        const uint32_t row = vt + key * (HD * 2);
 #pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          uint32_t b[4];
-          ldsm4t(row + (((2 * i + hi) ^ (key & 7)) << 4), b);
-          mma16816(o[2 * i], pf, b[0], b[1]);
-          mma16816(o[2 * i + 1], pf, b[2], b[3]);
-        }
+        for (int k2 = 0; k2 < NT / 2; ++k2)
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            uint32_t b[4];
+            ldsm4t(vt + (16 * k2 + key) * (HD * 2) + (((2 * i + hi) ^ (key & 7)) << 4), b);
+            mma16816(o[2 * i], pf[k2], b[0], b[1]);
+            mma16816(o[2 * i + 1], pf[k2], b[2], b[3]);
+          }
       }
       st = st + 1 == ST ? 0 : st + 1;
-      if (c.tile + 1 == c.tiles || t + 1 == n_tiles) {
+      if (++cu.tile == cu.tiles || t + 1 == n_tiles) {
         end();
-        ++c.tile;
-        c.settle(a);
+        cu.settle(a);
         first = true;
         if (t + 1 < n_tiles) begin();
-      } else {
-        ++c.tile;
       }
     }
     cp_wait<0>();
@@ -422,7 +432,7 @@ const void* attention_join_kernel(int head_dim) {
                         : reinterpret_cast<const void*>(&qkvp_attention_join_kernel<128>);
 }
 int attention_decode_smem_bytes(int head_dim) {
-  return kDecWarps * (head_dim == 64 ? DecSmem<64>::kWarpBytes : DecSmem<128>::kWarpBytes);
+  return kDecWarps * (head_dim == 64 ? DecShape<64>::kWarpBytes : DecShape<128>::kWarpBytes);
 }
 int attention_decode_threads() { return kDecThreads; }
 int attention_decode_warps() { return kDecWarps; }

@@ -391,7 +391,8 @@ int attention_bwd_smem_bytes(int head_dim);
 int attention_bwd_threads();
 
 // One query row per sequence over the paged pool.
-constexpr int kDecMinTiles = 4;   // tiles of 16 keys of a part (at least)
+constexpr int kDecMinKeys = 64;   // keys of a part (at least)
+QKVP_HD constexpr int dec_tile_keys(int head_dim) { return head_dim == 64 ? 32 : 16; }  // keys per tile: 8 KiB
 constexpr int kJoinWarps = 8;     // warps per CTA of the kernel that joins the partial results
 struct AttnDecodeArgs {
   int32_t n_q, n_kv, group;
@@ -407,7 +408,9 @@ struct AttnDecodeArgs {
   int32_t max_pages;
   const int32_t* lengths;
   const int32_t* prefix_pages;
-  int64_t joint_len;       // prefix keys that every sequence walks itself (0: none, or computed apart)
+  int32_t tile_keys;       // dec_tile_keys
+  int32_t page_shift;      // log2(page_size), or -1
+  int32_t joint_len;       // prefix keys that every sequence walks itself (0: none, or computed apart)
   int32_t prefix_chunks;   // key ranges of the prefix kernel's partial results (0: none)
   int32_t ranges;          // parts that the tiles of all sequences are cut into
   int32_t wph;             // join: warps per head
