@@ -140,7 +140,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_addr(smem_raw) + warp * SH::kWarpBytes;
   const float c = a.scale_log2;
-  griddep_wait();
+  // Behind the prefix kernel this one begins at once: it reads nothing of that
+  // kernel's, which itself waited for everything before it. It waits at its end, so
+  // that the joining kernel, which waits for this one, has both.
+  if (!a.prefix_chunks) griddep_wait();
   griddep_launch_dependents();
 
   int64_t before;
@@ -353,6 +356,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
     cp_wait<0>();
     __syncwarp();
   }
+  if (a.prefix_chunks) griddep_wait();
 }
 
 // Joins the partial results of each (sequence, head): its own in the ranges it
@@ -391,20 +395,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qkvp_attention_join_kernel(co
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     const float off = top == -INFINITY ? 0.f : top;
-    for (int i = lane; i < parts; i += 32) {
-      const float2 v = a.part_ml[row_of(i)];
-      sum += ex2(v.x - off) * v.y;
+    // 32 parts at a time: lane i holds part i's factor
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float f = 0.f;
+      if (i0 + lane < parts) {
+        const float2 v = a.part_ml[row_of(i0 + lane)];
+        f = ex2(v.x - off);
+        sum += f * v.y;
+      }
+      const int n = min(32, parts - i0);
+#pragma unroll 8
+      for (int i = sub; i < n; i += a.wph) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* src = a.part_o + row_of(i0 + i) * HD + V * lane;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(fi, src[e], o[e]);
+      }
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-#pragma unroll 4
-    for (int i = sub; i < parts; i += a.wph) {
-      const int64_t r = row_of(i);
-      const float f = ex2(a.part_ml[r].x - off);
-      const float* src = a.part_o + r * HD + V * lane;
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = fmaf(f, src[e], o[e]);
-    }
   }
   if (a.wph > 1) {
 #pragma unroll
