@@ -325,16 +325,16 @@ def qkv_newton_schulz_plan(L, cols, split=0, count=1):
 
 def qkv_attention_fwd(L, T, batch, cu_seqlens, q, k, v, scale, flags, out, lse=None, dev_status=None, stream=None,
                       check=True):
-    st = _lib.qkv_attention_fwd(ctypes.byref(L), int(T), int(batch), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
-                                float(scale), int(flags), _ptr(out), _ptr(lse), _ptr(dev_status), _stream(stream))
+    st = _lib.qkv_attention_fwd(ctypes.byref(L), T, batch, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
+                                scale, flags, _ptr(out), _ptr(lse), _ptr(dev_status), _stream(stream))
     return _ret(st, "qkv_attention_fwd", check)
 
 
 def qkv_attention_bwd(L, T, batch, cu_seqlens, dout, q, k, v, out, lse, scale, flags, dq, dk, dv, dev_status=None,
                       workspace=None, workspace_bytes=0, stream=None, check=True):
-    st = _lib.qkv_attention_bwd(ctypes.byref(L), int(T), int(batch), _ptr(cu_seqlens), _ptr(dout), _ptr(q), _ptr(k),
-                                _ptr(v), _ptr(out), _ptr(lse), float(scale), int(flags), _ptr(dq), _ptr(dk), _ptr(dv),
-                                _ptr(dev_status), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    st = _lib.qkv_attention_bwd(ctypes.byref(L), T, batch, _ptr(cu_seqlens), _ptr(dout), _ptr(q), _ptr(k),
+                                _ptr(v), _ptr(out), _ptr(lse), scale, flags, _ptr(dq), _ptr(dk), _ptr(dv),
+                                _ptr(dev_status), _ptr(workspace), workspace_bytes, _stream(stream))
     return _ret(st, "qkv_attention_bwd", check)
 
 
@@ -352,10 +352,10 @@ def qkv_attention_bwd_workspace(L, T, check=True):
 def qkv_attention_decode(L, batch, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages, table_stride,
                          lengths, prefix_pages, prefix_len, scale, out, lse=None, dev_status=None, workspace=None,
                          workspace_bytes=0, stream=None, check=True):
-    st = _lib.qkv_attention_decode(ctypes.byref(L), int(batch), _ptr(q), _ptr(k_pool), _ptr(v_pool), int(num_pages),
-                                   int(page_size), _ptr(page_table), int(max_pages), int(table_stride), _ptr(lengths),
-                                   _ptr(prefix_pages), int(prefix_len), float(scale), _ptr(out), _ptr(lse),
-                                   _ptr(dev_status), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    st = _lib.qkv_attention_decode(ctypes.byref(L), batch, _ptr(q), _ptr(k_pool), _ptr(v_pool), num_pages,
+                                   page_size, _ptr(page_table), max_pages, table_stride, _ptr(lengths),
+                                   _ptr(prefix_pages), prefix_len, scale, _ptr(out), _ptr(lse),
+                                   _ptr(dev_status), _ptr(workspace), workspace_bytes, _stream(stream))
     return _ret(st, "qkv_attention_decode", check)
 
 

@@ -8,6 +8,8 @@ packed qkv in, contiguous q, k, v out; its backward writes the gradient of the
 packed tensor in one pass.
 """
 
+import functools
+
 import torch
 
 from . import _lib as C
@@ -252,21 +254,45 @@ def mla_kv_path_beside(side, pos, w, page, offset, pool, kv_rows=None, kv_proj=N
     return on_side_stream(side, kv_path)
 
 
-def _attention_layout(q, k, v):
-    """The layout of q [rows, n_q, D] over k, v [rows, n_kv, D], all contiguous bf16 on one device."""
-    _check_dev(q, k, v)
+@functools.lru_cache(maxsize=None)
+def _heads(n_q, n_kv, head_dim):
+    """The layout struct of these heads (the library only reads it)."""
+    return C.layout("sectioned", n_q, n_kv, head_dim)
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_workspace(n_q, n_kv, head_dim, batch, page_size, max_pages, prefix_len, device_index):
+    return C.qkv_attention_decode_workspace(_heads(n_q, n_kv, head_dim), batch, page_size, max_pages, prefix_len)
+
+
+def _launch_stream(stream, device, *made):
+    """The raw handle of `stream` (default: the current one of `device`). Tensors
+    made for a call on a stream given must outlive its work there, whatever the
+    current stream does with their memory."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _check_qkv(q, k, v):
     for t in (q, k, v):
-        if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_contiguous():
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_contiguous():
             raise ValueError("q, k and v must be contiguous bf16 [T, heads, head_dim] tensors")
     if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
         raise ValueError("k and v must have one shape, and q's rows and head_dim")
-    if k.device != q.device or v.device != q.device:
-        raise ValueError("q, k and v must live on one device")
-    return C.layout("sectioned", q.shape[1], k.shape[1], q.shape[2])
+    if not q.is_cuda or k.device != q.device or v.device != q.device:
+        raise ValueError("q, k and v must live on one CUDA device")
 
 
 def _check_like(t, shape, dtype, device, name):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
 
 
@@ -274,7 +300,13 @@ def _check_offsets(cu_seqlens, device):
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [batch + 1]")
     _check_like(cu_seqlens, cu_seqlens.shape, torch.int32, device, "cu_seqlens")
-    return cu_seqlens.numel() - 1
+    return cu_seqlens.shape[0] - 1
+
+
+def _check_status(dev_status, device):
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.numel() < 1
+                                   or dev_status.device != device):
+        raise ValueError(f"dev_status must be an int32 tensor on {device}")
 
 
 def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None, dev_status=None, stream=None):
@@ -284,19 +316,24 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
     Returns out [T, n_q, D], or (out, lse [n_q, T] float32) with save_lse.
     scale defaults to D ** -0.5. Rows of no sequence are zero in an out made
     here, and left as they are in one given (lse: -inf, in both)."""
-    L = _attention_layout(q, k, v)
-    batch = _check_offsets(cu_seqlens, q.device)
-    flags = 0
+    _check_qkv(q, k, v)
+    dev = q.device
+    batch = _check_offsets(cu_seqlens, dev)
+    _check_status(dev_status, dev)
+    T, n_q, D = q.shape
+    flags, made = 0, None
     if out is None:
-        out, flags = torch.empty_like(q), C.QKVP_ZERO_REST
+        out = made = torch.empty_like(q)
+        flags = C.QKVP_ZERO_REST
     else:
-        _check_like(out, q.shape, torch.bfloat16, q.device, "out")
+        _check_like(out, q.shape, torch.bfloat16, dev, "out")
     lse = None
     if save_lse:
-        fill = torch.empty if flags else _neg_inf
-        lse = fill((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    C.qkv_attention_fwd(L, q.shape[0], batch, cu_seqlens, q, k, v, 0.0 if scale is None else scale, flags, out, lse,
-                        dev_status, stream)
+        lse = torch.empty((n_q, T), dtype=torch.float32, device=dev)
+        if not flags:
+            lse.fill_(float("-inf"))
+    C.qkv_attention_fwd(_heads(n_q, k.shape[1], D), T, batch, cu_seqlens, q, k, v, 0.0 if scale is None else scale,
+                        flags, out, lse, dev_status, _launch_stream(stream, dev, made, lse))
     return (out, lse) if save_lse else out
 
 
@@ -305,18 +342,21 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspac
     the upstream gradient dout [T, n_q, D] bf16, from the forward's out and lse.
     Rows of no sequence get zero gradients. `workspace` (a device tensor of at
     least 4 * n_q * T bytes) is allocated here when not given."""
-    L = _attention_layout(q, k, v)
-    T, n_q, _ = q.shape
-    batch = _check_offsets(cu_seqlens, q.device)
-    _check_like(dout, q.shape, torch.bfloat16, q.device, "dout")
-    _check_like(out, q.shape, torch.bfloat16, q.device, "out")
-    _check_like(lse, (n_q, T), torch.float32, q.device, "lse")
+    _check_qkv(q, k, v)
+    dev = q.device
+    T, n_q, D = q.shape
+    batch = _check_offsets(cu_seqlens, dev)
+    _check_status(dev_status, dev)
+    _check_like(dout, q.shape, torch.bfloat16, dev, "dout")
+    _check_like(out, q.shape, torch.bfloat16, dev, "out")
+    _check_like(lse, (n_q, T), torch.float32, dev, "lse")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    made = None
     if workspace is None:
-        workspace = torch.empty(max(4 * n_q * T, 16), dtype=torch.uint8, device=q.device)
-    C.qkv_attention_bwd(L, T, batch, cu_seqlens, dout, q, k, v, out, lse, 0.0 if scale is None else scale,
-                        C.QKVP_ZERO_REST, dq, dk, dv, dev_status, workspace,
-                        workspace.numel() * workspace.element_size(), stream)
+        workspace = made = torch.empty(max(n_q * T, 4), dtype=torch.float32, device=dev)
+    C.qkv_attention_bwd(_heads(n_q, k.shape[1], D), T, batch, cu_seqlens, dout, q, k, v, out, lse,
+                        0.0 if scale is None else scale, C.QKVP_ZERO_REST, dq, dk, dv, dev_status, workspace,
+                        workspace.numel() * workspace.element_size(), _launch_stream(stream, dev, dq, dk, dv, made))
     return dq, dk, dv
 
 
@@ -348,8 +388,7 @@ def _check_pages(pages, name, device, dim):
 
 def attention_decode_workspace_bytes(n_q, n_kv, head_dim, batch, page_size, max_pages, prefix_len=0):
     """Workspace bytes attention_decode needs for these sizes on the current device."""
-    return C.qkv_attention_decode_workspace(C.layout("sectioned", n_q, n_kv, head_dim), batch, page_size, max_pages,
-                                            prefix_len)
+    return C.qkv_attention_decode_workspace(_heads(n_q, n_kv, head_dim), batch, page_size, max_pages, prefix_len)
 
 
 def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, prefix_len=0, scale=None,
@@ -363,46 +402,46 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
     Returns out [B, n_q, D], or (out, lse [B, n_q] float32) with save_lse.
     `workspace` (a device tensor of attention_decode_workspace_bytes bytes) is
     allocated here when not given."""
-    _check_dev(q, k_pool, v_pool, page_table, lengths, prefix_pages)
     for t, n in ((q, 3), (k_pool, 4), (v_pool, 4)):
-        if t.dim() != n or t.dtype != torch.bfloat16 or not t.is_contiguous():
+        if t.dtype != torch.bfloat16 or t.dim() != n or not t.is_contiguous():
             raise ValueError("q must be a contiguous bf16 [B, n_q, D] and the pools contiguous bf16 "
                              "[num_pages, page_size, n_kv, D] tensors")
     dev, (B, n_q, D) = q.device, q.shape
-    if k_pool.shape != v_pool.shape or k_pool.shape[3] != D or k_pool.device != dev or v_pool.device != dev:
-        raise ValueError("k_pool and v_pool must have one shape, q's head_dim and q's device")
+    num_pages, page_size, n_kv, _ = k_pool.shape
+    if k_pool.shape != v_pool.shape or k_pool.shape[3] != D:
+        raise ValueError("k_pool and v_pool must have one shape, and q's head_dim")
+    if not q.is_cuda or k_pool.device != dev or v_pool.device != dev:
+        raise ValueError("q and the pools must live on one CUDA device")
     _check_pages(page_table, "page_table", dev, 2)
     max_pages = page_table.shape[1]
     if page_table.shape[0] != B or (B > 1 and page_table.stride(0) < max_pages):
         raise ValueError("page_table must have a row per sequence, and the rows must not overlap")
     _check_like(lengths, (B,), torch.int32, dev, "lengths")
-    num_pages, page_size = k_pool.shape[:2]
+    _check_status(dev_status, dev)
     if prefix_len:
         if prefix_pages is None or prefix_len < 0:
             raise ValueError("a prefix needs prefix_len >= 0 and its pages")
         _check_pages(prefix_pages, "prefix_pages", dev, 1)
-        if prefix_pages.numel() * page_size < prefix_len:
+        if prefix_pages.shape[0] * page_size < prefix_len:
             raise ValueError("prefix_pages must hold prefix_len tokens")
     else:
         prefix_pages = None
+    made_out = made_ws = lse = None
     if out is None:
-        out = torch.empty_like(q)
+        out = made_out = torch.empty_like(q)
     else:
         _check_like(out, q.shape, torch.bfloat16, dev, "out")
-    lse = torch.empty((B, n_q), dtype=torch.float32, device=dev) if save_lse else None
-    L = C.layout("sectioned", n_q, k_pool.shape[2], D)
-    need = C.qkv_attention_decode_workspace(L, B, page_size, max_pages, prefix_len)
+    if save_lse:
+        lse = torch.empty((B, n_q), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    C.qkv_attention_decode(L, B, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages,
-                           page_table.stride(0) if B > 1 else max_pages, lengths, prefix_pages,
-                           prefix_len, 0.0 if scale is None else scale, out, lse, dev_status, workspace,
-                           workspace.numel() * workspace.element_size(), stream)
+        need = _decode_workspace(n_q, n_kv, D, B, page_size, max_pages, prefix_len, dev.index)
+        workspace = made_ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    C.qkv_attention_decode(_heads(n_q, n_kv, D), B, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages,
+                           page_table.stride(0) if B > 1 else max_pages, lengths, prefix_pages, prefix_len,
+                           0.0 if scale is None else scale, out, lse, dev_status, workspace,
+                           workspace.numel() * workspace.element_size(),
+                           _launch_stream(stream, dev, made_out, lse, made_ws))
     return (out, lse) if save_lse else out
-
-
-def _neg_inf(shape, dtype, device):
-    return torch.full(shape, float("-inf"), dtype=dtype, device=device)
 
 
 class QKVPrologue(torch.autograd.Function):
