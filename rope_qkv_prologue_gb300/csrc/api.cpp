@@ -1396,12 +1396,10 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   const void* kkv = attention_bwd_kernel(hd, true);
   const void* kq = attention_bwd_kernel(hd, false);
   if (!allow_smem(kkv, smem) || !allow_smem(kq, smem)) return QKVP_ERR_LAUNCH;
-  const int64_t rows_per_cta = 8 * 32 / (hd / 8);
-  const int64_t dgrid = (T * a.n_q + rows_per_cta - 1) / rows_per_cta;
-  QKVP_TRY(launch(attention_delta_kernel(hd), std::min<int64_t>(dgrid, 16 * (int64_t)sms), 256, 0, st, &a));
+  QKVP_TRY(launch(attention_delta_kernel(hd), std::min<int64_t>((T + 7) / 8, 8 * (int64_t)sms), 256, 0, st, &a));
   void* args[] = {&tq, &td, &tk, &tv, &a};
-  QKVP_TRY(launch_args(kkv, std::min<int64_t>(blocks * a.n_kv, sms), attention_bwd_threads(), smem, st, args));
-  return launch_args(kq, std::min<int64_t>(blocks * a.n_q, sms), attention_bwd_threads(), smem, st, args);
+  QKVP_TRY(launch_args(kq, std::min<int64_t>(blocks * a.n_q, sms), attention_bwd_threads(), smem, st, args));
+  return launch_args(kkv, std::min<int64_t>(blocks * a.n_kv, sms), attention_bwd_threads(), smem, st, args);
 }
 
 int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,

@@ -167,6 +167,26 @@ __device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Whole warp: 64 consecutive fp32 columns, two loads and one wait. The empty asm
+// keeps the uses of the second load's registers behind the wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, float (&v)[64]) {
+  uint32_t r0[32], r1[32];
+  tmem_ld32_issue(addr, r0);
+  tmem_ld32_issue(addr + 32, r1);
+  tmem_wait_ld32(r0);
+  asm volatile(""
+               : "+r"(r1[0]), "+r"(r1[1]), "+r"(r1[2]), "+r"(r1[3]), "+r"(r1[4]), "+r"(r1[5]), "+r"(r1[6]), "+r"(r1[7]),
+                 "+r"(r1[8]), "+r"(r1[9]), "+r"(r1[10]), "+r"(r1[11]), "+r"(r1[12]), "+r"(r1[13]), "+r"(r1[14]),
+                 "+r"(r1[15]), "+r"(r1[16]), "+r"(r1[17]), "+r"(r1[18]), "+r"(r1[19]), "+r"(r1[20]), "+r"(r1[21]),
+                 "+r"(r1[22]), "+r"(r1[23]), "+r"(r1[24]), "+r"(r1[25]), "+r"(r1[26]), "+r"(r1[27]), "+r"(r1[28]),
+                 "+r"(r1[29]), "+r"(r1[30]), "+r"(r1[31]));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = __uint_as_float(r0[i]);
+    v[32 + i] = __uint_as_float(r1[i]);
+  }
+}
+
 // The maximum of 32 values, in two chains of three-input maxima.
 __device__ __forceinline__ float max32(const float* v) {
   float a = max3(v[0], v[1], v[2]), b = max3(v[3], v[4], v[5]);

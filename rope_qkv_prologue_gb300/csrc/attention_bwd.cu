@@ -6,11 +6,11 @@
 //     dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j,
 // dk and dv summed over the query heads of the group too. Three kernels:
 //   1. qkvp_attention_delta_kernel: delta, one pass over dout and out;
-//   2. the key/value kernel: a CTA owns 128 keys of one key/value head and goes
+//   2. the query kernel: a CTA owns 128 queries of one head and goes through its
+//      keys, adding dS K (and writes the delta of rows with few keys anew);
+//   3. the key/value kernel: a CTA owns 128 keys of one key/value head and goes
 //      through the query blocks and heads that attend them, forming the transposed
-//      S^T = K Q^T and dP^T = V dO^T and adding P^T dO and dS^T Q;
-//   3. the query kernel: a CTA owns 128 queries of one head and goes through its
-//      keys, adding dS K.
+//      S^T = K Q^T and dP^T = V dO^T and adding P^T dO and dS^T Q.
 // S and dP are formed twice (seven products instead of five), so that every result
 // is a sum in one CTA's tensor memory in a fixed order: no atomics, no partial
 // results in memory, the same bits every time.
@@ -20,11 +20,8 @@
 // to tensor memory, 256 threads turn them into bf16 P and dS in tensor memory (in
 // the columns they came from), and those are the first operands of the
 // accumulating products. A thread owns a row and half of a block's columns. MMAs
-// execute in order, so the next X may be issued over the P that the product before
-// it reads; the order (key/value kernel)
-//     P dO (i), X (i + 1), dS Q (i), Y (i + 1), ...
-// keeps the tensor cores on one pair of products while the threads work on the
-// other. P and dS are rounded to bf16 as operands; all sums are fp32.
+// execute in order, so a product may be issued over an operand of the one before it.
+// P and dS are rounded to bf16 as operands; all sums are fp32.
 //   warp 0      loads tiles (and zeroes rows behind a sequence's end in those that
 //               are summed over: 0 times whatever is there need not be 0);
 //   warp 1      issues the MMAs;
@@ -39,6 +36,7 @@ namespace {
 constexpr int kBwdThreads = 384;
 constexpr int kBwdSched = 2;
 constexpr int kStatStages = 2;
+constexpr int kDeltaHeads = 256;  // heads of the delta kernel's shared buffer
 constexpr int kStageBytes = 32 * 64;  // a warp's store buffer: 32 rows x 32 bf16
 
 template <int HD>
@@ -71,7 +69,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                               const AttnBwdArgs a) {
   using SM = BwdSmem<HD>;
   constexpr int ST = SM::kStages;
-  constexpr uint32_t tX = 0, tY = KV ? 128 : 256, tAcc1 = KV ? 256 : 384, tAcc2 = KV ? 256 + HD : 384;
+  // Tensor memory. X has two buffers where there is room for them (not in the
+  // key/value kernel at head_dim 128); a block's P lies over its X, and its dS in
+  // the columns of X that P leaves free, or over Y where X has one buffer.
+  constexpr bool kTwoX = !KV || HD == 64;
+  constexpr uint32_t tX = 0, tY = kTwoX ? 256 : 128, tAcc1 = tY + 128, tAcc2 = tAcc1 + HD;
+  constexpr uint32_t kDsOff = KV && kTwoX ? 32 : 0;  // columns of dS behind those of P, in each half
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ __align__(8) uint64_t a_full, a_empty, b1_full[ST], b1_empty[ST], b2_full[ST], b2_empty[ST], tail_bar,
@@ -81,7 +84,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __shared__ int s_fail;
   __shared__ BwdItem s_item[kBwdSched];
   __shared__ int s_cache[AttnOrder::kCached];
-  __shared__ __align__(16) float s_stat[KV ? kStatStages : 1][2][kAttnRows];  // lse log2(e), delta
+  // key/value kernel: -lse log2(e) and -delta of the streamed rows; query kernel: the
+  // halves' parts of a row's sums
+  __shared__ __align__(16) float s_stat[KV ? kStatStages : 2][2][kAttnRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
       wait(&b1_full[k % ST], (k / ST) & 1);
       tc_fence_after();
-      const uint32_t buf = KV ? 0 : k & 1;
+      const uint32_t buf = kTwoX ? k & 1 : 0;
       attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
       umma_commit_warp(&x_full[buf]);
     };
@@ -235,33 +240,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       product_x(it);
       product_y(it);
       if constexpr (!KV) umma_commit_warp(&b2_empty[it % ST]);
+      if (kTwoX && t.n > 1) product_x(it + 1);
       if (t.n == 1) umma_commit_warp(&a_empty);
       for (int i = 0; i < t.n; ++i, ++it) {
         const bool more = i + 1 < t.n;
+        const uint32_t x = tmem + tX + (kTwoX ? 128 * (it & 1) : 0);
         if constexpr (KV) {
           wait(&p_full, it & 1);
           if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
           tc_fence_after();
-          attn_mma_ts(tmem + tAcc1, tmem + tX, 64, b2(it), id_acc, i > 0);
+          attn_mma_ts(tmem + tAcc1, x, 64, b2(it), id_acc, i > 0);
           umma_commit_warp(&b2_empty[it % ST]);
-          if (more) product_x(it + 1);
+          if (!kTwoX && more) product_x(it + 1);
           wait(&ds_full, it & 1);
           tc_fence_after();
-          attn_mma_ts(tmem + tAcc2, tmem + tY, 64, b1(it), id_acc, i > 0);
+          if (kTwoX && more) product_y(it + 1);  // Y has been read: it need not wait behind dS Q
+          attn_mma_ts(tmem + tAcc2, kTwoX ? x + kDsOff : tmem + tY, 64, b1(it), id_acc, i > 0);
           umma_commit_warp(&b1_empty[it % ST]);
-          if (more) product_y(it + 1);
+          if (!kTwoX && more) product_y(it + 1);
         } else {
-          if (more) product_x(it + 1);
           wait(&ds_full, it & 1);
-          if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
-          tc_fence_after();
-          attn_mma_ts(tmem + tAcc1, tmem + tX + 128 * (it & 1), 64, b1(it), id_acc, i > 0);
-          umma_commit_warp(&b1_empty[it % ST]);
           if (more) {
             product_y(it + 1);
             umma_commit_warp(&b2_empty[(it + 1) % ST]);
           }
+          if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
+          tc_fence_after();
+          attn_mma_ts(tmem + tAcc1, x, 64, b1(it), id_acc, i > 0);
+          umma_commit_warp(&b1_empty[it % ST]);
         }
+        if (kTwoX && i + 2 < t.n) product_x(it + 2);
         if (i + 2 == t.n) umma_commit_warp(&a_empty);  // the last X and Y are issued
       }
       umma_commit_warp(&acc_done);
@@ -316,9 +324,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int r = kAttnRows * blk + 32 * x + lane;
             const bool in = r < t.len;
             const int64_t at = (int64_t)head * a.T + t.first + r;
-            ls[x] = in ? a.lse[at] * kLog2e : INFINITY;
-            de[x] = in ? a.delta[at] : 0.f;
-            if (ls[x] == -INFINITY) ls[x] = INFINITY;
+            ls[x] = in ? -a.lse[at] * kLog2e : -INFINITY;
+            de[x] = in ? -a.delta[at] : 0.f;
+            if (ls[x] == INFINITY) ls[x] = -INFINITY;  // a row without keys
           }
           if (it >= kStatStages) wait(&st_empty[s], ((it / kStatStages) - 1) & 1);
 #pragma unroll
@@ -342,85 +350,116 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     BwdItem t;
     while (next_item(t)) {
       if (t.n == 0) continue;
-      float r_lse = 0.f, r_delta = 0.f;
+      float r_lse = 0.f, r_delta = 0.f;  // query kernel: -lse log2(e) and -delta of this row
+      const bool in = kAttnRows * t.blk + row < t.len;
       if constexpr (!KV) {
         const int64_t at = (int64_t)t.head * a.T + t.own + row;
-        const bool in = kAttnRows * t.blk + row < t.len;
-        r_lse = in ? a.lse[at] * kLog2e : INFINITY;
-        r_delta = in ? a.delta[at] : 0.f;
-        if (r_lse == -INFINITY) r_lse = INFINITY;
+        r_lse = in ? -a.lse[at] * kLog2e : -INFINITY;
+        r_delta = in && t.n > 1 ? -a.delta[at] : 0.f;
+        if (r_lse == INFINITY) r_lse = -INFINITY;
       }
+      const uint64_t c2 = pair(c, c);
+#pragma unroll 1
       for (int i = 0; i < t.n; ++i, ++it) {
         int head;
         const bool diagonal = block_of(t, i, head) == t.blk;
-        const uint32_t buf = KV ? 0 : it & 1;
+        const uint32_t buf = kTwoX ? it & 1 : 0;
         const uint32_t t_x = tmem + lanes + tX + 128 * buf + 64 * wg, t_y = tmem + lanes + tY + 64 * wg;
-        wait(&x_full[buf], KV ? it & 1 : (it >> 1) & 1);
-        tc_fence_after();
-        float p[64];
-        tmem_ld32(t_x, p);
-        tmem_ld32(t_x + 32, p + 32);
         const float* st = s_stat[KV ? it % kStatStages : 0][0] + 64 * wg;
-        if constexpr (KV) {
+        uint64_t ls2[KV ? 32 : 1];
+        if constexpr (KV) {  // before X is here
           wait(&st_full[it % kStatStages], (it / kStatStages) & 1);
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(st + e);
-            p[e] = ex2(fmaf(p[e], c, -v.x));
-            p[e + 1] = ex2(fmaf(p[e + 1], c, -v.y));
-            p[e + 2] = ex2(fmaf(p[e + 2], c, -v.z));
-            p[e + 3] = ex2(fmaf(p[e + 3], c, -v.w));
+          for (int e = 0; e < 32; e += 2) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(st + 2 * e);
+            ls2[e] = v.x;
+            ls2[e + 1] = v.y;
           }
-          if (diagonal)  // queries before this key do not attend it
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (64 * wg + e < row) p[e] = 0.f;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pack2(p[32 * x + 2 * e], p[32 * x + 2 * e + 1]);
-            tmem_st16(t_x + 16 * x, w);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full);
         } else {
-#pragma unroll
-          for (int e = 0; e < 64; ++e) p[e] = ex2(fmaf(p[e], c, -r_lse));
+          ls2[0] = pair(r_lse, r_lse);
         }
-        wait(&y_full, it & 1);
+        wait(&x_full[buf], kTwoX ? (it >> 1) & 1 : it & 1);
         tc_fence_after();
-        float y[64];
-        tmem_ld32(t_y, y);
-        tmem_ld32(t_y + 32, y + 32);
-        if constexpr (KV) {
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(st + kAttnRows + e);
-            p[e] *= y[e] - v.x;
-            p[e + 1] *= y[e + 1] - v.y;
-            p[e + 2] *= y[e + 2] - v.z;
-            p[e + 3] *= y[e + 3] - v.w;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&st_empty[it % kStatStages]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 64; ++e) p[e] *= y[e] - r_delta;
-          if (diagonal)  // keys after the row (and so behind the sequence), whatever was computed there
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (64 * wg + e > row) p[e] = 0.f;
-        }
-        const uint32_t t_ds = KV ? t_y : t_x;
+        float p[64], y[64];
+        tmem_ld64(t_x, p);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = pack2(p[32 * x + 2 * e], p[32 * x + 2 * e + 1]);
+          for (int e = 0; e < 16; ++e) {
+            float &p0 = p[32 * x + 2 * e], &p1 = p[32 * x + 2 * e + 1];
+            unpair(fma2(pair(p0, p1), c2, ls2[KV ? 16 * x + e : 0]), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            if constexpr (KV) {
+              if (diagonal) {  // queries before this key do not attend it
+                if (64 * wg + 32 * x + 2 * e < row) p0 = 0.f;
+                if (64 * wg + 32 * x + 2 * e + 1 < row) p1 = 0.f;
+              }
+              w[e] = pack2(p0, p1);
+            }
+          }
+          if constexpr (KV) tmem_st16(t_x + 16 * x, w);
+        }
+        if constexpr (KV) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full);
+        }
+        wait(&y_full, it & 1);
+        tc_fence_after();
+        tmem_ld64(t_y, y);
+        if constexpr (!KV) {
+          if (diagonal) {  // keys after the row (and so behind the sequence), whatever was computed there
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (64 * wg + e > row) p[e] = y[e] = 0.f;
+          }
+          if (t.n == 1) {
+            // Rows with few keys: delta = sum_j p_ij dp_ij is summed here, from the p and
+            // dp that it is subtracted from. dout . out with out rounded to bf16 is off
+            // by 2^-9 of |dout| |out|, which a sharp row of few keys, whose ds are small
+            // differences, would feel; in later blocks it is lost among the others.
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              s0 += p[e];
+              s1 = fmaf(p[e], y[e], s1);
+            }
+            s_stat[wg][0][row] = s0;
+            s_stat[wg][1][row] = s1;
+            named_sync(1, 256);
+            r_delta = -(s_stat[0][1][row] + s_stat[1][1][row]) / (s_stat[0][0][row] + s_stat[1][0][row]);
+            named_sync(1, 256);
+            if (wg == 0 && in) a.delta[(int64_t)t.head * a.T + t.own + row] = -r_delta;
+          }
+        }
+        const uint32_t t_ds = KV && !kTwoX ? t_y : t_x + kDsOff;
+        const uint64_t d2 = pair(r_delta, r_delta);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            uint64_t n0 = d2, n1 = d2;  // -delta of two pairs of columns
+            if constexpr (KV) {
+              const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(st + kAttnRows + 32 * x + 2 * e);
+              n0 = v.x;
+              n1 = v.y;
+            }
+            const int k = 32 * x + 2 * e;
+            float a0, a1, b0, b1;
+            unpair(mul2(pair(p[k], p[k + 1]), add2(pair(y[k], y[k + 1]), n0)), a0, a1);
+            unpair(mul2(pair(p[k + 2], p[k + 3]), add2(pair(y[k + 2], y[k + 3]), n1)), b0, b1);
+            w[e] = pack2(a0, a1);
+            w[e + 1] = pack2(b0, b1);
+          }
           tmem_st16(t_ds + 16 * x, w);
+        }
+        if constexpr (KV) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st_empty[it % kStatStages]);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -474,30 +513,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // delta[h, t] = dout[t, h] . out[t, h] in fp32, and (where asked for) zeros in the
-// gradients' rows of no sequence. Bound by reading dout and out once.
+// gradients' rows of no sequence. Bound by reading dout and out once: a CTA takes
+// eight tokens, a warp one of them at a time, so that the reads are whole rows and
+// the writes whole sectors.
 template <int HD>
 __global__ void __launch_bounds__(256) qkvp_attention_delta_kernel(const AttnBwdArgs a) {
-  constexpr int L = HD / 8, RW = 32 / L;  // lanes per row, rows per warp
-  const int lane = threadIdx.x & 31;
+  constexpr int L = HD / 8, RW = 32 / L;  // lanes per head, heads per warp and step
+  __shared__ float s_d[kDeltaHeads][9];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t n = a.T * a.n_q;
-  const int64_t step = (int64_t)gridDim.x * 8 * RW;
-  for (int64_t r0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * RW; r0 < n; r0 += step) {
-    const int64_t r = r0 + lane / L;
-    float s = 0.f;
-    if (r < n) {
-      float x[8], y[8];
-      unpack8(a.out[r * L + lane % L], x);
-      unpack8(a.dout[r * L + lane % L], y);
+  for (int64_t t0 = 8 * (int64_t)blockIdx.x; t0 < a.T; t0 += 8 * (int64_t)gridDim.x)
+    for (int h0 = 0; h0 < a.n_q; h0 += kDeltaHeads) {
+      const int nh = min(kDeltaHeads, a.n_q - h0);
+      const int64_t t = t0 + warp;
+      if (t < a.T) {
+        const int64_t row = (t * a.n_q + h0) * L + lane;
+#pragma unroll 4
+        for (int h = 0; h < nh; h += RW) {
+          const bool in = h + lane / L < nh;
+          float x[8], y[8], s = 0.f;
+          unpack8(in ? a.out[row + h * L] : make_uint4(0, 0, 0, 0), x);
+          unpack8(in ? a.dout[row + h * L] : make_uint4(0, 0, 0, 0), y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+          for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+#pragma unroll
+          for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (in && lane % L == 0) s_d[h + lane / L][warp] = s;
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 8 * nh; i += 256)
+        if (t0 + (i & 7) < a.T) a.delta[(int64_t)(h0 + (i >> 3)) * a.T + t0 + (i & 7)] = s_d[i >> 3][i & 7];
+      __syncthreads();
     }
-#pragma unroll
-    for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane % L == 0 && r < n) a.delta[(r % a.n_q) * a.T + r / a.n_q] = s;
-  }
-  if (a.zero_rest && threadIdx.x < 32) {
+  if (a.zero_rest && warp == 0) {
     bool bad = false;
     for (int s = lane; s < a.batch; s += 32) bad |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T;
     bad = __any_sync(0xffffffffu, bad) || a.batch == 0;
