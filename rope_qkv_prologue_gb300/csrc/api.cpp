@@ -583,8 +583,8 @@ void plan_decode(const qkvp_layout* L, int32_t batch, int32_t page_size, int32_t
   p->rows = (int64_t)batch + p->ranges + (int64_t)p->chunks * batch;
 }
 
-size_t decode_workspace(const qkvp_layout* L, const DecodePlan& p) {
-  return (size_t)p.rows * L->n_q * ((size_t)L->head_dim + 2) * sizeof(float);
+size_t decode_workspace(const qkvp_layout* L, int32_t batch, const DecodePlan& p) {
+  return (size_t)p.rows * L->n_q * ((size_t)L->head_dim + 2) * sizeof(float) + (size_t)batch * sizeof(int2);
 }
 
 int check_decode(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages, int32_t prefix_len) {
@@ -1412,7 +1412,7 @@ int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
   plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, &p);
-  *bytes = decode_workspace(layout, p);
+  *bytes = decode_workspace(layout, batch, p);
   return QKVP_OK;
 }
 
@@ -1438,7 +1438,7 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
   plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, &p);
-  if (!workspace || workspace_bytes < decode_workspace(layout, p)) return QKVP_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < decode_workspace(layout, batch, p)) return QKVP_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int hd = layout->head_dim;
@@ -1508,12 +1508,14 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   a.ranges = p.ranges;
   a.part_o = part_o;
   a.part_ml = part_ml;
+  a.plan = reinterpret_cast<int2*>(part_ml + p.rows * layout->n_q);
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.dev_status = dev_status;
-  // warps per head of the join: about four partial results each
+  // warps per head of the join: eight partial results each (as many reads as a lane
+  // has in flight)
   const int64_t parts = p.ranges / batch + 2 + p.chunks;
-  a.wph = parts > 16 ? 8 : (parts > 8 ? 4 : (parts > 4 ? 2 : 1));
+  a.wph = parts > 32 ? 8 : (parts > 16 ? 4 : (parts > 8 ? 2 : 1));
   const void* kern = attention_decode_kernel(hd);
   const size_t smem = (size_t)attention_decode_smem_bytes(hd);
   if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;

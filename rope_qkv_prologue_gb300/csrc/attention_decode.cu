@@ -74,20 +74,13 @@ __device__ __forceinline__ int dec_tiles(const AttnDecodeArgs& a, int b) {
   return (int)(((uint32_t)a.joint_len + (uint32_t)dec_own(a, b) + (uint32_t)a.tile_keys - 1) / (uint32_t)a.tile_keys);
 }
 
-// Whole warp: all tiles of the batch, and those of the sequences before `b`.
-__device__ __forceinline__ int64_t dec_total(const AttnDecodeArgs& a, int b, int lane, int64_t* before) {
-  int64_t all = 0, pre = 0;
-  for (int s = lane; s < a.batch; s += 32) {
-    const int n = dec_tiles(a, s);
-    all += n;
-    if (s < b) pre += n;
-  }
+// Whole warp: all tiles of the batch.
+__device__ __forceinline__ int64_t dec_total(const AttnDecodeArgs& a, int lane) {
+  int64_t all = 0;
+#pragma unroll 8
+  for (int s = lane; s < a.batch; s += 32) all += dec_tiles(a, s);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    pre += __shfl_xor_sync(0xffffffffu, pre, o);
-  }
-  *before = pre;
+  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   return all;
 }
 
@@ -146,8 +139,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
   if (!a.prefix_chunks) griddep_wait();
   griddep_launch_dependents();
 
-  int64_t before;
-  const int64_t total = dec_total(a, 0, lane, &before);
+  const int64_t total = dec_total(a, lane);
   const int64_t quota = dec_quota(a, total);
   const int heads = a.n_kv * a.head_blocks;
   const int items = a.ranges * heads;
@@ -346,6 +338,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
           }
       }
       st = st + 1 == ST ? 0 : st + 1;
+      // the ranges that a sequence begins and ends in, for the joining kernel
+      if (hv == 0 && lane == 0) {
+        if (cu.tile == 0) a.plan[cu.b].x = range;
+        if (cu.tile + 1 == cu.tiles) a.plan[cu.b].y = range;
+      }
       if (++cu.tile == cu.tiles || t + 1 == n_tiles) {
         end();
         cu.settle(a);
@@ -361,68 +358,83 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
 
 // Joins the partial results of each (sequence, head): its own in the ranges it
 // lies in and the shared prefix's key ranges, in that order. kJoinWarps warps per
-// CTA, `wph` of them per head.
+// CTA, `wph` of them per head. A chain of dependent reads (lengths, maxima and
+// sums, results), so each is made by as many lanes at once as there are.
 template <int HD>
 __global__ void __launch_bounds__(32 * kJoinWarps) qkvp_attention_join_kernel(const AttnDecodeArgs a) {
-  constexpr int V = HD / 32;  // values per lane
-  __shared__ float s_o[kJoinWarps][HD];
+  constexpr int V = HD / 32;             // values per lane
+  constexpr int kCap = kJoinParts / kJoinWarps;  // factors in shared memory per warp
+  __shared__ float s_f[kJoinParts], s_top[kJoinWarps], s_sum[kJoinWarps], s_o[kJoinWarps][HD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = kJoinWarps / a.wph;  // heads per CTA
+  const int wph = a.wph, per = kJoinWarps / wph;  // heads per CTA
   const int groups = (a.n_q + per - 1) / per;
-  const int b = (int)(blockIdx.x / groups), head = (int)(blockIdx.x % groups) * per + warp / a.wph;
-  const int sub = warp % a.wph;
+  const int b = (int)(blockIdx.x / groups), grp = warp / wph, sub = warp % wph;
+  const int head = (int)(blockIdx.x % groups) * per + grp, tid = 32 * sub + lane;
   griddep_wait();
   griddep_launch_dependents();
-  int64_t before;
-  const int64_t quota = dec_quota(a, dec_total(a, b, lane, &before));
-  const int tiles = dec_tiles(a, b);
+  const int2 plan = a.plan[b];  // means nothing where the sequence has no tile
+  const int length = a.lengths[b];
   if (threadIdx.x == 0 && blockIdx.x % groups == 0 && a.dev_status &&
-      (a.lengths[b] < 0 || a.lengths[b] > (int64_t)a.max_pages * a.page_size))
+      (length < 0 || length > a.max_pages * a.page_size))
     atomicOr(a.dev_status, kDevBadLength);
-  const int64_t r0 = before / quota, r1 = tiles ? (before + tiles - 1) / quota : r0;
-  const int own = tiles ? (int)(r1 - r0) + 1 : 0, parts = own + a.prefix_chunks;
+  const int own = dec_tiles(a, b) ? plan.y - plan.x + 1 : 0, parts = own + a.prefix_chunks;
   const bool on = head < a.n_q;
   // row of partial result i in part_o / part_ml: [batch] first pieces, [ranges] later ones, [prefix chunks][batch]
   auto row_of = [&](int i) -> int64_t {
     const int64_t r = i == 0 && own ? (int64_t)b
-                      : i < own     ? a.batch + r0 + i
+                      : i < own     ? (int64_t)a.batch + plan.x + i
                                     : (int64_t)a.batch + a.ranges + (int64_t)(i - own) * a.batch + b;
     return r * a.n_q + head;
   };
   float top = -INFINITY, sum = 0.f, o[V] = {};
-  if (on) {
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[row_of(i)].x);
+#pragma unroll 4
+  for (int i = on ? tid : parts; i < parts; i += 32 * wph) top = fmaxf(top, a.part_ml[row_of(i)].x);
 #pragma unroll
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float off = top == -INFINITY ? 0.f : top;
-    // 32 parts at a time: lane i holds part i's factor
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      float f = 0.f;
-      if (i0 + lane < parts) {
-        const float2 v = a.part_ml[row_of(i0 + lane)];
-        f = ex2(v.x - off);
-        sum += f * v.y;
+  for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+  for (int x = 0; x < wph; ++x) top = fmaxf(top, s_top[grp * wph + x]);
+  const float off = top == -INFINITY ? 0.f : top;
+  float* f = s_f + grp * wph * kCap;
+  for (int i0 = 0; i0 < parts; i0 += kCap * wph) {  // as many parts as factors fit
+    const int n = min(kCap * wph, parts - i0);
+    if (i0) __syncthreads();
+    for (int i = on ? tid : n; i < n; i += 32 * wph) {
+      const float2 v = a.part_ml[row_of(i0 + i)];
+      f[i] = ex2(v.x - off);
+      sum += f[i] * v.y;
+    }
+    __syncthreads();
+    for (int i = on ? sub : n; i < n; i += 8 * wph) {
+      float v[8][V];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int ik = min(i + k * wph, n - 1);
+        const float* src = a.part_o + row_of(i0 + ik) * HD + V * lane;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[k][e] = src[e];
       }
-      const int n = min(32, parts - i0);
-#pragma unroll 8
-      for (int i = sub; i < n; i += a.wph) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* src = a.part_o + row_of(i0 + i) * HD + V * lane;
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(fi, src[e], o[e]);
+      for (int k = 0; k < 8; ++k) {
+        const float fk = i + k * wph < n ? f[i + k * wph] : 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fk != 0.f ? fmaf(fk, v[k][e], o[e]) : o[e];
       }
     }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   }
-  if (a.wph > 1) {
+#pragma unroll
+  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (wph > 1) {
+    if (lane == 0) s_sum[warp] = sum;
 #pragma unroll
     for (int e = 0; e < V; ++e) s_o[warp][V * lane + e] = o[e];
     __syncthreads();
     if (sub == 0)
-      for (int x = 1; x < a.wph; ++x)
+      for (int x = 1; x < wph; ++x) {
+        sum += s_sum[warp + x];
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] += s_o[warp + x][V * lane + e];
+      }
   }
   if (!on || sub != 0) return;
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);

@@ -394,6 +394,7 @@ int attention_bwd_threads();
 constexpr int kDecMinKeys = 64;   // keys of a part (at least)
 QKVP_HD constexpr int dec_tile_keys(int head_dim) { return head_dim == 64 ? 32 : 16; }  // keys per tile: 8 KiB
 constexpr int kJoinWarps = 8;     // warps per CTA of the kernel that joins the partial results
+constexpr int kJoinParts = 1024;  // partial results whose factors it holds in shared memory
 struct AttnDecodeArgs {
   int32_t n_q, n_kv, group;
   int32_t head_blocks;     // blocks of 16 query heads per key/value head
@@ -416,6 +417,7 @@ struct AttnDecodeArgs {
   int32_t wph;             // join: warps per head
   float* part_o;           // [batch + ranges + prefix_chunks * batch][n_q][head_dim]
   float2* part_ml;         // the same rows: (maximum in powers of two, sum)
+  int2* plan;              // [batch] first and last part that a sequence lies in
   uint16_t* out;           // bf16 [batch, n_q, head_dim]
   float* lse;              // [batch, n_q], or null
   int32_t* dev_status;
