@@ -325,19 +325,45 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// Tensor map of a row-major bf16 matrix [rows, cols] (cols contiguous, a
-// multiple of 8) read in boxes of 64 columns x box_rows rows with the 128-byte
-// swizzle the tcgen05 descriptors expect; outside the matrix a box reads 0.
-bool bf16_tile_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int box_rows) {
+// Tensor map of a bf16 array of `rank` dimensions (dims[0] contiguous) read in boxes
+// with the 128-byte swizzle the tcgen05 descriptors expect; outside the array a box
+// reads 0. The encoder wants the device's context current in the calling thread,
+// which a thread that has made no runtime call yet (an autograd worker) lacks:
+// cudaSetDevice binds it.
+bool encode_bf16_map(CUtensorMap* map, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
   EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
+  const cuuint32_t elem[3] = {1, 1, 1};
+  auto encode = [&] {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box,
+               elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return encode();
+}
+
+// A row-major matrix [rows, cols] (cols a multiple of 8) in boxes of 64 columns x
+// box_rows rows.
+bool bf16_tile_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int box_rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
   const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  const cuuint32_t elem[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, elem,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bf16_map(map, ptr, 2, dims, strides, box);
+}
+
+// [n2, n1, cols] in boxes of 64 x box1 x box2.
+bool bf16_box_map(CUtensorMap* map, const void* ptr, int64_t n2, int64_t n1, int64_t cols, int box2, int box1) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)n1, (cuuint64_t)n2};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(cols * n1) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+  return encode_bf16_map(map, ptr, 3, dims, strides, box);
 }
 
 // -------------------------------------------------------------- RoPE ----
@@ -596,20 +622,6 @@ int check_decode(const qkvp_layout* layout, int32_t batch, int32_t page_size, in
       batch > (1 << 20))
     return QKVP_ERR_SHAPE;
   return QKVP_OK;
-}
-
-// Tensor map of bf16 [n2, n1, cols] (cols contiguous) read in boxes of 64 x
-// box1 x box2 with the 128-byte swizzle; outside it a box reads 0.
-bool bf16_box_map(CUtensorMap* map, const void* ptr, int64_t n2, int64_t n1, int64_t cols, int box2, int box1) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)n1, (cuuint64_t)n2};
-  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(cols * n1) * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
-  const cuuint32_t elem[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, elem,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool overlaps(const void* p, size_t pn, const void* q, size_t qn) {

@@ -332,6 +332,8 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
         lse = torch.empty((n_q, T), dtype=torch.float32, device=dev)
         if not flags:
             lse.fill_(float("-inf"))
+    if T == 0:  # an empty tensor has no address to pass
+        return (out, lse) if save_lse else out
     C.qkv_attention_fwd(_heads(n_q, k.shape[1], D), T, batch, cu_seqlens, q, k, v, 0.0 if scale is None else scale,
                         flags, out, lse, dev_status, _launch_stream(stream, dev, made, lse))
     return (out, lse) if save_lse else out
@@ -351,6 +353,8 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspac
     _check_like(out, q.shape, torch.bfloat16, dev, "out")
     _check_like(lse, (n_q, T), torch.float32, dev, "lse")
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    if T == 0:
+        return dq, dk, dv
     made = None
     if workspace is None:
         workspace = made = torch.empty(max(n_q * T, 4), dtype=torch.float32, device=dev)
@@ -433,6 +437,8 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
         _check_like(out, q.shape, torch.bfloat16, dev, "out")
     if save_lse:
         lse = torch.empty((B, n_q), dtype=torch.float32, device=dev)
+    if B == 0:
+        return (out, lse) if save_lse else out
     if workspace is None:
         need = _decode_workspace(n_q, n_kv, D, B, page_size, max_pages, prefix_len, dev.index)
         workspace = made_ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)

@@ -82,3 +82,271 @@ def test_backward(lib, cuda, lengths, before, after, n_q, n_kv, D):
     ref = A.attention_bwd(f64(do), f64(q), f64(k), f64(v), cu, out_err=out_bound(fwd))
     for name, got in zip(("dq", "dk", "dv"), grads):
         assert_within(f64(got), ref[name], ref["e_" + name] + U * np.abs(ref[name]), name)
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(8, 2, 64), (4, 2, 128), (3, 3, 64)])
+@pytest.mark.parametrize("scale,sharp", [(0.02, 1.0), (None, 4.0), (1.0, 0.5)])
+def test_scales_and_sharp_rows(lib, cuda, n_q, n_kv, D, scale, sharp):
+    # scores far apart, so that a row's maximum moves by many powers of two from
+    # block to block; the largest |scale q k| stays below 2^6
+    F = lib.functional
+    cu = offsets([700, 130], 0)
+    q, k, v, do = inputs(830, n_q, n_kv, D, 5, sharp)
+    ref = A.attention_fwd(f64(q), f64(k), f64(v), cu, scale)
+    assert ref["s_abs"].max() < (64 if scale is None else 128)
+    dev = [t.to(cuda) for t in (q, k, v, do)]
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    out, lse = F.attention_forward(*dev[:3], cu_dev, scale, save_lse=True)
+    grads = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev, scale)
+    no_error(lib)
+    assert_within(f64(out), ref["out"], out_bound(ref), "out")
+    assert_lse(lse.cpu().numpy(), ref, 700, D, "lse")
+    g = A.attention_bwd(f64(do), f64(q), f64(k), f64(v), cu, scale, out_err=out_bound(ref))
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        assert_within(f64(got), g[name], g["e_" + name] + U * np.abs(g[name]), name)
+
+
+def test_growing_maxima(lib, cuda):
+    # keys that each outdo the ones before by far: every block rescales the result
+    n_q, n_kv, D, T = 2, 1, 128, 600
+    q = torch.ones(T, n_q, D, dtype=torch.bfloat16)
+    k = (torch.arange(T).float()[:, None, None] / 150).expand(T, n_kv, D).to(torch.bfloat16).contiguous()
+    v = inputs(T, n_q, n_kv, D, 6)[2]
+    cu = offsets([T])
+    out, lse = lib.functional.attention_forward(q.to(cuda), k.to(cuda), v.to(cuda), torch.from_numpy(cu).to(cuda),
+                                                save_lse=True)
+    no_error(lib)
+    ref = A.attention_fwd(f64(q), f64(k), f64(v), cu)
+    assert_within(f64(out), ref["out"], out_bound(ref), "out")
+    assert_lse(lse.cpu().numpy(), ref, T, D, "lse")
+
+
+@pytest.mark.parametrize("batch", [33, 200, 700])
+def test_many_sequences(lib, cuda, batch):
+    # more sequences than a warp, than the kernels keep counts of, and than work items per CTA
+    F = lib.functional
+    rng = np.random.default_rng(batch)
+    lengths = rng.integers(0, 9, size=batch).tolist()
+    lengths[batch // 2] = 200
+    cu = offsets(lengths)
+    T = int(cu[-1])
+    q, k, v, do = inputs(T, 4, 2, 64, batch)
+    dev = [t.to(cuda) for t in (q, k, v, do)]
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    out, lse = F.attention_forward(*dev[:3], cu_dev, save_lse=True)
+    grads = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev)
+    no_error(lib)
+    ref = A.attention_fwd(f64(q), f64(k), f64(v), cu)
+    assert_within(f64(out), ref["out"], out_bound(ref), "out")
+    g = A.attention_bwd(f64(do), f64(q), f64(k), f64(v), cu, out_err=out_bound(ref))
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        assert_within(f64(got), g[name], g["e_" + name] + U * np.abs(g[name]), name)
+
+
+def test_rows_of_no_sequence_are_left_alone_and_never_used(lib, cuda):
+    # NaN in every row of no sequence; out, lse and gradients of the others are
+    # those without them, bit for bit, and a given out keeps its other rows
+    F = lib.functional
+    cu = offsets([5, 260, 0, 64], 7)
+    T = int(cu[-1]) + 30
+    q, k, v, do = (t.to(cuda) for t in inputs(T, 8, 2, 64, 9))
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    inside = torch.zeros(T, dtype=torch.bool, device=cuda)
+    inside[7:int(cu[-1])] = True
+    out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True)
+    grads = F.attention_backward(do, q, k, v, out, lse, cu_dev)
+    for t in (out, *grads):
+        assert not t[~inside].any() and torch.isfinite(t[inside].float()).all()
+    assert torch.isneginf(lse[:, ~inside]).all()
+    bad = [t.clone() for t in (q, k, v, do)]
+    for t in bad:
+        t[~inside] = float("nan")
+    mine = torch.full_like(q, 3.0)
+    out2, lse2 = F.attention_forward(*bad[:3], cu_dev, save_lse=True, out=mine)
+    assert out2 is mine and (mine[~inside] == 3.0).all() and torch.isneginf(lse2[:, ~inside]).all()
+    assert torch.equal(mine[inside], out[inside]) and torch.equal(lse2[:, inside], lse[:, inside])
+    keep = out.clone()
+    keep[~inside] = float("nan")
+    for a, b in zip(F.attention_backward(bad[3], *bad[:3], keep, lse, cu_dev), grads):
+        assert torch.equal(a, b)
+    no_error(lib)
+
+
+def test_sequences_do_not_touch_each_other(lib, cuda):
+    # an infinity and a NaN in one sequence leave the others' bits alone, in both directions
+    F = lib.functional
+    lengths = [100, 30, 200]
+    cu = offsets(lengths)
+    T = int(cu[-1])
+    q, k, v, do = (t.to(cuda) for t in inputs(T, 4, 2, 64, 10))
+    cu_dev = torch.from_numpy(cu).to(cuda)
+
+    def step(q, k, v, do):
+        out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True)
+        return (out, *F.attention_backward(do, q, k, v, out, lse, cu_dev))
+
+    good = step(q, k, v, do)
+    bad = [t.clone() for t in (q, k, v, do)]
+    for i, t in enumerate(bad):
+        t[100:130] = float("nan") if i % 2 else float("inf")
+    others = torch.ones(T, dtype=torch.bool, device=cuda)
+    others[100:130] = False
+    for a, b in zip(step(*bad), good):
+        assert torch.equal(a[others], b[others])
+    # and a sequence alone gives what it gives in the pack
+    one = torch.tensor([0, 200], dtype=torch.int32, device=cuda)
+    alone = F.attention_forward(q[130:].contiguous(), k[130:].contiguous(), v[130:].contiguous(), one)
+    assert torch.equal(alone, good[0][130:])
+    no_error(lib)
+
+
+def test_offsets_that_do_not_ascend_are_refused_on_the_device(lib, cuda):
+    F = lib.functional
+    q, k, v, do = (t.to(cuda) for t in inputs(300, 4, 2, 64, 11))
+    for cu in ([0, 200, 100, 300], [-1, 300], [0, 301], [5, 2], [0, 2 ** 31 - 1]):
+        status = torch.zeros(1, dtype=torch.int32, device=cuda)
+        cu_dev = torch.tensor(cu, dtype=torch.int32, device=cuda)
+        mine = torch.full_like(q, 2.0)
+        F.attention_forward(q, k, v, cu_dev, out=mine, dev_status=status)
+        assert status.item() == lib.QKVP_DEV_BAD_SEQUENCE and (mine == 2.0).all()
+        out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True, dev_status=status)
+        assert not out.any() and torch.isneginf(lse).all()
+        status.zero_()
+        grads = F.attention_backward(do, q, k, v, out, lse, cu_dev, dev_status=status)
+        assert status.item() == lib.QKVP_DEV_BAD_SEQUENCE and not any(g.any() for g in grads)
+    no_error(lib)
+
+
+def test_nothing_to_do(lib, cuda):
+    F = lib.functional
+    q, k, v, do = (t.to(cuda) for t in inputs(5, 4, 2, 64, 12))
+    none = torch.zeros(1, dtype=torch.int32, device=cuda)
+    out, lse = F.attention_forward(q, k, v, none, save_lse=True)  # no sequence
+    assert not out.any() and torch.isneginf(lse).all()
+    assert not any(g.any() for g in F.attention_backward(do, q, k, v, out, lse, none))
+    empty = torch.zeros(4, dtype=torch.int32, device=cuda)  # three empty ones
+    assert not F.attention_forward(q, k, v, empty).any()
+    out, lse = F.attention_forward(q[:0], k[:0], v[:0], none, save_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (4, 0)
+    assert [tuple(g.shape) for g in F.attention_backward(do[:0], q[:0], k[:0], v[:0], out, lse, none)] == [
+        (0, 4, 64), (0, 2, 64), (0, 2, 64)]
+    no_error(lib)
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(8, 2, 64), (6, 2, 128)])
+def test_repeats_bit_for_bit_and_in_a_graph(lib, cuda, n_q, n_kv, D):
+    F = lib.functional
+    cu = offsets([333, 1, 129, 700])
+    T = int(cu[-1])
+    q, k, v, do = (t.to(cuda) for t in inputs(T, n_q, n_kv, D, 13))
+    cu_dev = torch.from_numpy(cu).to(cuda)
+
+    def step():
+        out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True)
+        return (out, lse, *F.attention_backward(do, q, k, v, out, lse, cu_dev))
+
+    first = [t.clone() for t in step()]
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(step(), first))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = step()
+    for _ in range(2):
+        for t in captured:
+            t.fill_(float("nan"))
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(captured, first))
+    # other data and other sequence lengths through the same graph
+    for t, new in zip((q, k, v, do), inputs(T, n_q, n_kv, D, 14)):
+        t.copy_(new)
+    cu_dev.copy_(torch.from_numpy(offsets([1000, 50, 0, 113])))
+    g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(captured, step()))
+    no_error(lib)
+
+
+def test_on_a_given_stream(lib, cuda):
+    F = lib.functional
+    cu_dev = torch.tensor([0, 500], dtype=torch.int32, device=cuda)
+    q, k, v, do = (t.to(cuda) for t in inputs(500, 8, 2, 64, 15))
+    want = F.attention_forward(q, k, v, cu_dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for s in (side, side.cuda_stream):
+        out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True, stream=s)
+        grads = F.attention_backward(do, q, k, v, out, lse, cu_dev, stream=s)
+        junk = [torch.full((n,), float("nan"), device=cuda) for n in (4000, 500 * 8, 10 ** 6)]  # takes freed memory
+        side.synchronize()
+        assert torch.equal(out, want) and all(torch.isfinite(x.float()).all() for x in grads)
+        del junk
+    no_error(lib)
+
+
+def test_autograd_and_gradients_against_differences(lib, cuda):
+    # PackedAttention's gradients are attention_backward's; and along random
+    # directions they are the oracle's central differences, within the same bounds
+    F = lib.functional
+    cu = offsets([3, 140, 1, 20])
+    T = int(cu[-1])
+    n_q, n_kv, D = 4, 2, 64
+    host = inputs(T, n_q, n_kv, D, 16)
+    q, k, v = (t.to(cuda).requires_grad_() for t in host[:3])
+    do = host[3].to(cuda)
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    out = F.PackedAttention.apply(q, k, v, cu_dev)
+    got = torch.autograd.grad(out, (q, k, v), do)
+    with torch.no_grad():
+        o, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True)
+        want = F.attention_backward(do, q, k, v, o, lse, cu_dev)
+    assert torch.equal(out, o) and all(torch.equal(a, b) for a, b in zip(got, want))
+    # an expanded (broadcast) upstream gradient
+    one = torch.ones(1, 1, 1, dtype=torch.bfloat16, device=cuda).expand(T, n_q, D)
+    a = torch.autograd.grad(F.PackedAttention.apply(q, k, v, cu_dev), (q, k, v), one)
+    b = F.attention_backward(one.contiguous(), q.detach(), k.detach(), v.detach(), o, lse, cu_dev)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    no_error(lib)
+
+    x = [f64(t) for t in host[:3]]
+    d = f64(host[3])
+    ref = A.attention_fwd(*x, cu)
+    err = A.attention_bwd(d, *x, cu, out_err=out_bound(ref))
+    rng = np.random.default_rng(17)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        way = rng.normal(size=x[i].shape)
+        step = 1e-5
+        loss = []
+        for sign in (1, -1):
+            y = list(x)
+            y[i] = x[i] + sign * step * way
+            loss.append((A.attention_fwd(*y, cu)["out"] * d).sum())
+        slope = (loss[0] - loss[1]) / (2 * step)
+        g = f64(got[i])
+        bound = ((err["e_" + name] + U * np.abs(err[name])) * np.abs(way)).sum()
+        assert abs((g * way).sum() - slope) <= bound + 1e-5 * abs(slope), name
+
+
+def test_behind_the_prologue(lib, cuda):
+    # one training step's attention region: packed qkv -> prologue -> attention, and back
+    import workloads
+
+    F = lib.functional
+    wl = workloads.gqa_inputs(300, 8, 2, 64, seed=21, rope_base=10000.0)
+    packed = wl.packed_rows().to(cuda).requires_grad_()
+    w_q, w_k = (w.to(cuda).requires_grad_() for w in (wl.w_q, wl.w_k))
+    cu = offsets([120, 180])
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    q, k, v = F.QKVPrologue.apply(packed, wl.pos.to(cuda), w_q, w_k, 8, 2, 64, "interleaved", wl.eps, wl.rope_base,
+                                  False)
+    out = F.PackedAttention.apply(q, k, v, cu_dev)
+    do = torch.randn(300, 8, 64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    d_packed, d_wq, d_wk = torch.autograd.grad(out, (packed, w_q, w_k), do.to(cuda))
+    no_error(lib)
+    ref = A.attention_fwd(f64(q), f64(k), f64(v), cu)
+    assert_within(f64(out), ref["out"], out_bound(ref), "out")
+    assert d_packed.shape == packed.shape and torch.isfinite(d_packed.float()).all() and d_packed.any()
+    assert torch.isfinite(d_wq).all() and torch.isfinite(d_wk).all()

@@ -89,3 +89,157 @@ def test_own_keys(lib, cuda, n_q, n_kv, D, page_size, lengths):
 def test_shared_prefix(lib, cuda, n_q, n_kv, D, page_size, prefix, lengths):
     w = Batch(n_q, n_kv, D, page_size, lengths, prefix, 70 + page_size + prefix)
     w.check(lib, *w.run(lib, cuda, save_lse=True))
+
+
+def test_prefix_in_several_ranges(lib, cuda):
+    # a prefix longer than one CTA's keys, for more rows than a tile, in both head sizes
+    for n_q, n_kv, D, B in ((16, 1, 64, 20), (8, 2, 128, 70)):
+        w = Batch(n_q, n_kv, D, 32, [3] * (B - 1) + [40], 9000, 3)
+        w.check(lib, *w.run(lib, cuda, save_lse=True), what=f"D {D}")
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_bad_pages_are_not_attended(lib, cuda, prefix):
+    w = Batch(8, 2, 64, 16, [100, 7, 33], prefix, 4)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    w.run(lib, cuda, dev_status=status)
+    assert status.item() == 0
+    keep = [list(range(n)) for n in (100, 7, 33)]
+    w.table[0, 2] = -1
+    w.table[2, 1] = w.k_pool.shape[0]
+    drop = {0: range(32, 48), 2: range(16, 32)}
+    for b, rows in drop.items():
+        keep[b] = [t for t in keep[b] if t not in rows]
+    shared = list(range(prefix))
+    if prefix:
+        w.prefix_pages[5] = 2 ** 31 - 1
+        w.prefix_pages[-1] = -2 ** 31
+        shared = [t for t in shared if t // 16 not in (5, len(w.prefix_pages) - 1)]
+    for b in range(3):
+        rows = shared + [prefix + t for t in keep[b]]
+        w.keys[b], w.values[b] = w.keys[b][rows], w.values[b][rows]
+    got = w.run(lib, cuda, save_lse=True, dev_status=status)
+    w.check(lib, *got)
+    assert status.item() == lib.QKVP_DEV_BAD_PAGE
+
+
+def test_bad_lengths_are_clamped(lib, cuda):
+    w = Batch(8, 2, 64, 16, [64, 5], 0, 5)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    want = w.run(lib, cuda)
+    w.lengths[0] = 10 ** 6
+    got = w.run(lib, cuda, dev_status=status)
+    assert status.item() == lib.QKVP_DEV_BAD_LENGTH and torch.equal(got, want)
+    w.lengths[0] = -3
+    got = w.run(lib, cuda, dev_status=status)
+    assert not got[0].any() and torch.equal(got[1], want[1])
+    torch.cuda.synchronize()
+    assert lib.qkv_prologue_device_error(clear=True) == 0
+
+
+def test_table_slices_out_and_workspace(lib, cuda):
+    F = lib.functional
+    w = Batch(8, 2, 128, 64, [200, 64, 1], 130, 6)
+    want = w.run(lib, cuda)
+    wide = torch.full((3, 11), 10 ** 6, dtype=torch.int32)
+    wide[:, 2:2 + w.table.shape[1]] = w.table
+    table = wide.to(cuda)[:, 2:2 + w.table.shape[1]]
+    need = F.attention_decode_workspace_bytes(8, 2, 128, 3, 64, table.shape[1], 130)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=cuda)
+    out = torch.full((3, 8, 128), 7.0, dtype=torch.bfloat16, device=cuda)
+    args = [t.to(cuda) for t in (w.q, w.k_pool, w.v_pool)]
+    got = F.attention_decode(*args, table, w.lengths.to(cuda), w.prefix_pages.to(cuda), 130, out=out, workspace=ws)
+    assert got is out and torch.equal(out, want)
+    with pytest.raises(lib.QkvpError):
+        F.attention_decode(*args, table, w.lengths.to(cuda), w.prefix_pages.to(cuda), 130, workspace=ws[:need - 16])
+    with pytest.raises(ValueError):
+        F.attention_decode(*args, table, w.lengths.to(cuda), w.prefix_pages.to(cuda)[:2], 130)
+    with pytest.raises(ValueError):
+        F.attention_decode(*args, table[:2], w.lengths.to(cuda))
+    with pytest.raises(ValueError):  # rows that overlap
+        F.attention_decode(*args, table[:1].expand(3, -1), w.lengths.to(cuda))
+    torch.cuda.synchronize()
+    assert lib.qkv_prologue_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_captured_call_follows_lengths_that_grow(lib, cuda, prefix):
+    F = lib.functional
+    w = Batch(8, 2, 64, 16, [90, 17, 260, 33], prefix, 7)
+    args = [t.to(cuda) for t in (w.q, w.k_pool, w.v_pool, w.table, w.lengths)]
+    pages = w.prefix_pages.to(cuda) if prefix else None
+    n = args[4]
+    F.attention_decode(*args, pages, prefix)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = F.attention_decode(*args, pages, prefix)
+    for lengths in ([1, 1, 1, 1], [0, 17, 100, 0], [90, 17, 260, 33]):
+        n.copy_(torch.tensor(lengths, dtype=torch.int32))
+        out.fill_(float("nan"))
+        g.replay()
+        short = [k[:prefix + m] for k, m in zip(w.keys, lengths)], [v[:prefix + m] for v, m in zip(w.values, lengths)]
+        ref = A.attention_decode(f64(w.q), *short)
+        assert_within(f64(out), ref["out"], out_bound(ref), str(lengths))
+        assert torch.equal(out, F.attention_decode(*args, pages, prefix))  # repeats bit for bit
+    torch.cuda.synchronize()
+    assert lib.qkv_prologue_device_error(clear=True) == 0
+
+
+def test_pool_beyond_32_bit_offsets(lib, cuda):
+    # the last pages of a pool of more than 2^32 bytes (and 2^31 values)
+    n_kv, D, page_size = 8, 128, 64
+    pages = (2 ** 31 + 2 ** 27) // (n_kv * D * page_size)
+    w = Batch(16, n_kv, D, page_size, [100, 70], 150, 8)
+    small = w.k_pool.shape[0]
+    big = [torch.empty(pages, page_size, n_kv, D, dtype=torch.bfloat16, device=cuda) for _ in range(2)]
+    for b, s in zip(big, (w.k_pool, w.v_pool)):
+        b[:small] = float("nan")
+        b[-small:] = s.to(cuda)
+    table, shared = w.table.clone(), w.prefix_pages.clone()
+    table[table >= 0] += pages - small
+    shared += pages - small
+    got = lib.functional.attention_decode(w.q.to(cuda), *big, table.to(cuda), w.lengths.to(cuda), shared.to(cuda), 150)
+    w.check(lib, got, None, "far pages")
+    got = lib.functional.attention_decode(w.q[:1].to(cuda), *big, table[:1].to(cuda), w.lengths[:1].to(cuda),
+                                          shared.to(cuda), 150)
+    assert_within(f64(got), *(lambda r: (r["out"], out_bound(r)))(A.attention_decode(f64(w.q[:1]), w.keys[:1],
+                                                                                     w.values[:1])), "one sequence")
+
+
+def test_nothing_to_do(lib, cuda):
+    F = lib.functional
+    w = Batch(8, 2, 64, 16, [5], 0, 9)
+    args = [t.to(cuda) for t in (w.q, w.k_pool, w.v_pool, w.table, w.lengths)]
+    assert F.attention_decode(args[0][:0], *args[1:3], args[3][:0], args[4][:0]).shape == (0, 8, 64)
+    out, lse = F.attention_decode(*args[:3], args[3][:, :0], torch.zeros_like(args[4]), save_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    torch.cuda.synchronize()
+    assert lib.qkv_prologue_device_error(clear=True) == 0
+
+
+def test_pool_write_then_decode_is_the_prompt(lib, cuda):
+    # the prompt's k and v written into the pool by the prologue; the decode of its
+    # last token is the last row of the prompt's attention, each within its bound
+    import workloads
+
+    F = lib.functional
+    T, n_q, n_kv, D, page_size = 150, 8, 2, 64, 16
+    wl = workloads.gqa_inputs(T, n_q, n_kv, D, seed=31, rope_base=10000.0)
+    g = torch.Generator().manual_seed(1)
+    order = torch.randperm(12, generator=g).to(torch.int32)
+    at = torch.arange(T)
+    page, off = order[at // page_size].to(cuda), (at % page_size).to(torch.int32).to(cuda)
+    pools = [torch.full((12, page_size, n_kv, D), float("nan"), dtype=torch.bfloat16, device=cuda) for _ in range(2)]
+    rows, pos = wl.packed_rows().to(cuda), wl.pos.to(cuda)
+    w_q, w_k = wl.w_q.to(cuda), wl.w_k.to(cuda)
+    q = F.prologue_pool_write(rows, pos, w_q, w_k, page, off, *pools, n_q, n_kv, D, eps=wl.eps, rope_base=wl.rope_base)
+    _, k, v = F.prologue_forward(rows, pos, w_q, w_k, n_q, n_kv, D, eps=wl.eps, rope_base=wl.rope_base)
+    cu = np.array([0, T])
+    ref = A.attention_fwd(f64(q), f64(k), f64(v), cu)
+    prompt = F.attention_forward(q, k, v, torch.tensor([0, T], dtype=torch.int32, device=cuda))
+    assert_within(f64(prompt), ref["out"], out_bound(ref), "prompt")
+    n = torch.tensor([T], dtype=torch.int32, device=cuda)
+    one = F.attention_decode(q[-1:].contiguous(), *pools, order[None].to(cuda), n)
+    assert_within(f64(one)[0], ref["out"][-1], out_bound(ref)[-1], "decode")
+    torch.cuda.synchronize()
+    assert lib.qkv_prologue_device_error(clear=True) == 0
