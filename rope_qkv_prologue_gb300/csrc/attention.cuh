@@ -32,6 +32,10 @@ __device__ __forceinline__ int attn_swz(int row, int chunk) { return row * 128 +
 // kWaitLimitNs, and at once when another warp already gave up (*fail): after one
 // timeout the rest of the kernel runs through without waiting, every loop still
 // ends, and attn_report tells the host.
+// A wait by parity sees a phase only until the next one completes. So for every
+// barrier here, whatever completes phase k + 1 is behind each waiter's having seen
+// phase k: a producer that could run ahead waits for something that the waiter does
+// after its wait.
 __device__ __forceinline__ uint32_t global_ns_lo() {
   uint32_t t;
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));

@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // the columns of X that P leaves free, or over Y where X has one buffer.
   constexpr bool kTwoX = !KV || HD == 64;
   constexpr uint32_t tX = 0, tY = kTwoX ? 256 : 128, tAcc1 = tY + 128, tAcc2 = tAcc1 + HD;
+  constexpr bool kAhead = kTwoX && ST >= 4;  // X is issued two blocks ahead: three streamed tiles in use
   constexpr uint32_t kDsOff = KV && kTwoX ? 32 : 0;  // columns of dS behind those of P, in each half
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       product_x(it);
       product_y(it);
       if constexpr (!KV) umma_commit_warp(&b2_empty[it % ST]);
-      if (kTwoX && t.n > 1) product_x(it + 1);
+      if (kAhead && t.n > 1) product_x(it + 1);
       if (t.n == 1) umma_commit_warp(&a_empty);
       for (int i = 0; i < t.n; ++i, ++it) {
         const bool more = i + 1 < t.n;
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           umma_commit_warp(&b1_empty[it % ST]);
           if (!kTwoX && more) product_y(it + 1);
         } else {
+          if (!kAhead && more) product_x(it + 1);
           wait(&ds_full, it & 1);
           if (more) {
             product_y(it + 1);
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           attn_mma_ts(tmem + tAcc1, x, 64, b1(it), id_acc, i > 0);
           umma_commit_warp(&b1_empty[it % ST]);
         }
-        if (kTwoX && i + 2 < t.n) product_x(it + 2);
+        if (kAhead && i + 2 < t.n) product_x(it + 2);
         if (i + 2 == t.n) umma_commit_warp(&a_empty);  // the last X and Y are issued
       }
       umma_commit_warp(&acc_done);
@@ -391,19 +393,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             unpair(fma2(pair(p0, p1), c2, ls2[KV ? 16 * x + e : 0]), p0, p1);
             p0 = ex2(p0);
             p1 = ex2(p1);
-            if constexpr (KV) {
-              if (diagonal) {  // queries before this key do not attend it
-                if (64 * wg + 32 * x + 2 * e < row) p0 = 0.f;
-                if (64 * wg + 32 * x + 2 * e + 1 < row) p1 = 0.f;
-              }
-              w[e] = pack2(p0, p1);
-            }
           }
-          if constexpr (KV) tmem_st16(t_x + 16 * x, w);
+          if constexpr (KV) {
+            if (diagonal && 2 * wg + x <= qtr) {  // queries before this key do not attend it
+              asm volatile("");                   // a branch, not selects in every block
+              const int first = 2 * wg + x < qtr ? 32 : lane;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e < first) p[32 * x + e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = pack2(p[32 * x + 2 * e], p[32 * x + 2 * e + 1]);
+            tmem_st16(t_x + 16 * x, w);
+          }
         }
         if constexpr (KV) {
           tmem_wait_st();
           tc_fence_before();
+          // Where X has two buffers, nothing else keeps a warp from P of this block while the
+          // issuer has yet to see p_full of the block before (or another warp to arrive
+          // there). P dO of the block before, issued after that, frees its streamed tile.
+          if (kTwoX && it > 0) wait(&b2_empty[(it - 1) % ST], ((it - 1) / ST) & 1);
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full);
         }
@@ -412,6 +422,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_ld64(t_y, y);
         if constexpr (!KV) {
           if (diagonal) {  // keys after the row (and so behind the sequence), whatever was computed there
+            asm volatile("");
 #pragma unroll
             for (int e = 0; e < 64; ++e)
               if (64 * wg + e > row) p[e] = y[e] = 0.f;

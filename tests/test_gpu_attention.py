@@ -350,3 +350,23 @@ def test_behind_the_prologue(lib, cuda):
     assert_within(f64(out), ref["out"], out_bound(ref), "out")
     assert d_packed.shape == packed.shape and torch.isfinite(d_packed.float()).all() and d_packed.any()
     assert torch.isfinite(d_wq).all() and torch.isfinite(d_wk).all()
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(32, 4, 64), (8, 2, 128)])
+def test_many_steps_of_ragged_sequences(lib, cuda, n_q, n_kv, D):
+    # the pipelines' barriers over some ten million phases: no wait runs out, and
+    # the last step has the first one's bits
+    F = lib.functional
+    cu = offsets([3, 176, 122, 359, 532, 951, 473, 440, 796, 121, 123])
+    q, k, v, do = (t.to(cuda) for t in inputs(int(cu[-1]), n_q, n_kv, D, 18))
+    cu_dev = torch.from_numpy(cu).to(cuda)
+
+    def step():
+        out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True)
+        return (out, lse, *F.attention_backward(do, q, k, v, out, lse, cu_dev))
+
+    first = step()
+    for _ in range(400):
+        last = step()
+    assert all(torch.equal(a, b) for a, b in zip(first, last))
+    no_error(lib)
