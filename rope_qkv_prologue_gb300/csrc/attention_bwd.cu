@@ -39,15 +39,20 @@ constexpr int kStatStages = 2;
 constexpr int kDeltaHeads = 256;  // heads of the delta kernel's shared buffer
 constexpr int kStageBytes = 32 * 64;  // a warp's store buffer: 32 rows x 32 bf16
 
+// Shared memory. The first streamed operand stays until the accumulating product of
+// its block, two products after the first use, so it has the deeper ring (with two
+// tiles the query kernel at head_dim 128 waited 1500 of 2800 cycles a block for K).
+// At head_dim 128 that fills the SM's 227 KiB, and the results are stored from
+// registers; at 64 they pass through a buffer that makes whole sectors of them.
 template <int HD>
 struct BwdSmem {
   static constexpr int kTile = (HD / 64) * kAttnBox;
-  static constexpr int kStages = HD == 128 ? 2 : 4;  // of each streamed operand
+  static constexpr int kS1 = HD == 128 ? 3 : 4, kS2 = HD == 128 ? 2 : 4;  // tiles of each streamed operand
   static constexpr int kA = 0;
   static constexpr int kB1 = 2 * kTile;
-  static constexpr int kB2 = kB1 + kStages * kTile;
-  static constexpr int kOut = kB2 + kStages * kTile;
-  static constexpr int kBytes = kOut + 8 * kStageBytes;
+  static constexpr int kB2 = kB1 + kS1 * kTile;
+  static constexpr int kOut = kB2 + kS2 * kTile;
+  static constexpr int kBytes = kOut + (HD == 128 ? 0 : 8 * kStageBytes);
 };
 
 struct BwdItem {
@@ -68,17 +73,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                               const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                               const AttnBwdArgs a) {
   using SM = BwdSmem<HD>;
-  constexpr int ST = SM::kStages;
+  constexpr int S1 = SM::kS1, S2 = SM::kS2;
   // Tensor memory. X has two buffers where there is room for them (not in the
   // key/value kernel at head_dim 128); a block's P lies over its X, and its dS in
   // the columns of X that P leaves free, or over Y where X has one buffer.
   constexpr bool kTwoX = !KV || HD == 64;
   constexpr uint32_t tX = 0, tY = kTwoX ? 256 : 128, tAcc1 = tY + 128, tAcc2 = tAcc1 + HD;
-  constexpr bool kAhead = kTwoX && ST >= 4;  // X is issued two blocks ahead: three streamed tiles in use
+  constexpr bool kAhead = kTwoX && S1 >= 4;  // X is issued two blocks ahead: three streamed tiles in use
   constexpr uint32_t kDsOff = KV && kTwoX ? 32 : 0;  // columns of dS behind those of P, in each half
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* base = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t a_full, a_empty, b1_full[ST], b1_empty[ST], b2_full[ST], b2_empty[ST], tail_bar,
+  unsigned char* base = smem_raw;  // all of the SM's shared memory at head_dim 128: no room to round it up
+  if ((smem_addr(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(a.err, kErrWaitTimeout);  // no result; the declared alignment rules it out
+    return;
+  }
+  __shared__ __align__(8) uint64_t a_full, a_empty, b1_full[S1], b1_empty[S1], b2_full[S2], b2_empty[S2], tail_bar,
       x_full[2], y_full, p_full, ds_full, acc_done, acc_free, st_full[kStatStages], st_empty[kStatStages],
       it_full[kBwdSched], it_empty[kBwdSched], mma_done;
   __shared__ uint32_t s_tmem;
@@ -93,9 +102,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&a_full, 1);
     mbar_init(&a_empty, 1);
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < S1; ++s) {
       mbar_init(&b1_full[s], 1);
       mbar_init(&b1_empty[s], 1);
+    }
+    for (int s = 0; s < S2; ++s) {
       mbar_init(&b2_full[s], 1);
       mbar_init(&b2_empty[s], 1);
     }
@@ -177,12 +188,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int i = 0; i < t.n; ++i, ++it) {
         int head;
         const int blk = block_of(t, i, head);
-        const uint32_t s = it % ST;
         const int rows = t.len - kAttnRows * blk;  // of the sequence in this block
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
+          const uint32_t n = which ? S2 : S1, s = it % n;
           uint64_t* full = which ? &b2_full[s] : &b1_full[s];
-          if (it >= ST) wait(which ? &b2_empty[s] : &b1_empty[s], ((it / ST) - 1) & 1);
+          wait(which ? &b2_empty[s] : &b1_empty[s], ((it / n) & 1) ^ 1);  // (the first time round it passes)
           unsigned char* dst = base + (which ? SM::kB2 : SM::kB1) + s * SM::kTile;
           const CUtensorMap* map = KV ? (which ? &tmap_do : &tmap_q) : (which ? &tmap_v : &tmap_k);
           const bool patch = rows < kAttnRows && (KV || which == 0);
@@ -206,10 +217,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     // every copy has landed before the CTA may exit (phases already consumed return at once)
     if (lane == 0) {
-      for (uint32_t k = it > ST ? it - ST : 0; k < it; ++k) {
-        mbar_wait(&b1_full[k % ST], (k / ST) & 1, a.err);
-        mbar_wait(&b2_full[k % ST], (k / ST) & 1, a.err);
-      }
+      for (uint32_t k = it > S1 ? it - S1 : 0; k < it; ++k) mbar_wait(&b1_full[k % S1], (k / S1) & 1, a.err);
+      for (uint32_t k = it > S2 ? it - S2 : 0; k < it; ++k) mbar_wait(&b2_full[k % S2], (k / S2) & 1, a.err);
       if (items) mbar_wait(&a_full, (items - 1) & 1, a.err);
     }
   } else if (warp == 1) {
@@ -218,17 +227,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t it = 0, items = 0;
     const uint32_t tmem = uniform(s_tmem);
     BwdItem t;
-    auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % ST) * SM::kTile; };
-    auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % ST) * SM::kTile; };
+    auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % S1) * SM::kTile; };
+    auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % S2) * SM::kTile; };
     auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
-      wait(&b1_full[k % ST], (k / ST) & 1);
+      wait(&b1_full[k % S1], (k / S1) & 1);
       tc_fence_after();
       const uint32_t buf = kTwoX ? k & 1 : 0;
       attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
       umma_commit_warp(&x_full[buf]);
     };
     auto product_y = [&](uint32_t k) {
-      wait(&b2_full[k % ST], (k / ST) & 1);
+      wait(&b2_full[k % S2], (k / S2) & 1);
       tc_fence_after();
       attn_mma_ss<HD>(tmem + tY, base + SM::kA + SM::kTile, b2(k), id_x);
       umma_commit_warp(&y_full);
@@ -240,7 +249,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after();
       product_x(it);
       product_y(it);
-      if constexpr (!KV) umma_commit_warp(&b2_empty[it % ST]);
+      if constexpr (!KV) umma_commit_warp(&b2_empty[it % S2]);
       if (kAhead && t.n > 1) product_x(it + 1);
       if (t.n == 1) umma_commit_warp(&a_empty);
       for (int i = 0; i < t.n; ++i, ++it) {
@@ -251,25 +260,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
           tc_fence_after();
           attn_mma_ts(tmem + tAcc1, x, 64, b2(it), id_acc, i > 0);
-          umma_commit_warp(&b2_empty[it % ST]);
+          umma_commit_warp(&b2_empty[it % S2]);
           if (!kTwoX && more) product_x(it + 1);
           wait(&ds_full, it & 1);
           tc_fence_after();
           if (kTwoX && more) product_y(it + 1);  // Y has been read: it need not wait behind dS Q
           attn_mma_ts(tmem + tAcc2, kTwoX ? x + kDsOff : tmem + tY, 64, b1(it), id_acc, i > 0);
-          umma_commit_warp(&b1_empty[it % ST]);
+          umma_commit_warp(&b1_empty[it % S1]);
           if (!kTwoX && more) product_y(it + 1);
         } else {
           if (!kAhead && more) product_x(it + 1);
           wait(&ds_full, it & 1);
           if (more) {
             product_y(it + 1);
-            umma_commit_warp(&b2_empty[(it + 1) % ST]);
+            umma_commit_warp(&b2_empty[(it + 1) % S2]);
           }
           if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
           tc_fence_after();
           attn_mma_ts(tmem + tAcc1, x, 64, b1(it), id_acc, i > 0);
-          umma_commit_warp(&b1_empty[it % ST]);
+          umma_commit_warp(&b1_empty[it % S1]);
         }
         if (kAhead && i + 2 < t.n) product_x(it + 2);
         if (i + 2 == t.n) umma_commit_warp(&a_empty);  // the last X and Y are issued
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           // Where X has two buffers, nothing else keeps a warp from P of this block while the
           // issuer has yet to see p_full of the block before (or another warp to arrive
           // there). P dO of the block before, issued after that, frees its streamed tile.
-          if (kTwoX && it > 0) wait(&b2_empty[(it - 1) % ST], ((it - 1) / ST) & 1);
+          if (kTwoX && it > 0) wait(&b2_empty[(it - 1) % S2], ((it - 1) / S2) & 1);
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full);
         }
@@ -492,27 +501,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float f = KV && wg == 0 ? 1.f : a.scale;
       uint4* out = KV ? (wg ? a.dk : a.dv) : a.dq;
       const int heads = KV ? a.n_kv : a.n_q, col0 = KV ? 0 : COLS * wg;
-      unsigned char* sbuf = base + SM::kOut + (warp - 4) * kStageBytes;
       const int row0 = t.own + 32 * qtr, rows = t.first + t.len - row0;
-      constexpr int CHU = UNIT / 8, RP = 32 / CHU;  // chunks per staged row, rows per pass
-      auto at = [](int r, int ch) { return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4); };  // no bank conflicts either way
+      if constexpr (HD == 128) {
+        uint4* dst = out + ((int64_t)(row0 + lane) * heads + t.head) * (HD / 8) + col0 / 8;
+        if (lane < rows)
 #pragma unroll
-      for (int x = 0; x < COLS / UNIT; ++x) {
+          for (int ch = 0; ch < COLS / 8; ++ch) {
+            const float* v = o + 8 * ch;
+            dst[ch] = make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
+                                 pack2(v[6] * f, v[7] * f));
+          }
+      } else if (rows > 0) {
+        unsigned char* sbuf = base + SM::kOut + (warp - 4) * kStageBytes;
+        constexpr int CHU = UNIT / 8, RP = 32 / CHU;  // chunks per staged row, rows per pass
+        auto at = [](int r, int ch) { return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4); };  // no bank conflicts either way
 #pragma unroll
-        for (int ch = 0; ch < CHU; ++ch) {
-          const float* v = o + UNIT * x + 8 * ch;
-          *reinterpret_cast<uint4*>(sbuf + at(lane, ch)) =
-              make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
-                         pack2(v[6] * f, v[7] * f));
+        for (int x = 0; x < COLS / UNIT; ++x) {
+#pragma unroll
+          for (int ch = 0; ch < CHU; ++ch) {
+            const float* v = o + UNIT * x + 8 * ch;
+            *reinterpret_cast<uint4*>(sbuf + at(lane, ch)) =
+                make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f),
+                           pack2(v[6] * f, v[7] * f));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += RP) {
+            const int r = r0 + lane / CHU, ch = lane % CHU;
+            const uint4 v = *reinterpret_cast<const uint4*>(sbuf + at(r, ch));
+            if (r < rows) out[((int64_t)(row0 + r) * heads + t.head) * (HD / 8) + (col0 + UNIT * x) / 8 + ch] = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += RP) {
-          const int r = r0 + lane / CHU, ch = lane % CHU;
-          const uint4 v = *reinterpret_cast<const uint4*>(sbuf + at(r, ch));
-          if (r < rows) out[((int64_t)(row0 + r) * heads + t.head) * (HD / 8) + (col0 + UNIT * x) / 8 + ch] = v;
-        }
-        __syncwarp();
       }
     }
   }
@@ -581,7 +601,7 @@ const void* attention_delta_kernel(int head_dim) {
                         : reinterpret_cast<const void*>(&qkvp_attention_delta_kernel<128>);
 }
 int attention_bwd_smem_bytes(int head_dim) {
-  return (head_dim == 64 ? BwdSmem<64>::kBytes : BwdSmem<128>::kBytes) + 1024;
+  return head_dim == 64 ? BwdSmem<64>::kBytes : BwdSmem<128>::kBytes;
 }
 int attention_bwd_threads() { return kBwdThreads; }
 
