@@ -483,8 +483,8 @@ QKVP_API int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t bat
  * flags       QKVP_ZERO_REST: rows of no sequence of dq, dk and dv become zero
  *             instead of being left as they are.
  * dq          bf16 [T, n_q, head_dim] out; dk, dv bf16 [T, n_kv, head_dim] out.
- * workspace   at least qkv_attention_bwd_workspace() bytes (float32 [n_q, T]),
- *             16-byte aligned, any contents. Two calls whose work can overlap on
+ * workspace   at least qkv_attention_bwd_workspace() bytes for the same T and
+ *             batch, 16-byte aligned, any contents. Two calls whose work can overlap on
  *             the GPU must not share a workspace.
  * ------------------------------------------------------------------------- */
 QKVP_API int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const int32_t* cu_seqlens,
@@ -492,8 +492,10 @@ QKVP_API int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t bat
                                const float* lse, float scale, uint32_t flags, void* dq, void* dk, void* dv,
                                int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of qkv_attention_bwd (host only; needs no device). */
-QKVP_API int qkv_attention_bwd_workspace(const qkvp_layout* layout, int64_t T, size_t* bytes);
+/* Workspace bytes of qkv_attention_bwd (host only; needs no device): float32
+ * [n_q, T], and for small problems the fp32 sums of parts of each group's query
+ * heads. */
+QKVP_API int qkv_attention_bwd_workspace(const qkvp_layout* layout, int64_t T, int32_t batch, size_t* bytes);
 
 /* ---------------------------------------------------------------------------
  * qkv_attention_decode -- attention of one new token per sequence over the

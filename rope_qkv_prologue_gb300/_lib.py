@@ -113,7 +113,7 @@ _SIGS = {
     "qkv_attention_fwd": ([_LP, _i64, _i32, _vp, _vp, _vp, _vp, _f32, _u32, _vp, _vp, _vp, _vp], ctypes.c_int),
     "qkv_attention_bwd": ([_LP, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _u32, _vp, _vp, _vp, _vp, _vp,
                            ctypes.c_size_t, _vp], ctypes.c_int),
-    "qkv_attention_bwd_workspace": ([_LP, _i64, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "qkv_attention_bwd_workspace": ([_LP, _i64, _i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "qkv_attention_decode": ([_LP, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _i32, _f32, _vp, _vp,
                               _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
     "qkv_attention_decode_workspace": ([_LP, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
@@ -338,11 +338,11 @@ def qkv_attention_bwd(L, T, batch, cu_seqlens, dout, q, k, v, out, lse, scale, f
     return _ret(st, "qkv_attention_bwd", check)
 
 
-def qkv_attention_bwd_workspace(L, T, check=True):
+def qkv_attention_bwd_workspace(L, T, batch, check=True):
     """Workspace bytes of qkv_attention_bwd (a status code instead when check is
     False and the call fails)."""
     n = ctypes.c_size_t(0)
-    st = _lib.qkv_attention_bwd_workspace(ctypes.byref(L), int(T), ctypes.byref(n))
+    st = _lib.qkv_attention_bwd_workspace(ctypes.byref(L), int(T), int(batch), ctypes.byref(n))
     if not check and st != QKVP_OK:
         return st
     _ret(st, "qkv_attention_bwd_workspace", True)

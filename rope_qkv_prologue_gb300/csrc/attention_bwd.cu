@@ -10,10 +10,11 @@
 //      keys, adding dS K (and writes the delta of rows with few keys anew);
 //   3. the key/value kernel: a CTA owns 128 keys of one key/value head and goes
 //      through the query blocks and heads that attend them, forming the transposed
-//      S^T = K Q^T and dP^T = V dO^T and adding P^T dO and dS^T Q.
+//      S^T = K Q^T and dP^T = V dO^T and adding P^T dO and dS^T Q. Where that leaves
+//      SMs idle (few tokens, few key/value heads), a group's query heads are divided
+//      among CTAs, whose fp32 sums the folding kernel adds in a fixed order.
 // S and dP are formed twice (seven products instead of five), so that every result
-// is a sum in one CTA's tensor memory in a fixed order: no atomics, no partial
-// results in memory, the same bits every time.
+// is a sum in tensor memory in a fixed order: no atomics, the same bits every time.
 //
 // Both kernels are one template: two tiles of the CTA's own rows stay in shared
 // memory, pairs of tiles stream past them by TMA, X = A1 B1^T and Y = A2 B2^T go
@@ -62,12 +63,15 @@ struct BwdItem {
   int len;    // its rows
   int blk;    // the own block's index in the sequence
   int head;   // key/value head, or query head
+  int split;  // SPLIT: which of the group's parts of query heads
   int valid;
 };
 
 }  // namespace
 
-template <int HD, bool KV>
+// KV: the key/value kernel; SPLIT: of it, with the heads of a group divided (an instance
+// of its own: the division inside the one kernel cost it a tenth on ragged sequences).
+template <int HD, bool KV, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     qkvp_attention_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
                               const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -157,8 +161,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // kernel) the query head.
   auto block_of = [&](const BwdItem& t, int i, int& head) {
     if constexpr (KV) {
-      const int per = t.n / a.group;
-      head = t.head * a.group + i / per;
+      const int heads = SPLIT ? a.group / a.splits : a.group, per = t.n / heads;
+      head = t.head * a.group + (SPLIT ? t.split * heads : 0) + i / per;
       return t.blk + i % per;
     } else {
       head = t.head / a.group;
@@ -168,189 +172,193 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   // 12 warps launched with 168 registers a thread: 4 warps x 88 + 8 x 208 = 12 x 168
   if (warp < 4) {
-  regs_less<88>();
-  if (warp == 0) {
-    // ---- loader
-    uint32_t it = 0, tails = 0, items = 0;
-    BwdItem t;
-    while (next_item(t)) {
-      if (t.n == 0) continue;
-      if (items > 0) wait(&a_empty, (items - 1) & 1);
-      ++items;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&a_full, 2 * SM::kTile);
-        for (int x = 0; x < HD / 64; ++x) {
-          tma_load_2d(base + SM::kA + x * kAttnBox, KV ? &tmap_k : &tmap_q, t.head * HD + 64 * x, t.own, &a_full);
-          tma_load_2d(base + SM::kA + SM::kTile + x * kAttnBox, KV ? &tmap_v : &tmap_do, t.head * HD + 64 * x, t.own,
-                      &a_full);
-        }
-      }
-      for (int i = 0; i < t.n; ++i, ++it) {
-        int head;
-        const int blk = block_of(t, i, head);
-        const int rows = t.len - kAttnRows * blk;  // of the sequence in this block
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          const uint32_t n = which ? S2 : S1, s = it % n;
-          uint64_t* full = which ? &b2_full[s] : &b1_full[s];
-          wait(which ? &b2_empty[s] : &b1_empty[s], ((it / n) & 1) ^ 1);  // (the first time round it passes)
-          unsigned char* dst = base + (which ? SM::kB2 : SM::kB1) + s * SM::kTile;
-          const CUtensorMap* map = KV ? (which ? &tmap_do : &tmap_q) : (which ? &tmap_v : &tmap_k);
-          const bool patch = rows < kAttnRows && (KV || which == 0);
-          uint64_t* bar = patch ? &tail_bar : full;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar, SM::kTile);
-            for (int x = 0; x < HD / 64; ++x)
-              tma_load_2d(dst + x * kAttnBox, map, head * HD + 64 * x, t.first + kAttnRows * blk, bar);
-          }
-          if (patch) {
-            wait(&tail_bar, tails++ & 1);
-            for (int r = rows + (lane >> 3); r < kAttnRows; r += 4)
-              for (int x = 0; x < HD / 64; ++x)
-                *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_cta();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full);
-          }
-        }
-      }
-    }
-    // every copy has landed before the CTA may exit (phases already consumed return at once)
-    if (lane == 0) {
-      for (uint32_t k = it > S1 ? it - S1 : 0; k < it; ++k) mbar_wait(&b1_full[k % S1], (k / S1) & 1, a.err);
-      for (uint32_t k = it > S2 ? it - S2 : 0; k < it; ++k) mbar_wait(&b2_full[k % S2], (k / S2) & 1, a.err);
-      if (items) mbar_wait(&a_full, (items - 1) & 1, a.err);
-    }
-  } else if (warp == 1) {
-    // ---- MMA issuer
-    constexpr uint32_t id_x = umma_idesc_bf16(kAttnRows, kAttnRows), id_acc = umma_idesc_bf16_bmn(kAttnRows, HD);
-    uint32_t it = 0, items = 0;
-    const uint32_t tmem = uniform(s_tmem);
-    BwdItem t;
-    auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % S1) * SM::kTile; };
-    auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % S2) * SM::kTile; };
-    auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
-      wait(&b1_full[k % S1], (k / S1) & 1);
-      tc_fence_after();
-      const uint32_t buf = kTwoX ? k & 1 : 0;
-      attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
-      umma_commit_warp(&x_full[buf]);
-    };
-    auto product_y = [&](uint32_t k) {
-      wait(&b2_full[k % S2], (k / S2) & 1);
-      tc_fence_after();
-      attn_mma_ss<HD>(tmem + tY, base + SM::kA + SM::kTile, b2(k), id_x);
-      umma_commit_warp(&y_full);
-    };
-    while (next_item(t)) {
-      t.n = (int)uniform(t.n);
-      if (t.n == 0) continue;
-      wait(&a_full, items & 1);
-      tc_fence_after();
-      product_x(it);
-      product_y(it);
-      if constexpr (!KV) umma_commit_warp(&b2_empty[it % S2]);
-      if (kAhead && t.n > 1) product_x(it + 1);
-      if (t.n == 1) umma_commit_warp(&a_empty);
-      for (int i = 0; i < t.n; ++i, ++it) {
-        const bool more = i + 1 < t.n;
-        const uint32_t x = tmem + tX + (kTwoX ? 128 * (it & 1) : 0);
-        if constexpr (KV) {
-          wait(&p_full, it & 1);
-          if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
-          tc_fence_after();
-          attn_mma_ts(tmem + tAcc1, x, 64, b2(it), id_acc, i > 0);
-          umma_commit_warp(&b2_empty[it % S2]);
-          if (!kTwoX && more) product_x(it + 1);
-          wait(&ds_full, it & 1);
-          tc_fence_after();
-          if (kTwoX && more) product_y(it + 1);  // Y has been read: it need not wait behind dS Q
-          attn_mma_ts(tmem + tAcc2, kTwoX ? x + kDsOff : tmem + tY, 64, b1(it), id_acc, i > 0);
-          umma_commit_warp(&b1_empty[it % S1]);
-          if (!kTwoX && more) product_y(it + 1);
-        } else {
-          if (!kAhead && more) product_x(it + 1);
-          wait(&ds_full, it & 1);
-          if (more) {
-            product_y(it + 1);
-            umma_commit_warp(&b2_empty[(it + 1) % S2]);
-          }
-          if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
-          tc_fence_after();
-          attn_mma_ts(tmem + tAcc1, x, 64, b1(it), id_acc, i > 0);
-          umma_commit_warp(&b1_empty[it % S1]);
-        }
-        if (kAhead && i + 2 < t.n) product_x(it + 2);
-        if (i + 2 == t.n) umma_commit_warp(&a_empty);  // the last X and Y are issued
-      }
-      umma_commit_warp(&acc_done);
-      ++items;
-    }
-    umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
-    if (lane == 0) mbar_wait(&mma_done, 0, a.err);
-  } else if (warp == 2) {
-    // ---- finder
-    AttnOrder ord{a.cu, a.batch, kAttnRows, s_cache, 0, 0};
-    const bool ok = ord.init(a.T, lane);
-    if (!ok && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
-    const int units = KV ? a.n_kv : a.n_q;
-    const uint32_t work = ord.total * (uint32_t)units;  // below 2^31: the host checks
-    for (uint32_t k = 0;; ++k) {
-      const uint32_t s = k % kBwdSched;
-      if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kBwdSched) & 1) ^ 1))) break;
-      const uint32_t w = attn_deal(k, blockIdx.x, gridDim.x);
-      BwdItem t = {};
-      t.valid = k * gridDim.x < work;  // else no CTA has any left
-      if (w < work) {                  // (an empty item: this CTA has none in the last round)
-        int seq, cost;
-        const uint32_t rank = w / (uint32_t)units;
-        ord.find(rank, lane, seq, cost);
-        t.head = (int)(w - rank * (uint32_t)units);
-        t.first = a.cu[seq];
-        t.len = a.cu[seq + 1] - t.first;
-        t.blk = KV ? (t.len + kAttnRows - 1) / kAttnRows - cost : cost - 1;
-        t.own = t.first + kAttnRows * t.blk;
-        t.n = KV ? cost * a.group : cost;
-      }
-      if (lane == 0) {
-        s_item[s] = t;
-        mbar_arrive(&it_full[s]);
-      }
-      __syncwarp();
-      if (!t.valid) break;
-    }
-  } else if (warp == 3) {
-    if constexpr (KV) {
-      // ---- lse and delta of the streamed rows; a row behind the end gets p = 2^(x - inf) = 0
-      uint32_t it = 0;
+    regs_less<88>();
+    if (warp == 0) {
+      // ---- loader
+      uint32_t it = 0, tails = 0, items = 0;
       BwdItem t;
       while (next_item(t)) {
+        if (t.n == 0) continue;
+        if (items > 0) wait(&a_empty, (items - 1) & 1);
+        ++items;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&a_full, 2 * SM::kTile);
+          for (int x = 0; x < HD / 64; ++x) {
+            tma_load_2d(base + SM::kA + x * kAttnBox, KV ? &tmap_k : &tmap_q, t.head * HD + 64 * x, t.own, &a_full);
+            tma_load_2d(base + SM::kA + SM::kTile + x * kAttnBox, KV ? &tmap_v : &tmap_do, t.head * HD + 64 * x, t.own,
+                        &a_full);
+          }
+        }
         for (int i = 0; i < t.n; ++i, ++it) {
           int head;
           const int blk = block_of(t, i, head);
-          const uint32_t s = it % kStatStages;
-          float ls[4], de[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = kAttnRows * blk + 32 * x + lane;
-            const bool in = r < t.len;
-            const int64_t at = (int64_t)head * a.T + t.first + r;
-            ls[x] = in ? -a.lse[at] * kLog2e : -INFINITY;
-            de[x] = in ? -a.delta[at] : 0.f;
-            if (ls[x] == INFINITY) ls[x] = -INFINITY;  // a row without keys
+          const int rows = t.len - kAttnRows * blk;  // of the sequence in this block
+  #pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            const uint32_t n = which ? S2 : S1, s = it % n;
+            uint64_t* full = which ? &b2_full[s] : &b1_full[s];
+            wait(which ? &b2_empty[s] : &b1_empty[s], ((it / n) & 1) ^ 1);  // (the first time round it passes)
+            unsigned char* dst = base + (which ? SM::kB2 : SM::kB1) + s * SM::kTile;
+            const CUtensorMap* map = KV ? (which ? &tmap_do : &tmap_q) : (which ? &tmap_v : &tmap_k);
+            const bool patch = rows < kAttnRows && (KV || which == 0);
+            uint64_t* bar = patch ? &tail_bar : full;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar, SM::kTile);
+              for (int x = 0; x < HD / 64; ++x)
+                tma_load_2d(dst + x * kAttnBox, map, head * HD + 64 * x, t.first + kAttnRows * blk, bar);
+            }
+            if (patch) {
+              wait(&tail_bar, tails++ & 1);
+              for (int r = rows + (lane >> 3); r < kAttnRows; r += 4)
+                for (int x = 0; x < HD / 64; ++x)
+                  *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_cta();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(full);
+            }
           }
-          if (it >= kStatStages) wait(&st_empty[s], ((it / kStatStages) - 1) & 1);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            s_stat[s][0][32 * x + lane] = ls[x];
-            s_stat[s][1][32 * x + lane] = de[x];
+        }
+      }
+      // every copy has landed before the CTA may exit (phases already consumed return at once)
+      if (lane == 0) {
+        for (uint32_t k = it > S1 ? it - S1 : 0; k < it; ++k) mbar_wait(&b1_full[k % S1], (k / S1) & 1, a.err);
+        for (uint32_t k = it > S2 ? it - S2 : 0; k < it; ++k) mbar_wait(&b2_full[k % S2], (k / S2) & 1, a.err);
+        if (items) mbar_wait(&a_full, (items - 1) & 1, a.err);
+      }
+    } else if (warp == 1) {
+      // ---- MMA issuer
+      constexpr uint32_t id_x = umma_idesc_bf16(kAttnRows, kAttnRows), id_acc = umma_idesc_bf16_bmn(kAttnRows, HD);
+      uint32_t it = 0, items = 0;
+      const uint32_t tmem = uniform(s_tmem);
+      BwdItem t;
+      auto b1 = [&](uint32_t k) { return base + SM::kB1 + (k % S1) * SM::kTile; };
+      auto b2 = [&](uint32_t k) { return base + SM::kB2 + (k % S2) * SM::kTile; };
+      auto product_x = [&](uint32_t k) {  // streamed block k (counted over all items)
+        wait(&b1_full[k % S1], (k / S1) & 1);
+        tc_fence_after();
+        const uint32_t buf = kTwoX ? k & 1 : 0;
+        attn_mma_ss<HD>(tmem + tX + 128 * buf, base + SM::kA, b1(k), id_x);
+        umma_commit_warp(&x_full[buf]);
+      };
+      auto product_y = [&](uint32_t k) {
+        wait(&b2_full[k % S2], (k / S2) & 1);
+        tc_fence_after();
+        attn_mma_ss<HD>(tmem + tY, base + SM::kA + SM::kTile, b2(k), id_x);
+        umma_commit_warp(&y_full);
+      };
+      while (next_item(t)) {
+        t.n = (int)uniform(t.n);
+        if (t.n == 0) continue;
+        wait(&a_full, items & 1);
+        tc_fence_after();
+        product_x(it);
+        product_y(it);
+        if constexpr (!KV) umma_commit_warp(&b2_empty[it % S2]);
+        if (kAhead && t.n > 1) product_x(it + 1);
+        if (t.n == 1) umma_commit_warp(&a_empty);
+        for (int i = 0; i < t.n; ++i, ++it) {
+          const bool more = i + 1 < t.n;
+          const uint32_t x = tmem + tX + (kTwoX ? 128 * (it & 1) : 0);
+          if constexpr (KV) {
+            wait(&p_full, it & 1);
+            if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
+            tc_fence_after();
+            attn_mma_ts(tmem + tAcc1, x, 64, b2(it), id_acc, i > 0);
+            umma_commit_warp(&b2_empty[it % S2]);
+            if (!kTwoX && more) product_x(it + 1);
+            wait(&ds_full, it & 1);
+            tc_fence_after();
+            if (kTwoX && more) product_y(it + 1);  // Y has been read: it need not wait behind dS Q
+            attn_mma_ts(tmem + tAcc2, kTwoX ? x + kDsOff : tmem + tY, 64, b1(it), id_acc, i > 0);
+            umma_commit_warp(&b1_empty[it % S1]);
+            if (!kTwoX && more) product_y(it + 1);
+          } else {
+            if (!kAhead && more) product_x(it + 1);
+            wait(&ds_full, it & 1);
+            if (more) {
+              product_y(it + 1);
+              umma_commit_warp(&b2_empty[(it + 1) % S2]);
+            }
+            if (i == 0 && items > 0) wait(&acc_free, (items - 1) & 1);
+            tc_fence_after();
+            attn_mma_ts(tmem + tAcc1, x, 64, b1(it), id_acc, i > 0);
+            umma_commit_warp(&b1_empty[it % S1]);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&st_full[s]);
+          if (kAhead && i + 2 < t.n) product_x(it + 2);
+          if (i + 2 == t.n) umma_commit_warp(&a_empty);  // the last X and Y are issued
+        }
+        umma_commit_warp(&acc_done);
+        ++items;
+      }
+      umma_commit_warp(&mma_done);  // nothing it issued may still run when the CTA exits
+      if (lane == 0) mbar_wait(&mma_done, 0, a.err);
+    } else if (warp == 2) {
+      // ---- finder
+      AttnOrder ord{a.cu, a.batch, kAttnRows, s_cache, 0, 0};
+      const bool ok = ord.init(a.T, lane);
+      if (!ok && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
+      const int units = KV ? (SPLIT ? a.n_kv * a.splits : a.n_kv) : a.n_q;
+      const uint32_t work = ord.total * (uint32_t)units;  // below 2^31: the host checks
+      for (uint32_t k = 0;; ++k) {
+        const uint32_t s = k % kBwdSched;
+        if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kBwdSched) & 1) ^ 1))) break;
+        const uint32_t w = attn_deal(k, blockIdx.x, gridDim.x);
+        BwdItem t = {};
+        t.valid = k * gridDim.x < work;  // else no CTA has any left
+        if (w < work) {                  // (an empty item: this CTA has none in the last round)
+          int seq, cost;
+          const uint32_t rank = w / (uint32_t)units;
+          ord.find(rank, lane, seq, cost);
+          t.head = (int)(w - rank * (uint32_t)units);
+          if constexpr (SPLIT) {
+            t.split = t.head / a.n_kv;
+            t.head -= t.split * a.n_kv;
+          }
+          t.first = a.cu[seq];
+          t.len = a.cu[seq + 1] - t.first;
+          t.blk = KV ? (t.len + kAttnRows - 1) / kAttnRows - cost : cost - 1;
+          t.own = t.first + kAttnRows * t.blk;
+          t.n = KV ? cost * (SPLIT ? a.group / a.splits : a.group) : cost;
+        }
+        if (lane == 0) {
+          s_item[s] = t;
+          mbar_arrive(&it_full[s]);
+        }
+        __syncwarp();
+        if (!t.valid) break;
+      }
+    } else if (warp == 3) {
+      if constexpr (KV) {
+        // ---- lse and delta of the streamed rows; a row behind the end gets p = 2^(x - inf) = 0
+        uint32_t it = 0;
+        BwdItem t;
+        while (next_item(t)) {
+          for (int i = 0; i < t.n; ++i, ++it) {
+            int head;
+            const int blk = block_of(t, i, head);
+            const uint32_t s = it % kStatStages;
+            float ls[4], de[4];
+  #pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = kAttnRows * blk + 32 * x + lane;
+              const bool in = r < t.len;
+              const int64_t at = (int64_t)head * a.T + t.first + r;
+              ls[x] = in ? -a.lse[at] * kLog2e : -INFINITY;
+              de[x] = in ? -a.delta[at] : 0.f;
+              if (ls[x] == INFINITY) ls[x] = -INFINITY;  // a row without keys
+            }
+            if (it >= kStatStages) wait(&st_empty[s], ((it / kStatStages) - 1) & 1);
+  #pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              s_stat[s][0][32 * x + lane] = ls[x];
+              s_stat[s][1][32 * x + lane] = de[x];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st_full[s]);
+          }
         }
       }
     }
-  }
   } else {
     regs_more<208>();
     // ---- P and dS, and the results
@@ -502,7 +510,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint4* out = KV ? (wg ? a.dk : a.dv) : a.dq;
       const int heads = KV ? a.n_kv : a.n_q, col0 = KV ? 0 : COLS * wg;
       const int row0 = t.own + 32 * qtr, rows = t.first + t.len - row0;
-      if constexpr (HD == 128) {
+      if constexpr (SPLIT) {  // sums over this part of the group, for the folding kernel
+        if (lane < rows) {
+          float4* dst = reinterpret_cast<float4*>(
+              a.part + (((2 * t.split + wg) * a.T + row0 + lane) * (int64_t)a.n_kv + t.head) * HD);
+#pragma unroll
+          for (int e = 0; e < COLS / 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      } else if constexpr (HD == 128) {
         uint4* dst = out + ((int64_t)(row0 + lane) * heads + t.head) * (HD / 8) + col0 / 8;
         if (lane < rows)
 #pragma unroll
@@ -589,12 +604,47 @@ __global__ void __launch_bounds__(256) qkvp_attention_delta_kernel(const AttnBwd
   }
 }
 
-const void* attention_bwd_kernel(int head_dim, bool kv) {
-  if (head_dim == 64)
-    return kv ? reinterpret_cast<const void*>(&qkvp_attention_bwd_kernel<64, true>)
-              : reinterpret_cast<const void*>(&qkvp_attention_bwd_kernel<64, false>);
-  return kv ? reinterpret_cast<const void*>(&qkvp_attention_bwd_kernel<128, true>)
-            : reinterpret_cast<const void*>(&qkvp_attention_bwd_kernel<128, false>);
+// dv and dk from the parts of each group's query heads, in their order. Rows of the
+// sequences only.
+__global__ void __launch_bounds__(256) qkvp_attention_fold_kernel(const AttnBwdArgs a, int row4) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int s_bad;
+  if (threadIdx.x == 0) s_bad = a.batch == 0;
+  __syncthreads();
+  for (int s = threadIdx.x; s < a.batch; s += 256)
+    if (a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T) s_bad = 1;
+  __syncthreads();
+  if (s_bad) return;
+  const int64_t first = (int64_t)a.cu[0] * row4, n = (int64_t)a.cu[a.batch] * row4 - first, all = a.T * row4;
+  const float4* part = reinterpret_cast<const float4*>(a.part);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * n; i += (int64_t)gridDim.x * 256) {
+    const bool dk = i >= n;
+    const int64_t at = first + (dk ? i - n : i);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < a.splits; ++k) {
+      const float4 x = part[(2 * k + dk) * all + at];
+      v.x += x.x;
+      v.y += x.y;
+      v.z += x.z;
+      v.w += x.w;
+    }
+    const float f = dk ? a.scale : 1.f;
+    reinterpret_cast<uint2*>(dk ? a.dk : a.dv)[at] = make_uint2(pack2(v.x * f, v.y * f), pack2(v.z * f, v.w * f));
+  }
+}
+
+const void* attention_fold_kernel() { return reinterpret_cast<const void*>(&qkvp_attention_fold_kernel); }
+
+template <int HD>
+static const void* bwd_kernel(bool kv, bool split) {
+  if (!kv) return reinterpret_cast<const void*>(&qkvp_attention_bwd_kernel<HD, false, false>);
+  return split ? reinterpret_cast<const void*>(&qkvp_attention_bwd_kernel<HD, true, true>)
+               : reinterpret_cast<const void*>(&qkvp_attention_bwd_kernel<HD, true, false>);
+}
+const void* attention_bwd_kernel(int head_dim, bool kv, bool split) {
+  return head_dim == 64 ? bwd_kernel<64>(kv, split) : bwd_kernel<128>(kv, split);
 }
 const void* attention_delta_kernel(int head_dim) {
   return head_dim == 64 ? reinterpret_cast<const void*>(&qkvp_attention_delta_kernel<64>)

@@ -378,6 +378,8 @@ struct AttnBwdArgs {
   const uint4* dout;
   const float* lse;        // [n_q, T]
   float* delta;            // [n_q, T]: workspace
+  int32_t splits;          // parts of a group's query heads (a divisor of group), each its own CTAs
+  float* part;             // splits > 1: [splits][dv, dk][T, n_kv, head_dim], workspace
   int32_t zero_rest;
   uint4* dq;
   uint4* dk;
@@ -385,8 +387,9 @@ struct AttnBwdArgs {
   int32_t* dev_status;
   int* err;
 };
-const void* attention_bwd_kernel(int head_dim, bool kv);
+const void* attention_bwd_kernel(int head_dim, bool kv, bool split);
 const void* attention_delta_kernel(int head_dim);
+const void* attention_fold_kernel();
 int attention_bwd_smem_bytes(int head_dim);
 int attention_bwd_threads();
 

@@ -339,11 +339,17 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
     return (out, lse) if save_lse else out
 
 
+@functools.lru_cache(maxsize=1024)
+def attention_backward_workspace_bytes(n_q, n_kv, head_dim, T, batch):
+    """Workspace bytes attention_backward needs for T rows in `batch` sequences."""
+    return C.qkv_attention_bwd_workspace(_heads(n_q, n_kv, head_dim), T, batch)
+
+
 def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspace=None, dev_status=None, stream=None):
     """Gradients (dq, dk, dv) of attention_forward(q, k, v, cu_seqlens, scale) for
     the upstream gradient dout [T, n_q, D] bf16, from the forward's out and lse.
-    Rows of no sequence get zero gradients. `workspace` (a device tensor of at
-    least 4 * n_q * T bytes) is allocated here when not given."""
+    Rows of no sequence get zero gradients. `workspace` (a device tensor of
+    attention_backward_workspace_bytes bytes) is allocated here when not given."""
     _check_qkv(q, k, v)
     dev = q.device
     T, n_q, D = q.shape
@@ -357,7 +363,8 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspac
         return dq, dk, dv
     made = None
     if workspace is None:
-        workspace = made = torch.empty(max(n_q * T, 4), dtype=torch.float32, device=dev)
+        need = attention_backward_workspace_bytes(n_q, k.shape[1], D, T, batch)
+        workspace = made = torch.empty(need, dtype=torch.uint8, device=dev)
     C.qkv_attention_bwd(_heads(n_q, k.shape[1], D), T, batch, cu_seqlens, dout, q, k, v, out, lse,
                         0.0 if scale is None else scale, C.QKVP_ZERO_REST, dq, dk, dv, dev_status, workspace,
                         workspace.numel() * workspace.element_size(), _launch_stream(stream, dev, dq, dk, dv, made))

@@ -119,9 +119,13 @@ def test_forward_refusals(lib):
 def test_backward_refusals(lib):
     C = lib
     L = C.layout("sectioned", 8, 2, 64)
-    need = C.qkv_attention_bwd_workspace(L, 4)
-    assert need == 4 * 8 * 4 and C.qkv_attention_bwd_workspace(L, 0) == 0
-    assert C.qkv_attention_bwd_workspace(L, -1, check=False) == C.QKVP_ERR_SHAPE
+    # delta [n_q, T], and the sums of the group's four heads apart: [4, dv and dk, T, n_kv, D]
+    need = C.qkv_attention_bwd_workspace(L, 4, 1)
+    assert need == 4 * (8 * 4 + 4 * 2 * 4 * 2 * 64) and C.qkv_attention_bwd_workspace(L, 0, 1) == 0
+    assert C.qkv_attention_bwd_workspace(C.layout("sectioned", 32, 8, 128), 8192, 1) == 4 * 32 * 8192  # one part
+    assert C.qkv_attention_bwd_workspace(C.layout("sectioned", 5, 5, 128), 100, 3) == 4 * 5 * 100  # no group to divide
+    assert C.qkv_attention_bwd_workspace(L, -1, 1, check=False) == C.QKVP_ERR_SHAPE
+    assert C.qkv_attention_bwd_workspace(L, 4, -1, check=False) == C.QKVP_ERR_SHAPE
 
     def bwd(**kw):
         a = dict(L=L, T=4, batch=1, cu=P, do=P, q=P, k=P, v=P, out=P, lse=P, scale=0.0, flags=0, dq=P, dk=P, dv=P,

@@ -370,3 +370,28 @@ def test_many_steps_of_ragged_sequences(lib, cuda, n_q, n_kv, D):
         last = step()
     assert all(torch.equal(a, b) for a, b in zip(first, last))
     no_error(lib)
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(6, 2, 64), (7, 1, 128), (8, 1, 64), (5, 5, 128)])
+@pytest.mark.parametrize("lengths,before,after", [([1], 0, 0), ([300], 2, 5), ([0, 129, 1, 0, 257], 0, 40)])
+def test_heads_of_a_group_in_parts(lib, cuda, lengths, before, after, n_q, n_kv, D):
+    # small problems divide a group's query heads among CTAs, whose sums lie in the
+    # workspace: the same bits again from one full of NaN
+    F = lib.functional
+    cu = offsets(lengths, before)
+    T = int(cu[-1]) + after
+    need = F.attention_backward_workspace_bytes(n_q, n_kv, D, T, len(lengths))
+    assert (need > 4 * (n_q * T + 3)) == (n_q != n_kv)
+    q, k, v, do = inputs(T, n_q, n_kv, D, 700 + T)
+    dev = [t.to(cuda) for t in (q, k, v, do)]
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    out, lse = F.attention_forward(*dev[:3], cu_dev, save_lse=True)
+    grads = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev)
+    room = torch.full((need,), 255, dtype=torch.uint8, device=cuda)
+    again = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev, workspace=room)
+    no_error(lib)
+    fwd = A.attention_fwd(f64(q), f64(k), f64(v), cu)
+    ref = A.attention_bwd(f64(do), f64(q), f64(k), f64(v), cu, out_err=out_bound(fwd))
+    for name, got, other in zip(("dq", "dk", "dv"), grads, again):
+        assert torch.equal(got, other)
+        assert_within(f64(got), ref[name], ref["e_" + name] + U * np.abs(ref[name]), name)
