@@ -460,6 +460,7 @@ QKVP_API int qkv_newton_schulz_plan(const qkvp_layout* layout, int64_t count, in
  * lse         float32 [n_q, T] or NULL: log sum_j exp(scale q_i . k_j), which
  *             the backward needs. Rows of no sequence: as out (-inf for zero).
  * dev_status  int32 or NULL, bits OR-ed in.
+ * out and lse overlap none of q, k, v and each other (QKVP_ERR_VALUE).
  * A NaN or infinity in a row of k or v reaches the rows that attend it, and may
  * reach the other rows of its sequence in the same block of 128.
  * ------------------------------------------------------------------------- */
@@ -484,8 +485,10 @@ QKVP_API int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t bat
  *             instead of being left as they are.
  * dq          bf16 [T, n_q, head_dim] out; dk, dv bf16 [T, n_kv, head_dim] out.
  * workspace   at least qkv_attention_bwd_workspace() bytes for the same T and
- *             batch, 16-byte aligned, any contents. Two calls whose work can overlap on
- *             the GPU must not share a workspace.
+ *             batch, 16-byte aligned, any contents. Two calls whose work can
+ *             overlap on the GPU must not share a workspace.
+ * dq, dk, dv and the workspace overlap no input and not each other
+ * (QKVP_ERR_VALUE).
  * ------------------------------------------------------------------------- */
 QKVP_API int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const int32_t* cu_seqlens,
                                const void* dout, const void* q, const void* k, const void* v, const void* out,
@@ -531,6 +534,8 @@ QKVP_API int qkv_attention_bwd_workspace(const qkvp_layout* layout, int64_t T, i
  * workspace    at least qkv_attention_decode_workspace() bytes, 16-byte
  *              aligned, any contents. Two calls whose work can overlap on the
  *              GPU must not share a workspace.
+ * out, lse and the workspace overlap none of q, the pools and each other
+ * (QKVP_ERR_VALUE).
  * ------------------------------------------------------------------------- */
 QKVP_API int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q, const void* k_pool,
                                   const void* v_pool, int32_t num_pages, int32_t page_size, const int32_t* page_table,

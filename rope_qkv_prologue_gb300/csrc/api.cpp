@@ -629,6 +629,21 @@ bool overlaps(const void* p, size_t pn, const void* q, size_t qn) {
   return a < b + qn && b < a + pn;
 }
 
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+// True where a span that a call writes overlaps another of them, or one that it reads.
+bool written_overlaps(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* o = w + 1; o != written.end(); ++o)
+      if (overlaps(w->p, w->bytes, o->p, o->bytes)) return true;
+    for (const Span& r : read)
+      if (overlaps(w->p, w->bytes, r.p, r.bytes)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace qkvp
 
@@ -1314,6 +1329,10 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   for (const void* p : {q, k, v})  // tensor maps cover this GPU's own memory
     if (!on_current_device(p)) return QKVP_ERR_VALUE;
   const int hd = layout->head_dim;
+  const size_t q_bytes = (size_t)T * layout->n_q * hd * 2, k_bytes = (size_t)T * layout->n_kv * hd * 2;
+  const size_t lse_bytes = lse ? (size_t)T * layout->n_q * sizeof(float) : 0;
+  if (written_overlaps({{out, q_bytes}, {lse, lse_bytes}}, {{q, q_bytes}, {k, k_bytes}, {v, k_bytes}}))
+    return QKVP_ERR_VALUE;
   CUtensorMap tq, tk, tv;
   if (!bf16_tile_map(&tq, q, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
       !bf16_tile_map(&tk, k, T, (int64_t)layout->n_kv * hd, kAttnBlock) ||
@@ -1397,6 +1416,11 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   for (const void* p : {dout, q, k, v})  // tensor maps cover this GPU's own memory
     if (!on_current_device(p)) return QKVP_ERR_VALUE;
   const int hd = layout->head_dim;
+  const size_t q_bytes = (size_t)T * layout->n_q * hd * 2, k_bytes = (size_t)T * layout->n_kv * hd * 2;
+  if (written_overlaps({{dq, q_bytes}, {dk, k_bytes}, {dv, k_bytes}, {workspace, need}},
+                       {{dout, q_bytes}, {q, q_bytes}, {k, k_bytes}, {v, k_bytes}, {out, q_bytes},
+                        {lse, (size_t)T * layout->n_q * sizeof(float)}}))
+    return QKVP_ERR_VALUE;
   CUtensorMap tq, td, tk, tv;
   if (!bf16_tile_map(&tq, q, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
       !bf16_tile_map(&td, dout, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
@@ -1476,10 +1500,17 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
   plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, &p);
-  if (!workspace || workspace_bytes < decode_workspace(layout, batch, p)) return QKVP_ERR_WORKSPACE;
+  const size_t need = decode_workspace(layout, batch, p);
+  if (!workspace || workspace_bytes < need) return QKVP_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int hd = layout->head_dim;
+  const size_t q_bytes = (size_t)batch * layout->n_q * hd * 2;
+  const size_t pool_bytes = (size_t)num_pages * page_size * layout->n_kv * hd * 2;
+  const size_t lse_bytes = lse ? (size_t)batch * layout->n_q * sizeof(float) : 0;
+  if (written_overlaps({{out, q_bytes}, {lse, lse_bytes}, {workspace, need}},
+                       {{q, q_bytes}, {k_pool, pool_bytes}, {v_pool, pool_bytes}}))
+    return QKVP_ERR_VALUE;
   float* part_o = static_cast<float*>(workspace);
   float2* part_ml = reinterpret_cast<float2*>(part_o + p.rows * layout->n_q * hd);
   const int group = layout->n_q / layout->n_kv;

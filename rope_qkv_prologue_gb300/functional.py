@@ -254,7 +254,7 @@ def mla_kv_path_beside(side, pos, w, page, offset, pool, kv_rows=None, kv_proj=N
     return on_side_stream(side, kv_path)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)
 def _heads(n_q, n_kv, head_dim):
     """The layout struct of these heads (the library only reads it)."""
     return C.layout("sectioned", n_q, n_kv, head_dim)
@@ -265,20 +265,29 @@ def _decode_workspace(n_q, n_kv, head_dim, batch, page_size, max_pages, prefix_l
     return C.qkv_attention_decode_workspace(_heads(n_q, n_kv, head_dim), batch, page_size, max_pages, prefix_len)
 
 
-def _launch_stream(stream, device, *made):
-    """The raw handle of `stream` (default: the current one of `device`). Tensors
-    made for a call on a stream given must outlive its work there, whatever the
-    current stream does with their memory."""
+def _current_stream(device):
+    """The raw handle of the current stream of `device`, the current device."""
     if device.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {device}, which is not the current device")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on_stream(stream, like, call, *args):
+    """call(*args) with `stream` (a torch.cuda.Stream or a raw handle) as the current
+    one: what it allocates is then that stream's memory, in its order. The results may
+    be used on the caller's stream (after it waited), so their memory is kept for it too."""
+    if not like.is_cuda:
+        raise ValueError("the tensors must live on a CUDA device")
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device)
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+        stream = torch.cuda.ExternalStream(stream, like.device)
+    if stream.device != like.device:
+        raise ValueError(f"the tensors are on {like.device}, the stream is of {stream.device}")
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    home = torch.cuda.current_stream(like.device)
+    for t in got if isinstance(got, tuple) else (got,):
+        t.record_stream(home)
+    return got
 
 
 def _check_qkv(q, k, v):
@@ -303,6 +312,11 @@ def _check_offsets(cu_seqlens, device):
     return cu_seqlens.shape[0] - 1
 
 
+def _check_workspace(workspace, device):
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+
+
 def _check_status(dev_status, device):
     if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.numel() < 1
                                    or dev_status.device != device):
@@ -315,15 +329,18 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
     device (sequence s is the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1).
     Returns out [T, n_q, D], or (out, lse [n_q, T] float32) with save_lse.
     scale defaults to D ** -0.5. Rows of no sequence are zero in an out made
-    here, and left as they are in one given (lse: -inf, in both)."""
+    here, and left as they are in one given (lse: -inf, in both). The work is
+    queued on `stream` (default: the current one)."""
+    if stream is not None:
+        return _on_stream(stream, q, attention_forward, q, k, v, cu_seqlens, scale, save_lse, out, dev_status)
     _check_qkv(q, k, v)
     dev = q.device
     batch = _check_offsets(cu_seqlens, dev)
     _check_status(dev_status, dev)
     T, n_q, D = q.shape
-    flags, made = 0, None
+    flags = 0
     if out is None:
-        out = made = torch.empty_like(q)
+        out = torch.empty_like(q)
         flags = C.QKVP_ZERO_REST
     else:
         _check_like(out, q.shape, torch.bfloat16, dev, "out")
@@ -335,7 +352,7 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
     if T == 0:  # an empty tensor has no address to pass
         return (out, lse) if save_lse else out
     C.qkv_attention_fwd(_heads(n_q, k.shape[1], D), T, batch, cu_seqlens, q, k, v, 0.0 if scale is None else scale,
-                        flags, out, lse, dev_status, _launch_stream(stream, dev, made, lse))
+                        flags, out, lse, dev_status, _current_stream(dev))
     return (out, lse) if save_lse else out
 
 
@@ -349,7 +366,11 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspac
     """Gradients (dq, dk, dv) of attention_forward(q, k, v, cu_seqlens, scale) for
     the upstream gradient dout [T, n_q, D] bf16, from the forward's out and lse.
     Rows of no sequence get zero gradients. `workspace` (a device tensor of
-    attention_backward_workspace_bytes bytes) is allocated here when not given."""
+    attention_backward_workspace_bytes bytes) is allocated here when not given.
+    The work is queued on `stream` (default: the current one)."""
+    if stream is not None:
+        return _on_stream(stream, q, attention_backward, dout, q, k, v, out, lse, cu_seqlens, scale, workspace,
+                          dev_status)
     _check_qkv(q, k, v)
     dev = q.device
     T, n_q, D = q.shape
@@ -361,20 +382,23 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspac
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if T == 0:
         return dq, dk, dv
-    made = None
     if workspace is None:
         need = attention_backward_workspace_bytes(n_q, k.shape[1], D, T, batch)
-        workspace = made = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check_workspace(workspace, dev)
     C.qkv_attention_bwd(_heads(n_q, k.shape[1], D), T, batch, cu_seqlens, dout, q, k, v, out, lse,
                         0.0 if scale is None else scale, C.QKVP_ZERO_REST, dq, dk, dv, dev_status, workspace,
-                        workspace.numel() * workspace.element_size(), _launch_stream(stream, dev, dq, dk, dv, made))
+                        workspace.numel() * workspace.element_size(), _current_stream(dev))
     return dq, dk, dv
 
 
 class PackedAttention(torch.autograd.Function):
     """apply(q, k, v, cu_seqlens, scale=None) -> out: causal attention over packed
     sequences with its gradients, the step after QKVPrologue.apply. The offsets
-    receive no gradient."""
+    receive no gradient, and the gradients have none of their own. In a CUDA graph,
+    capture the forward and its backward together, and let no eager autograd graph
+    of the same leaves be alive then: their accumulation would wait for the stream
+    of that graph, which a capture does not allow."""
 
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, scale=None):
@@ -384,6 +408,7 @@ class PackedAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
         dq, dk, dv = attention_backward(dout.contiguous(), q, k, v, out, lse, cu_seqlens, ctx.scale)
@@ -412,7 +437,11 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
     them in every sequence: stored once, and read once for the whole batch.
     Returns out [B, n_q, D], or (out, lse [B, n_q] float32) with save_lse.
     `workspace` (a device tensor of attention_decode_workspace_bytes bytes) is
-    allocated here when not given."""
+    allocated here when not given. The work is queued on `stream` (default: the
+    current one)."""
+    if stream is not None:
+        return _on_stream(stream, q, attention_decode, q, k_pool, v_pool, page_table, lengths, prefix_pages,
+                          prefix_len, scale, save_lse, out, workspace, dev_status)
     for t, n in ((q, 3), (k_pool, 4), (v_pool, 4)):
         if t.dtype != torch.bfloat16 or t.dim() != n or not t.is_contiguous():
             raise ValueError("q must be a contiguous bf16 [B, n_q, D] and the pools contiguous bf16 "
@@ -437,9 +466,9 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
             raise ValueError("prefix_pages must hold prefix_len tokens")
     else:
         prefix_pages = None
-    made_out = made_ws = lse = None
+    lse = None
     if out is None:
-        out = made_out = torch.empty_like(q)
+        out = torch.empty_like(q)
     else:
         _check_like(out, q.shape, torch.bfloat16, dev, "out")
     if save_lse:
@@ -448,12 +477,12 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
         return (out, lse) if save_lse else out
     if workspace is None:
         need = _decode_workspace(n_q, n_kv, D, B, page_size, max_pages, prefix_len, dev.index)
-        workspace = made_ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _check_workspace(workspace, dev)
     C.qkv_attention_decode(_heads(n_q, n_kv, D), B, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages,
                            page_table.stride(0) if B > 1 else max_pages, lengths, prefix_pages, prefix_len,
                            0.0 if scale is None else scale, out, lse, dev_status, workspace,
-                           workspace.numel() * workspace.element_size(),
-                           _launch_stream(stream, dev, made_out, lse, made_ws))
+                           workspace.numel() * workspace.element_size(), _current_stream(dev))
     return (out, lse) if save_lse else out
 
 

@@ -395,3 +395,119 @@ def test_heads_of_a_group_in_parts(lib, cuda, lengths, before, after, n_q, n_kv,
     for name, got, other in zip(("dq", "dk", "dv"), grads, again):
         assert torch.equal(got, other)
         assert_within(f64(got), ref[name], ref["e_" + name] + U * np.abs(ref[name]), name)
+
+
+def test_rows_beyond_32_bit_offsets(lib, cuda):
+    # the last sequence of tensors of more than 2^31 values
+    F = lib.functional
+    n_q, n_kv, D, before = 128, 1, 128, 2 ** 17
+    T = before + 100
+    host = inputs(100, n_q, n_kv, D, 800)
+    dev = [torch.zeros(T, t.shape[1], D, dtype=torch.bfloat16, device=cuda) for t in host]
+    for t, last in zip(dev, host):
+        t[before:] = last.to(cuda)
+    cu_dev = torch.tensor([before - 300, before - 1, before, T], dtype=torch.int32, device=cuda)
+    out, lse = F.attention_forward(*dev[:3], cu_dev, save_lse=True)
+    grads = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev)
+    no_error(lib)
+    cu = offsets([100])
+    x = [f64(t) for t in host]
+    ref = A.attention_fwd(*x[:3], cu)
+    assert_within(f64(out[before:]), ref["out"], out_bound(ref), "out")
+    assert_lse(lse[:, before:].cpu().numpy(), ref, 100, D, "lse")
+    g = A.attention_bwd(x[3], *x[:3], cu, out_err=out_bound(ref))
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        assert_within(f64(got[before:]), g[name], g["e_" + name] + U * np.abs(g[name]), name)
+        assert not got[:before].any()
+    assert not out[:before].any()
+
+
+def test_refusals_of_what_overlaps_or_lies_elsewhere(lib, cuda):
+    F = lib.functional
+    q, k, v, do = (t.to(cuda) for t in inputs(60, 2, 2, 64, 18))
+    cu_dev = torch.tensor([0, 60], dtype=torch.int32, device=cuda)
+    out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True)
+    for bad in (q, k, v):
+        with pytest.raises(lib.QkvpError):
+            F.attention_forward(q, k, v, cu_dev, out=bad)
+    need = F.attention_backward_workspace_bytes(2, 2, 64, 60, 1)
+    room = torch.zeros(need, dtype=torch.uint8, device=cuda)
+    for bad in (room.cpu(), torch.zeros(2 * need, dtype=torch.uint8, device=cuda)[::2]):
+        with pytest.raises(ValueError):
+            F.attention_backward(do, q, k, v, out, lse, cu_dev, workspace=bad)
+    for bad in (room[:need - 16], lse, do):  # too small, or an input
+        with pytest.raises(lib.QkvpError):
+            F.attention_backward(do, q, k, v, out, lse, cu_dev, workspace=bad)
+    with pytest.raises(ValueError):
+        F.attention_forward(q, k, v, cu_dev, dev_status=torch.zeros(1, dtype=torch.int32))
+    L = lib.layout("sectioned", 2, 2, 64)
+    grads = [torch.empty_like(q) for _ in range(3)]
+
+    def raw(dq, dk, dv):
+        return lib.qkv_attention_bwd(L, 60, 1, cu_dev, do, q, k, v, out, lse, 0.0, 0, dq, dk, dv, None, room, need,
+                                     check=False)
+
+    assert raw(*grads) == lib.QKVP_OK
+    for bad in ((grads[0], grads[0], grads[2]), (q, *grads[1:]), (grads[0], k, grads[2]), (*grads[:2], out)):
+        assert raw(*bad) == lib.QKVP_ERR_VALUE
+    no_error(lib)
+
+
+def test_two_calls_at_once(lib, cuda):
+    # on two streams, each result its own; the caller's stream is busy meanwhile
+    F = lib.functional
+    cu_dev = torch.tensor([3, 500, 900], dtype=torch.int32, device=cuda)
+    sets = [[t.to(cuda) for t in inputs(950, 8, 2, 64, 900 + i)] for i in range(2)]
+
+    def step(q, k, v, do, stream=None):
+        mine = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True, out=mine, stream=stream)
+        return (out, lse, *F.attention_backward(do, q, k, v, out, lse, cu_dev, stream=stream))
+
+    want = [step(*s) for s in sets]
+    mine = [torch.zeros_like(s[0]) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    busy = torch.randn(8192, 8192, device=cuda)
+    for _ in range(3):
+        busy = busy @ busy * 1e-4
+    got = []
+    for (q, k, v, do), s, o in zip(sets, streams, mine):
+        out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True, out=o, stream=s)
+        got.append((out, lse, *F.attention_backward(do, q, k, v, out, lse, cu_dev, stream=s)))
+    for s in streams:
+        s.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    no_error(lib)
+
+
+def test_autograd_in_a_graph_and_twice(lib, cuda):
+    F = lib.functional
+    q, k, v, do = (t.to(cuda) for t in inputs(200, 4, 2, 128, 19))
+    cu_dev = torch.tensor([0, 150, 200], dtype=torch.int32, device=cuda)
+
+    def step():
+        x = [t.detach().requires_grad_() for t in (q, k, v)]
+        return torch.autograd.grad(F.PackedAttention.apply(*x, cu_dev), x, do)
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for t in got:
+        t.fill_(float("nan"))
+    g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # gradients of the gradients are refused, not silently zero
+    x = q.clone().requires_grad_()
+    first, = torch.autograd.grad(F.PackedAttention.apply(x, k, v, cu_dev), x, do, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(first.float().square().sum(), x)
+    no_error(lib)

@@ -243,3 +243,46 @@ def test_pool_write_then_decode_is_the_prompt(lib, cuda):
     assert_within(f64(one)[0], ref["out"][-1], out_bound(ref)[-1], "decode")
     torch.cuda.synchronize()
     assert lib.qkv_prologue_device_error(clear=True) == 0
+
+
+def test_pages_named_twice(lib, cuda):
+    # two sequences with the same pages, a page twice in one sequence, and the
+    # prefix's first page among the own ones
+    w = Batch(8, 2, 64, 16, [48, 48, 20], 144, 41)
+    w.table[1, :3] = w.table[0, :3]
+    w.table[2, 0], w.table[2, 1] = w.prefix_pages[0], w.prefix_pages[0]
+    for b, pages in ((1, w.table[1, :3]), (2, w.table[2, :2])):
+        n = int(w.lengths[b])
+        for kept, pool in ((w.keys, w.k_pool), (w.values, w.v_pool)):
+            own = f64(pool[pages.long()].reshape(-1, *pool.shape[2:])[:n].contiguous())
+            kept[b] = np.concatenate([kept[b][:144], own])
+    w.check(lib, *w.run(lib, cuda, save_lse=True))
+
+
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_two_calls_at_once_and_refusals(lib, cuda, prefix):
+    F = lib.functional
+    sets = [Batch(8, 2, 64, 16, [700, 30, 0, 5], prefix, 50 + i) for i in range(2)]
+    want = [w.run(lib, cuda, save_lse=True) for w in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    dev = [[t.to(cuda) for t in (w.q, w.k_pool, w.v_pool, w.table, w.lengths, w.prefix_pages)] for w in sets]
+    torch.cuda.synchronize()
+    busy = torch.randn(8192, 8192, device=cuda)
+    for _ in range(3):
+        busy = busy @ busy * 1e-4
+    got = [[F.attention_decode(*x, prefix, save_lse=True, stream=s) for _ in range(4)] for x, s in zip(dev, streams)]
+    for s in streams:
+        s.synchronize()
+    for each, ref in zip(got, want):
+        assert all(torch.equal(a, b) for one in each for a, b in zip(one, ref))
+    x = dev[0]
+    need = F.attention_decode_workspace_bytes(8, 2, 64, 4, 16, x[3].shape[1], prefix)
+    for bad in (torch.zeros(need, dtype=torch.uint8), torch.zeros(2 * need, dtype=torch.uint8, device=cuda)[::2]):
+        with pytest.raises(ValueError):
+            F.attention_decode(*x, prefix, workspace=bad)
+    with pytest.raises(lib.QkvpError):
+        F.attention_decode(*x, prefix, out=x[0])
+    with pytest.raises(lib.QkvpError):
+        F.attention_decode(*x, prefix, out=x[1].flatten()[:x[0].numel()].view(x[0].shape))
+    torch.cuda.synchronize()
+    assert lib.qkv_prologue_device_error(clear=True) == 0
