@@ -1453,7 +1453,6 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   const void* kkv = attention_bwd_kernel(hd, true, a.splits > 1);
   const void* kq = attention_bwd_kernel(hd, false, false);
   if (!allow_smem(kkv, smem) || !allow_smem(kq, smem)) return QKVP_ERR_LAUNCH;
-  QKVP_TRY(launch(attention_delta_kernel(hd), std::min<int64_t>((T + 7) / 8, 8 * (int64_t)sms), 256, 0, st, &a));
   void* args[] = {&tq, &td, &tk, &tv, &a};
   QKVP_TRY(launch_args(kq, std::min<int64_t>(blocks * a.n_q, sms), attention_bwd_threads(), smem, st, args));
   QKVP_TRY(launch_args(kkv, std::min<int64_t>(blocks * a.n_kv * a.splits, sms), attention_bwd_threads(), smem, st, args));

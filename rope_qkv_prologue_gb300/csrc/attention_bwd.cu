@@ -4,11 +4,12 @@
 // With p_ij = e^(s_ij - lse_i), delta_i = dout_i . out_i, dp_ij = dout_i . v_j and
 // ds_ij = p_ij (dp_ij - delta_i):
 //     dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j,
-// dk and dv summed over the query heads of the group too. Three kernels:
-//   1. qkvp_attention_delta_kernel: delta, one pass over dout and out;
-//   2. the query kernel: a CTA owns 128 queries of one head and goes through its
-//      keys, adding dS K (and writes the delta of rows with few keys anew);
-//   3. the key/value kernel: a CTA owns 128 keys of one key/value head and goes
+// dk and dv summed over the query heads of the group too. Two kernels:
+//   1. the query kernel: a CTA owns 128 queries of one head and goes through its
+//      keys, adding dS K. Its dout is in shared memory, so it also forms delta and
+//      leaves it for the other (against a kernel of its own for delta, 4096 tokens in
+//      11 sequences take the same time, 700 in 3 take 55 us instead of 65);
+//   2. the key/value kernel: a CTA owns 128 keys of one key/value head and goes
 //      through the query blocks and heads that attend them, forming the transposed
 //      S^T = K Q^T and dP^T = V dO^T and adding P^T dO and dS^T Q. Where that leaves
 //      SMs idle (few tokens, few key/value heads), a group's query heads are divided
@@ -27,7 +28,8 @@
 //               are summed over: 0 times whatever is there need not be 0);
 //   warp 1      issues the MMAs;
 //   warp 2      finds work items (AttnOrder), one ahead;
-//   warp 3      key/value kernel: lse and delta of the streamed rows;
+//   warp 3      key/value kernel: lse and delta of the streamed rows; query kernel:
+//               zeros in the rows of no sequence, where the caller asked for them;
 //   warps 4-11  the arithmetic between the products, and the results' stores.
 #include "attention.cuh"
 
@@ -37,7 +39,6 @@ namespace {
 constexpr int kBwdThreads = 384;
 constexpr int kBwdSched = 2;
 constexpr int kStatStages = 2;
-constexpr int kDeltaHeads = 256;  // heads of the delta kernel's shared buffer
 constexpr int kStageBytes = 32 * 64;  // a warp's store buffer: 32 rows x 32 bf16
 
 // Shared memory. The first streamed operand stays until the accumulating product of
@@ -357,6 +358,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (lane == 0) mbar_arrive(&st_full[s]);
           }
         }
+      } else if (a.zero_rest) {
+        bool none = a.batch == 0;
+        for (int s = lane; s < a.batch; s += 32) none |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T;
+        none = __any_sync(0xffffffffu, none);
+        const int64_t first = none ? 0 : a.cu[0], last = none ? 0 : a.cu[a.batch];
+        attn_zero_rows(a.dq, a.T, a.n_q * (HD / 8), first, last, lane);
+        attn_zero_rows(a.dk, a.T, a.n_kv * (HD / 8), first, last, lane);
+        attn_zero_rows(a.dv, a.T, a.n_kv * (HD / 8), first, last, lane);
       }
     }
   } else {
@@ -374,8 +383,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if constexpr (!KV) {
         const int64_t at = (int64_t)t.head * a.T + t.own + row;
         r_lse = in ? -a.lse[at] * kLog2e : -INFINITY;
-        r_delta = in && t.n > 1 ? -a.delta[at] : 0.f;
         if (r_lse == INFINITY) r_lse = -INFINITY;
+        if (t.n > 1) {  // delta = dout . out: half a row's columns each, dout from the CTA's own tile
+          constexpr int CH = HD / 16;
+          const uint4* src = a.out + ((int64_t)(t.own + row) * a.n_q + t.head) * (HD / 8) + CH * wg;
+          const unsigned char* tile = base + SM::kA + SM::kTile + (HD / 64 - 1) * wg * kAttnBox;
+          uint4 w[CH];
+#pragma unroll
+          for (int ch = 0; ch < CH; ++ch) w[ch] = in ? src[ch] : make_uint4(0, 0, 0, 0);
+          wait(&a_full, items & 1);
+          float s = 0.f;
+#pragma unroll
+          for (int ch = 0; ch < CH; ++ch) {
+            float x[8], y[8];
+            unpack8(w[ch], x);
+            unpack8(*reinterpret_cast<const uint4*>(tile + attn_swz(row, (HD == 64 ? CH * wg : 0) + ch)), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+          }
+          s_stat[wg][0][row] = s;
+          named_sync(1, 256);  // (nobody writes there again before every warp's dS of this item)
+          r_delta = -(s_stat[0][0][row] + s_stat[1][0][row]);
+          if (wg == 0 && in) a.delta[at] = -r_delta;
+        }
       }
       const uint64_t c2 = pair(c, c);
 #pragma unroll 1
@@ -459,7 +489,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             s_stat[wg][1][row] = s1;
             named_sync(1, 256);
             r_delta = -(s_stat[0][1][row] + s_stat[1][1][row]) / (s_stat[0][0][row] + s_stat[1][0][row]);
-            named_sync(1, 256);
             if (wg == 0 && in) a.delta[(int64_t)t.head * a.T + t.own + row] = -r_delta;
           }
         }
@@ -558,52 +587,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   attn_report(fail, a.err);
 }
 
-// delta[h, t] = dout[t, h] . out[t, h] in fp32, and (where asked for) zeros in the
-// gradients' rows of no sequence. Bound by reading dout and out once: a CTA takes
-// eight tokens, a warp one of them at a time, so that the reads are whole rows and
-// the writes whole sectors.
-template <int HD>
-__global__ void __launch_bounds__(256) qkvp_attention_delta_kernel(const AttnBwdArgs a) {
-  constexpr int L = HD / 8, RW = 32 / L;  // lanes per head, heads per warp and step
-  __shared__ float s_d[kDeltaHeads][9];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
-  griddep_launch_dependents();
-  for (int64_t t0 = 8 * (int64_t)blockIdx.x; t0 < a.T; t0 += 8 * (int64_t)gridDim.x)
-    for (int h0 = 0; h0 < a.n_q; h0 += kDeltaHeads) {
-      const int nh = min(kDeltaHeads, a.n_q - h0);
-      const int64_t t = t0 + warp;
-      if (t < a.T) {
-        const int64_t row = (t * a.n_q + h0) * L + lane;
-#pragma unroll 4
-        for (int h = 0; h < nh; h += RW) {
-          const bool in = h + lane / L < nh;
-          float x[8], y[8], s = 0.f;
-          unpack8(in ? a.out[row + h * L] : make_uint4(0, 0, 0, 0), x);
-          unpack8(in ? a.dout[row + h * L] : make_uint4(0, 0, 0, 0), y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
-#pragma unroll
-          for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (in && lane % L == 0) s_d[h + lane / L][warp] = s;
-        }
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < 8 * nh; i += 256)
-        if (t0 + (i & 7) < a.T) a.delta[(int64_t)(h0 + (i >> 3)) * a.T + t0 + (i & 7)] = s_d[i >> 3][i & 7];
-      __syncthreads();
-    }
-  if (a.zero_rest && warp == 0) {
-    bool bad = false;
-    for (int s = lane; s < a.batch; s += 32) bad |= a.cu[s] < 0 || a.cu[s + 1] < a.cu[s] || a.cu[s + 1] > a.T;
-    bad = __any_sync(0xffffffffu, bad) || a.batch == 0;
-    const int64_t first = bad ? 0 : a.cu[0], last = bad ? 0 : a.cu[a.batch];
-    attn_zero_rows(a.dq, a.T, a.n_q * L, first, last, lane);
-    attn_zero_rows(a.dk, a.T, a.n_kv * L, first, last, lane);
-    attn_zero_rows(a.dv, a.T, a.n_kv * L, first, last, lane);
-  }
-}
-
 // dv and dk from the parts of each group's query heads, in their order. Rows of the
 // sequences only.
 __global__ void __launch_bounds__(256) qkvp_attention_fold_kernel(const AttnBwdArgs a, int row4) {
@@ -645,10 +628,6 @@ static const void* bwd_kernel(bool kv, bool split) {
 }
 const void* attention_bwd_kernel(int head_dim, bool kv, bool split) {
   return head_dim == 64 ? bwd_kernel<64>(kv, split) : bwd_kernel<128>(kv, split);
-}
-const void* attention_delta_kernel(int head_dim) {
-  return head_dim == 64 ? reinterpret_cast<const void*>(&qkvp_attention_delta_kernel<64>)
-                        : reinterpret_cast<const void*>(&qkvp_attention_delta_kernel<128>);
 }
 int attention_bwd_smem_bytes(int head_dim) {
   return head_dim == 64 ? BwdSmem<64>::kBytes : BwdSmem<128>::kBytes;

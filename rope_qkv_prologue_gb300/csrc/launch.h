@@ -388,7 +388,6 @@ struct AttnBwdArgs {
   int* err;
 };
 const void* attention_bwd_kernel(int head_dim, bool kv, bool split);
-const void* attention_delta_kernel(int head_dim);
 const void* attention_fold_kernel();
 int attention_bwd_smem_bytes(int head_dim);
 int attention_bwd_threads();
