@@ -290,6 +290,7 @@ struct AttnOrder {
   __device__ __forceinline__ bool init(int64_t T, int lane) {
     bool bad = false;
     uint32_t sum = 0, top = 0;
+#pragma unroll 1  // (code size, here and below)
     for (int s = lane; s < batch; s += 32) {
       const int64_t a = cu[s], b = cu[s + 1];
       const bool ok = a >= 0 && b >= a && b <= T;
@@ -310,9 +311,11 @@ struct AttnOrder {
   __device__ __forceinline__ void find(uint32_t r, int lane, int& seq, int& cost) const {
     int lo = 0, hi = most;  // F(hi) <= r, and F(lo - 1) > r or lo == 0
     uint32_t f_hi = 0;
+#pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       uint32_t f = 0;
+#pragma unroll 1
       for (int s = lane; s < batch; s += 32) {
         const int n = blocks(s) - mid;
         f += n > 0 ? (uint32_t)n : 0u;
@@ -328,6 +331,7 @@ struct AttnOrder {
     cost = hi;
     uint32_t idx = r - f_hi;
     seq = 0;
+#pragma unroll 1
     for (int s0 = 0; s0 < batch; s0 += 32) {
       const int s = s0 + lane;
       const bool in = s < batch && blocks(s) >= cost;
@@ -351,8 +355,10 @@ __device__ __forceinline__ uint32_t attn_deal(uint32_t k, uint32_t b, uint32_t g
 // Rows of no sequence ([0, first) and [last, T)): `chunks` 16-byte pieces per row
 // set to zero, one warp of each CTA.
 __device__ __forceinline__ void attn_zero_rows(uint4* out, int64_t T, int chunks, int64_t first, int64_t last, int lane) {
+#pragma unroll 1
   for (int64_t r = blockIdx.x; r < first + T - last; r += gridDim.x) {
     uint4* row = out + (r < first ? r : last + (r - first)) * chunks;
+#pragma unroll 1
     for (int c = lane; c < chunks; c += 32) row[c] = make_uint4(0, 0, 0, 0);
   }
 }

@@ -365,7 +365,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int64_t first = none ? 0 : a.cu[0], last = none ? 0 : a.cu[a.batch];
         attn_zero_rows(a.out, a.T, a.n_q * (HD / 8), first, last, lane);
         if (a.lse)
+#pragma unroll 1
           for (int h = blockIdx.x; h < a.n_q; h += gridDim.x)
+#pragma unroll 1
             for (int64_t r = lane; r < first + a.T - last; r += 32)
               a.lse[h * a.T + (r < first ? r : last + (r - first))] = -INFINITY;
       }
