@@ -1333,8 +1333,9 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   const size_t lse_bytes = lse ? (size_t)T * layout->n_q * sizeof(float) : 0;
   if (written_overlaps({{out, q_bytes}, {lse, lse_bytes}}, {{q, q_bytes}, {k, k_bytes}, {v, k_bytes}}))
     return QKVP_ERR_VALUE;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, pq;
   if (!bf16_tile_map(&tq, q, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
+      !bf16_tile_map(&pq, q, T, (int64_t)layout->n_q * hd, 32) ||
       !bf16_tile_map(&tk, k, T, (int64_t)layout->n_kv * hd, kAttnBlock) ||
       !bf16_tile_map(&tv, v, T, (int64_t)layout->n_kv * hd, kAttnBlock))
     return QKVP_ERR_LAUNCH;
@@ -1348,6 +1349,7 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   a.cu = cu_seqlens;
   a.pair_heads = a.group % 2 == 0;
   a.units = a.pair_heads ? a.n_q / 2 : a.n_q;
+  a.small = a.group % 8 == 0 ? 2 : (a.group % 4 == 0 ? 1 : 0);
   a.zero_rest = (flags & QKVP_ZERO_REST) != 0;
   a.out = static_cast<uint4*>(out);
   a.lse = lse;
@@ -1358,7 +1360,7 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   const int64_t unit_rows = a.pair_heads ? kAttnBlock : 2 * kAttnBlock;
   const int64_t most = (T / unit_rows + std::max(batch, 1)) * a.units;  // at least the number of work items
   if (most > INT32_MAX / 2) return QKVP_ERR_SHAPE;
-  void* args[] = {&tq, &tk, &tv, &a};
+  void* args[] = {&tq, &tk, &tv, &pq, &a};
   return launch_args(kern, most < sms ? most : sms, attention_fwd_threads(), smem, static_cast<cudaStream_t>(stream),
                      args);
 }
@@ -1421,8 +1423,10 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
                        {{dout, q_bytes}, {q, q_bytes}, {k, k_bytes}, {v, k_bytes}, {out, q_bytes},
                         {lse, (size_t)T * layout->n_q * sizeof(float)}}))
     return QKVP_ERR_VALUE;
-  CUtensorMap tq, td, tk, tv;
-  if (!bf16_tile_map(&tq, q, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
+  CUtensorMap tq, td, tk, tv, pq, pd;
+  if (!bf16_tile_map(&pq, q, T, (int64_t)layout->n_q * hd, 32) ||
+      !bf16_tile_map(&pd, dout, T, (int64_t)layout->n_q * hd, 32) ||
+      !bf16_tile_map(&tq, q, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
       !bf16_tile_map(&td, dout, T, (int64_t)layout->n_q * hd, kAttnBlock) ||
       !bf16_tile_map(&tk, k, T, (int64_t)layout->n_kv * hd, kAttnBlock) ||
       !bf16_tile_map(&tv, v, T, (int64_t)layout->n_kv * hd, kAttnBlock))
@@ -1441,6 +1445,9 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   a.lse = lse;
   a.delta = static_cast<float*>(workspace);
   a.splits = attention_bwd_splits(layout, T, batch);
+  auto small = [](int heads) { return heads % 4 == 0 ? 2 : (heads % 2 == 0 ? 1 : 0); };
+  a.small_q = small(a.group);
+  a.small_kv = small(a.group / a.splits);
   a.part = a.delta + (((T * a.n_q) + 3) & ~(int64_t)3);
   a.zero_rest = (flags & QKVP_ZERO_REST) != 0;
   a.dq = static_cast<uint4*>(dq);
@@ -1453,7 +1460,7 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   const void* kkv = attention_bwd_kernel(hd, true, a.splits > 1);
   const void* kq = attention_bwd_kernel(hd, false, false);
   if (!allow_smem(kkv, smem) || !allow_smem(kq, smem)) return QKVP_ERR_LAUNCH;
-  void* args[] = {&tq, &td, &tk, &tv, &a};
+  void* args[] = {&tq, &td, &tk, &tv, &pq, &pd, &a};
   QKVP_TRY(launch_args(kq, std::min<int64_t>(blocks * a.n_q, sms), attention_bwd_threads(), smem, st, args));
   QKVP_TRY(launch_args(kkv, std::min<int64_t>(blocks * a.n_kv * a.splits, sms), attention_bwd_threads(), smem, st, args));
   if (a.splits == 1) return QKVP_OK;
@@ -1548,7 +1555,7 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
     const void* kern = attention_fwd_kernel(hd, true);
     const size_t smem = (size_t)attention_fwd_smem_bytes(hd, true);
     if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
-    void* args[] = {&tq, &tk, &tv, &f};
+    void* args[] = {&tq, &tk, &tv, &tq, &f};  // (no short sequences: the last map is not read)
     QKVP_TRY(launch_args(kern, (int64_t)p.chunks * p.pairs * layout->n_kv, attention_fwd_threads(), smem, st, args));
   }
   AttnDecodeArgs a;

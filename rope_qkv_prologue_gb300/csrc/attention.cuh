@@ -264,6 +264,23 @@ __device__ __forceinline__ void attn_mma_ts(uint32_t d, uint32_t w, int half, co
   }
 }
 
+// Whole warp, lanes taking copies in turn: a tile of 128 rows of q or dout. With hs = 2
+// it is 128 rows of one head (`map`); for short sequences it has four pieces of 32 rows
+// (`pieces`, a box of 32): with hs = 1 the 64 rows of two heads, with hs = 0 the 32 rows of
+// four; piece p is the rows 32 (p mod 2^hs) .. of head p / 2^hs, from (col, row) on.
+template <int HD>
+__device__ __forceinline__ void attn_load_tile(unsigned char* dst, const CUtensorMap* map, const CUtensorMap* pieces,
+                                               int col, int row, int hs, uint64_t* bar, int lane) {
+  constexpr int X = HD / 64;
+  const int x = lane % X, p = lane / X;
+  if (hs == 2) {
+    if (p == 0) tma_load_2d(dst + x * kAttnBox, map, col + 64 * x, row, bar);
+  } else if (p < 4) {
+    tma_load_2d(dst + x * kAttnBox + p * (kAttnBox / 4), pieces, col + (p >> hs) * HD + 64 * x,
+                row + 32 * (p & ((1 << hs) - 1)), bar);
+  }
+}
+
 // The blocks of packed sequences, taken from the most expensive to the
 // cheapest. Sequence s has n_s = ceil(len_s / unit) blocks, one of each cost
 // 1 .. n_s (with the causal mask the block at distance c from the sequence's
@@ -272,45 +289,90 @@ __device__ __forceinline__ void attn_mma_ts(uint32_t d, uint32_t w, int half, co
 // with F(c) <= r, and is the (r - F(c))-th sequence with n_s >= c. Evaluated by
 // one warp from the sequence offsets alone: no list in memory, no launch before
 // the kernel that uses it.
+//
+// Short sequences come last and are counted apart, since one work item holds
+// several heads of them: those of at most 64 rows (two heads to a tile of 128
+// rows), and of at most 32 (four), where the caller can place them (`small`: 0
+// none, 1 up to 64 rows, 2 both).
 struct AttnOrder {
   static constexpr int kCached = 128;  // sequences whose block counts are kept in shared memory
   const int32_t* cu;
   int batch;
   int unit;
+  int small;
   int* cache;      // [kCached]
   int most;        // largest n_s
   uint32_t total;  // sum of n_s
+  uint32_t n64, n32;
 
-  __device__ __forceinline__ int blocks(int s) const {
-    if (s < kCached) return cache[s];
-    return (int)(((int64_t)cu[s + 1] - cu[s] + unit - 1) / unit);
+  // n_s, or -1 (one of n64) or -2 (of n32)
+  __device__ __forceinline__ int count(int64_t rows) const {
+    if (small && rows <= 64 && rows > 0) return small == 2 && rows <= 32 ? -2 : -1;
+    return (int)((rows + unit - 1) / unit);
   }
+  __device__ __forceinline__ int blocks(int s) const { return s < kCached ? cache[s] : count((int64_t)cu[s + 1] - cu[s]); }
 
   // Whole warp. False (and no blocks) when the offsets do not ascend in [0, T].
   __device__ __forceinline__ bool init(int64_t T, int lane) {
     bool bad = false;
-    uint32_t sum = 0, top = 0;
+    uint32_t sum = 0, top = 0, a64 = 0, a32 = 0;
 #pragma unroll 1  // (code size, here and below)
     for (int s = lane; s < batch; s += 32) {
       const int64_t a = cu[s], b = cu[s + 1];
       const bool ok = a >= 0 && b >= a && b <= T;
       bad |= !ok;
-      const uint32_t n = ok ? (uint32_t)((b - a + unit - 1) / unit) : 0u;
-      if (s < kCached) cache[s] = (int)n;
-      sum += n;
-      top = n > top ? n : top;
+      const int n = ok ? count(b - a) : 0;
+      if (s < kCached) cache[s] = n;
+      a64 += n == -1;
+      a32 += n == -2;
+      sum += max(n, 0);
+      top = max((int)top, n);
     }
     bad = __any_sync(0xffffffffu, bad);
     total = bad ? 0u : __reduce_add_sync(0xffffffffu, sum);
+    n64 = bad ? 0u : __reduce_add_sync(0xffffffffu, a64);
+    n32 = bad ? 0u : __reduce_add_sync(0xffffffffu, a32);
     most = bad ? 0 : (int)__reduce_max_sync(0xffffffffu, top);
     __syncwarp();
     return !bad;
   }
 
-  // Whole warp: the sequence and cost of rank r < total.
-  __device__ __forceinline__ void find(uint32_t r, int lane, int& seq, int& cost) const {
-    int lo = 0, hi = most;  // F(hi) <= r, and F(lo - 1) > r or lo == 0
+  // Whole warp: the idx-th sequence whose blocks() lies in [lo, hi].
+  __device__ __forceinline__ int select(uint32_t idx, int lo, int hi, int lane) const {
+    int seq = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < batch; s0 += 32) {
+      const int s = s0 + lane, n = s < batch ? blocks(s) : 0;
+      const bool in = s < batch && n >= lo && n <= hi;
+      const uint32_t m = __ballot_sync(0xffffffffu, in), found = __popc(m);
+      if (idx < found) {
+        const bool it = in && __popc(m & ((1u << lane) - 1u)) == idx;
+        seq = s0 + __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+        break;
+      }
+      idx -= found;
+    }
+    return seq;
+  }
+
+  // Work items, with `units` heads (or pairs of heads) to every block; DIVIDE: those of
+  // short sequences hold several.
+  template <bool DIVIDE>
+  __device__ __forceinline__ uint32_t work(uint32_t units) const {
+    return total * units + n64 * (DIVIDE ? units / 2 : units) + n32 * (DIVIDE ? units / 4 : units);
+  }
+
+  // Whole warp: work item w < work(units) is unit `unit_of` of the block of cost `cost`
+  // of sequence `seq`; hs as in attn_load_tile.
+  template <bool DIVIDE>
+  __device__ __forceinline__ void find(uint32_t w, uint32_t units, int lane, int& seq, int& cost, int& unit_of,
+                                       int& hs) const {
+    const uint32_t w0 = total * units, w1 = w0 + n64 * (DIVIDE ? units / 2 : units);
+    hs = w < w0 ? 2 : (w < w1 ? 1 : 0);
+    const uint32_t at = w - (hs == 2 ? 0u : (hs == 1 ? w0 : w1)), per = DIVIDE ? units >> (2 - hs) : units, r = at / per;
+    unit_of = (int)(at - r * per);
     uint32_t f_hi = 0;
+    int lo = 0, hi = hs == 2 ? most : 0;  // F(hi) <= r, and F(lo - 1) > r or lo == 0
 #pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -328,21 +390,8 @@ struct AttnOrder {
         lo = mid + 1;
       }
     }
-    cost = hi;
-    uint32_t idx = r - f_hi;
-    seq = 0;
-#pragma unroll 1
-    for (int s0 = 0; s0 < batch; s0 += 32) {
-      const int s = s0 + lane;
-      const bool in = s < batch && blocks(s) >= cost;
-      const uint32_t m = __ballot_sync(0xffffffffu, in), n = __popc(m);
-      if (idx < n) {
-        const bool it = in && __popc(m & ((1u << lane) - 1u)) == idx;
-        seq = s0 + __ffs(__ballot_sync(0xffffffffu, it)) - 1;
-        break;
-      }
-      idx -= n;
-    }
+    cost = hs == 2 ? hi : 1;
+    seq = hs == 2 ? select(r - f_hi, cost, most, lane) : select(r, hs - 2, hs - 2, lane);
   }
 };
 

@@ -4,7 +4,9 @@
 // With p_ij = e^(s_ij - lse_i), delta_i = dout_i . out_i, dp_ij = dout_i . v_j and
 // ds_ij = p_ij (dp_ij - delta_i):
 //     dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j,
-// dk and dv summed over the query heads of the group too. Two kernels:
+// dk and dv summed over the query heads of the group too. Sequences of at most 64 (32)
+// rows have two (four) heads in a tile of 128 queries, where the group has them (25 tokens
+// in 19 sequences, 256 over 16 heads of 64, both directions: 183 -> 64 us). Two kernels:
 //   1. the query kernel: a CTA owns 128 queries of one head and goes through its
 //      keys, adding dS K. Its dout is in shared memory, so it also forms delta and
 //      leaves it for the other (against a kernel of its own for delta, 4096 tokens in
@@ -64,6 +66,7 @@ struct BwdItem {
   int len;    // its rows
   int blk;    // the own block's index in the sequence
   int head;   // key/value head, or query head
+  int hs;     // heads in a tile of queries, as in attn_load_tile
   int split;  // SPLIT: which of the group's parts of query heads
   int valid;
 };
@@ -76,7 +79,8 @@ template <int HD, bool KV, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     qkvp_attention_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
                               const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                              const AttnBwdArgs a) {
+                              const __grid_constant__ CUtensorMap pieces_q,
+                              const __grid_constant__ CUtensorMap pieces_do, const AttnBwdArgs a) {
   using SM = BwdSmem<HD>;
   constexpr int S1 = SM::kS1, S2 = SM::kS2;
   // Tensor memory. X has two buffers where there is room for them (not in the
@@ -162,8 +166,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // kernel) the query head.
   auto block_of = [&](const BwdItem& t, int i, int& head) {
     if constexpr (KV) {
-      const int heads = SPLIT ? a.group / a.splits : a.group, per = t.n / heads;
-      head = t.head * a.group + (SPLIT ? t.split * heads : 0) + i / per;
+      const int heads = SPLIT ? a.group / a.splits : a.group, tiles = heads >> (2 - t.hs), per = t.n / tiles;
+      head = t.head * a.group + (SPLIT ? t.split * heads : 0) + ((i / per) << (2 - t.hs));
       return t.blk + i % per;
     } else {
       head = t.head / a.group;
@@ -182,36 +186,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (t.n == 0) continue;
         if (items > 0) wait(&a_empty, (items - 1) & 1);
         ++items;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&a_full, 2 * SM::kTile);
-          for (int x = 0; x < HD / 64; ++x) {
-            tma_load_2d(base + SM::kA + x * kAttnBox, KV ? &tmap_k : &tmap_q, t.head * HD + 64 * x, t.own, &a_full);
-            tma_load_2d(base + SM::kA + SM::kTile + x * kAttnBox, KV ? &tmap_v : &tmap_do, t.head * HD + 64 * x, t.own,
-                        &a_full);
-          }
+        if (lane == 0) mbar_arrive_expect_tx(&a_full, 2 * SM::kTile);
+        __syncwarp();
+        if constexpr (!KV) {
+          attn_load_tile<HD>(base + SM::kA, &tmap_q, &pieces_q, t.head * HD, t.own, t.hs, &a_full, lane);
+          attn_load_tile<HD>(base + SM::kA + SM::kTile, &tmap_do, &pieces_do, t.head * HD, t.own, t.hs, &a_full, lane);
+        } else if (lane < HD / 64) {
+          tma_load_2d(base + SM::kA + lane * kAttnBox, &tmap_k, t.head * HD + 64 * lane, t.own, &a_full);
+          tma_load_2d(base + SM::kA + SM::kTile + lane * kAttnBox, &tmap_v, t.head * HD + 64 * lane, t.own, &a_full);
         }
         for (int i = 0; i < t.n; ++i, ++it) {
           int head;
           const int blk = block_of(t, i, head);
           const int rows = t.len - kAttnRows * blk;  // of the sequence in this block
-  #pragma unroll
+#pragma unroll
           for (int which = 0; which < 2; ++which) {
             const uint32_t n = which ? S2 : S1, s = it % n;
             uint64_t* full = which ? &b2_full[s] : &b1_full[s];
             wait(which ? &b2_empty[s] : &b1_empty[s], ((it / n) & 1) ^ 1);  // (the first time round it passes)
             unsigned char* dst = base + (which ? SM::kB2 : SM::kB1) + s * SM::kTile;
             const CUtensorMap* map = KV ? (which ? &tmap_do : &tmap_q) : (which ? &tmap_v : &tmap_k);
-            const bool patch = rows < kAttnRows && (KV || which == 0);
+            const int piece = KV ? 32 << t.hs : kAttnRows;  // rows of a head in the tile
+            const bool patch = rows < piece && (KV || which == 0);
             uint64_t* bar = patch ? &tail_bar : full;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(bar, SM::kTile);
-              for (int x = 0; x < HD / 64; ++x)
-                tma_load_2d(dst + x * kAttnBox, map, head * HD + 64 * x, t.first + kAttnRows * blk, bar);
-            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, SM::kTile);
+            __syncwarp();
+            if constexpr (KV)
+              attn_load_tile<HD>(dst, map, which ? &pieces_do : &pieces_q, head * HD, t.first + kAttnRows * blk, t.hs, bar,
+                                 lane);
+            else if (lane < HD / 64)
+              tma_load_2d(dst + lane * kAttnBox, map, head * HD + 64 * lane, t.first + kAttnRows * blk, bar);
             if (patch) {
               wait(&tail_bar, tails++ & 1);
               for (int r = rows + (lane >> 3); r < kAttnRows; r += 4)
-                for (int x = 0; x < HD / 64; ++x)
+                for (int x = 0; x < HD / 64 && (r & (piece - 1)) >= rows; ++x)
                   *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_cta();
               __syncwarp();
@@ -295,11 +303,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) mbar_wait(&mma_done, 0, a.err);
     } else if (warp == 2) {
       // ---- finder
-      AttnOrder ord{a.cu, a.batch, kAttnRows, s_cache, 0, 0};
+      AttnOrder ord{a.cu, a.batch, kAttnRows, KV ? a.small_kv : a.small_q, s_cache};
       const bool ok = ord.init(a.T, lane);
       if (!ok && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
       const int units = KV ? (SPLIT ? a.n_kv * a.splits : a.n_kv) : a.n_q;
-      const uint32_t work = ord.total * (uint32_t)units;  // below 2^31: the host checks
+      // (a key/value item has all its query heads, whether a tile holds one or several)
+      const uint32_t work = ord.work<!KV>((uint32_t)units);  // below 2^31: the host checks
       for (uint32_t k = 0;; ++k) {
         const uint32_t s = k % kBwdSched;
         if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kBwdSched) & 1) ^ 1))) break;
@@ -308,9 +317,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         t.valid = k * gridDim.x < work;  // else no CTA has any left
         if (w < work) {                  // (an empty item: this CTA has none in the last round)
           int seq, cost;
-          const uint32_t rank = w / (uint32_t)units;
-          ord.find(rank, lane, seq, cost);
-          t.head = (int)(w - rank * (uint32_t)units);
+          ord.find<!KV>(w, (uint32_t)units, lane, seq, cost, t.head, t.hs);
+          if constexpr (!KV) t.head <<= 2 - t.hs;
           if constexpr (SPLIT) {
             t.split = t.head / a.n_kv;
             t.head -= t.split * a.n_kv;
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           t.len = a.cu[seq + 1] - t.first;
           t.blk = KV ? (t.len + kAttnRows - 1) / kAttnRows - cost : cost - 1;
           t.own = t.first + kAttnRows * t.blk;
-          t.n = KV ? cost * (SPLIT ? a.group / a.splits : a.group) : cost;
+          t.n = KV ? cost * ((SPLIT ? a.group / a.splits : a.group) >> (2 - t.hs)) : cost;
         }
         if (lane == 0) {
           s_item[s] = t;
@@ -339,17 +347,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int blk = block_of(t, i, head);
             const uint32_t s = it % kStatStages;
             float ls[4], de[4];
-  #pragma unroll
+#pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int r = kAttnRows * blk + 32 * x + lane;
+              const int r = kAttnRows * blk + 32 * (x & ((1 << t.hs) - 1)) + lane;
               const bool in = r < t.len;
-              const int64_t at = (int64_t)head * a.T + t.first + r;
+              const int64_t at = (int64_t)(head + (x >> t.hs)) * a.T + t.first + r;
               ls[x] = in ? -a.lse[at] * kLog2e : -INFINITY;
               de[x] = in ? -a.delta[at] : 0.f;
               if (ls[x] == INFINITY) ls[x] = -INFINITY;  // a row without keys
             }
             if (it >= kStatStages) wait(&st_empty[s], ((it / kStatStages) - 1) & 1);
-  #pragma unroll
+#pragma unroll
             for (int x = 0; x < 4; ++x) {
               s_stat[s][0][32 * x + lane] = ls[x];
               s_stat[s][1][32 * x + lane] = de[x];
@@ -379,9 +387,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     while (next_item(t)) {
       if (t.n == 0) continue;
       float r_lse = 0.f, r_delta = 0.f;  // query kernel: -lse log2(e) and -delta of this row
-      const bool in = kAttnRows * t.blk + row < t.len;
+      // query kernel: the head and the row in the block that this thread's row is
+      const int q_head = t.head + (KV ? 0 : qtr >> t.hs), q_row = KV ? row : 32 * (qtr & ((1 << t.hs) - 1)) + lane;
+      const bool in = kAttnRows * t.blk + q_row < t.len;
       if constexpr (!KV) {
-        const int64_t at = (int64_t)t.head * a.T + t.own + row;
+        const int64_t at = (int64_t)q_head * a.T + t.own + q_row;
         r_lse = in ? -a.lse[at] * kLog2e : -INFINITY;
         if (r_lse == INFINITY) r_lse = -INFINITY;
         if (t.n > 1) {  // delta = dout . out: half a row's columns each, dout from the CTA's own tile
@@ -442,9 +452,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             p1 = ex2(p1);
           }
           if constexpr (KV) {
-            if (diagonal && 2 * wg + x <= qtr) {  // queries before this key do not attend it
-              asm volatile("");                   // a branch, not selects in every block
-              const int first = 2 * wg + x < qtr ? 32 : lane;
+            const int piece = (2 * wg + x) & ((1 << t.hs) - 1);
+            if (diagonal && piece <= qtr) {  // queries before this key do not attend it
+              asm volatile("");              // a branch, not selects in every block
+              const int first = piece < qtr ? 32 : lane;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (e < first) p[32 * x + e] = 0.f;
@@ -472,7 +483,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             asm volatile("");
 #pragma unroll
             for (int e = 0; e < 64; ++e)
-              if (64 * wg + e > row) p[e] = y[e] = 0.f;
+              if (64 * wg + e > q_row) p[e] = y[e] = 0.f;
           }
           if (t.n == 1) {
             // Rows with few keys: delta = sum_j p_ij dp_ij is summed here, from the p and
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             s_stat[wg][1][row] = s1;
             named_sync(1, 256);
             r_delta = -(s_stat[0][1][row] + s_stat[1][1][row]) / (s_stat[0][0][row] + s_stat[1][0][row]);
-            if (wg == 0 && in) a.delta[(int64_t)t.head * a.T + t.own + row] = -r_delta;
+            if (wg == 0 && in) a.delta[(int64_t)q_head * a.T + t.own + q_row] = -r_delta;
           }
         }
         const uint32_t t_ds = KV && !kTwoX ? t_y : t_x + kDsOff;
@@ -538,16 +549,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float f = KV && wg == 0 ? 1.f : a.scale;
       uint4* out = KV ? (wg ? a.dk : a.dv) : a.dq;
       const int heads = KV ? a.n_kv : a.n_q, col0 = KV ? 0 : COLS * wg;
-      const int row0 = t.own + 32 * qtr, rows = t.first + t.len - row0;
+      const int row0 = t.own + q_row - lane, rows = t.first + t.len - row0;
       if constexpr (SPLIT) {  // sums over this part of the group, for the folding kernel
         if (lane < rows) {
           float4* dst = reinterpret_cast<float4*>(
-              a.part + (((2 * t.split + wg) * a.T + row0 + lane) * (int64_t)a.n_kv + t.head) * HD);
+              a.part + (((2 * t.split + wg) * a.T + row0 + lane) * (int64_t)a.n_kv + q_head) * HD);
 #pragma unroll
           for (int e = 0; e < COLS / 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       } else if constexpr (HD == 128) {
-        uint4* dst = out + ((int64_t)(row0 + lane) * heads + t.head) * (HD / 8) + col0 / 8;
+        uint4* dst = out + ((int64_t)(row0 + lane) * heads + q_head) * (HD / 8) + col0 / 8;
         if (lane < rows)
 #pragma unroll
           for (int ch = 0; ch < COLS / 8; ++ch) {
@@ -573,7 +584,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int r0 = 0; r0 < 32; r0 += RP) {
             const int r = r0 + lane / CHU, ch = lane % CHU;
             const uint4 v = *reinterpret_cast<const uint4*>(sbuf + at(r, ch));
-            if (r < rows) out[((int64_t)(row0 + r) * heads + t.head) * (HD / 8) + (col0 + UNIT * x) / 8 + ch] = v;
+            if (r < rows) out[((int64_t)(row0 + r) * heads + q_head) * (HD / 8) + (col0 + UNIT * x) / 8 + ch] = v;
           }
           __syncwarp();
         }

@@ -21,7 +21,10 @@
 //
 // One CTA per SM holds two blocks of 128 query rows ("slots") that share every
 // key block: two heads of the same group at the same rows where the group is
-// even, else two consecutive row blocks of a head. Sharing halves what K and V
+// even, else two consecutive row blocks of a head. Of a sequence of at most 64 (32) rows a
+// slot holds two (four) heads, where the group has them: a block costs a CTA some 6700
+// cycles however few of its rows are there (60 sequences of 67 rows, 128 over 16 heads of
+// 64: 122 us with a head a slot, 92 so). Sharing halves what K and V
 // cost to fetch (64 KiB per 2 x 8.4 MFLOP at head_dim 128), and while one slot's
 // softmax runs, the tensor cores work on the other's products:
 //   warp 0      loads Q, K, V tiles with TMA into 128B-swizzled shared memory;
@@ -70,6 +73,7 @@ struct FwdItem {
   int kvh;           // key/value head
   int kv0;           // first key row (prompt)
   int len;           // keys (of the sequence, or of this key range of the prefix)
+  int hs;            // prompt: heads in a tile, as in attn_load_tile
   int valid;
 };
 
@@ -78,7 +82,8 @@ struct FwdItem {
 template <int HD, bool PREFIX>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     qkvp_attention_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                              const __grid_constant__ CUtensorMap tmap_v, const AttnFwdArgs a) {
+                              const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap pieces_q,
+                              const AttnFwdArgs a) {
   using SM = FwdSmem<HD>;
   constexpr int ST = SM::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -195,18 +200,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if ((j ? t.n1 : t.n0) == 0) continue;
           wait(&q_empty[j], ((q_ph >> j) & 1) ^ 1);
           q_ph ^= 1u << j;
-          if (lane == 0) {
-            unsigned char* dst = base + SM::kQ + j * SM::kTile;
-            const int row = j ? t.row1 : t.row0, head = j ? t.head1 : t.head0;
+          unsigned char* dst = base + SM::kQ + j * SM::kTile;
+          const int row = j ? t.row1 : t.row0, head = j ? t.head1 : t.head0;
+          if (lane == 0)
             mbar_arrive_expect_tx(&q_full[j], PREFIX ? (uint32_t)(a.bpt * a.group * HD * 2) : (uint32_t)SM::kTile);
-#pragma unroll
-            for (int x = 0; x < HD / 64; ++x) {
-              if constexpr (PREFIX)
-                tma_load_3d(dst + x * kAttnBox, &tmap_q, 64 * x, t.kvh * a.group, row * a.bpt, &q_full[j]);
-              else
-                tma_load_2d(dst + x * kAttnBox, &tmap_q, head * HD + 64 * x, row, &q_full[j]);
-            }
-          }
+          __syncwarp();
+          if constexpr (!PREFIX)
+            attn_load_tile<HD>(dst, &tmap_q, &pieces_q, head * HD, row, t.hs, &q_full[j], lane);
+          else if (lane < HD / 64)
+            tma_load_3d(dst + lane * kAttnBox, &tmap_q, 64 * lane, t.kvh * a.group, row * a.bpt, &q_full[j]);
         }
         const int n = max(t.n0, t.n1);
 #pragma unroll 1
@@ -320,10 +322,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (lane == 0) mbar_wait(&mma_done, 0, a.err);
     } else if (warp == 2 && !PREFIX) {
       // ---- finder
-      AttnOrder ord{a.cu, a.batch, a.pair_heads ? kAttnRows : 2 * kAttnRows, s_cache, 0, 0};
+      AttnOrder ord{a.cu, a.batch, a.pair_heads ? kAttnRows : 2 * kAttnRows, a.small, s_cache};
       const bool good = ord.init(a.T, lane);
       if (!good && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
-      const uint32_t work = ord.total * (uint32_t)a.units;  // below 2^31: the host checks
+      const uint32_t work = ord.work<true>((uint32_t)a.units);  // below 2^31: the host checks
       for (uint32_t k = 0;; ++k) {
         const uint32_t s = k % kFwdSched;
         if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kFwdSched) & 1) ^ 1))) break;
@@ -331,14 +333,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         FwdItem t = {};
         t.valid = k * gridDim.x < work;  // else no CTA has any left
         if (w < work) {                  // (an empty item: this CTA has none in the last round)
-          int seq, cost;
-          const uint32_t rank = w / (uint32_t)a.units;
-          ord.find(rank, lane, seq, cost);
-          const int hu = (int)(w - rank * (uint32_t)a.units);
+          int seq, cost, hu;
+          ord.find<true>(w, (uint32_t)a.units, lane, seq, cost, hu, t.hs);
           const int start = a.cu[seq], len = a.cu[seq + 1] - start;
           if (a.pair_heads) {
-            t.head0 = 2 * hu;
-            t.head1 = t.head0 + 1;
+            const int heads = 4 >> t.hs;  // of a tile
+            t.head0 = 2 * hu * heads;
+            t.head1 = t.head0 + heads;
             t.row0 = t.row1 = start + kAttnRows * (cost - 1);
             t.n0 = t.n1 = cost;
           } else {
@@ -384,7 +385,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     while (next_item(t)) {
       const int n = j ? t.n1 : t.n0;
       if (n == 0) continue;
-      const int row0 = (j ? t.row1 : t.row0) + 32 * qtr;
+      // this warp's 32 rows of its head's (PREFIX: hs plays no part)
+      const int vq = PREFIX ? qtr : qtr & ((1 << t.hs) - 1);
+      const int row0 = (j ? t.row1 : t.row0) + 32 * vq;
       const int rows = t.kv0 + t.len - row0;  // prompt: rows of this warp that belong to the sequence
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -425,17 +428,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           // seen. The warp's rows see the quarters before their own whole, their own up
           // to the lane, and none after it. (The empty asm makes a branch of each quarter:
           // selects run at half rate, and all 128 of them took longer than the exponentials.)
-          quarters = qtr + 1;
+          quarters = vq + 1;
           top = -INFINITY;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            if (x == qtr) {
+            if (x == vq) {
               asm volatile("");
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (e > lane) s[32 * x + e] = -INFINITY;
             }
-            if (x <= qtr) {
+            if (x <= vq) {
               asm volatile("");
               top = fmaxf(top, max32(s + 32 * x));
             }
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // O / l through shared memory, 64 columns at a time, so that whole 128-byte lines
         // leave: eight lanes per row, four rows per store
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
-        const int head = j ? t.head1 : t.head0, r0 = lane >> 3, ch0 = lane & 7;
+        const int head = (j ? t.head1 : t.head0) + (qtr >> t.hs), r0 = lane >> 3, ch0 = lane & 7;
         unsigned char* buf = base + SM::kOut + (warp - 4) * kStageBytes;
         const int64_t stride = (int64_t)a.n_q * (HD / 8);
         uint4* dst = a.out + (row0 + r0) * stride + head * (HD / 8) + ch0;

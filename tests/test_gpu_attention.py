@@ -511,3 +511,31 @@ def test_autograd_in_a_graph_and_twice(lib, cuda):
     with pytest.raises(RuntimeError):
         torch.autograd.grad(first.float().square().sum(), x)
     no_error(lib)
+
+
+# sequences at the lengths where a tile of 128 rows holds four heads, two, or one, enough
+# of them that the heads of a group are not divided among CTAs (`times`), and few
+@pytest.mark.parametrize("n_q,n_kv,D", [(16, 2, 64), (16, 1, 128), (8, 2, 128), (12, 3, 64), (6, 3, 64), (10, 2, 64)])
+@pytest.mark.parametrize("lengths,times,before,after", [
+    ([1, 31, 32, 33, 0, 63, 64, 65, 5, 130], 16, 0, 0),
+    ([32, 33, 1, 64], 1, 3, 70),
+    ([2] * 40 + [129, 0, 40], 4, 1, 0),
+])
+def test_short_sequences_with_several_heads_in_a_tile(lib, cuda, lengths, times, before, after, n_q, n_kv, D):
+    F = lib.functional
+    cu = offsets(lengths * times, before)
+    T = int(cu[-1]) + after
+    q, k, v, do = inputs(T, n_q, n_kv, D, 1000 + T)
+    dev = [t.to(cuda) for t in (q, k, v, do)]
+    for t in dev:  # rows of no sequence are in the tiles, but in no result
+        t[:before] = t[T - after:] = float("nan")
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    out, lse = F.attention_forward(*dev[:3], cu_dev, save_lse=True)
+    grads = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev)
+    no_error(lib)
+    ref = A.attention_fwd(f64(q), f64(k), f64(v), cu)
+    assert_within(f64(out), ref["out"], out_bound(ref), "out")
+    assert_lse(lse.cpu().numpy(), ref, max(lengths), D, "lse")
+    g = A.attention_bwd(f64(do), f64(q), f64(k), f64(v), cu, out_err=out_bound(ref))
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        assert_within(f64(got), g[name], g["e_" + name] + U * np.abs(g[name]), name)
