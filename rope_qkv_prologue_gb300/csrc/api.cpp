@@ -1462,7 +1462,8 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   if (!allow_smem(kkv, smem) || !allow_smem(kq, smem)) return QKVP_ERR_LAUNCH;
   void* args[] = {&tq, &td, &tk, &tv, &pq, &pd, &a};
   QKVP_TRY(launch_args(kq, std::min<int64_t>(blocks * a.n_q, sms), attention_bwd_threads(), smem, st, args));
-  QKVP_TRY(launch_args(kkv, std::min<int64_t>(blocks * a.n_kv * a.splits, sms), attention_bwd_threads(), smem, st, args));
+  const int64_t kv_work = blocks * a.n_kv * a.splits;
+  QKVP_TRY(launch_args(kkv, std::min<int64_t>(kv_work, sms), attention_bwd_threads(), smem, st, args));
   if (a.splits == 1) return QKVP_OK;
   int row4 = a.n_kv * hd / 4;
   void* fargs[] = {&a, &row4};
@@ -1494,7 +1495,8 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   float sc = 0.f;
   QKVP_TRY(check_attention(layout, batch, scale, &sc));
   if (table_stride < max_pages) return QKVP_ERR_SHAPE;
-  if (!q || !k_pool || !v_pool || !lengths || !out || (max_pages > 0 && !page_table) || (prefix_len > 0 && !prefix_pages))
+  if (!q || !k_pool || !v_pool || !lengths || !out || (max_pages > 0 && !page_table) ||
+      (prefix_len > 0 && !prefix_pages))
     return QKVP_ERR_NULL;
   for (const void* p : {q, k_pool, v_pool, (const void*)out})
     if (!aligned16(p)) return QKVP_ERR_ALIGN;
@@ -1596,7 +1598,8 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
   QKVP_TRY(launch(kern, p.grid, attention_decode_threads(), smem, st, &a));
   const int per = kJoinWarps / a.wph;
-  return launch(attention_join_kernel(hd), (int64_t)batch * ((layout->n_q + per - 1) / per), 32 * kJoinWarps, 0, st, &a);
+  const int64_t joins = (int64_t)batch * ((layout->n_q + per - 1) / per);
+  return launch(attention_join_kernel(hd), joins, 32 * kJoinWarps, 0, st, &a);
 }
 
 int qkv_prologue_wait_selftest(void* stream) {

@@ -65,13 +65,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to global memory.
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)),
-               "r"(bytes)
-               : "memory");
-}
-
 // Registers per thread of this warp's group of four warps, which calls it together.
 // The shares of a CTA's groups add up to no more than what it was launched with.
 template <int N>
@@ -136,17 +129,7 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
-// Whole warp: 32 consecutive 32-bit columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
+// Whole warp: 16 consecutive 32-bit columns of this warp's 32 TMEM lanes.
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -232,8 +215,8 @@ __device__ __forceinline__ float tmem_ld128_max(uint32_t addr, float (&v)[128]) 
 // 3-D tensor-map load (c0: the contiguous coordinate).
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_addr(dst)),
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(smem_addr(dst)),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
       : "memory");
 }
@@ -310,7 +293,9 @@ struct AttnOrder {
     if (small && rows <= 64 && rows > 0) return small == 2 && rows <= 32 ? -2 : -1;
     return (int)((rows + unit - 1) / unit);
   }
-  __device__ __forceinline__ int blocks(int s) const { return s < kCached ? cache[s] : count((int64_t)cu[s + 1] - cu[s]); }
+  __device__ __forceinline__ int blocks(int s) const {
+    return s < kCached ? cache[s] : count((int64_t)cu[s + 1] - cu[s]);
+  }
 
   // Whole warp. False (and no blocks) when the offsets do not ascend in [0, T].
   __device__ __forceinline__ bool init(int64_t T, int lane) {
@@ -369,7 +354,8 @@ struct AttnOrder {
                                        int& hs) const {
     const uint32_t w0 = total * units, w1 = w0 + n64 * (DIVIDE ? units / 2 : units);
     hs = w < w0 ? 2 : (w < w1 ? 1 : 0);
-    const uint32_t at = w - (hs == 2 ? 0u : (hs == 1 ? w0 : w1)), per = DIVIDE ? units >> (2 - hs) : units, r = at / per;
+    const uint32_t at = w - (hs == 2 ? 0u : (hs == 1 ? w0 : w1)), per = DIVIDE ? units >> (2 - hs) : units;
+    const uint32_t r = at / per;
     unit_of = (int)(at - r * per);
     uint32_t f_hi = 0;
     int lo = 0, hi = hs == 2 ? most : 0;  // F(hi) <= r, and F(lo - 1) > r or lo == 0
@@ -403,7 +389,8 @@ __device__ __forceinline__ uint32_t attn_deal(uint32_t k, uint32_t b, uint32_t g
 
 // Rows of no sequence ([0, first) and [last, T)): `chunks` 16-byte pieces per row
 // set to zero, one warp of each CTA.
-__device__ __forceinline__ void attn_zero_rows(uint4* out, int64_t T, int chunks, int64_t first, int64_t last, int lane) {
+__device__ __forceinline__ void attn_zero_rows(uint4* out, int64_t T, int chunks, int64_t first, int64_t last,
+                                               int lane) {
 #pragma unroll 1
   for (int64_t r = blockIdx.x; r < first + T - last; r += gridDim.x) {
     uint4* row = out + (r < first ? r : last + (r - first)) * chunks;

@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(bar, SM::kTile);
             __syncwarp();
             if constexpr (KV)
-              attn_load_tile<HD>(dst, map, which ? &pieces_do : &pieces_q, head * HD, t.first + kAttnRows * blk, t.hs, bar,
-                                 lane);
+              attn_load_tile<HD>(dst, map, which ? &pieces_do : &pieces_q, head * HD, t.first + kAttnRows * blk, t.hs,
+                                 bar, lane);
             else if (lane < HD / 64)
               tma_load_2d(dst + lane * kAttnBox, map, head * HD + 64 * lane, t.first + kAttnRows * blk, bar);
             if (patch) {

@@ -505,7 +505,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           tmem_ld32(t_o + 32 * x, o);
           if (in)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[8 * x + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e)
+              dst[8 * x + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
         tc_fence_before();
         __syncwarp();
