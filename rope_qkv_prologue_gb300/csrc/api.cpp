@@ -1349,7 +1349,8 @@ int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   a.cu = cu_seqlens;
   a.pair_heads = a.group % 2 == 0;
   a.units = a.pair_heads ? a.n_q / 2 : a.n_q;
-  a.small = a.group % 8 == 0 ? 2 : (a.group % 4 == 0 ? 1 : 0);
+  a.units64 = a.group > 2 ? a.n_kv * ((a.group + 3) / 4) : 0;  // two slots of two heads
+  a.units32 = a.group > 2 ? a.n_kv * ((a.group + 7) / 8) : 0;  // ... of four
   a.zero_rest = (flags & QKVP_ZERO_REST) != 0;
   a.out = static_cast<uint4*>(out);
   a.lse = lse;
@@ -1445,9 +1446,6 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   a.lse = lse;
   a.delta = static_cast<float*>(workspace);
   a.splits = attention_bwd_splits(layout, T, batch);
-  auto small = [](int heads) { return heads % 4 == 0 ? 2 : (heads % 2 == 0 ? 1 : 0); };
-  a.small_q = small(a.group);
-  a.small_kv = small(a.group / a.splits);
   a.part = a.delta + (((T * a.n_q) + 3) & ~(int64_t)3);
   a.zero_rest = (flags & QKVP_ZERO_REST) != 0;
   a.dq = static_cast<uint4*>(dq);

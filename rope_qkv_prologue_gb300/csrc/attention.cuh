@@ -273,16 +273,16 @@ __device__ __forceinline__ void attn_load_tile(unsigned char* dst, const CUtenso
 // one warp from the sequence offsets alone: no list in memory, no launch before
 // the kernel that uses it.
 //
-// Short sequences come last and are counted apart, since one work item holds
-// several heads of them: those of at most 64 rows (two heads to a tile of 128
-// rows), and of at most 32 (four), where the caller can place them (`small`: 0
-// none, 1 up to 64 rows, 2 both).
+// Every block is `units` work items (heads, pairs of heads, ...). Short sequences
+// come last and have counts of their own, since one tile of 128 rows holds several
+// heads of them: units64 for those of at most 64 rows (two heads to a tile) and
+// units32 for those of at most 32 (four); 0 where the caller has no use for that.
 struct AttnOrder {
   static constexpr int kCached = 128;  // sequences whose block counts are kept in shared memory
   const int32_t* cu;
   int batch;
   int unit;
-  int small;
+  uint32_t units, units64, units32;
   int* cache;      // [kCached]
   int most;        // largest n_s
   uint32_t total;  // sum of n_s
@@ -290,7 +290,7 @@ struct AttnOrder {
 
   // n_s, or -1 (one of n64) or -2 (of n32)
   __device__ __forceinline__ int count(int64_t rows) const {
-    if (small && rows <= 64 && rows > 0) return small == 2 && rows <= 32 ? -2 : -1;
+    if (units64 && rows <= 64 && rows > 0) return rows <= 32 ? -2 : -1;
     return (int)((rows + unit - 1) / unit);
   }
   __device__ __forceinline__ int blocks(int s) const {
@@ -340,21 +340,14 @@ struct AttnOrder {
     return seq;
   }
 
-  // Work items, with `units` heads (or pairs of heads) to every block; DIVIDE: those of
-  // short sequences hold several.
-  template <bool DIVIDE>
-  __device__ __forceinline__ uint32_t work(uint32_t units) const {
-    return total * units + n64 * (DIVIDE ? units / 2 : units) + n32 * (DIVIDE ? units / 4 : units);
-  }
+  __device__ __forceinline__ uint32_t work() const { return total * units + n64 * units64 + n32 * units32; }
 
-  // Whole warp: work item w < work(units) is unit `unit_of` of the block of cost `cost`
-  // of sequence `seq`; hs as in attn_load_tile.
-  template <bool DIVIDE>
-  __device__ __forceinline__ void find(uint32_t w, uint32_t units, int lane, int& seq, int& cost, int& unit_of,
-                                       int& hs) const {
-    const uint32_t w0 = total * units, w1 = w0 + n64 * (DIVIDE ? units / 2 : units);
+  // Whole warp: work item w < work() is unit `unit_of` of the block of cost `cost` of
+  // sequence `seq`; hs as in attn_load_tile.
+  __device__ __forceinline__ void find(uint32_t w, int lane, int& seq, int& cost, int& unit_of, int& hs) const {
+    const uint32_t w0 = total * units, w1 = w0 + n64 * units64;
     hs = w < w0 ? 2 : (w < w1 ? 1 : 0);
-    const uint32_t at = w - (hs == 2 ? 0u : (hs == 1 ? w0 : w1)), per = DIVIDE ? units >> (2 - hs) : units;
+    const uint32_t at = w - (hs == 2 ? 0u : (hs == 1 ? w0 : w1)), per = hs == 2 ? units : (hs == 1 ? units64 : units32);
     const uint32_t r = at / per;
     unit_of = (int)(at - r * per);
     uint32_t f_hi = 0;

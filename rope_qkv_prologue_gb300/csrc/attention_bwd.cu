@@ -5,8 +5,8 @@
 // ds_ij = p_ij (dp_ij - delta_i):
 //     dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j,
 // dk and dv summed over the query heads of the group too. Sequences of at most 64 (32)
-// rows have two (four) heads in a tile of 128 queries, where the group has them (25 tokens
-// in 19 sequences, 256 over 16 heads of 64, both directions: 183 -> 64 us). Two kernels:
+// rows have two (four) heads of the group in a tile of 128 queries (25 tokens in 19
+// sequences, 256 over 16 heads of 64, both directions: 183 -> 64 us). Two kernels:
 //   1. the query kernel: a CTA owns 128 queries of one head and goes through its
 //      keys, adding dS K. Its dout is in shared memory, so it also forms delta and
 //      leaves it for the other (against a kernel of its own for delta, 4096 tokens in
@@ -67,6 +67,7 @@ struct BwdItem {
   int blk;    // the own block's index in the sequence
   int head;   // key/value head, or query head
   int hs;     // heads in a tile of queries, as in attn_load_tile
+  int end;    // end of the query heads (a tile may have room for more)
   int split;  // SPLIT: which of the group's parts of query heads
   int valid;
 };
@@ -166,8 +167,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // kernel) the query head.
   auto block_of = [&](const BwdItem& t, int i, int& head) {
     if constexpr (KV) {
-      const int heads = SPLIT ? a.group / a.splits : a.group, tiles = heads >> (2 - t.hs), per = t.n / tiles;
-      head = t.head * a.group + (SPLIT ? t.split * heads : 0) + ((i / per) << (2 - t.hs));
+      const int heads = SPLIT ? a.group / a.splits : a.group, per = t.n / ((heads + (4 >> t.hs) - 1) >> (2 - t.hs));
+      head = t.end - heads + ((i / per) << (2 - t.hs));
       return t.blk + i % per;
     } else {
       head = t.head / a.group;
@@ -207,7 +208,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             unsigned char* dst = base + (which ? SM::kB2 : SM::kB1) + s * SM::kTile;
             const CUtensorMap* map = KV ? (which ? &tmap_do : &tmap_q) : (which ? &tmap_v : &tmap_k);
             const int piece = KV ? 32 << t.hs : kAttnRows;  // rows of a head in the tile
-            const bool patch = rows < piece && (KV || which == 0);
+            const int held = KV ? piece * (t.end - head) : kAttnRows;  // rows of its heads (or more)
+            const bool patch = (rows < piece || held < kAttnRows) && (KV || which == 0);
             uint64_t* bar = patch ? &tail_bar : full;
             if (lane == 0) mbar_arrive_expect_tx(bar, SM::kTile);
             __syncwarp();
@@ -218,8 +220,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               tma_load_2d(dst + lane * kAttnBox, map, head * HD + 64 * lane, t.first + kAttnRows * blk, bar);
             if (patch) {
               wait(&tail_bar, tails++ & 1);
-              for (int r = rows + (lane >> 3); r < kAttnRows; r += 4)
-                for (int x = 0; x < HD / 64 && (r & (piece - 1)) >= rows; ++x)
+              for (int r = min(rows, held) + (lane >> 3); r < kAttnRows; r += 4)
+                for (int x = 0; x < HD / 64 && ((r & (piece - 1)) >= rows || r >= held); ++x)
                   *reinterpret_cast<uint4*>(dst + x * kAttnBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_cta();
               __syncwarp();
@@ -303,12 +305,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) mbar_wait(&mma_done, 0, a.err);
     } else if (warp == 2) {
       // ---- finder
-      AttnOrder ord{a.cu, a.batch, kAttnRows, KV ? a.small_kv : a.small_q, s_cache};
+      // A key/value item has all query heads of its part, whether a tile holds one or several.
+      const uint32_t units = KV ? (SPLIT ? a.n_kv * a.splits : a.n_kv) : a.n_q;
+      const bool several = a.group > (SPLIT ? a.splits : 1);
+      AttnOrder ord{a.cu,
+                    a.batch,
+                    kAttnRows,
+                    units,
+                    several ? (KV ? units : (uint32_t)(a.n_kv * ((a.group + 1) / 2))) : 0u,
+                    several ? (KV ? units : (uint32_t)(a.n_kv * ((a.group + 3) / 4))) : 0u,
+                    s_cache};
       const bool ok = ord.init(a.T, lane);
       if (!ok && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
-      const int units = KV ? (SPLIT ? a.n_kv * a.splits : a.n_kv) : a.n_q;
-      // (a key/value item has all its query heads, whether a tile holds one or several)
-      const uint32_t work = ord.work<!KV>((uint32_t)units);  // below 2^31: the host checks
+      const uint32_t work = ord.work();  // below 2^31: the host checks
       for (uint32_t k = 0;; ++k) {
         const uint32_t s = k % kBwdSched;
         if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kBwdSched) & 1) ^ 1))) break;
@@ -317,17 +326,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         t.valid = k * gridDim.x < work;  // else no CTA has any left
         if (w < work) {                  // (an empty item: this CTA has none in the last round)
           int seq, cost;
-          ord.find<!KV>(w, (uint32_t)units, lane, seq, cost, t.head, t.hs);
-          if constexpr (!KV) t.head <<= 2 - t.hs;
-          if constexpr (SPLIT) {
+          ord.find(w, lane, seq, cost, t.head, t.hs);
+          const int heads = SPLIT ? a.group / a.splits : a.group, fit = 4 >> t.hs;  // heads that fit a tile
+          const int tiles = (heads + fit - 1) >> (2 - t.hs);
+          if constexpr (KV) {
             t.split = t.head / a.n_kv;
             t.head -= t.split * a.n_kv;
+            t.end = t.head * a.group + (t.split + 1) * heads;
+          } else {
+            const int kvh = t.head / (t.hs == 2 ? a.group : tiles);
+            if (t.hs != 2) t.head = kvh * a.group + (t.head - kvh * tiles) * fit;
+            t.end = (kvh + 1) * a.group;
           }
           t.first = a.cu[seq];
           t.len = a.cu[seq + 1] - t.first;
           t.blk = KV ? (t.len + kAttnRows - 1) / kAttnRows - cost : cost - 1;
           t.own = t.first + kAttnRows * t.blk;
-          t.n = KV ? cost * ((SPLIT ? a.group / a.splits : a.group) >> (2 - t.hs)) : cost;
+          t.n = KV ? cost * tiles : cost;
         }
         if (lane == 0) {
           s_item[s] = t;
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int r = kAttnRows * blk + 32 * (x & ((1 << t.hs) - 1)) + lane;
-              const bool in = r < t.len;
+              const bool in = r < t.len && head + (x >> t.hs) < t.end;
               const int64_t at = (int64_t)(head + (x >> t.hs)) * a.T + t.first + r;
               ls[x] = in ? -a.lse[at] * kLog2e : -INFINITY;
               de[x] = in ? -a.delta[at] : 0.f;
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       float r_lse = 0.f, r_delta = 0.f;  // query kernel: -lse log2(e) and -delta of this row
       // query kernel: the head and the row in the block that this thread's row is
       const int q_head = t.head + (KV ? 0 : qtr >> t.hs), q_row = KV ? row : 32 * (qtr & ((1 << t.hs) - 1)) + lane;
-      const bool in = kAttnRows * t.blk + q_row < t.len;
+      const bool in = kAttnRows * t.blk + q_row < t.len && (KV || q_head < t.end);
       if constexpr (!KV) {
         const int64_t at = (int64_t)q_head * a.T + t.own + q_row;
         r_lse = in ? -a.lse[at] * kLog2e : -INFINITY;
@@ -549,7 +564,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float f = KV && wg == 0 ? 1.f : a.scale;
       uint4* out = KV ? (wg ? a.dk : a.dv) : a.dq;
       const int heads = KV ? a.n_kv : a.n_q, col0 = KV ? 0 : COLS * wg;
-      const int row0 = t.own + q_row - lane, rows = t.first + t.len - row0;
+      const int row0 = t.own + q_row - lane, rows = KV || q_head < t.end ? t.first + t.len - row0 : 0;
       if constexpr (SPLIT) {  // sums over this part of the group, for the folding kernel
         if (lane < rows) {
           float4* dst = reinterpret_cast<float4*>(

@@ -22,7 +22,7 @@
 // One CTA per SM holds two blocks of 128 query rows ("slots") that share every
 // key block: two heads of the same group at the same rows where the group is
 // even, else two consecutive row blocks of a head. Of a sequence of at most 64 (32) rows a
-// slot holds two (four) heads, where the group has them: a block costs a CTA some 6700
+// slot holds two (four) heads of the group: a block costs a CTA some 6700
 // cycles however few of its rows are there (60 sequences of 67 rows, 128 over 16 heads of
 // 64: 122 us with a head a slot, 92 so). Sharing halves what K and V
 // cost to fetch (64 KiB per 2 x 8.4 MFLOP at head_dim 128), and while one slot's
@@ -74,6 +74,7 @@ struct FwdItem {
   int kv0;           // first key row (prompt)
   int len;           // keys (of the sequence, or of this key range of the prefix)
   int hs;            // prompt: heads in a tile, as in attn_load_tile
+  int end;           // prompt: end of the group's query heads (a tile may have room for more)
   int valid;
 };
 
@@ -322,10 +323,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (lane == 0) mbar_wait(&mma_done, 0, a.err);
     } else if (warp == 2 && !PREFIX) {
       // ---- finder
-      AttnOrder ord{a.cu, a.batch, a.pair_heads ? kAttnRows : 2 * kAttnRows, a.small, s_cache};
+      AttnOrder ord{a.cu, a.batch, a.pair_heads ? kAttnRows : 2 * kAttnRows, (uint32_t)a.units, (uint32_t)a.units64,
+                    (uint32_t)a.units32, s_cache};
       const bool good = ord.init(a.T, lane);
       if (!good && blockIdx.x == 0 && lane == 0 && a.dev_status) atomicOr(a.dev_status, kDevBadSequence);
-      const uint32_t work = ord.work<true>((uint32_t)a.units);  // below 2^31: the host checks
+      const uint32_t work = ord.work();  // below 2^31: the host checks
       for (uint32_t k = 0;; ++k) {
         const uint32_t s = k % kFwdSched;
         if (!__all_sync(0xffffffffu, wait(&it_empty[s], ((k / kFwdSched) & 1) ^ 1))) break;
@@ -334,12 +336,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         t.valid = k * gridDim.x < work;  // else no CTA has any left
         if (w < work) {                  // (an empty item: this CTA has none in the last round)
           int seq, cost, hu;
-          ord.find<true>(w, (uint32_t)a.units, lane, seq, cost, hu, t.hs);
+          ord.find(w, lane, seq, cost, hu, t.hs);
           const int start = a.cu[seq], len = a.cu[seq + 1] - start;
-          if (a.pair_heads) {
-            const int heads = 4 >> t.hs;  // of a tile
-            t.head0 = 2 * hu * heads;
-            t.head1 = t.head0 + heads;
+          if (t.hs != 2) {  // a slot holds up to 4 >> hs heads of the group
+            const int items = (t.hs ? a.units64 : a.units32) / a.n_kv, kvh = hu / items;
+            t.head0 = kvh * a.group + (hu - kvh * items) * (8 >> t.hs);
+            t.head1 = t.head0 + (4 >> t.hs);
+            t.row0 = t.row1 = start;
+            t.n0 = 1;
+            t.n1 = t.head1 < (kvh + 1) * a.group;
+          } else if (a.pair_heads) {
+            t.head0 = 2 * hu;
+            t.head1 = t.head0 + 1;
             t.row0 = t.row1 = start + kAttnRows * (cost - 1);
             t.n0 = t.n1 = cost;
           } else {
@@ -350,6 +358,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             t.n1 = t.row1 < start + len ? 2 * cost : 0;
           }
           t.kvh = t.head0 / a.group;
+          t.end = (t.kvh + 1) * a.group;
           t.kv0 = start;
           t.len = len;
         }
@@ -388,7 +397,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // this warp's 32 rows of its head's (PREFIX: hs plays no part)
       const int vq = PREFIX ? qtr : qtr & ((1 << t.hs) - 1);
       const int row0 = (j ? t.row1 : t.row0) + 32 * vq;
-      const int rows = t.kv0 + t.len - row0;  // prompt: rows of this warp that belong to the sequence
+      const int head = (j ? t.head1 : t.head0) + (PREFIX ? 0 : qtr >> t.hs);
+      // prompt: rows of this warp that belong to the sequence
+      const int rows = PREFIX || head < t.end ? t.kv0 + t.len - row0 : 0;
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++done) {
@@ -517,7 +528,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // O / l through shared memory, 64 columns at a time, so that whole 128-byte lines
         // leave: eight lanes per row, four rows per store
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
-        const int head = (j ? t.head1 : t.head0) + (qtr >> t.hs), r0 = lane >> 3, ch0 = lane & 7;
+        const int r0 = lane >> 3, ch0 = lane & 7;
         unsigned char* buf = base + SM::kOut + (warp - 4) * kStageBytes;
         const int64_t stride = (int64_t)a.n_q * (HD / 8);
         uint4* dst = a.out + (row0 + r0) * stride + head * (HD / 8) + ch0;

@@ -349,7 +349,7 @@ struct AttnFwdArgs {
   const int32_t* cu;       // [batch + 1] row offsets of the sequences
   int32_t pair_heads;      // a CTA's two slots: two heads at the same rows, else two row blocks of a head
   int32_t units;           // head units: n_q / 2 or n_q
-  int32_t small;           // short sequences with several heads in a slot (AttnOrder)
+  int32_t units64, units32;  // the same of a short sequence, with several heads in a slot (AttnOrder)
   int32_t zero_rest;       // zero the rows of no sequence
   uint4* out;              // bf16 [T, n_q, head_dim]
   float* lse;              // [n_q, T], or null
@@ -379,7 +379,6 @@ struct AttnBwdArgs {
   const uint4* dout;
   const float* lse;        // [n_q, T]
   float* delta;            // [n_q, T]: workspace
-  int32_t small_q, small_kv;  // short sequences with several heads in a tile (AttnOrder)
   int32_t splits;          // parts of a group's query heads (a divisor of group), each its own CTAs
   float* part;             // splits > 1: [splits][dv, dk][T, n_kv, head_dim], workspace
   int32_t zero_rest;

@@ -515,7 +515,8 @@ def test_autograd_in_a_graph_and_twice(lib, cuda):
 
 # sequences at the lengths where a tile of 128 rows holds four heads, two, or one, enough
 # of them that the heads of a group are not divided among CTAs (`times`), and few
-@pytest.mark.parametrize("n_q,n_kv,D", [(16, 2, 64), (16, 1, 128), (8, 2, 128), (12, 3, 64), (6, 3, 64), (10, 2, 64)])
+@pytest.mark.parametrize("n_q,n_kv,D", [(16, 2, 64), (16, 1, 128), (8, 2, 128), (12, 3, 64), (6, 3, 64), (10, 2, 64),
+                                        (6, 2, 128), (14, 2, 64), (12, 1, 64), (3, 3, 128)])
 @pytest.mark.parametrize("lengths,times,before,after", [
     ([1, 31, 32, 33, 0, 63, 64, 65, 5, 130], 16, 0, 0),
     ([32, 33, 1, 64], 1, 3, 70),
