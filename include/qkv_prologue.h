@@ -448,7 +448,7 @@ QKVP_API int qkv_newton_schulz_plan(const qkvp_layout* layout, int64_t count, in
  *
  * layout      GQA layout; n_q, n_kv, head_dim are used, the packing is not.
  * T           rows of q, k, v and out (at most 2^31 - 257).
- * batch       sequences (>= 0; empty ones are allowed).
+ * batch       sequences (0 .. 2^20; empty ones are allowed).
  * cu_seqlens  int32 [batch + 1], ascending within [0, T]. Where they do not
  *             ascend, no row is computed and QKVP_DEV_BAD_SEQUENCE is set.
  * q, k, v     bf16 [T, n_q | n_kv, head_dim], memory of the current device.

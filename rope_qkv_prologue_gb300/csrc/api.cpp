@@ -559,7 +559,7 @@ int check_ns(const qkvp_layout* layout, int64_t count, int64_t cols, int32_t spl
 int check_attention(const qkvp_layout* layout, int32_t batch, float scale, float* scale_out) {
   Gqa g;
   QKVP_TRY(check_gqa(layout, 0, &g));
-  if (batch < 0) return QKVP_ERR_SHAPE;
+  if (batch < 0 || batch > (1 << 20)) return QKVP_ERR_SHAPE;  // (the kernels search the offsets, or the lengths)
   if (!std::isfinite(scale) || scale < 0.f) return QKVP_ERR_VALUE;
   *scale_out = scale == 0.f ? (float)(1.0 / std::sqrt((double)layout->head_dim)) : scale;
   return QKVP_OK;
@@ -618,8 +618,7 @@ int check_decode(const qkvp_layout* layout, int32_t batch, int32_t page_size, in
   QKVP_TRY(check_attention(layout, batch, 0.f, &unused));
   if (page_size <= 0) return QKVP_ERR_VALUE;
   if (max_pages < 0 || (int64_t)max_pages * page_size > INT32_MAX || prefix_len < 0 ||
-      (int64_t)max_pages * page_size + prefix_len > INT32_MAX - 4096 ||
-      batch > (1 << 20))
+      (int64_t)max_pages * page_size + prefix_len > INT32_MAX - 4096)
     return QKVP_ERR_SHAPE;
   return QKVP_OK;
 }

@@ -328,7 +328,7 @@ def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None,
     bf16 as prologue_forward returns them, cu_seqlens int32 [batch + 1] on the
     device (sequence s is the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1).
     Returns out [T, n_q, D], or (out, lse [n_q, T] float32) with save_lse.
-    scale defaults to D ** -0.5. Rows of no sequence are zero in an out made
+    scale defaults to D ** -0.5 (0 is that too). Rows of no sequence are zero in an out made
     here, and left as they are in one given (lse: -inf, in both). The work is
     queued on `stream` (default: the current one)."""
     if stream is not None:

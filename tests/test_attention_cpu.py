@@ -98,7 +98,7 @@ def test_forward_refusals(lib):
     assert _fwd(C, T=0) == C.QKVP_OK
     assert _fwd(C, T=-1) == C.QKVP_ERR_SHAPE
     assert _fwd(C, T=2 ** 31) == C.QKVP_ERR_SHAPE
-    assert _fwd(C, batch=-1) == C.QKVP_ERR_SHAPE
+    assert _fwd(C, batch=-1) == C.QKVP_ERR_SHAPE and _fwd(C, batch=2 ** 20 + 1) == C.QKVP_ERR_SHAPE
     assert _fwd(C, batch=0) == C.QKVP_ERR_ARCH
     for bad in (C.layout("sectioned", 8, 3, 64), C.layout("sectioned", 8, 2, 96), C.layout("sectioned", 0, 2, 64),
                 C.layout("latent", norm_dim=512, rope_dim=64)):

@@ -521,6 +521,7 @@ def test_autograd_in_a_graph_and_twice(lib, cuda):
     ([1, 31, 32, 33, 0, 63, 64, 65, 5, 130], 16, 0, 0),
     ([32, 33, 1, 64], 1, 3, 70),
     ([2] * 40 + [129, 0, 40], 4, 1, 0),
+    ([1, 31, 32, 33, 0, 63, 64, 65, 5, 130], 4, 2, 1),  # in several parts of several heads
 ])
 def test_short_sequences_with_several_heads_in_a_tile(lib, cuda, lengths, times, before, after, n_q, n_kv, D):
     F = lib.functional

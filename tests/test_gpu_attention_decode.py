@@ -286,3 +286,30 @@ def test_two_calls_at_once_and_refusals(lib, cuda, prefix):
         F.attention_decode(*x, prefix, out=x[1].flatten()[:x[0].numel()].view(x[0].shape))
     torch.cuda.synchronize()
     assert lib.qkv_prologue_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(160, 1, 64), (130, 1, 128)])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_groups_wider_than_a_tile(lib, cuda, n_q, n_kv, D, prefix):
+    # more query heads per key/value head than the shared prefix's kernel has rows
+    w = Batch(n_q, n_kv, D, 16, [70, 0, 33], prefix, 60)
+    w.check(lib, *w.run(lib, cuda, save_lse=True))
+
+
+def test_results_on_a_side_stream_in_a_graph(lib, cuda):
+    # a captured call on a stream forked from the capturing one
+    F = lib.functional
+    w = Batch(8, 2, 64, 16, [70, 0, 33], 150, 61)
+    x = [t.to(cuda) for t in (w.q, w.k_pool, w.v_pool, w.table, w.lengths, w.prefix_pages)]
+    want = F.attention_decode(*x, 150)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = F.attention_decode(*x, 150, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    got.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and lib.qkv_prologue_device_error(clear=True) == 0
