@@ -368,7 +368,8 @@ const void* attention_fwd_kernel(int head_dim, bool prefix);
 int attention_fwd_smem_bytes(int head_dim, bool prefix);
 int attention_fwd_threads();
 
-// Backward over whole prompts: delta, then the key/value and the query kernel.
+// Backward over whole prompts: the query kernel (and delta), then the key/value kernel
+// (and the folding kernel where splits > 1).
 struct AttnBwdArgs {
   int64_t T;
   int32_t n_q, n_kv, group;
