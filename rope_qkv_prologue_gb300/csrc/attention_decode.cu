@@ -98,11 +98,21 @@ struct DecCursor {
   int b;      // sequence
   int tile;   // tile of it
   int tiles;  // its tiles
-  __device__ __forceinline__ void settle(const AttnDecodeArgs& a) {
-    while (tile >= tiles && b + 1 < a.batch) {
-      tile -= tiles;
-      ++b;
-      tiles = dec_tiles(a, b);
+  // Whole warp, behind a sequence's last tile: to the next sequence that has any, 32 at a
+  // time (there may be many empty ones between); past the last one it stays there, at its end.
+  __device__ __forceinline__ void settle(const AttnDecodeArgs& a, int lane) {
+    if (tile < tiles) return;
+#pragma unroll 1
+    for (int s0 = b + 1; s0 < a.batch; s0 += 32) {
+      const int n = s0 + lane < a.batch ? dec_tiles(a, s0 + lane) : 0;
+      const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+      if (some) {
+        const int src = __ffs(some) - 1;
+        b = s0 + src;
+        tiles = __shfl_sync(0xffffffffu, n, src);
+        tile = 0;
+        return;
+      }
     }
   }
 };
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
     };
     auto advance = [&]() {
       if (++ld.tile < ld.tiles) return;
-      ld.settle(a);
+      ld.settle(a, lane);
       ld_keys = (uint32_t)(a.joint_len + dec_own(a, ld.b));
     };
     const int ch = lane % CH, row_ch = a.n_kv * CH;
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
       }
       if (++cu.tile == cu.tiles || t + 1 == n_tiles) {
         end();
-        cu.settle(a);
+        cu.settle(a, lane);
         first = true;
         if (t + 1 < n_tiles) begin();
       }

@@ -541,3 +541,29 @@ def test_short_sequences_with_several_heads_in_a_tile(lib, cuda, lengths, times,
     g = A.attention_bwd(f64(do), f64(q), f64(k), f64(v), cu, out_err=out_bound(ref))
     for name, got in zip(("dq", "dk", "dv"), grads):
         assert_within(f64(got), g[name], g["e_" + name] + U * np.abs(g[name]), name)
+
+
+def test_as_many_sequences_as_allowed(lib, cuda):
+    # 2^20, all but a few empty
+    F = lib.functional
+    lengths = np.zeros(2 ** 20, dtype=np.int64)
+    for at, n in ((0, 3), (500000, 200), (2 ** 20 - 2, 60), (2 ** 20 - 1, 129)):
+        lengths[at] = n
+    cu = offsets(lengths)
+    T = int(cu[-1])
+    host = inputs(T, 2, 1, 64, 1100)
+    dev = [t.to(cuda) for t in host]
+    cu_dev = torch.from_numpy(cu).to(cuda)
+    out, lse = F.attention_forward(*dev[:3], cu_dev, save_lse=True)
+    grads = F.attention_backward(dev[3], *dev[:3], out, lse, cu_dev)
+    no_error(lib)
+    few = offsets([3, 200, 60, 129])
+    x = [f64(t) for t in host]
+    ref = A.attention_fwd(*x[:3], few)
+    assert_within(f64(out), ref["out"], out_bound(ref), "out")
+    g = A.attention_bwd(x[3], *x[:3], few, out_err=out_bound(ref))
+    for name, got in zip(("dq", "dk", "dv"), grads):
+        assert_within(f64(got), g[name], g["e_" + name] + U * np.abs(g[name]), name)
+    more = torch.zeros(2 ** 20 + 2, dtype=torch.int32, device=cuda)
+    with pytest.raises(lib.QkvpError):
+        F.attention_forward(*dev[:3], more)

@@ -313,3 +313,22 @@ def test_results_on_a_side_stream_in_a_graph(lib, cuda):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want) and lib.qkv_prologue_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("prefix", [0, 130])
+def test_as_many_sequences_as_allowed(lib, cuda, prefix):
+    # 2^20, all but a few without tokens of their own
+    F = lib.functional
+    n_q, n_kv, D, size, batch = 2, 1, 64, 16, 2 ** 20
+    w = Batch(n_q, n_kv, D, size, [3, 40, 17], prefix, 70)
+    at = torch.tensor([0, 500000, batch - 1])
+    q = torch.zeros(batch, n_q, D, dtype=torch.bfloat16)
+    table, lengths = torch.zeros(batch, w.table.shape[1], dtype=torch.int32), torch.zeros(batch, dtype=torch.int32)
+    q[at], table[at], lengths[at] = w.q, w.table, w.lengths
+    x = [t.to(cuda) for t in (q, w.k_pool, w.v_pool, table, lengths, w.prefix_pages)]
+    out, lse = F.attention_decode(*x[:5], x[5] if prefix else None, prefix, save_lse=True)
+    w.check(lib, out[at.to(cuda)], lse[at.to(cuda)])
+    if not prefix:
+        rest = torch.ones(batch, dtype=torch.bool, device=cuda)
+        rest[at.to(cuda)] = False
+        assert not out[rest].any() and torch.isneginf(lse[rest]).all()
