@@ -407,6 +407,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const int head = (j ? t.head1 : t.head0) + (PREFIX ? 0 : qtr >> t.hs);
       // prompt: rows of this warp that belong to the sequence
       const int rows = PREFIX || head < t.end ? t.kv0 + t.len - row0 : 0;
+      // A row of something else (another sequence, unused memory) has no say in when its warp
+      // rescales: that would show in the other rows' last bits.
+      const bool live = PREFIX ? row < a.bpt * a.group : lane < rows;
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++done) {
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         if (i == 0) {
           m = top;
-        } else if (__any_sync(0xffffffffu, (top - m) * c > kRescale)) {  // also where m is -inf and top is not
+        } else if (__any_sync(0xffffffffu, live && (top - m) * c > kRescale)) {  // also where m is -inf and top is not
           const float m_new = fmaxf(m, top);
           const float f = m_new == m ? 1.f : ex2((m - m_new) * c);
           m = m_new;

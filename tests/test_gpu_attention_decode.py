@@ -332,3 +332,19 @@ def test_as_many_sequences_as_allowed(lib, cuda, prefix):
         rest = torch.ones(batch, dtype=torch.bool, device=cuda)
         rest[at.to(cuda)] = False
         assert not out[rest].any() and torch.isneginf(lse[rest]).all()
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(5, 1, 64), (14, 2, 128), (6, 2, 64)])
+def test_the_same_bits_whatever_ran_before(lib, cuda, n_q, n_kv, D):
+    # groups whose rows do not fill the prefix kernel's tiles: what an earlier kernel left
+    # in shared memory is in the rest, and does not show
+    F = lib.functional
+    w = Batch(n_q, n_kv, D, 16, [30] * 60, 2000, 80)
+    want = w.run(lib, cuda, save_lse=True)
+    w.check(lib, *want)
+    other = Batch(128 * n_kv, n_kv, D, 16, [3, 5], 400, 81)
+    for factor in (1.0, 1e4, float("nan")):
+        other.q.copy_(torch.randn_like(other.q.float()) * factor)
+        for _ in range(3):
+            other.run(lib, cuda)
+            assert all(torch.equal(a, b) for a, b in zip(w.run(lib, cuda, save_lse=True), want))
