@@ -552,8 +552,9 @@ QKVP_API int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t b
  * qkv_prologue_device_error -- read (and with clear != 0, reset) the
  * library's device error word on the current device. Bit 1 means a
  * pipelined kernel's bounded wait on its shared-memory pipeline gave up
- * (after 2 s) and the kernel returned early: the results of that launch are
- * invalid. Synchronises with the device (it copies the word to the host).
+ * (after 2 s; in the attention calls after 2 s in which a CTA fetched nothing)
+ * and the kernel returned early: the results of that launch are invalid.
+ * Synchronises with the device (it copies the word to the host).
  * ------------------------------------------------------------------------- */
 QKVP_API int qkv_prologue_device_error(int clear, int* value);
 

@@ -27,35 +27,49 @@ __device__ __forceinline__ int attn_swz(int row, int chunk) { return row * 128 +
 // fetches were a quarter of the stalls (60 sequences of 67 rows). So what is in
 // many places, like a wait, is kept short.
 
-// Bounded wait, every lane of the calling warp: with one lane polling and the
-// others waiting for it, the kernels measured up to half slower. Gives up after
-// kWaitLimitNs, and at once when another warp already gave up (*fail): after one
-// timeout the rest of the kernel runs through without waiting, every loop still
-// ends, and attn_report tells the host.
-// A wait by parity sees a phase only until the next one completes. So for every
-// barrier here, whatever completes phase k + 1 is behind each waiter's having seen
-// phase k: a producer that could run ahead waits for something that the waiter does
-// after its wait.
+// What the waits of a CTA watch, in shared memory.
+struct __align__(8) AttnWatch {
+  uint32_t fail;  // a wait gave up
+  uint32_t beat;  // when this CTA last began to fetch a tile (low word of the nanosecond timer)
+};
 __device__ __forceinline__ uint32_t global_ns_lo() {
   uint32_t t;
   asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
   return t;
 }
-__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+__device__ __forceinline__ void attn_beat(AttnWatch* watch) {
+  *(volatile uint32_t*)&watch->beat = global_ns_lo();
+}
+
+// Bounded wait, every lane of the calling warp: with one lane polling and the
+// others waiting for it, the kernels measured up to half slower. What is bounded is
+// the time without progress, not the wait: some warps have nothing to do while the
+// others work on a long item (the finder, the softmax of a slot that is idle), for
+// seconds where a sequence has very many blocks or a group very many heads. The
+// rings are a few tiles deep, so as long as anything moves the loader does. Gives up
+// kWaitLimitNs after the CTA's last beat, and at once when another warp already gave
+// up: after one timeout the rest of the kernel runs through without waiting, every
+// loop still ends, and attn_report tells the host.
+// A wait by parity sees a phase only until the next one completes. So for every
+// barrier here, whatever completes phase k + 1 is behind each waiter's having seen
+// phase k: a producer that could run ahead waits for something that the waiter does
+// after its wait.
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, AttnWatch* watch) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint32_t t0 = global_ns_lo();
+  uint32_t fail, beat;
   do {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*fail) return false;
-  } while (global_ns_lo() - t0 < (uint32_t)kWaitLimitNs);
-  *fail = 1;
+    asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];" : "=r"(fail), "=r"(beat) : "r"(smem_addr(watch)));
+    if (fail) return false;
+  } while ((int32_t)(global_ns_lo() - beat) < (int32_t)kWaitLimitNs);  // (a beat newer than the timer read is no age)
+  *(volatile uint32_t*)&watch->fail = 1;
   return false;
 }
 static_assert(kWaitLimitNs < (1ull << 31), "the waits count nanoseconds in 32 bits");
 
 // At the kernel's end, behind a barrier.
-__device__ __forceinline__ void attn_report(volatile int* fail, int* err) {
-  if (threadIdx.x == 0 && *fail) atomicOr(err, kErrWaitTimeout);
+__device__ __forceinline__ void attn_report(const AttnWatch* watch, int* err) {
+  if (threadIdx.x == 0 && *(const volatile uint32_t*)&watch->fail) atomicOr(err, kErrWaitTimeout);
 }
 
 // True in one lane of the (converged) warp, always the same one.

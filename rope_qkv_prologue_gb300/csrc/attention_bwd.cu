@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       x_full[2], y_full, p_full, ds_full, acc_done, acc_free, st_full[kStatStages], st_empty[kStatStages],
       it_full[kBwdSched], it_empty[kBwdSched], mma_done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_fail;
+  __shared__ AttnWatch s_watch;
   __shared__ BwdItem s_item[kBwdSched];
   __shared__ int s_cache[AttnOrder::kCached];
   // key/value kernel: -lse log2(e) and -delta of the streamed rows; query kernel: the
@@ -143,19 +143,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(&it_empty[s], KV ? 11 : 10);  // loader, issuer, 8 arithmetic warps, the statistics' loader
     }
     mbar_init(&mma_done, 1);
-    s_fail = 0;
+    s_watch.fail = 0;
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(&s_tmem, 512);
   griddep_wait();
   griddep_launch_dependents();
+  if (threadIdx.x == 0) attn_beat(&s_watch);  // (not before: the launches before this one may take any time)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  volatile int* fail = &s_fail;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = attn_wait(bar, parity, fail);
+    const bool ok = attn_wait(bar, parity, &s_watch);
     __syncwarp();
     return ok;
   };
@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t n = which ? S2 : S1, s = it % n;
             uint64_t* full = which ? &b2_full[s] : &b1_full[s];
             wait(which ? &b2_empty[s] : &b1_empty[s], ((it / n) & 1) ^ 1);  // (the first time round it passes)
+            if (lane == 0) attn_beat(&s_watch);
             unsigned char* dst = base + (which ? SM::kB2 : SM::kB1) + s * SM::kTile;
             const CUtensorMap* map = KV ? (which ? &tmap_do : &tmap_q) : (which ? &tmap_v : &tmap_k);
             const int piece = KV ? 32 << t.hs : kAttnRows;  // rows of a head in the tile
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
-  attn_report(fail, a.err);
+  attn_report(&s_watch, a.err);
 }
 
 // dv and dk from the parts of each group's query heads, in their order. Rows of the

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __shared__ __align__(8) uint64_t full[ST], empty[ST], tail_bar, mma_done, q_full[2], q_empty[2], s_full[2],
       s_read[2], p_full[2], o_done[2], o_free[2], it_full[kFwdSched], it_empty[kFwdSched];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_fail;
+  __shared__ AttnWatch s_watch;
   __shared__ FwdItem s_item[kFwdSched];
   __shared__ int s_cache[PREFIX ? 1 : AttnOrder::kCached];
   __shared__ int s_slot[PREFIX ? kAttnMaxChunk / 8 : 1];  // pool row of each page box of the key range, or -1
@@ -126,20 +126,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&it_full[j], 1);
       mbar_init(&it_empty[j], 10);  // loader, issuer, 8 softmax warps
     }
-    s_fail = 0;
+    s_watch.fail = 0;
     s_whole = 0xffffffffu;
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(&s_tmem, 512);
   griddep_wait();
   griddep_launch_dependents();
+  if (threadIdx.x == 0) attn_beat(&s_watch);  // (not before: the launches before this one may take any time)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  volatile int* fail = &s_fail;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = attn_wait(bar, parity, fail);
+    const bool ok = attn_wait(bar, parity, &s_watch);
     __syncwarp();
     return ok;
   };
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const int i = i2 >> 1, which = i2 & 1;
           const uint32_t s = it % ST;
           wait(&empty[s], ((it / ST) & 1) ^ 1);
+          if (lane == 0) attn_beat(&s_watch);
           unsigned char* dst = base + SM::kRing + s * SM::kTile;
           const CUtensorMap* map = which ? &tmap_v : &tmap_k;
           const bool part = PREFIX ? ((s_whole >> i) & 1) == 0 : kAttnRows * (i + 1) > t.len;
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
-  attn_report(fail, a.err);
+  attn_report(&s_watch, a.err);
 }
 
 const void* attention_fwd_kernel(int head_dim, bool prefix) {

@@ -591,3 +591,26 @@ def test_what_the_next_sequence_holds_does_not_show(lib, cuda, n_q, n_kv, D):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
         want = got
     no_error(lib)
+
+
+def test_a_work_item_of_more_than_two_seconds(lib, cuda):
+    # 640 blocks of 128 rows and 4094 query heads over one key/value head: the first keys'
+    # block goes through 2.6 million blocks of queries at about 1 us, longer than any wait may
+    # last without progress, while the warp that finds work has nothing to do. All is zero but the
+    # last row: with k = v = 0 and lse = 12 ln 2 every p is 2^-12, so that
+    # dv_j = 4094 2^-12 dout and ds = -2^-12 dout . out = -2^-6 in that row.
+    F = lib.functional
+    n_q, D, T = 4094, 64, 640 * 128
+    if torch.cuda.mem_get_info()[0] < 110 * 2 ** 30:
+        pytest.skip("needs 110 GB of device memory")
+    x = torch.zeros(T, n_q, D, dtype=torch.bfloat16, device=cuda)  # q, dout and out
+    x[-1] = 1.0
+    k, v = (torch.zeros(T, 1, D, dtype=torch.bfloat16, device=cuda) for _ in range(2))
+    lse = torch.full((n_q, T), 12 * float(np.log(2.0)), dtype=torch.float32, device=cuda)
+    cu_dev = torch.tensor([0, T], dtype=torch.int32, device=cuda)
+    dq, dk, dv = F.attention_backward(x, x, k, v, x, lse, cu_dev)
+    no_error(lib)
+    assert not dq.any()
+    # one rounding to bf16 (p and ds are powers of two, their sums exact in fp32)
+    for got, exact in ((dv, n_q / 4096), (dk, -n_q / 64 * D ** -0.5)):
+        assert float((got.double() - exact).abs().max()) <= U * abs(exact)
