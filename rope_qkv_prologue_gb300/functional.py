@@ -275,13 +275,18 @@ def _current_stream(device):
 def _on_stream(stream, like, call, *args):
     """call(*args) with `stream` (a torch.cuda.Stream or a raw handle) as the current
     one: what it allocates is then that stream's memory, in its order. The results may
-    be used on the caller's stream (after it waited), so their memory is kept for it too."""
+    be used on the caller's stream (after it waited), so their memory is kept for it too;
+    and the arguments' memory is kept for `stream`, so that the caller may drop them
+    before it has read them."""
     if not like.is_cuda:
         raise ValueError("the tensors must live on a CUDA device")
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, like.device)
     if stream.device != like.device:
         raise ValueError(f"the tensors are on {like.device}, the stream is of {stream.device}")
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
     with torch.cuda.stream(stream):
         got = call(*args)
     home = torch.cuda.current_stream(like.device)

@@ -614,3 +614,40 @@ def test_a_work_item_of_more_than_two_seconds(lib, cuda):
     # one rounding to bf16 (p and ds are powers of two, their sums exact in fp32)
     for got, exact in ((dv, n_q / 4096), (dk, -n_q / 64 * D ** -0.5)):
         assert float((got.double() - exact).abs().max()) <= U * abs(exact)
+
+
+def test_inputs_dropped_after_a_call_on_another_stream(lib, cuda):
+    # what a call on a given stream reads is not handed out again while it may still be
+    # reading: the inputs are gone when the call returns, their sizes are taken and filled on
+    # the caller's stream, and the other stream has not begun
+    F = lib.functional
+    cu_dev = torch.tensor([0, 700, 1500], dtype=torch.int32, device=cuda)
+    q, k, v, do = (t.to(cuda) for t in inputs(1500, 16, 8, 64, 1300))
+    out, lse = F.attention_forward(q, k, v, cu_dev, save_lse=True)
+    grads = F.attention_backward(do, q, k, v, out, lse, cu_dev)
+    pool = torch.randn(300, 16, 8, 64, device=cuda).to(torch.bfloat16)
+    rows = torch.randn(64, 16, 64, device=cuda).to(torch.bfloat16)
+    table = torch.randperm(300, device=cuda)[:256].to(torch.int32).view(64, 4)
+    lengths = torch.full((64,), 50, dtype=torch.int32, device=cuda)
+    one = F.attention_decode(rows, pool, pool, table, lengths)
+    side = torch.cuda.Stream()
+    calls = {
+        "forward": ((q, k, v), lambda s, *t: F.attention_forward(*t, cu_dev, stream=s), (out,)),
+        "backward": ((do, q, k, v, out, lse), lambda s, *t: F.attention_backward(*t, cu_dev, stream=s), grads),
+        "decode": ((rows, pool), lambda s, r, p: F.attention_decode(r, p, p, table, lengths, stream=s), (one,)),
+    }
+    for name, (given, call, want) in calls.items():
+        for stream in (side, side.cuda_stream):
+            torch.cuda.synchronize()
+            temporary = [t.clone() for t in given]
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(200_000_000)  # about 0.1 s
+            got = call(stream, *temporary)
+            del temporary
+            junk = [torch.full_like(t, float("nan")) for t in given for _ in range(2)]
+            side.synchronize()
+            got = got if isinstance(got, tuple) else (got,)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+            del junk, got
+    no_error(lib)
