@@ -480,6 +480,7 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
         lse = torch.empty((B, n_q), dtype=torch.float32, device=dev)
     if B == 0:
         return (out, lse) if save_lse else out
+    here = _current_stream(dev)  # before a size is asked for: it is the current device's
     if workspace is None:
         need = _decode_workspace(n_q, n_kv, D, B, page_size, max_pages, prefix_len, dev.index)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
@@ -487,7 +488,7 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
     C.qkv_attention_decode(_heads(n_q, n_kv, D), B, q, k_pool, v_pool, num_pages, page_size, page_table, max_pages,
                            page_table.stride(0) if B > 1 else max_pages, lengths, prefix_pages, prefix_len,
                            0.0 if scale is None else scale, out, lse, dev_status, workspace,
-                           workspace.numel() * workspace.element_size(), _current_stream(dev))
+                           workspace.numel() * workspace.element_size(), here)
     return (out, lse) if save_lse else out
 
 

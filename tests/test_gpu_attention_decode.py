@@ -348,3 +348,16 @@ def test_the_same_bits_whatever_ran_before(lib, cuda, n_q, n_kv, D):
         for _ in range(3):
             other.run(lib, cuda)
             assert all(torch.equal(a, b) for a, b in zip(w.run(lib, cuda, save_lse=True), want))
+
+
+def test_a_refused_call_leaves_no_workspace_size_behind(lib, cuda, monkeypatch):
+    # sizes are kept by device: not the current device's under the tensors' one
+    F = lib.functional
+    x = Batch(4, 2, 64, 16, [37], 0, 70, wide=5)
+    kept = F._decode_workspace.cache_info().currsize
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: cuda.index + 1)
+        with pytest.raises(ValueError):
+            x.run(lib, cuda)
+    assert F._decode_workspace.cache_info().currsize == kept
+    x.check(lib, *x.run(lib, cuda, save_lse=True))
