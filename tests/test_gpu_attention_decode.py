@@ -361,3 +361,18 @@ def test_a_refused_call_leaves_no_workspace_size_behind(lib, cuda, monkeypatch):
             x.run(lib, cuda)
     assert F._decode_workspace.cache_info().currsize == kept
     x.check(lib, *x.run(lib, cuda, save_lse=True))
+
+
+def test_one_sequence_in_more_parts_than_factors_fit(lib, cuda):
+    # 70,000 keys of one head: more than 1024 partial results, joined in two rounds
+    x = Batch(4, 1, 64, 64, [70000], 0, 71)
+    x.check(lib, *x.run(lib, cuda, save_lse=True))
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(4, 1, 64), (3, 1, 128)])
+def test_one_long_sequence_among_many_short_ones(lib, cuda, n_q, n_kv, D):
+    # nearly all parts are one sequence's: one warp joins them, 128 a round
+    lengths = [3 + i % 7 for i in range(200)]
+    lengths[77] = 60000
+    x = Batch(n_q, n_kv, D, 64, lengths, 0, 72)
+    x.check(lib, *x.run(lib, cuda, save_lse=True))
