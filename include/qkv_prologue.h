@@ -463,6 +463,8 @@ QKVP_API int qkv_newton_schulz_plan(const qkvp_layout* layout, int64_t count, in
  * out and lse overlap none of q, k, v and each other (QKVP_ERR_VALUE).
  * A NaN or infinity in a row of k or v reaches the rows that attend it, and may
  * reach the other rows of its sequence in the same block of 128.
+ * Every row attends all rows of its sequence up to its own: no sliding window,
+ * no attention sink. A layer that has them is another function than this.
  * ------------------------------------------------------------------------- */
 QKVP_API int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t batch, const int32_t* cu_seqlens,
                                const void* q, const void* k, const void* v, float scale, uint32_t flags, void* out,
@@ -477,9 +479,13 @@ QKVP_API int qkv_attention_fwd(const qkvp_layout* layout, int64_t T, int32_t bat
  *     dv_j = sum_i p_ij dout_i,
  * dk and dv summed over the n_q / n_kv query heads of their group. p and ds are
  * rounded to bf16 as operands of products with fp32 accumulation; one rounding
- * of each gradient to bf16. Deterministic (no atomics).
+ * of each gradient to bf16. Deterministic (no atomics): the same bits for the
+ * same T, batch and offsets. (How dk and dv are divided into sums depends on T and
+ * batch, so other sequences in the pack can show in their last bits, not in dq.)
  *
- * T, batch, cu_seqlens, q, k, v, scale: as the forward's.
+ * T, batch, cu_seqlens, q, k, v, scale: as the forward's. A NaN or infinity in a
+ *             row reaches gradients of the rows it attends or is attended by, and
+ *             may reach the other rows of its sequence in the same block of 128.
  * dout, out   bf16 [T, n_q, head_dim]; lse float32 [n_q, T]: the forward's.
  * flags       QKVP_ZERO_REST: rows of no sequence of dq, dk and dv become zero
  *             instead of being left as they are.

@@ -34,11 +34,12 @@
 //               zeros in the rows of no sequence, where the caller asked for them;
 //   warps 4-11  the arithmetic between the products, and the results' stores.
 //
-// Measured: 8192 tokens, 32 over 8 heads of 128: query kernel 535 us, key/value kernel
-// 657 us, tensor pipe 65 and 71 % active (1580 us with the forward: 0.64 of the library
-// rate in the five products that a backward needs). 4096 tokens in 11 sequences, 128 over
-// 16 heads of 64: 168 and 150 us; a block's products have N = 64 there, which run at half
-// the rate, and one block is in flight.
+// Measured: 8192 tokens, 32 over 8 heads of 128: query kernel 528 us, key/value kernel
+// 655 us, tensor pipe 67 and 72 % active (1580 us with the forward, 1664 in a steady loop:
+// 0.64 and 0.61 of the library rate in the five products that a backward needs). 4096 tokens
+// in 11 sequences, 128 over 16 heads of 64: 167 and 152 us, tensor pipe 22 and 33 % active;
+// some 3400 and 3100 cycles a block, with one block in flight: X, P, dP, dS and the products
+// in turn, all eight warps on the same block.
 #include "attention.cuh"
 
 namespace qkvp {
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (t.n == 1) {
             // Rows with few keys: delta = sum_j p_ij dp_ij is summed here, from the p and
             // dp that it is subtracted from. dout . out with out rounded to bf16 is off
-            // by 2^-9 of |dout| |out|, which a sharp row of few keys, whose ds are small
+            // by up to 2^-8 of |dout| |out|, which a sharp row of few keys, whose ds are small
             // differences, would feel; in later blocks it is lost among the others.
             float s0 = 0.f, s1 = 0.f;
 #pragma unroll

@@ -24,7 +24,7 @@
 // even, else two consecutive row blocks of a head. Of a sequence of at most 64 (32) rows a
 // slot holds two (four) heads of the group: a block costs a CTA some 6700
 // cycles however few of its rows are there (60 sequences of 67 rows, 128 over 16 heads of
-// 64: 122 us with a head a slot, 92 so). Sharing halves what K and V
+// 64: 122 us with a head a slot, 92 so when that was built). Sharing halves what K and V
 // cost to fetch (64 KiB per 2 x 8.4 MFLOP at head_dim 128), and while one slot's
 // softmax runs, the tensor cores work on the other's products:
 //   warp 0      loads Q, K, V tiles with TMA into 128B-swizzled shared memory;
@@ -43,12 +43,13 @@
 // memory): their scores are replaced, not added to, and their V rows are zeroed
 // in shared memory, since 0 times a NaN is not 0.
 //
-// Measured: 16384 tokens, 32 over 8 heads of 128: 1362 us, 1616 TFLOP/s (0.85 of a large
+// Measured: 16384 tokens, 32 over 8 heads of 128: 1356 us, 1622 TFLOP/s (0.85 of a large
 // library product's burst rate), tensor pipe 68 % active; what is missing is the time
 // between a block's scores and its weights, with registers and tensor memory full at two
-// blocks. 8192 tokens in 23 sequences, 64 over 8 heads of 64: 96 us, bound by the chain of
-// steps that a block of few keys goes through. The prefix of 32768 keys for 64 sequences,
-// 32 over 8 heads of 128: 35 us (134 MB, 34 GFLOP), 13 of them ramp-up and results.
+// blocks. 8192 tokens in 23 sequences, 64 over 8 heads of 64: 93 us, bound by the chain of
+// steps that a block of few keys goes through (some 3900 cycles a pair of blocks). The
+// prefix of 32768 keys for 64 sequences, 32 over 8 heads of 128: 35 us (134 MB, 34 GFLOP),
+// 13 of them ramp-up and results.
 #include "attention.cuh"
 
 namespace qkvp {

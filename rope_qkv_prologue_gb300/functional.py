@@ -331,11 +331,13 @@ def _check_status(dev_status, device):
 def attention_forward(q, k, v, cu_seqlens, scale=None, save_lse=False, out=None, dev_status=None, stream=None):
     """Causal attention over packed sequences: q [T, n_q, D], k, v [T, n_kv, D]
     bf16 as prologue_forward returns them, cu_seqlens int32 [batch + 1] on the
-    device (sequence s is the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1).
+    device (sequence s is the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1). A row
+    attends all of its sequence up to itself: no sliding window, no sink.
     Returns out [T, n_q, D], or (out, lse [n_q, T] float32) with save_lse.
     scale defaults to D ** -0.5 (0 is that too). Rows of no sequence are zero in an out made
     here, and left as they are in one given (lse: -inf, in both). The work is
-    queued on `stream` (default: the current one)."""
+    queued on `stream` (default: the current one), which waits for nothing by
+    itself; the arguments may be dropped as soon as the call returns."""
     if stream is not None:
         return _on_stream(stream, q, attention_forward, q, k, v, cu_seqlens, scale, save_lse, out, dev_status)
     _check_qkv(q, k, v)
@@ -372,7 +374,7 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=None, workspac
     the upstream gradient dout [T, n_q, D] bf16, from the forward's out and lse.
     Rows of no sequence get zero gradients. `workspace` (a device tensor of
     attention_backward_workspace_bytes bytes) is allocated here when not given.
-    The work is queued on `stream` (default: the current one)."""
+    The work is queued on `stream` (default: the current one), as attention_forward's."""
     if stream is not None:
         return _on_stream(stream, q, attention_backward, dout, q, k, v, out, lse, cu_seqlens, scale, workspace,
                           dev_status)
@@ -443,7 +445,7 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
     Returns out [B, n_q, D], or (out, lse [B, n_q] float32) with save_lse.
     `workspace` (a device tensor of attention_decode_workspace_bytes bytes) is
     allocated here when not given. The work is queued on `stream` (default: the
-    current one)."""
+    current one), as attention_forward's."""
     if stream is not None:
         return _on_stream(stream, q, attention_decode, q, k_pool, v_pool, page_table, lengths, prefix_pages,
                           prefix_len, scale, save_lse, out, workspace, dev_status)
