@@ -285,7 +285,7 @@ def _on_stream(stream, like, call, *args):
     if stream.device != like.device:
         raise ValueError(f"the tensors are on {like.device}, the stream is of {stream.device}")
     for t in args:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
+        if isinstance(t, torch.Tensor) and t.device == like.device:  # (what lies elsewhere is refused)
             t.record_stream(stream)
     with torch.cuda.stream(stream):
         got = call(*args)
