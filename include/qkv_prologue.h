@@ -110,9 +110,25 @@ enum {
                               GPT-OSS). w_q / w_k may be NULL; the backward
                               reads neither q_pre nor k_pre and has no weight
                               gradients (dw_q / dw_k may be NULL, untouched). */
-  QKVP_ZERO_REST = 32      /* attention over packed sequences: rows of no
+  QKVP_ZERO_REST = 32,     /* attention over packed sequences: rows of no
                               sequence are set to zero instead of left alone  */
+  QKVP_ROPE_PAIRS = 64,    /* GQA layouts: rotate adjacent pairs of values
+                              (2i, 2i + 1) instead of (i, i + R/2)            */
+  QKVP_ROPE_PART = 128     /* GQA layouts: rotate only the first R =
+                              layout->rope_dim values of each head            */
 };
+
+/* Rotary layouts (GQA; qkv_prologue_fwd, _pool_write, _bwd and their forms, the
+ * 8-bit pool write). The first R values of each q and k head are rotated, R =
+ * head_dim or, with QKVP_ROPE_PART, layout->rope_dim (a multiple of 16, at most
+ * head_dim); the values behind them only see the norm. For i < R/2,
+ * theta = pos * inv_freq_i with inv_freq_i = rope_base^(-2 i / R) or the
+ * variant's table, which then has R/2 entries, and with (a, b) = (y_i, y_{i+R/2}),
+ * or (y_{2i}, y_{2i+1}) with QKVP_ROPE_PAIRS,
+ *     o_a = f (a cos(theta) - b sin(theta)),  o_b = f (b cos(theta) + a sin(theta)),
+ * f = the variant's rope_scale (values that are not rotated are not scaled). The
+ * backward rotates the gradients back. QKVP_NOPE excludes both flags
+ * (QKVP_ERR_FLAGS); the fused projection and the LATENT layout have neither. */
 
 /* Options of the GQAttention variant (the *_ex entry points; NULL = none).
  *
@@ -122,8 +138,8 @@ enum {
  * frequencies (Llama 3's and YaRN's scalings) and YaRN multiplies cos and sin
  * by a factor; both only change the inputs below, the rotation is the same.
  *
- * inv_freq    HOST array of head_dim / 2 (LATENT: rope_dim / 2) float64
- *             frequencies replacing rope_base^(-2 i / D), or NULL. Finite.
+ * inv_freq    HOST array of head_dim / 2 (LATENT and QKVP_ROPE_PART: rope_dim / 2)
+ *             float64 frequencies replacing rope_base^(-2 i / D), or NULL. Finite.
  * rope_scale  factor on cos and sin (o = scale * R(theta) y); 0 means 1.
  * bias        DEVICE float32 [(n_q + 2 n_kv) * head_dim], 16-byte aligned, in
  *             the packed row's own order (the fused linear's output bias), or

@@ -44,6 +44,8 @@ QKVP_ACCUMULATE_DW = 4
 QKVP_FORCE_GENERIC = 8
 QKVP_NORM_OFF = 16
 QKVP_ZERO_REST = 32
+QKVP_ROPE_PAIRS = 64
+QKVP_ROPE_PART = 128
 
 QKVP_DEV_BAD_PAGE = 1
 QKVP_DEV_BAD_OFFSET = 2

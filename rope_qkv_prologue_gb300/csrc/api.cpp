@@ -480,6 +480,27 @@ void gqa_items(int64_t T, int cpt, int chunks_per_thread, int64_t* item_chunks, 
 
 int64_t bwd_parts(int64_t n_items) { return n_items < kMaxBwdParts ? n_items : kMaxBwdParts; }
 
+// The rotary layout of a GQA call: how many values of each head are rotated, and how
+// they pair up.
+struct Rotary {
+  int dim = 0;
+  bool adjacent = false;
+  bool other = false;  // not halves of the whole head
+};
+
+int check_rotary(const qkvp_layout* L, uint32_t flags, Rotary* r) {
+  r->dim = L->head_dim;
+  if (!(flags & (QKVP_ROPE_PAIRS | QKVP_ROPE_PART))) return QKVP_OK;
+  if (flags & QKVP_NOPE) return QKVP_ERR_FLAGS;
+  if (flags & QKVP_ROPE_PART) {
+    if (L->rope_dim < 16 || L->rope_dim > L->head_dim || L->rope_dim % 16) return QKVP_ERR_SHAPE;
+    r->dim = L->rope_dim;
+  }
+  r->adjacent = (flags & QKVP_ROPE_PAIRS) != 0;
+  r->other = r->adjacent || r->dim != L->head_dim;
+  return QKVP_OK;
+}
+
 // The GQAttention variant options of a call, checked.
 struct Variant {
   const double* inv_freq = nullptr;
@@ -503,6 +524,13 @@ int check_variant(const qkvp_variant* v, int rope_dim, bool gqa, Variant* out) {
     out->bias = v->bias;
   }
   return QKVP_OK;
+}
+
+// The table of a GQA call's rotary layout.
+void rope_table(double base, const Rotary& rot, const double* inv_freq, float scale, RopeTable* out) {
+  rope_table(base, rot.dim, inv_freq, scale, out);
+  out->half = (int16_t)(rot.dim / 2);
+  out->adjacent = rot.adjacent;
 }
 
 // Bias gradient limits: the pipelined backward keeps at most kBiasMaxSteps
@@ -678,13 +706,15 @@ static int gqa_forward(const qkvp_layout* L, const qkvp_variant* variant, int64_
   Gqa g;
   QKVP_TRY(check_gqa(L, T, &g));
   const uint32_t allowed = (pool ? (uint32_t)QKVP_NOPE : (uint32_t)(QKVP_NOPE | QKVP_SAVE_PRE)) |
-                           (uint32_t)(QKVP_FORCE_GENERIC | QKVP_NORM_OFF);
+                           (uint32_t)(QKVP_FORCE_GENERIC | QKVP_NORM_OFF | QKVP_ROPE_PAIRS | QKVP_ROPE_PART);
   if (flags & ~allowed) return QKVP_ERR_FLAGS;
+  Rotary rot;
+  QKVP_TRY(check_rotary(L, flags, &rot));
   const bool rope = !(flags & QKVP_NOPE);
   const bool save = (flags & QKVP_SAVE_PRE) != 0;
   const bool norm = !(flags & QKVP_NORM_OFF);
   Variant vr;
-  QKVP_TRY(check_variant(variant, L->head_dim, true, &vr));
+  QKVP_TRY(check_variant(variant, rot.dim, true, &vr));
   QKVP_TRY(check_scalars(eps, rope_base, rope && !vr.inv_freq));
   if (!packed || (norm && (!w_q || !w_k)) || !q || (rope && !pos)) return QKVP_ERR_NULL;
   if (pool) {
@@ -735,9 +765,9 @@ static int gqa_forward(const qkvp_layout* L, const qkvp_variant* variant, int64_
   a.page_size = page_size;
   a.dev_status = dev_status;
   a.bias = vr.bias;
-  if (rope) rope_table(rope_base, L->head_dim, vr.inv_freq, vr.scale, &a.rope);
+  if (rope) rope_table(rope_base, rot, vr.inv_freq, vr.scale, &a.rope);
 
-  const FwdVariant var{L->head_dim, L->kind == QKVP_SECTIONED, rope, save, pool, norm, vr.bias != nullptr};
+  const FwdVariant var{L->head_dim, L->kind == QKVP_SECTIONED, rope, save, pool, norm, vr.bias != nullptr, rot.other};
   const int bias_bytes = vr.bias ? a.cpt * 8 * (int)sizeof(float) : 0;
   size_t smem = 0;
   if (!(flags & QKVP_FORCE_GENERIC) &&
@@ -974,7 +1004,11 @@ size_t qkv_prologue_bwd_workspace_size(const qkvp_layout* layout, int64_t T) {
 
 size_t qkv_prologue_bwd_workspace_size_ex(const qkvp_layout* layout, const qkvp_variant* variant, int64_t T) {
   Variant vr;
-  if (!layout || check_variant(variant, layout->head_dim, true, &vr) != QKVP_OK) return 0;
+  // (no frequency is looked at: the size does not depend on them, and how many there are
+  // is the flags' to say)
+  qkvp_variant v = variant ? *variant : qkvp_variant{};
+  v.inv_freq = nullptr;
+  if (!layout || check_variant(&v, layout->head_dim, true, &vr) != QKVP_OK) return 0;
   // The size does not depend on the norm flag: a norm-off call needs less.
   return bwd_workspace(layout, vr, true, T);
 }
@@ -986,13 +1020,16 @@ int qkv_prologue_bwd_ex(const qkvp_layout* layout, const qkvp_variant* variant, 
                         size_t workspace_bytes, void* stream) {
   Gqa g;
   QKVP_TRY(check_gqa(layout, T, &g));
-  if (flags & ~(uint32_t)(QKVP_NOPE | QKVP_ACCUMULATE_DW | QKVP_FORCE_GENERIC | QKVP_NORM_OFF))
+  if (flags & ~(uint32_t)(QKVP_NOPE | QKVP_ACCUMULATE_DW | QKVP_FORCE_GENERIC | QKVP_NORM_OFF | QKVP_ROPE_PAIRS |
+                          QKVP_ROPE_PART))
     return QKVP_ERR_FLAGS;
+  Rotary rot;
+  QKVP_TRY(check_rotary(layout, flags, &rot));
   const bool rope = !(flags & QKVP_NOPE);
   const bool accumulate = (flags & QKVP_ACCUMULATE_DW) != 0;
   const bool norm = !(flags & QKVP_NORM_OFF);
   Variant vr;
-  QKVP_TRY(check_variant(variant, layout->head_dim, true, &vr));
+  QKVP_TRY(check_variant(variant, rot.dim, true, &vr));
   const bool bias = vr.bias != nullptr;
   QKVP_TRY(check_scalars(eps, rope_base, rope && !vr.inv_freq));
   if (!dq || !dk || !dv || !dpacked || (rope && !pos)) return QKVP_ERR_NULL;
@@ -1050,9 +1087,9 @@ int qkv_prologue_bwd_ex(const qkvp_layout* layout, const qkvp_variant* variant, 
   a.dpacked = static_cast<uint4*>(dpacked);
   a.row_stride16 = g.stride / 8;
   a.bias = vr.bias;
-  if (rope) rope_table(rope_base, hd, vr.inv_freq, vr.scale, &a.rope);
+  if (rope) rope_table(rope_base, rot, vr.inv_freq, vr.scale, &a.rope);
 
-  BwdVariant var{hd, layout->kind == QKVP_SECTIONED, rope, norm, bias, 0};
+  BwdVariant var{hd, layout->kind == QKVP_SECTIONED, rope, norm, bias, 0, rot.other};
   const int64_t heads_qkv = norm ? (2 * layout->n_q + 3 * layout->n_kv) : (layout->n_q + 2 * layout->n_kv);
   const int64_t token_bytes = heads_qkv * hd * 2;
   const StreamShape shape = bwd_stream_shape();

@@ -92,14 +92,20 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// Sum of squares of this lane's 8 values, then over the CPH lanes of the head.
+// The sum over a head as a function object, for the code that two lane orders share.
 template <int CPH>
-__device__ __forceinline__ float head_sum_sq(const float2 (&x)[4]) {
+struct HeadSum {
+  __device__ __forceinline__ float operator()(float v) const { return head_sum<CPH>(v); }
+};
+
+// Sum of squares of this lane's 8 values, then over the lanes of the head.
+template <class Sum>
+__device__ __forceinline__ float head_sum_sq(const float2 (&x)[4], const Sum& sum) {
   float2 a = __fmul2_rn(x[0], x[0]);
   a = __ffma2_rn(x[1], x[1], a);
   a = __ffma2_rn(x[2], x[2], a);
   a = __ffma2_rn(x[3], x[3], a);
-  return head_sum<CPH>(a.x + a.y);
+  return sum(a.x + a.y);
 }
 
 // x + b on pairs (the qkv bias of the GQAttention variant, added before
@@ -114,11 +120,12 @@ __device__ __forceinline__ void add_bias_pairs(float2 (&x)[4], const float2 (&b)
 // (y = x when NORM is off), then rotate-half: o = y * cos + y_partner * ssin,
 // where the partner (element +- D/2) is in lane ^ CPH/2 and ssin = -sin for
 // the first half of the head, +sin for the second.
-template <int CPH, bool ROPE, bool NORM>
+template <int CPH, bool ROPE, bool NORM, class Sum = HeadSum<CPH>>
 __device__ __forceinline__ void chunk_forward(const float2 (&x)[4], const float2 (&w)[4], float eps, float inv_hd,
-                                              const float2 (&c)[4], const float2 (&ssin)[4], float2 (&y)[4]) {
+                                              const float2 (&c)[4], const float2 (&ssin)[4], float2 (&y)[4],
+                                              const Sum& sum = Sum()) {
   if (NORM) {
-    const float r = rsqrtf(fmaf(head_sum_sq<CPH>(x), inv_hd, eps));
+    const float r = rsqrtf(fmaf(head_sum_sq(x, sum), inv_hd, eps));
     const float2 rr = f2(r, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(__fmul2_rn(x[i], rr), w[i]);
@@ -143,11 +150,11 @@ __device__ __forceinline__ void chunk_forward(const float2 (&x)[4], const float2
 //   dx = r (w g) - x (r^3 / D) sum(x w g)
 // Also returns gx = g * x (the weight gradient is gx * r) and r. Without the
 // norm dx = g (x, w, gx and r unused).
-template <int CPH, bool ROPE, bool NORM>
+template <int CPH, bool ROPE, bool NORM, class Sum = HeadSum<CPH>>
 __device__ __forceinline__ void chunk_backward(const float2 (&d)[4], const float2 (&x)[4], const float2 (&w)[4],
                                                float eps, float inv_hd, const float2 (&c)[4],
                                                const float2 (&ssin)[4], float2 (&dx)[4], float2 (&gx)[4],
-                                               float& r_out) {
+                                               float& r_out, const Sum& sum = Sum()) {
   float2 g[4], wg[4];
   if (ROPE) {
 #pragma unroll
@@ -174,7 +181,7 @@ __device__ __forceinline__ void chunk_backward(const float2 (&d)[4], const float
     sq = __ffma2_rn(x[i], x[i], sq);
     dt = __ffma2_rn(x[i], wg[i], dt);
   }
-  const float ss = head_sum<CPH>(sq.x + sq.y), dot = head_sum<CPH>(dt.x + dt.y);
+  const float ss = sum(sq.x + sq.y), dot = sum(dt.x + dt.y);
   const float r = rsqrtf(fmaf(ss, inv_hd, eps));
   const float kx = r * r * r * dot * inv_hd;
   const float2 rr = f2(r, r), nk = f2(-kx, -kx);
@@ -311,6 +318,119 @@ __device__ __forceinline__ void pair_backward(const float2 (&dlo)[4], const floa
   }
   r_out = r;
 }
+
+// ------------------------------------------------ other rotary layouts ----
+//
+// The first 2 * half values of a head are rotated, in pairs (i, i + half) or, when
+// `adjacent`, (2i, 2i + 1); the others pass through (entries f >= half of a cos/sin
+// table are 1, 0). A unit of the head is still two of its chunks: in adjacent pairs
+// a chunk holds its own partners and the unit is (e, e + CPH/2) as ever; in halves
+// of the first half / 8 * 2 chunks it is (e, e + half / 8), and the chunks behind
+// them go two by two. So everything around the rotation stays the same, and it costs
+// nothing beside the memory traffic.
+struct RotUnit {
+  int lo;    // the unit's first chunk
+  int dist;  // its second chunk is lo + dist
+  int fa;    // table entries of its coefficients 0..3 (adjacent: of the first chunk's pairs)
+  int fb;    // ... 4..7 (adjacent: of the second chunk's pairs)
+};
+template <int CPH>
+__device__ __forceinline__ RotUnit rot_unit(int e, const RopeTable& rope) {
+  constexpr int PPH = CPH / 2;
+  if (rope.adjacent) return RotUnit{e, PPH, 4 * e, 4 * (e + PPH)};
+  const int r = rope.half >> 3;
+  if (e < r) return RotUnit{e, r, 8 * e, 8 * e + 4};
+  return RotUnit{r + e, PPH - r, 8 * e, 8 * e + 4};
+}
+
+// A unit's values rotated; back: by the negative angles. c[0..3] and c[4..7] as
+// pairs are the coefficients at fa and fb.
+__device__ __forceinline__ void rotate_adjacent(float2 (&y)[4], const float2 (&c)[2], const float2 (&sn)[2], float sign) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float ci = (i & 1) ? c[i >> 1].y : c[i >> 1].x;
+    const float si = sign * ((i & 1) ? sn[i >> 1].y : sn[i >> 1].x);
+    y[i] = __ffma2_rn(y[i], f2(ci, ci), __fmul2_rn(f2(y[i].y, y[i].x), f2(-si, si)));
+  }
+}
+__device__ __forceinline__ void rotate_unit(float2 (&lo)[4], float2 (&hi)[4], const float2 (&c)[4], const float2 (&sn)[4],
+                                            bool adjacent, float sign) {
+  if (adjacent) {
+    const float2 ca[2] = {c[0], c[1]}, cb[2] = {c[2], c[3]}, sa[2] = {sn[0], sn[1]}, sb[2] = {sn[2], sn[3]};
+    rotate_adjacent(lo, ca, sa, sign);
+    rotate_adjacent(hi, cb, sb, sign);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 s = __fmul2_rn(sn[i], f2(sign, sign)), ns = __fmul2_rn(sn[i], f2(-sign, -sign));
+    const float2 a = __ffma2_rn(lo[i], c[i], __fmul2_rn(hi[i], ns));
+    const float2 b = __ffma2_rn(hi[i], c[i], __fmul2_rn(lo[i], s));
+    lo[i] = a;
+    hi[i] = b;
+  }
+}
+
+// The same for kernels that hold one chunk per lane: where the lanes of a head find
+// their partners. Head sums are added in the order of the units (a chunk and its
+// partner, then xor rounds over the units), so that both kinds of kernel give the
+// same bits.
+template <int CPH>
+struct RotLane {
+  static constexpr int ROUNDS = CPH == 8 ? 2 : 3;
+  int partner;       // lane of the unit's other chunk
+  int next[ROUNDS];  // lane of the chunk on the same side of unit u ^ 1, u ^ 2, ...
+  int fa, fb;        // as in RotUnit (adjacent: fa alone, this chunk's pairs)
+  float side;        // -1 in a unit's first chunk, +1 in its second
+  __device__ __forceinline__ RotLane(int lane, const RopeTable& rope) {
+    constexpr int PPH = CPH / 2;
+    const int ch = lane & (CPH - 1), base = lane - ch;
+    int u = 0;
+    bool second = false;
+    for (int e = 0; e < PPH; ++e) {
+      const RotUnit k = rot_unit<CPH>(e, rope);
+      if (k.lo == ch || k.lo + k.dist == ch) {
+        u = e;
+        second = k.lo != ch;
+      }
+    }
+    const RotUnit me = rot_unit<CPH>(u, rope);
+    partner = base + (second ? me.lo : me.lo + me.dist);
+    fa = rope.adjacent && second ? me.fb : me.fa;
+    fb = rope.adjacent ? fa : me.fb;
+    side = second ? 1.f : -1.f;
+#pragma unroll
+    for (int o = 0; o < ROUNDS; ++o) {
+      const RotUnit k = rot_unit<CPH>(u ^ (1 << o), rope);
+      next[o] = base + k.lo + (second ? k.dist : 0);
+    }
+  }
+  __device__ __forceinline__ float operator()(float v) const {
+    v += __shfl_sync(0xffffffffu, v, partner);
+#pragma unroll
+    for (int o = 0; o < ROUNDS; ++o) v += __shfl_sync(0xffffffffu, v, next[o]);
+    return v;
+  }
+  // y rotated (sign 1) or rotated back (-1), with the table row's cos and sin.
+  __device__ __forceinline__ void rotate(float2 (&y)[4], const float* s_cos, const float* s_sin, bool adjacent,
+                                         float sign) const {
+    const float4 c0 = *reinterpret_cast<const float4*>(s_cos + fa), c1 = *reinterpret_cast<const float4*>(s_cos + fb);
+    const float4 s0 = *reinterpret_cast<const float4*>(s_sin + fa), s1 = *reinterpret_cast<const float4*>(s_sin + fb);
+    if (adjacent) {
+      const float2 c[2] = {f2(c0.x, c0.y), f2(c0.z, c0.w)}, sn[2] = {f2(s0.x, s0.y), f2(s0.z, s0.w)};
+      rotate_adjacent(y, c, sn, sign);
+      return;
+    }
+    const float2 c[4] = {f2(c0.x, c0.y), f2(c0.z, c0.w), f2(c1.x, c1.y), f2(c1.z, c1.w)};
+    const float2 sn[4] = {f2(s0.x, s0.y), f2(s0.z, s0.w), f2(s1.x, s1.y), f2(s1.z, s1.w)};
+    const float2 sg = f2(side * sign, side * sign);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 yp = f2(__shfl_sync(0xffffffffu, y[i].x, partner), __shfl_sync(0xffffffffu, y[i].y, partner));
+      y[i] = __ffma2_rn(y[i], c[i], __fmul2_rn(yp, __fmul2_rn(sn[i], sg)));
+    }
+  }
+};
 
 // ------------------------------------------------------ MLA latent rows ----
 //

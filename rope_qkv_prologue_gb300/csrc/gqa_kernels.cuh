@@ -73,8 +73,9 @@ __device__ __forceinline__ void read_cos_sin(const float* s_cos, const float* s_
   for (int i = 0; i < 4; ++i) ssin[i] = __fmul2_rn(sn[i], sg);
 }
 
-// Fill the shared cos/sin table for tokens t_first .. t_first + ntok - 1.
-template <int HALF>
+// Fill the shared cos/sin table for tokens t_first .. t_first + ntok - 1 (ROT: entries
+// behind the rotated ones are 1, 0).
+template <int HALF, bool ROT = false>
 __device__ __forceinline__ void fill_rope_table(const int32_t* pos, const RopeTable& rope,
                                                 int64_t t_first, int ntok, float* s_cos,
                                                 float* s_sin) {
@@ -82,7 +83,7 @@ __device__ __forceinline__ void fill_rope_table(const int32_t* pos, const RopeTa
     const int tl = i / HALF;
     const int f = i % HALF;
     float c, s;
-    rope_cos_sin(pos[t_first + tl], rope.turns[f], rope.scale, &c, &s);
+    rope_cos_sin(pos[t_first + tl], rope.turns[f], ROT && f >= rope.half ? 1.f : rope.scale, &c, &s);
     s_cos[i] = c;
     s_sin[i] = s;
   }
@@ -90,7 +91,7 @@ __device__ __forceinline__ void fill_rope_table(const int32_t* pos, const RopeTa
 
 // ------------------------------------------------------------- forward ----
 
-template <int HD, bool SECTIONED, bool ROPE, bool SAVE, bool POOL, bool NORM, bool BIAS>
+template <int HD, bool SECTIONED, bool ROPE, bool SAVE, bool POOL, bool NORM, bool BIAS, bool ROT = false>
 __global__ void __launch_bounds__(kThreads, 2) qkvp_fwd_kernel(const FwdArgs a) {
   griddep_wait();
   using G = Geom<HD>;
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_fwd_kernel(const FwdArgs a) 
   const int e = tid & (CPH - 1);
   const float sign = e < CPH / 2 ? -1.f : 1.f;
   const int f0 = (e & (CPH / 2 - 1)) * 8;
+  const RotLane<CPH> rot(ROT ? tid & 31 : 0, a.rope);
   float2 wq[4], wk[4];
   if (NORM) {
     load_pairs(a.w_q + 8 * e, wq);
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_fwd_kernel(const FwdArgs a) 
     }
 
     __syncthreads();  // readers of the previous item's table are done
-    if (ROPE) fill_rope_table<HALF>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
+    if (ROPE) fill_rope_table<HALF, ROT>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
     if (POOL) {
       for (int i = tid; i < ntok; i += kThreads) {
         const int32_t pg = a.page[t_first + i], of = a.offset[t_first + i];
@@ -165,8 +167,13 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_fwd_kernel(const FwdArgs a) 
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = NORM ? (role == kRoleQ ? wq[i] : wk[i]) : f2(1.f, 1.f);
-      if (ROPE) read_cos_sin<HALF>(s_cos, s_sin, tl, f0, sign, c, ssin);
-      chunk_forward<CPH, ROPE, NORM>(x, w, a.eps, a.inv_head_dim, c, ssin, y);
+      if constexpr (ROT) {
+        chunk_forward<CPH, false, NORM>(x, w, a.eps, a.inv_head_dim, c, ssin, y, rot);
+        rot.rotate(y, s_cos + tl * HALF, s_sin + tl * HALF, a.rope.adjacent != 0, 1.f);
+      } else {
+        if (ROPE) read_cos_sin<HALF>(s_cos, s_sin, tl, f0, sign, c, ssin);
+        chunk_forward<CPH, ROPE, NORM>(x, w, a.eps, a.inv_head_dim, c, ssin, y);
+      }
       if (!valid) continue;
 
       const int64_t t = t_first + tl;
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_fwd_kernel(const FwdArgs a) 
 // of float sums in shared memory (no two threads share a chunk; the order is
 // fixed), written out as one row of `db_partials`.
 
-template <int HD, bool SECTIONED, bool ROPE, bool NORM, bool BIAS>
+template <int HD, bool SECTIONED, bool ROPE, bool NORM, bool BIAS, bool ROT = false>
 __global__ void __launch_bounds__(kThreads, 2) qkvp_bwd_kernel(const BwdArgs a) {
   griddep_wait();
   using G = Geom<HD>;
@@ -229,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_bwd_kernel(const BwdArgs a) 
   const int e = tid & (CPH - 1);
   const float sign = e < CPH / 2 ? 1.f : -1.f;  // R(theta)^T: the partner term flips sign
   const int f0 = (e & (CPH / 2 - 1)) * 8;
+  const RotLane<CPH> rot(ROT ? tid & 31 : 0, a.rope);
   float2 wq[4], wk[4], accq[4], acck[4];
   if (NORM) {
     load_pairs(a.w_q + 8 * e, wq);
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_bwd_kernel(const BwdArgs a) 
     }
 
     __syncthreads();
-    if (ROPE) fill_rope_table<HALF>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
+    if (ROPE) fill_rope_table<HALF, ROT>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
     __syncthreads();
 
 #pragma unroll
@@ -303,8 +311,16 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_bwd_kernel(const BwdArgs a) 
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = NORM ? (role == kRoleQ ? wq[i] : wk[i]) : f2(1.f, 1.f);
-      if (ROPE) read_cos_sin<HALF>(s_cos, s_sin, tl, f0, sign, c, ssin);
-      chunk_backward<CPH, ROPE, NORM>(d, x, w, a.eps, a.inv_head_dim, c, ssin, dx, gx, r);
+      if constexpr (ROT) {
+        float2 g[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] = d[i];
+        rot.rotate(g, s_cos + tl * HALF, s_sin + tl * HALF, a.rope.adjacent != 0, -1.f);
+        chunk_backward<CPH, false, NORM>(g, x, w, a.eps, a.inv_head_dim, c, ssin, dx, gx, r, rot);
+      } else {
+        if (ROPE) read_cos_sin<HALF>(s_cos, s_sin, tl, f0, sign, c, ssin);
+        chunk_backward<CPH, ROPE, NORM>(d, x, w, a.eps, a.inv_head_dim, c, ssin, dx, gx, r);
+      }
       if (!valid) continue;
 
       if (NORM) {

@@ -51,7 +51,7 @@ __device__ __forceinline__ void fill_split_weights(const float* w_q, const float
 }
 
 template <int HD>
-__device__ __forceinline__ void load_split_weights(const float* s_w, int role, int e, float2 (&w)[4]) {
+__device__ __forceinline__ void load_split_weights(const float* s_w, int role, int e, float2 (&w)[4]) {  // e: chunk
   constexpr int CPH = HD / 8;
   const float* p = s_w + (role == kRoleQ ? 0 : HD) + 4 * e;
   const float4 a = *reinterpret_cast<const float4*>(p);
@@ -82,7 +82,9 @@ constexpr int stream_max_regs(int ncw, int cps) {
 // forward and the norm-off backward do not: there the position load paces the
 // reads, and without it they go out in bursts that interleave worse with the
 // writes (forward 147 -> 162 us; Llama 3 backward 67.5 -> 70.1 us).
-template <int HALF, bool ROPE, bool POOL, bool STAGE_POS = false, bool POS_AHEAD = false, class LoadTile>
+// ROT: entries of the table behind the rotated ones are 1, 0.
+template <int HALF, bool ROPE, bool POOL, bool STAGE_POS = false, bool POS_AHEAD = false, bool ROT = false,
+          class LoadTile>
 __device__ __forceinline__ void stream_producer(unsigned char* smem, int hd, int tpt, int stages,
                                                 int stage_bytes, int64_t n_tiles, int64_t T,
                                                 const int32_t* pos, const RopeTable& rope,
@@ -131,7 +133,7 @@ __device__ __forceinline__ void stream_producer(unsigned char* smem, int hd, int
         const int tl = i / HALF, f = i - (i / HALF) * HALF;
         const int32_t pt = pos_ahead ? __shfl_sync(0xffffffffu, pos_cur, tl) : pos[t0 + tl];
         float c, sn;
-        rope_cos_sin(pt, rope.turns[f], rope.scale, &c, &sn);
+        rope_cos_sin(pt, rope.turns[f], ROT && f >= rope.half ? 1.f : rope.scale, &c, &sn);
         tab[i] = c;
         tab[tpt * HALF + i] = sn;
       }
@@ -174,12 +176,13 @@ __device__ __forceinline__ void stream_producer(unsigned char* smem, int hd, int
 // float4 pieces (lo values 0-3, lo 4-7, hi 0-3, hi 4-7), piece k at
 // s_b[k * upt + j]. A warp's lanes hold consecutive units, so each 16-byte
 // read covers consecutive words (no bank conflicts).
-template <int HD>
-__device__ __forceinline__ void fill_bias(const float* bias, int upt, float4* s_b) {
+template <int HD, bool ROT = false>
+__device__ __forceinline__ void fill_bias(const float* bias, int upt, float4* s_b, const RopeTable& rope) {
   constexpr int CPH = HD / 8, PPH = CPH / 2;
   for (int i = threadIdx.x; i < 4 * upt; i += blockDim.x) {
     const int k = i / upt, j = i - k * upt;
-    const int chunk = (j / PPH) * CPH + (j % PPH) + (k >= 2 ? PPH : 0);
+    const RotUnit ru = ROT ? rot_unit<CPH>(j % PPH, rope) : RotUnit{j % PPH, PPH, 0, 0};
+    const int chunk = (j / PPH) * CPH + ru.lo + (k >= 2 ? ru.dist : 0);
     s_b[i] = reinterpret_cast<const float4*>(bias)[2 * chunk + (k & 1)];
   }
 }
@@ -192,10 +195,23 @@ __device__ __forceinline__ void load_bias_unit(const float4* s_b, int upt, int j
   hi[0] = f2(c.x, c.y); hi[1] = f2(c.z, c.w); hi[2] = f2(d.x, d.y); hi[3] = f2(d.z, d.w);
 }
 
+// cos or sin of a unit's pairs from a table row.
+template <bool ROT>
+__device__ __forceinline__ void load_unit_angles(const float* row, const RotUnit& ru, float2 (&c)[4]) {
+  if (!ROT) {
+    load_pairs(row + ru.fa, c);
+    return;
+  }
+  const float4 a = *reinterpret_cast<const float4*>(row + ru.fa), b = *reinterpret_cast<const float4*>(row + ru.fb);
+  c[0] = f2(a.x, a.y); c[1] = f2(a.z, a.w); c[2] = f2(b.x, b.y); c[3] = f2(b.z, b.w);
+}
+
 // NORM: RMSNorm of q and k (off: split -> RoPE only). BIAS: the qkv bias,
 // staged in shared memory after the ring, is added to every input chunk first;
 // v then stores the rounded biased value instead of a copy of the input.
-template <int HD, bool SECTIONED, bool ROPE, bool SAVE, bool POOL, bool NORM, bool BIAS, int NCW, int CPS>
+// ROT (with ROPE): another rotary layout; a unit is then the chunks that rot_unit names.
+template <int HD, bool SECTIONED, bool ROPE, bool SAVE, bool POOL, bool NORM, bool BIAS, int NCW, int CPS,
+          bool ROT = false>
 __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(const FwdArgs a) {
   griddep_wait();
   using G = Geom<HD>;
@@ -215,13 +231,13 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
     mbar_init_fence();
   }
   if (NORM) fill_split_weights<HD>(a.w_q, a.w_k, s_w);
-  if (BIAS) fill_bias<HD>(a.bias, a.cpt / 2, s_b);
+  if (BIAS) fill_bias<HD, ROT>(a.bias, a.cpt / 2, s_b, a.rope);
   __syncthreads();
 
   if (threadIdx.x >= NCT) {
     const uint32_t row_bytes = (uint32_t)a.cpt * 16u;
     const bool dense = a.sg.dense != 0;
-    stream_producer<HALF, ROPE, POOL>(
+    stream_producer<HALF, ROPE, POOL, false, false, ROT>(
         smem, HD, tpt, stages, stage_bytes, a.sg.n_tiles, a.T, a.pos, a.rope, a.page, a.offset, a.num_pages,
         // L2 policy of the loads, measured at T = 16384: with the pre-norm save
         // normal aging is faster (149.2 -> 147.8 us), without it evict-first
@@ -249,6 +265,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
   const int tl = ct / tpg;              // token of the tile this thread works on
   const int ig = ct - tl * tpg;         // index inside the group
   const int e = ig & (PPH - 1);         // the same for every step (tpg is a multiple of PPH)
+  const RotUnit ru = ROT ? rot_unit<CPH>(e, a.rope) : RotUnit{e, PPH, 8 * e, 8 * e + 4};
   // Per step: output head, role and packed-head parity, fixed for the whole kernel.
   uint32_t info[MAXM];
 #pragma unroll
@@ -275,8 +292,8 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
     const float* tab = reinterpret_cast<const float*>(smem + StreamSmem::tables(HD) + s * StreamSmem::table_stride(HD, tpt));
     float2 c2[4], s2[4];
     if (ROPE) {
-      load_pairs(tab + tl * HALF + 8 * e, c2);
-      load_pairs(tab + tpt * HALF + tl * HALF + 8 * e, s2);
+      load_unit_angles<ROT>(tab + tl * HALF, ru, c2);
+      load_unit_angles<ROT>(tab + tpt * HALF + tl * HALF, ru, s2);
     }
     int32_t slot = -1;
     if (POOL) slot = reinterpret_cast<const int32_t*>(tab + 2 * tpt * HALF)[tl];
@@ -293,13 +310,13 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
       const bool in_row = j < upt;
       // stage chunks of the pair; odd heads read hi first so that the two heads a
       // quarter-warp covers fall in different shared-memory banks
-      const int clo = in_row ? ((j >> LOG_PPH) * CPH + e) : 0;
+      const int clo = in_row ? ((j >> LOG_PPH) * CPH + ru.lo) : 0;
       const bool odd = (info[m] >> 18) & 1u;
-      const uint4 first = sx[odd ? clo + PPH : clo];
-      const uint4 second = sx[odd ? clo : clo + PPH];
+      const uint4 first = sx[odd ? clo + ru.dist : clo];
+      const uint4 second = sx[odd ? clo : clo + ru.dist];
       const uint4 xlo = odd ? second : first, xhi = odd ? first : second;
       const int role = (int)((info[m] >> 16) & 3u);
-      const int olo = (int)(info[m] & 0xffffu) * CPH + e;
+      const int olo = (int)(info[m] & 0xffffu) * CPH + ru.lo;
       float2 lo[4], hi[4], wlo[4], whi[4], ylo[4], yhi[4];
       unpack_pairs(xlo, lo);
       unpack_pairs(xhi, hi);
@@ -310,10 +327,11 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
         add_bias_pairs(hi, bhi);
       }
       if (NORM) {
-        load_split_weights<HD>(s_w, role, e, wlo);
-        load_split_weights<HD>(s_w, role, e + PPH, whi);
+        load_split_weights<HD>(s_w, role, ru.lo, wlo);
+        load_split_weights<HD>(s_w, role, ru.lo + ru.dist, whi);
       }
-      pair_forward<CPH, ROPE, NORM>(lo, hi, wlo, whi, a.eps, a.inv_head_dim, c2, s2, ylo, yhi);
+      pair_forward<CPH, ROPE && !ROT, NORM>(lo, hi, wlo, whi, a.eps, a.inv_head_dim, c2, s2, ylo, yhi);
+      if (ROT) rotate_unit(ylo, yhi, c2, s2, a.rope.adjacent != 0, 1.f);
       if (!valid || !in_row) continue;
       // Plain contiguous forward: cache-streaming stores (measured faster on GB300
       // at every size tried); with the pre-norm save, or into a pool that
@@ -325,23 +343,23 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
       };
       if (role == kRoleQ) {
         put(qrow + olo, pack_pairs(ylo));
-        put(qrow + olo + PPH, pack_pairs(yhi));
+        put(qrow + olo + ru.dist, pack_pairs(yhi));
         if (SAVE) {
           st_stream(qprow + olo, xlo);
-          st_stream(qprow + olo + PPH, xhi);
+          st_stream(qprow + olo + ru.dist, xhi);
         }
       } else if (role == kRoleK) {
         if (!POOL || slot >= 0) {
           put(krow + olo, pack_pairs(ylo));
-          put(krow + olo + PPH, pack_pairs(yhi));
+          put(krow + olo + ru.dist, pack_pairs(yhi));
         }
         if (SAVE) {
           st_stream(kprow + olo, xlo);
-          st_stream(kprow + olo + PPH, xhi);
+          st_stream(kprow + olo + ru.dist, xhi);
         }
       } else if (!POOL || slot >= 0) {
         put(vrow + olo, BIAS ? pack_pairs(lo) : xlo);
-        put(vrow + olo + PPH, BIAS ? pack_pairs(hi) : xhi);
+        put(vrow + olo + ru.dist, BIAS ? pack_pairs(hi) : xhi);
       }
     }
     __syncwarp();
@@ -367,7 +385,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
 // the same token slot in every tile and keeps their running sums in registers
 // (the host keeps steps <= kBiasMaxSteps); at the end the token slots' sums
 // are added in a fixed order into the CTA's row of db_partials.
-template <int HD, bool SECTIONED, bool ROPE, bool NORM, bool BIAS, int NCW, int CPS, int STEPS>
+template <int HD, bool SECTIONED, bool ROPE, bool NORM, bool BIAS, int NCW, int CPS, int STEPS, bool ROT = false>
 __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(const BwdArgs a) {
   griddep_wait();
   using G = Geom<HD>;
@@ -394,11 +412,11 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
     mbar_init_fence();
   }
   if (NORM) fill_split_weights<HD>(a.w_q, a.w_k, s_w);
-  if (NORM && BIAS) fill_bias<HD>(a.bias, a.cpt / 2, s_b);
+  if (NORM && BIAS) fill_bias<HD, ROT>(a.bias, a.cpt / 2, s_b, a.rope);
   __syncthreads();
 
   if (threadIdx.x >= NCT) {
-    stream_producer<HALF, ROPE, false, false, NORM>(
+    stream_producer<HALF, ROPE, false, false, NORM, ROT>(
         smem, HD, tpt, stages, stage_bytes, a.sg.n_tiles, a.T, a.pos, a.rope, nullptr, nullptr, 0, 0, nullptr, a.err,
         true, [&](unsigned char* dst, int64_t t0, int ntok, uint64_t* bar, uint64_t pol) {
           const uint32_t qb = (uint32_t)qc * 16u, kb = (uint32_t)kc * 16u;
@@ -424,6 +442,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
   const int tl = ct / tpg;
   const int ig = ct - tl * tpg;
   const int e = ig & (PPH - 1);
+  const RotUnit ru = ROT ? rot_unit<CPH>(e, a.rope) : RotUnit{e, PPH, 8 * e, 8 * e + 4};
   // Per step: stage chunk of d_lo (low 16 bits) and of x_lo (high 16 bits);
   // 2 role bits and 1 parity bit (of the output head) per step.
   uint32_t offs[MAXM];
@@ -439,13 +458,13 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
     if (!in_row) {
       d_off = x_off = 0;  // any chunk of the stage; the step is skipped
     } else if (role == kRoleQ) {
-      d_off = (tl * a.n_q + oh) * CPH + e;
+      d_off = (tl * a.n_q + oh) * CPH + ru.lo;
       x_off = sec_qp + d_off;
     } else if (role == kRoleK) {
-      d_off = sec_dk + (tl * a.n_kv + oh) * CPH + e;
-      x_off = sec_kp + (tl * a.n_kv + oh) * CPH + e;
+      d_off = sec_dk + (tl * a.n_kv + oh) * CPH + ru.lo;
+      x_off = sec_kp + (tl * a.n_kv + oh) * CPH + ru.lo;
     } else {
-      d_off = sec_dv + (tl * a.n_kv + oh) * CPH + e;
+      d_off = sec_dv + (tl * a.n_kv + oh) * CPH + ru.lo;
       x_off = d_off;  // unused
     }
     offs[m] = d_off | (x_off << 16);
@@ -478,8 +497,8 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
     const float* tab = reinterpret_cast<const float*>(smem + StreamSmem::tables(HD) + s * StreamSmem::table_stride(HD, tpt));
     float2 c2[4], s2[4];
     if (ROPE) {
-      load_pairs(tab + tl * HALF + 8 * e, c2);
-      load_pairs(tab + tpt * HALF + tl * HALF + 8 * e, s2);
+      load_unit_angles<ROT>(tab + tl * HALF, ru, c2);
+      load_unit_angles<ROT>(tab + tpt * HALF + tl * HALF, ru, s2);
     }
     uint4* drow = a.dpacked + t * a.row_stride16;
 
@@ -491,11 +510,11 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
       const bool odd = (odds >> m) & 1u;
       const int dl = (int)(offs[m] & 0xffffu), xl = (int)(offs[m] >> 16);
       // odd output heads read hi first (different shared-memory banks)
-      const uint4 d1 = sx[odd ? dl + PPH : dl], d2 = sx[odd ? dl : dl + PPH];
+      const uint4 d1 = sx[odd ? dl + ru.dist : dl], d2 = sx[odd ? dl : dl + ru.dist];
       uint4 x1 = d1, x2 = d2;
       if (NORM) {
-        x1 = sx[odd ? xl + PPH : xl];
-        x2 = sx[odd ? xl : xl + PPH];
+        x1 = sx[odd ? xl + ru.dist : xl];
+        x2 = sx[odd ? xl : xl + ru.dist];
       }
       const uint4 dlo = odd ? d2 : d1, dhi = odd ? d1 : d2;
       float2 dl2[4], dh2[4], xl2[4], xh2[4], wlo[4], whi[4], dxlo[4], dxhi[4], gxlo[4], gxhi[4];
@@ -511,13 +530,25 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
           add_bias_pairs(xl2, blo);
           add_bias_pairs(xh2, bhi);
         }
-        load_split_weights<HD>(s_w, role, e, wlo);
-        load_split_weights<HD>(s_w, role, e + PPH, whi);
+        load_split_weights<HD>(s_w, role, ru.lo, wlo);
+        load_split_weights<HD>(s_w, role, ru.lo + ru.dist, whi);
       }
-      pair_backward<CPH, ROPE, NORM>(dl2, dh2, xl2, xh2, wlo, whi, a.eps, a.inv_head_dim, c2, s2, dxlo, dxhi,
-                                     gxlo, gxhi, r);
+      if constexpr (ROT) {
+        float2 gl2[4], gh2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          gl2[i] = dl2[i];
+          gh2[i] = dh2[i];
+        }
+        rotate_unit(gl2, gh2, c2, s2, a.rope.adjacent != 0, -1.f);
+        pair_backward<CPH, false, NORM>(gl2, gh2, xl2, xh2, wlo, whi, a.eps, a.inv_head_dim, c2, s2, dxlo, dxhi,
+                                        gxlo, gxhi, r);
+      } else {
+        pair_backward<CPH, ROPE, NORM>(dl2, dh2, xl2, xh2, wlo, whi, a.eps, a.inv_head_dim, c2, s2, dxlo, dxhi,
+                                       gxlo, gxhi, r);
+      }
       const bool live = valid && j < upt;
-      const int plo = (j >> LOG_PPH) * CPH + e;  // packed-row chunk of lo
+      const int plo = (j >> LOG_PPH) * CPH + ru.lo;  // packed-row chunk of lo
       if (PERSTEP) {
         // Selects and predicated stores instead of a branch per step: the
         // steps stay one block of straight-line code, so the arithmetic of
@@ -533,7 +564,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
         }
         if (live) {
           st_keep(drow + plo, role == kRoleV ? dlo : pack_pairs(dxlo));
-          st_keep(drow + plo + PPH, role == kRoleV ? dhi : pack_pairs(dxhi));
+          st_keep(drow + plo + ru.dist, role == kRoleV ? dhi : pack_pairs(dxhi));
         }
         continue;
       }
@@ -558,7 +589,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
         }
       }
       st_keep(drow + plo, role == kRoleV ? dlo : pack_pairs(dxlo));
-      st_keep(drow + plo + PPH, role == kRoleV ? dhi : pack_pairs(dxhi));
+      st_keep(drow + plo + ru.dist, role == kRoleV ? dhi : pack_pairs(dxhi));
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
@@ -582,9 +613,9 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
         for (int m = 0; m < MAXM; ++m) {
           const int j = ig + tpg * m;
           if (m >= steps || j >= upt) break;
-          const int plo = (j >> LOG_PPH) * CPH + e;
+          const int plo = (j >> LOG_PPH) * CPH + ru.lo;
           float2* lo = reinterpret_cast<float2*>(red + 8 * plo);
-          float2* hi = reinterpret_cast<float2*>(red + 8 * (plo + PPH));
+          float2* hi = reinterpret_cast<float2*>(red + 8 * (plo + ru.dist));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             lo[i] = g == 0 ? dbl[m][i] : __fadd2_rn(lo[i], dbl[m][i]);
@@ -635,13 +666,13 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
     }
   }
   const int warp = ct >> 5;
-  if (lane < PPH) {
+  if (lane < PPH) {  // (lane is the thread's e: its unit's chunks)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      s_red[warp][0][lane * 8 + i] = ql[i];
-      s_red[warp][0][(lane + PPH) * 8 + i] = qh[i];
-      s_red[warp][1][lane * 8 + i] = kl[i];
-      s_red[warp][1][(lane + PPH) * 8 + i] = kh[i];
+      s_red[warp][0][ru.lo * 8 + i] = ql[i];
+      s_red[warp][0][(ru.lo + ru.dist) * 8 + i] = qh[i];
+      s_red[warp][1][ru.lo * 8 + i] = kl[i];
+      s_red[warp][1][(ru.lo + ru.dist) * 8 + i] = kh[i];
     }
   }
   asm volatile("bar.sync 1, %0;" ::"r"(NCT) : "memory");  // consumer warps only

@@ -9,17 +9,18 @@
 namespace qkvp {
 namespace inst {
 
-// Forward, pipelined (STREAM) or general, for one head_dim and norm setting.
-template <int HD, bool NORM, bool STREAM>
+// Forward, pipelined (STREAM) or general, for one head_dim and norm setting. ROT:
+// the other rotary layouts (always with RoPE).
+template <int HD, bool NORM, bool STREAM, bool ROT = false>
 struct FwdPick {
   template <bool S, bool R, bool SV, bool P, bool B>
   static const void* get() {
     if constexpr (STREAM) {
       constexpr StreamShape sh = fwd_stream_shape(SV);
       return reinterpret_cast<const void*>(
-          &qkvp_fwd_stream_kernel<HD, S, R, SV, P, NORM, B, sh.warps, sh.ctas_per_sm>);
+          &qkvp_fwd_stream_kernel<HD, S, R, SV, P, NORM, B, sh.warps, sh.ctas_per_sm, ROT>);
     } else {
-      return reinterpret_cast<const void*>(&qkvp_fwd_kernel<HD, S, R, SV, P, NORM, B>);
+      return reinterpret_cast<const void*>(&qkvp_fwd_kernel<HD, S, R, SV, P, NORM, B, ROT>);
     }
   }
   template <bool S, bool R, bool B>
@@ -32,21 +33,22 @@ struct FwdPick {
     return v.bias ? dest<S, R, true>(v) : dest<S, R, false>(v);
   }
   static const void* pick(const FwdVariant& v) {
+    if constexpr (ROT) return v.sectioned ? bias<true, true>(v) : bias<false, true>(v);
     if (v.sectioned) return v.rope ? bias<true, true>(v) : bias<true, false>(v);
     return v.rope ? bias<false, true>(v) : bias<false, false>(v);
   }
 };
 
 // Backward, pipelined or general, for one norm setting (both head_dims).
-template <bool NORM, bool STREAM>
+template <bool NORM, bool STREAM, bool ROT = false>
 struct BwdPick {
   template <int HD, bool S, bool R, bool B>
   static const void* get() {
     if constexpr (STREAM) {
       constexpr StreamShape sh = bwd_stream_shape();
-      return reinterpret_cast<const void*>(&qkvp_bwd_stream_kernel<HD, S, R, NORM, B, sh.warps, sh.ctas_per_sm, 0>);
+      return reinterpret_cast<const void*>(&qkvp_bwd_stream_kernel<HD, S, R, NORM, B, sh.warps, sh.ctas_per_sm, 0, ROT>);
     } else {
-      return reinterpret_cast<const void*>(&qkvp_bwd_kernel<HD, S, R, NORM, B>);
+      return reinterpret_cast<const void*>(&qkvp_bwd_kernel<HD, S, R, NORM, B, ROT>);
     }
   }
   template <int HD, bool S, bool R>
@@ -55,6 +57,7 @@ struct BwdPick {
   }
   template <int HD>
   static const void* layout(const BwdVariant& v) {
+    if constexpr (ROT) return v.sectioned ? bias<HD, true, true>(v) : bias<HD, false, true>(v);
     if (v.sectioned) return v.rope ? bias<HD, true, true>(v) : bias<HD, true, false>(v);
     return v.rope ? bias<HD, false, true>(v) : bias<HD, false, false>(v);
   }
@@ -64,6 +67,9 @@ struct BwdPick {
       // the weight-gradient sums are kept per step
       constexpr StreamShape sh = bwd_stream_shape();
       if (v.steps == 2 && v.head_dim == 64 && !v.bias) {
+        if constexpr (ROT)
+          return v.sectioned ? reinterpret_cast<const void*>(&qkvp_bwd_stream_kernel<64, true, true, true, false, sh.warps, sh.ctas_per_sm, 2, true>)
+                             : reinterpret_cast<const void*>(&qkvp_bwd_stream_kernel<64, false, true, true, false, sh.warps, sh.ctas_per_sm, 2, true>);
         if (v.sectioned)
           return v.rope ? reinterpret_cast<const void*>(&qkvp_bwd_stream_kernel<64, true, true, true, false, sh.warps, sh.ctas_per_sm, 2>)
                         : reinterpret_cast<const void*>(&qkvp_bwd_stream_kernel<64, true, false, true, false, sh.warps, sh.ctas_per_sm, 2>);

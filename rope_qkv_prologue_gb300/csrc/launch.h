@@ -79,7 +79,8 @@ struct StreamGeom {
 struct RopeTable {
   uint64_t turns[kMaxHalf];  // frac(inv_freq_i / 2pi) * 2^64
   float scale;               // factor on cos and sin (1 for plain RoPE)
-  int32_t pad_;
+  int16_t half;              // rotated pairs per head (the kernels of the other rotary layouts read it)
+  int16_t adjacent;          // pairs are (2i, 2i + 1), else (i, i + half)
 };
 
 // Bias gradient of the backward: at most this many chunk pairs per consumer
@@ -199,6 +200,7 @@ struct FwdVariant {
   bool pool;
   bool norm;          // RMSNorm of q and k (off: split -> RoPE only)
   bool bias;          // qkv bias added first
+  bool rot;           // another rotary layout than halves of the whole head
 };
 
 struct BwdVariant {
@@ -208,6 +210,7 @@ struct BwdVariant {
   bool norm;
   bool bias;
   int steps;  // chunk pairs per consumer thread of the pipelined kernel (0: not known yet)
+  bool rot;   // another rotary layout than halves of the whole head
 };
 
 // Kernel entry points (host stubs for cudaLaunchKernel / occupancy queries).
@@ -225,17 +228,30 @@ const void* fwd_stream_kernel_d128_norm(const FwdVariant& v);
 const void* fwd_stream_kernel_d128_nonorm(const FwdVariant& v);
 const void* bwd_stream_kernel_norm(const BwdVariant& v);
 const void* bwd_stream_kernel_nonorm(const BwdVariant& v);
+// The same for the other rotary layouts.
+const void* fwd_rotary_kernel_norm(const FwdVariant& v);
+const void* fwd_rotary_kernel_nonorm(const FwdVariant& v);
+const void* bwd_rotary_kernel(const BwdVariant& v);
+const void* fwd_stream_rotary_kernel_norm(const FwdVariant& v);
+const void* fwd_stream_rotary_kernel_nonorm(const FwdVariant& v);
+const void* bwd_stream_rotary_kernel(const BwdVariant& v);
 
 inline const void* fwd_kernel(const FwdVariant& v) {
+  if (v.rot) return v.norm ? fwd_rotary_kernel_norm(v) : fwd_rotary_kernel_nonorm(v);
   if (v.head_dim == 64) return v.norm ? fwd_kernel_d64_norm(v) : fwd_kernel_d64_nonorm(v);
   return v.norm ? fwd_kernel_d128_norm(v) : fwd_kernel_d128_nonorm(v);
 }
 inline const void* fwd_stream_kernel(const FwdVariant& v) {
+  if (v.rot) return v.norm ? fwd_stream_rotary_kernel_norm(v) : fwd_stream_rotary_kernel_nonorm(v);
   if (v.head_dim == 64) return v.norm ? fwd_stream_kernel_d64_norm(v) : fwd_stream_kernel_d64_nonorm(v);
   return v.norm ? fwd_stream_kernel_d128_norm(v) : fwd_stream_kernel_d128_nonorm(v);
 }
-inline const void* bwd_kernel(const BwdVariant& v) { return v.norm ? bwd_kernel_norm(v) : bwd_kernel_nonorm(v); }
+inline const void* bwd_kernel(const BwdVariant& v) {
+  if (v.rot) return bwd_rotary_kernel(v);
+  return v.norm ? bwd_kernel_norm(v) : bwd_kernel_nonorm(v);
+}
 inline const void* bwd_stream_kernel(const BwdVariant& v) {
+  if (v.rot) return bwd_stream_rotary_kernel(v);
   return v.norm ? bwd_stream_kernel_norm(v) : bwd_stream_kernel_nonorm(v);
 }
 const void* dw_finalize_kernel();

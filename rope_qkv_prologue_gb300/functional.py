@@ -9,22 +9,28 @@ packed tensor in one pass.
 """
 
 import functools
+import math
 
 import torch
 
 from . import _lib as C
 
 
-def _layout_of(packed, n_q, n_kv, head_dim, kind):
+def _layout_of(packed, n_q, n_kv, head_dim, kind, rotary_dim=None):
     T = packed.shape[0]
-    row = packed.reshape(T, -1) if packed.is_contiguous() else None
-    if row is None:
+    if not packed.is_contiguous():
         raise ValueError("packed must be contiguous ([T, ...] rows)")
-    width = row.shape[1]
+    width = math.prod(packed.shape[1:])
     if width != (n_q + 2 * n_kv) * head_dim:
         raise ValueError(f"packed row has {width} values, expected (n_q + 2 n_kv) * head_dim = "
                          f"{(n_q + 2 * n_kv) * head_dim}")
-    return C.layout(kind, n_q, n_kv, head_dim), T
+    return _layout(kind, n_q, n_kv, head_dim, rotary_dim), T
+
+
+@functools.lru_cache(maxsize=1024)
+def _layout(kind, n_q, n_kv, head_dim, rotary_dim=None):
+    """The layout struct (the library only reads it)."""
+    return C.layout(kind, n_q, n_kv, head_dim, rope_dim=rotary_dim or 0)
 
 
 def _check_dev(*ts):
@@ -33,8 +39,10 @@ def _check_dev(*ts):
             raise ValueError("all tensors must live on a CUDA device")
 
 
-def _variant(bias=None, inv_freq=None, rope_scale=1.0):
+def _variant(bias=None, inv_freq=None, rope_scale=1.0, rotary_dim=None):
     """The qkvp_variant of the GQAttention options, or None for the plain call."""
+    if rotary_dim is not None and inv_freq is not None and len(inv_freq) != rotary_dim // 2:
+        raise ValueError(f"inv_freq has {len(inv_freq)} frequencies, expected rotary_dim / 2 = {rotary_dim // 2}")
     if bias is None and inv_freq is None and rope_scale in (None, 0.0, 1.0):
         return None
     if bias is not None:
@@ -45,64 +53,84 @@ def _variant(bias=None, inv_freq=None, rope_scale=1.0):
                      rope_scale=0.0 if rope_scale is None else float(rope_scale), bias=bias)
 
 
-def _flags(nope=False, save_pre=False, norm=True):
-    return (C.QKVP_NOPE if nope else 0) | (C.QKVP_SAVE_PRE if save_pre else 0) | (0 if norm else C.QKVP_NORM_OFF)
+def _flags(nope=False, save_pre=False, norm=True, rotary_dim=None, rotary_pairs=False):
+    return ((C.QKVP_NOPE if nope else 0) | (C.QKVP_SAVE_PRE if save_pre else 0) | (0 if norm else C.QKVP_NORM_OFF)
+            | (0 if rotary_dim is None else C.QKVP_ROPE_PART) | (C.QKVP_ROPE_PAIRS if rotary_pairs else 0))
 
 
 def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interleaved", eps=1e-6,
                      rope_base=500000.0, nope=False, save_pre=False, stream=None, norm=True, bias=None,
-                     inv_freq=None, rope_scale=1.0):
+                     inv_freq=None, rope_scale=1.0, rotary_dim=None, rotary_pairs=False):
     """Split + per-head RMSNorm + RoPE. Returns (q, k, v) or (q, k, v, q_pre, k_pre).
 
     The GQAttention variant options: norm=False (split -> RoPE only; w_q, w_k
     may be None), bias (float32 [(n_q + 2 n_kv) * head_dim] in the packed
     row's order, added first), inv_freq (head_dim / 2 frequencies replacing
-    rope_base**(-2i/D)) and rope_scale (factor on cos and sin)."""
+    rope_base**(-2i/D)) and rope_scale (factor on cos and sin).
+
+    Rotary layouts: rotary_dim (a multiple of 16) rotates only the first
+    rotary_dim values of each head, with frequencies rope_base**(-2i/rotary_dim)
+    or rotary_dim / 2 given ones; rotary_pairs rotates adjacent pairs (2i, 2i + 1)
+    instead of (i, i + rotary_dim / 2)."""
     _check_dev(packed, pos, w_q, w_k)
-    L, T = _layout_of(packed, n_q, n_kv, head_dim, kind)
+    L, T = _layout_of(packed, n_q, n_kv, head_dim, kind, rotary_dim)
     dev = packed.device
     q = torch.empty(T, n_q, head_dim, dtype=torch.bfloat16, device=dev)
     k = torch.empty(T, n_kv, head_dim, dtype=torch.bfloat16, device=dev)
     v = torch.empty(T, n_kv, head_dim, dtype=torch.bfloat16, device=dev)
     q_pre = torch.empty_like(q) if save_pre else None
     k_pre = torch.empty_like(k) if save_pre else None
-    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale), T, packed, pos, w_q, w_k, eps, rope_base,
-                          _flags(nope, save_pre, norm), q, k, v, q_pre, k_pre, stream)
+    if T == 0:  # an empty tensor has no address to pass
+        return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
+    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale, rotary_dim), T, packed, pos, w_q, w_k, eps, rope_base,
+                          _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
     return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
 
 
 def prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_dim=64,
                       kind="interleaved", eps=1e-6, rope_base=500000.0, nope=False, stream=None,
-                      workspace=None, norm=True, bias=None, inv_freq=None, rope_scale=1.0):
+                      workspace=None, norm=True, bias=None, inv_freq=None, rope_scale=1.0, rotary_dim=None,
+                      rotary_pairs=False):
     """Packed gradient [T, (n_q + 2 n_kv) * head_dim] and fp32 (dw_q, dw_k), plus
     the fp32 bias gradient when a bias is given: (dpacked, dw_q, dw_k[, dbias]).
-    Without the norm dw_q, dw_k are None and q_pre, k_pre, w_q, w_k may be None."""
+    Without the norm dw_q, dw_k are None and q_pre, k_pre, w_q, w_k may be None.
+    rotary_dim, rotary_pairs: the forward's rotary layout."""
     _check_dev(dq, dk, dv, q_pre, k_pre, w_q, w_k)
     T = dq.shape[0]
-    L = C.layout(kind, n_q, n_kv, head_dim)
+    L = _layout(kind, n_q, n_kv, head_dim, rotary_dim)
     dev = dq.device
-    V = _variant(bias, inv_freq, rope_scale)
+    V = _variant(bias, inv_freq, rope_scale, rotary_dim)
     dpacked = torch.empty(T, (n_q + 2 * n_kv) * head_dim, dtype=torch.bfloat16, device=dev)
     dw_q = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dw_k = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dbias = torch.empty((n_q + 2 * n_kv) * head_dim, dtype=torch.float32, device=dev) if bias is not None else None
+    if T == 0:
+        for t in (dw_q, dw_k, dbias):
+            if t is not None:
+                t.zero_()
+        return (dpacked, dw_q, dw_k, dbias) if bias is not None else (dpacked, dw_q, dw_k)
     need = C.qkv_prologue_bwd_workspace_size_ex(L, V, T)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     C.qkv_prologue_bwd_ex(L, V, T, dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, eps, rope_base,
-                          _flags(nope, False, norm), dpacked, dw_q, dw_k, dbias, workspace, need, stream)
+                          _flags(nope, False, norm, rotary_dim, rotary_pairs), dpacked, dw_q, dw_k, dbias, workspace,
+                          need, stream)
     return (dpacked, dw_q, dw_k, dbias) if bias is not None else (dpacked, dw_q, dw_k)
 
 
 def prologue_pool_write(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, n_q, n_kv, head_dim=64,
                         kind="interleaved", eps=1e-6, rope_base=500000.0, nope=False, dev_status=None,
-                        stream=None, norm=True, bias=None, inv_freq=None, rope_scale=1.0):
+                        stream=None, norm=True, bias=None, inv_freq=None, rope_scale=1.0, rotary_dim=None,
+                        rotary_pairs=False):
     """q contiguous; normed(+roped) k and raw v into the paged pools. Returns q."""
     _check_dev(packed, pos, w_q, w_k, page, offset, k_pool, v_pool)
-    L, T = _layout_of(packed, n_q, n_kv, head_dim, kind)
+    L, T = _layout_of(packed, n_q, n_kv, head_dim, kind, rotary_dim)
     q = torch.empty(T, n_q, head_dim, dtype=torch.bfloat16, device=packed.device)
-    C.qkv_prologue_pool_write_ex(L, _variant(bias, inv_freq, rope_scale), T, packed, pos, w_q, w_k, eps,
-                                 rope_base, _flags(nope, False, norm), q, page, offset, k_pool, v_pool,
+    if T == 0:
+        return q
+    C.qkv_prologue_pool_write_ex(L, _variant(bias, inv_freq, rope_scale, rotary_dim), T, packed, pos, w_q, w_k, eps,
+                                 rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
+                                 v_pool,
                                  k_pool.shape[0], k_pool.shape[1], dev_status, stream)
     return q
 
@@ -526,26 +554,31 @@ class GQAttentionPrologue(torch.autograd.Function):
     pass and returns the norm-weight and bias gradients where they exist.
 
     apply(packed, pos, w_q, w_k, bias, n_q, n_kv, head_dim, kind, eps, rope_base,
-          nope, norm, inv_freq, rope_scale); w_q / w_k / bias may be None.
+          nope, norm, inv_freq, rope_scale, rotary_dim=None, rotary_pairs=False);
+    w_q / w_k / bias may be None; the last two as in prologue_forward.
     """
 
     @staticmethod
     def forward(ctx, packed, pos, w_q, w_k, bias, n_q, n_kv, head_dim, kind, eps, rope_base, nope, norm,
-                inv_freq, rope_scale):
+                inv_freq, rope_scale, rotary_dim=None, rotary_pairs=False):
         out = prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim, kind, eps, rope_base, nope,
-                               save_pre=norm, norm=norm, bias=bias, inv_freq=inv_freq, rope_scale=rope_scale)
+                               save_pre=norm, norm=norm, bias=bias, inv_freq=inv_freq, rope_scale=rope_scale,
+                               rotary_dim=rotary_dim, rotary_pairs=rotary_pairs)
         q, k, v = out[:3]
         q_pre, k_pre = (out[3], out[4]) if norm else (None, None)
         ctx.save_for_backward(q_pre, k_pre, pos, w_q, w_k, bias)
-        ctx.cfg = (n_q, n_kv, head_dim, kind, eps, rope_base, nope, norm, inv_freq, rope_scale, packed.shape)
+        ctx.cfg = (n_q, n_kv, head_dim, kind, eps, rope_base, nope, norm, inv_freq, rope_scale, rotary_dim, rotary_pairs,
+                   packed.shape)
         return q, k, v
 
     @staticmethod
     def backward(ctx, dq, dk, dv):
         q_pre, k_pre, pos, w_q, w_k, bias = ctx.saved_tensors
-        n_q, n_kv, head_dim, kind, eps, rope_base, nope, norm, inv_freq, rope_scale, shape = ctx.cfg
+        (n_q, n_kv, head_dim, kind, eps, rope_base, nope, norm, inv_freq, rope_scale, rotary_dim, rotary_pairs,
+         shape) = ctx.cfg
         dq, dk, dv = (g.contiguous() for g in (dq, dk, dv))
         out = prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_dim, kind, eps, rope_base,
-                                nope, norm=norm, bias=bias, inv_freq=inv_freq, rope_scale=rope_scale)
+                                nope, norm=norm, bias=bias, inv_freq=inv_freq, rope_scale=rope_scale,
+                                rotary_dim=rotary_dim, rotary_pairs=rotary_pairs)
         dbias = out[3] if bias is not None else None
-        return (out[0].view(shape), None, out[1], out[2], dbias) + (None,) * 10
+        return (out[0].view(shape), None, out[1], out[2], dbias) + (None,) * (len(ctx.needs_input_grad) - 5)
