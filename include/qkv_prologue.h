@@ -238,6 +238,41 @@ QKVP_API int qkv_prologue_pool_scatter(const qkvp_layout* layout, int64_t T, con
                               int32_t* dev_status, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * qkv_prologue_pool_write8 -- qkv_prologue_pool_write_ex into a pool in 8 bits.
+ *
+ * A pool holds e4m3 codes (uint8 [num_pages, page_size, n_kv, head_dim]) and a
+ * float32 scale for each block of `block` tokens of a page and head ([num_pages,
+ * page_size / block, n_kv]); what is held is code * scale. k (normed and rotated)
+ * and v are quantised from float32, once. With amax the largest finite magnitude
+ * that the call writes into a block of one head:
+ *   - the call writes the block's first token: s = max(amax / 448, 2^-100);
+ *   - else the tokens of the block below the lowest one written are held (those
+ *     above it are not): s = s_old 2^k with the least k >= 0 for which amax <=
+ *     448 s (compared by exponent and significand), and the held codes are
+ *     divided by 2^k (rounded to nearest even).
+ * A new code is x / s rounded to nearest even (within one rounding of 1 / s in
+ * float32), so its error is at most 2^-4 |x|, or 2^-10 s where that is more. NaN
+ * and infinities become NaN and do not enter amax. Scales of k_scale and v_scale
+ * outside [2^-100, 2^120] are taken as the nearest bound (NaN: 2^-100).
+ *
+ * T, packed, pos, w_q, w_k, eps, rope_base, q, page, offset, dev_status: as
+ * qkv_prologue_pool_write; variant as in the _ex calls (NULL: none).
+ * GQA layouts; flags: QKVP_NOPE, QKVP_NORM_OFF, QKVP_ROPE_PAIRS, QKVP_ROPE_PART.
+ * block   divides page_size (QKVP_ERR_VALUE).
+ * The tokens of one block that a call writes must follow each other in the call,
+ * with no other token between them (else their scales and codes do not fit each
+ * other: they race). No two tokens may name the same slot.
+ * q, the pools and the scales overlap neither packed nor each other
+ * (QKVP_ERR_VALUE).
+ * ------------------------------------------------------------------------- */
+QKVP_API int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* variant, int64_t T,
+                                      const void* packed, const int32_t* pos, const float* w_q, const float* w_k,
+                                      float eps, double rope_base, uint32_t flags, void* q, const int32_t* page,
+                                      const int32_t* offset, void* k_pool, void* v_pool, float* k_scale,
+                                      float* v_scale, int32_t num_pages, int32_t page_size, int32_t block,
+                                      int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
  * qkv_prologue_bwd_workspace_size -- bytes of device workspace that
  * qkv_prologue_bwd needs for this layout and T on the CURRENT device
  * (0 when T == 0; returns 0 for an invalid layout).
@@ -569,6 +604,40 @@ QKVP_API int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, cons
  * device (host only; batch 0: 0). */
 QKVP_API int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size,
                                             int32_t max_pages, int32_t prefix_len, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
+ * qkv_attention_decode8 -- attention of one new token per sequence over the pool
+ * in 8 bits that qkv_prologue_pool_write8 fills.
+ *
+ * As qkv_attention_decode without a shared prefix (sequences that share pages
+ * name them in their rows of the table), with the key and value of pool slot
+ * [page, i] being code * scale of that slot and of its block i / block:
+ *     out[b, h] = sum_t softmax_t(scale q[b, h] . k_t[g]) v_t[g].
+ * The products take the codes as they are (exact in 16 bits); q is scaled by a
+ * power of two of its row and rounded to 11 significant bits at most (exact within
+ * 2^-14 of the row's largest value), the softmax weights times the values' scales
+ * to 11; sums, maxima and scales are fp32. Scales outside [2^-100, 2^120] are taken
+ * as the nearest bound. Slots that no sequence names are never used.
+ *
+ * layout, batch, q, page_table, max_pages, table_stride, lengths, scale, out,
+ * lse, dev_status, stream: as qkv_attention_decode. k_pool, v_pool, k_scale,
+ * v_scale, num_pages, page_size, block: as qkv_prologue_pool_write8.
+ * workspace    at least qkv_attention_decode8_workspace() bytes, 16-byte
+ *              aligned, any contents. Two calls whose work can overlap on the
+ *              GPU must not share a workspace.
+ * out, lse and the workspace overlap none of q, the pools, the scales and each
+ * other (QKVP_ERR_VALUE).
+ * ------------------------------------------------------------------------- */
+QKVP_API int qkv_attention_decode8(const qkvp_layout* layout, int32_t batch, const void* q, const void* k_pool,
+                                   const void* v_pool, const float* k_scale, const float* v_scale, int32_t num_pages,
+                                   int32_t page_size, int32_t block, const int32_t* page_table, int32_t max_pages,
+                                   int64_t table_stride, const int32_t* lengths, float scale, void* out, float* lse,
+                                   int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of qkv_attention_decode8 for these arguments on the current
+ * device (host only; batch 0: 0). */
+QKVP_API int qkv_attention_decode8_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size,
+                                             int32_t max_pages, size_t* bytes);
 
 /* ---------------------------------------------------------------------------
  * qkv_prologue_device_error -- read (and with clear != 0, reset) the

@@ -119,6 +119,11 @@ _SIGS = {
     "qkv_attention_decode": ([_LP, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _i32, _f32, _vp, _vp,
                               _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
     "qkv_attention_decode_workspace": ([_LP, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "qkv_prologue_pool_write8": ([_LP, _VP, _i64, _vp, _vp, _vp, _vp, _f32, _f64, _u32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _vp, _i32, _i32, _i32, _vp, _vp], ctypes.c_int),
+    "qkv_attention_decode8": ([_LP, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _vp, _f32, _vp,
+                               _vp, _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+    "qkv_attention_decode8_workspace": ([_LP, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
     "qkv_prologue_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "qkv_prologue_version": ([], ctypes.c_int),
     "qkv_prologue_device_error": ([ctypes.c_int, ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
@@ -370,4 +375,35 @@ def qkv_attention_decode_workspace(L, batch, page_size, max_pages, prefix_len, c
     if not check and st != QKVP_OK:
         return st
     _ret(st, "qkv_attention_decode_workspace", True)
+    return n.value
+
+
+def qkv_prologue_pool_write8(L, V, T, packed, pos, w_q, w_k, eps, rope_base, flags, q, page, offset, k_pool, v_pool,
+                             k_scale, v_scale, num_pages, page_size, block, dev_status=None, stream=None, check=True):
+    st = _lib.qkv_prologue_pool_write8(ctypes.byref(L), _vref(V), T, _ptr(packed), _ptr(pos), _ptr(w_q), _ptr(w_k),
+                                       eps, rope_base, flags, _ptr(q), _ptr(page), _ptr(offset), _ptr(k_pool),
+                                       _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), num_pages, page_size, block,
+                                       _ptr(dev_status), _stream(stream))
+    return _ret(st, "qkv_prologue_pool_write8", check)
+
+
+def qkv_attention_decode8(L, batch, q, k_pool, v_pool, k_scale, v_scale, num_pages, page_size, block, page_table,
+                          max_pages, table_stride, lengths, scale, out, lse=None, dev_status=None, workspace=None,
+                          workspace_bytes=0, stream=None, check=True):
+    st = _lib.qkv_attention_decode8(ctypes.byref(L), batch, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
+                                    _ptr(v_scale), num_pages, page_size, block, _ptr(page_table), max_pages,
+                                    table_stride, _ptr(lengths), scale, _ptr(out), _ptr(lse), _ptr(dev_status),
+                                    _ptr(workspace), workspace_bytes, _stream(stream))
+    return _ret(st, "qkv_attention_decode8", check)
+
+
+def qkv_attention_decode8_workspace(L, batch, page_size, max_pages, check=True):
+    """Workspace bytes of qkv_attention_decode8 for these arguments (a status code
+    instead when check is False and the call fails)."""
+    n = ctypes.c_size_t(0)
+    st = _lib.qkv_attention_decode8_workspace(ctypes.byref(L), int(batch), int(page_size), int(max_pages),
+                                              ctypes.byref(n))
+    if not check and st != QKVP_OK:
+        return st
+    _ret(st, "qkv_attention_decode8_workspace", True)
     return n.value

@@ -17,6 +17,12 @@
 namespace qkvp {
 namespace {
 
+#define QKVP_TRY(expr)          \
+  do {                          \
+    const int _st = (expr);     \
+    if (_st != QKVP_OK) return _st; \
+  } while (0)
+
 constexpr int kMaxDevices = 64;
 constexpr int kMaxHeadsTimesChunks = 32768;  // keeps in-item chunk indices below 2^16
 
@@ -208,10 +214,10 @@ bool stream_geometry(const StreamShape& shape, int upt, int lph, int hd, int64_t
 // Launch with programmatic stream serialization: the kernel may be launched
 // while the previous kernel in the stream is still running; every kernel of the
 // library waits (griddepcontrol.wait) for it before touching memory.
-int launch(const void* kernel, int64_t grid, int threads, size_t smem, cudaStream_t s, void* arg) {
+int launch(const void* kernel, int64_t grid, int threads, size_t smem, cudaStream_t s, void* arg, unsigned grid_y = 1) {
   void* args[] = {arg};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)grid, grid_y);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -466,6 +472,19 @@ int check_pool(int32_t num_pages, int32_t page_size) {
   return QKVP_OK;
 }
 
+// The 8-bit pool: blocks of tokens that share a scale divide a page.
+int check_pool8(int32_t num_pages, int32_t page_size, int32_t block) {
+  QKVP_TRY(check_pool(num_pages, page_size));
+  return block > 0 && page_size % block == 0 ? QKVP_OK : QKVP_ERR_VALUE;
+}
+
+struct Pool8Bytes {
+  size_t codes, scales;
+  Pool8Bytes(const qkvp_layout* L, int32_t num_pages, int32_t page_size, int32_t block)
+      : codes((size_t)num_pages * page_size * L->n_kv * L->head_dim),
+        scales((size_t)num_pages * (page_size / block) * L->n_kv * sizeof(float)) {}
+};
+
 uint32_t magic(uint32_t d) { return (uint32_t)((1ull << 32) / d + 1); }
 
 // Work items of the GQA kernels: `chunks_per_thread * kThreads` consecutive
@@ -537,12 +556,6 @@ void rope_table(double base, const Rotary& rot, const double* inv_freq, float sc
 // chunk pairs per thread; the general backward takes one-token work items of
 // at most kThreads * kBwdChunksPerThread chunks.
 constexpr int kBiasMaxChunks = kThreads * kBwdChunksPerThread;
-
-#define QKVP_TRY(expr)          \
-  do {                          \
-    const int _st = (expr);     \
-    if (_st != QKVP_OK) return _st; \
-  } while (0)
 
 // ------------------------------------------- per-head Newton-Schulz ----
 
@@ -650,6 +663,9 @@ int check_decode(const qkvp_layout* layout, int32_t batch, int32_t page_size, in
     return QKVP_ERR_SHAPE;
   return QKVP_OK;
 }
+
+// log2 of a power of two, else -1.
+int shift_of(int32_t n) { return (n & (n - 1)) == 0 ? __builtin_ctz((unsigned)n) : -1; }
 
 bool overlaps(const void* p, size_t pn, const void* q, size_t qn) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
@@ -915,6 +931,83 @@ int qkv_prologue_pool_write(const qkvp_layout* layout, int64_t T, const void* pa
                             int32_t page_size, int32_t* dev_status, void* stream) {
   return qkv_prologue_pool_write_ex(layout, nullptr, T, packed, pos, w_q, w_k, eps, rope_base, flags, q, page,
                                     offset, k_pool, v_pool, num_pages, page_size, dev_status, stream);
+}
+
+int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* variant, int64_t T, const void* packed,
+                             const int32_t* pos, const float* w_q, const float* w_k, float eps, double rope_base,
+                             uint32_t flags, void* q, const int32_t* page, const int32_t* offset, void* k_pool,
+                             void* v_pool, float* k_scale, float* v_scale, int32_t num_pages, int32_t page_size,
+                             int32_t block, int32_t* dev_status, void* stream) {
+  Gqa g;
+  QKVP_TRY(check_gqa(layout, T, &g));
+  if (flags & ~(uint32_t)(QKVP_NOPE | QKVP_NORM_OFF | QKVP_ROPE_PAIRS | QKVP_ROPE_PART)) return QKVP_ERR_FLAGS;
+  Rotary rot;
+  QKVP_TRY(check_rotary(layout, flags, &rot));
+  const bool rope = !(flags & QKVP_NOPE), norm = !(flags & QKVP_NORM_OFF);
+  Variant vr;
+  QKVP_TRY(check_variant(variant, rot.dim, true, &vr));
+  QKVP_TRY(check_scalars(eps, rope_base, rope && !vr.inv_freq));
+  if (!packed || (norm && (!w_q || !w_k)) || !q || (rope && !pos) || !page || !offset || !k_pool || !v_pool ||
+      !k_scale || !v_scale)
+    return QKVP_ERR_NULL;
+  QKVP_TRY(check_pool8(num_pages, page_size, block));
+  for (const void* p : {packed, norm ? (const void*)w_q : nullptr, norm ? (const void*)w_k : nullptr, (const void*)q,
+                        (const void*)k_pool, (const void*)v_pool})
+    if (p && !aligned16(p)) return QKVP_ERR_ALIGN;
+  for (const void* p : {(const void*)pos, (const void*)page, (const void*)offset, (const void*)k_scale,
+                        (const void*)v_scale, (const void*)dev_status})
+    if (p && !aligned4(p)) return QKVP_ERR_ALIGN;
+  if (T == 0) return QKVP_OK;
+  int sms = 0;
+  QKVP_TRY(current_device(&sms));
+  const int hd = layout->head_dim;
+  const Pool8Bytes pb(layout, num_pages, page_size, block);
+  if (written_overlaps({{q, (size_t)T * layout->n_q * hd * 2}, {k_pool, pb.codes}, {v_pool, pb.codes},
+                        {k_scale, pb.scales}, {v_scale, pb.scales}},
+                       {{packed, ((size_t)(T - 1) * g.stride + g.row) * 2}}))
+    return QKVP_ERR_VALUE;
+  Write8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.packed = static_cast<const uint4*>(packed);
+  a.row_stride16 = g.stride / 8;
+  a.pos = pos;
+  a.w_q = w_q;
+  a.w_k = w_k;
+  a.bias = vr.bias;
+  a.eps = eps;
+  a.inv_head_dim = 1.0f / (float)hd;
+  a.T = T;
+  a.n_q = layout->n_q;
+  a.n_kv = layout->n_kv;
+  a.group = layout->n_q / layout->n_kv;
+  a.sectioned = layout->kind == QKVP_SECTIONED;
+  a.norm = norm;
+  a.rope_on = rope;
+  a.q = static_cast<uint4*>(q);
+  a.page = page;
+  a.offset = offset;
+  a.k_pool = static_cast<uint8_t*>(k_pool);
+  a.v_pool = static_cast<uint8_t*>(v_pool);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.block = block;
+  a.dev_status = dev_status;
+  if (rope) rope_table(rope_base, rot, vr.inv_freq, vr.scale, &a.rope);
+  // Tokens per CTA: as many as leave two CTAs per SM busy, and at most 16; a CTA's
+  // work is then divided among CTAs along y while there are too few of them.
+  const int64_t slots = 2 * (int64_t)sms;
+  a.tile = 16;
+  while (a.tile > 1 && (T + a.tile - 1) / a.tile < slots) a.tile /= 2;
+  a.tab_rows = a.tile + std::min(block - 1, 47);
+  const int64_t tiles = (T + a.tile - 1) / a.tile;
+  const int64_t units = (int64_t)a.tile * (2 * a.n_kv + (a.n_q + 15) / 16);
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, (units + 7) / 8));
+  const void* kern = pool_write8_kernel(hd);
+  const size_t smem = rope ? (size_t)a.tab_rows * hd * sizeof(float) : 0;
+  if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
+  return launch(kern, tiles, pool_write8_threads(), smem, static_cast<cudaStream_t>(stream), &a, (unsigned)parts);
 }
 
 int qkv_prologue_pool_scatter(const qkvp_layout* layout, int64_t T, const void* k_rows,
@@ -1505,6 +1598,42 @@ int qkv_attention_bwd(const qkvp_layout* layout, int64_t T, int32_t batch, const
   return launch_args(attention_fold_kernel(), std::min<int64_t>(fgrid, 8 * (int64_t)sms), 256, 0, st, fargs);
 }
 
+// The kernel over each sequence's own keys and the join: the arguments that a planned
+// decode call has whatever its pool holds, and both launches.
+static int launch_decode(const qkvp_layout* layout, int32_t batch, const DecodePlan& p, const void* q, int32_t page_size,
+                         int32_t max_pages, float scale_log2, void* out, float* lse, int32_t* dev_status,
+                         void* workspace, const void* kern, int threads, size_t smem, cudaStream_t st,
+                         AttnDecodeArgs* a) {
+  const int hd = layout->head_dim;
+  a->n_q = layout->n_q;
+  a->n_kv = layout->n_kv;
+  a->group = layout->n_q / layout->n_kv;
+  a->head_blocks = p.head_blocks;
+  a->batch = batch;
+  a->scale_log2 = scale_log2;
+  a->q = static_cast<const uint16_t*>(q);
+  a->page_size = page_size;
+  a->max_pages = max_pages;
+  a->page_shift = shift_of(page_size);
+  a->prefix_chunks = p.chunks;
+  a->ranges = p.ranges;
+  a->part_o = static_cast<float*>(workspace);
+  a->part_ml = reinterpret_cast<float2*>(a->part_o + p.rows * layout->n_q * hd);
+  a->plan = reinterpret_cast<int2*>(a->part_ml + p.rows * layout->n_q);
+  a->out = static_cast<uint16_t*>(out);
+  a->lse = lse;
+  a->dev_status = dev_status;
+  // warps per head of the join: eight partial results each (as many reads as a lane
+  // has in flight)
+  const int64_t parts = p.ranges / batch + 2 + p.chunks;
+  a->wph = parts > 32 ? 8 : (parts > 16 ? 4 : (parts > 8 ? 2 : 1));
+  if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
+  QKVP_TRY(launch(kern, p.grid, threads, smem, st, a));
+  const int per = kJoinWarps / a->wph;
+  const int64_t joins = (int64_t)batch * ((layout->n_q + per - 1) / per);
+  return launch(attention_join_kernel(hd), joins, 32 * kJoinWarps, 0, st, a);
+}
+
 int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,
                                    int32_t prefix_len, size_t* bytes) {
   QKVP_TRY(check_decode(layout, batch, page_size, max_pages, prefix_len));
@@ -1596,44 +1725,74 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   }
   AttnDecodeArgs a;
   std::memset(&a, 0, sizeof(a));
-  a.n_q = layout->n_q;
-  a.n_kv = layout->n_kv;
-  a.group = group;
-  a.head_blocks = p.head_blocks;
-  a.batch = batch;
-  a.scale_log2 = scale_log2;
-  a.q = static_cast<const uint16_t*>(q);
   a.k_pool = static_cast<const uint4*>(k_pool);
   a.v_pool = static_cast<const uint4*>(v_pool);
   a.num_pages = num_pages;
-  a.page_size = page_size;
   a.page_table = page_table;
   a.table_stride = table_stride;
-  a.max_pages = max_pages;
   a.lengths = lengths;
   a.prefix_pages = prefix_pages;
   a.tile_keys = dec_tile_keys(hd);
-  a.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1;
   a.joint_len = p.apart ? 0 : prefix_len;
-  a.prefix_chunks = p.chunks;
-  a.ranges = p.ranges;
-  a.part_o = part_o;
-  a.part_ml = part_ml;
-  a.plan = reinterpret_cast<int2*>(part_ml + p.rows * layout->n_q);
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.dev_status = dev_status;
-  // warps per head of the join: eight partial results each (as many reads as a lane
-  // has in flight)
-  const int64_t parts = p.ranges / batch + 2 + p.chunks;
-  a.wph = parts > 32 ? 8 : (parts > 16 ? 4 : (parts > 8 ? 2 : 1));
-  const void* kern = attention_decode_kernel(hd);
-  const size_t smem = (size_t)attention_decode_smem_bytes(hd);
-  if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
-  QKVP_TRY(launch(kern, p.grid, attention_decode_threads(), smem, st, &a));
-  const int per = kJoinWarps / a.wph;
-  const int64_t joins = (int64_t)batch * ((layout->n_q + per - 1) / per);
-  return launch(attention_join_kernel(hd), joins, 32 * kJoinWarps, 0, st, &a);
+  return launch_decode(layout, batch, p, q, page_size, max_pages, scale_log2, out, lse, dev_status, workspace,
+                       attention_decode_kernel(hd), attention_decode_threads(),
+                       (size_t)attention_decode_smem_bytes(hd), st, &a);
+}
+
+int qkv_attention_decode8_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,
+                                    size_t* bytes) {
+  return qkv_attention_decode_workspace(layout, batch, page_size, max_pages, 0, bytes);
+}
+
+int qkv_attention_decode8(const qkvp_layout* layout, int32_t batch, const void* q, const void* k_pool,
+                          const void* v_pool, const float* k_scale, const float* v_scale, int32_t num_pages,
+                          int32_t page_size, int32_t block, const int32_t* page_table, int32_t max_pages,
+                          int64_t table_stride, const int32_t* lengths, float scale, void* out, float* lse,
+                          int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream) {
+  QKVP_TRY(check_decode(layout, batch, page_size, max_pages, 0));
+  QKVP_TRY(check_pool8(num_pages, page_size, block));
+  float sc = 0.f;
+  QKVP_TRY(check_attention(layout, batch, scale, &sc));
+  if (table_stride < max_pages) return QKVP_ERR_SHAPE;
+  if (!q || !k_pool || !v_pool || !k_scale || !v_scale || !lengths || !out || (max_pages > 0 && !page_table))
+    return QKVP_ERR_NULL;
+  for (const void* p : {q, k_pool, v_pool, (const void*)out})
+    if (!aligned16(p)) return QKVP_ERR_ALIGN;
+  for (const void* p : {(const void*)k_scale, (const void*)v_scale, (const void*)lengths, (const void*)page_table,
+                        (const void*)lse, (const void*)dev_status})
+    if (p && !aligned4(p)) return QKVP_ERR_ALIGN;
+  if (batch == 0) return QKVP_OK;
+  int sms = 0;
+  QKVP_TRY(current_device(&sms));
+  DecodePlan p;
+  plan_decode(layout, batch, page_size, max_pages, 0, sms, &p);
+  const size_t need = decode_workspace(layout, batch, p);
+  if (!workspace || workspace_bytes < need) return QKVP_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
+  const int hd = layout->head_dim;
+  const size_t q_bytes = (size_t)batch * layout->n_q * hd * 2;
+  const size_t lse_bytes = lse ? (size_t)batch * layout->n_q * sizeof(float) : 0;
+  const Pool8Bytes pb(layout, num_pages, page_size, block);
+  if (written_overlaps({{out, q_bytes}, {lse, lse_bytes}, {workspace, need}},
+                       {{q, q_bytes}, {k_pool, pb.codes}, {v_pool, pb.codes}, {k_scale, pb.scales},
+                        {v_scale, pb.scales}}))
+    return QKVP_ERR_VALUE;
+  AttnDecodeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.k_pool = static_cast<const uint4*>(k_pool);
+  a.v_pool = static_cast<const uint4*>(v_pool);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block = block;
+  a.block_shift = shift_of(block);
+  a.num_pages = num_pages;
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  a.lengths = lengths;
+  a.tile_keys = kDec8Keys;
+  return launch_decode(layout, batch, p, q, page_size, max_pages, (float)((double)sc * 1.4426950408889634), out, lse,
+                       dev_status, workspace, attention_decode8_kernel(hd), attention_decode8_threads(),
+                       (size_t)attention_decode8_smem_bytes(hd), static_cast<cudaStream_t>(stream), &a);
 }
 
 int qkv_prologue_wait_selftest(void* stream) {

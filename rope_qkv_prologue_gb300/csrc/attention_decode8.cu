@@ -1,0 +1,317 @@
+// Attention of one new token per sequence over the paged pool in 8 bits, split over the
+// keys: the walk, the split and the join are those of attention_decode.cu.
+//
+// With codes K, V and scales a_j, b_j of key j's blocks (float32),
+//     t_j = c a_j q . K_j,   l = sum_j 2^(t_j - m),             m >= max t_j - 8,
+//     u_j = t_j + log2(b_j), O = sum_j 2^(u_j - n) V_j,         n >= max u_j - 8,
+//     out = 2^(n - m) O / l:
+// the value scale is part of the weight, and the weights have a reference of their own,
+// so their 11 significant bits are those of the largest contributions however far apart
+// the blocks' scales are. A partial result leaves as (m + log2 l, 1, 2^(n - m) O / l),
+// which joins as plain softmax's do. A key that is not attended has t = -inf.
+//
+// Codes go to the matrix units (m16n8k16, f16 with fp32 accumulation) as f16, which
+// holds every e4m3 value exactly; one conversion instruction makes two values. A row of
+// q is scaled by a power of two that brings its largest magnitude into [1, 2). The order
+// of d in S = Q K^T is free: a lane's four consecutive codes are the two operand
+// registers of one step, so ldmatrix on bytes needs no shuffling. For O = W V the
+// transposing ldmatrix moves pairs of codes (d, d + 1) of two keys; a byte permutation
+// makes the pairs of keys of d and of d + 1, and even and odd d go to accumulators of
+// their own.
+#include <cuda_fp16.h>
+
+#include "attention_decode.cuh"
+#include "e4m3.cuh"
+
+namespace qkvp {
+namespace {
+
+constexpr int kDec8Warps = 8;
+
+template <int HD>
+struct Dec8Shape {
+  static constexpr int kKeys = kDec8Keys;
+  static constexpr int kTileBytes = 2 * kKeys * HD;         // k codes, then v codes
+  static constexpr int kStages = 24 * 1024 / kTileBytes;    // 24 KiB a warp, 192 KiB an SM
+  static constexpr int kWarpBytes = kStages * kTileBytes;
+};
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void mma16816h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Maximum over the four lanes of a row.
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+
+// Place of 16-byte chunk ch of a tile's row, so that the 8 rows of a matrix of ldmatrix
+// lie in different banks: rows of 128 bytes, or of 64 (two to a line).
+template <int HD>
+__device__ __forceinline__ int dec8_at(int row, int ch) {
+  return row * HD + ((HD == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4);
+}
+
+}  // namespace
+
+template <int HD>
+__global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_kernel(const AttnDecodeArgs a) {
+  using SH = Dec8Shape<HD>;
+  constexpr int ST = SH::kStages, KT = SH::kKeys, NT = KT / 8;
+  constexpr int CH = HD / 16, RPI = 32 / CH;  // 16-byte chunks per row, rows per copy instruction
+  static_assert(KT == 32, "a lane per key");
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ uint32_t s_in[kDec8Warps][ST];          // bit i: key i of the stage's tile is attended
+  __shared__ float s_scale[kDec8Warps][ST][2][KT];   // its keys' scales as they are stored
+  __shared__ float4 s_key[kDec8Warps][KT];           // a, 0 (-inf: not attended), log2 b of the tile at work
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = smem_addr(smem_raw) + warp * SH::kWarpBytes;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int64_t total = dec_total(a, lane);
+  const int64_t quota = dec_quota(a, total);
+  const int heads = a.n_kv * a.head_blocks;
+  const int items = a.ranges * heads;
+  for (int w = blockIdx.x * kDec8Warps + warp; w < items; w += gridDim.x * kDec8Warps) {
+    const int range = w / heads;
+    const int64_t t0 = range * quota;
+    if (t0 >= total) break;
+    const int n_tiles = (int)min(quota, total - t0);
+    const int hv = w % heads, kvh = hv / a.head_blocks, hb = hv % a.head_blocks;
+    const int head0 = kvh * a.group + hb * 16, n_heads = min(16, a.group - hb * 16);
+    DecCursor cu = dec_begin(a, t0, lane);  // where the range begins
+
+    // Loads run ST - 1 tiles ahead of the arithmetic, and the page lookup of a
+    // tile one step ahead of its loads.
+    DecCursor ld = cu;
+    uint32_t ld_keys = (uint32_t)dec_own(a, ld.b);
+    int slot = -1;
+    auto look_up = [&]() { slot = dec_slot(a, ld.b, ld_keys, (uint32_t)(ld.tile * KT + lane)); };
+    auto advance = [&]() {
+      if (++ld.tile < ld.tiles) return;
+      ld.settle(a, lane);
+      ld_keys = (uint32_t)dec_own(a, ld.b);
+    };
+    const int ch = lane % CH, row_ch = a.n_kv * CH;
+    const uint4* k_src = a.k_pool + kvh * CH + ch;
+    const uint4* v_src = a.v_pool + kvh * CH + ch;
+    auto issue = [&](uint32_t st) {
+      const uint32_t in = __ballot_sync(0xffffffffu, slot >= 0);
+      if (lane == 0) s_in[warp][st] = in;
+      const uint32_t mine = (uint32_t)max(slot, 0);
+      const int64_t at = (int64_t)(a.block_shift >= 0 ? mine >> a.block_shift : mine / (uint32_t)a.block) * a.n_kv + kvh;
+      cp_async4(smem_addr(&s_scale[warp][st][0][lane]), a.k_scale + at, slot >= 0);
+      cp_async4(smem_addr(&s_scale[warp][st][1][lane]), a.v_scale + at, slot >= 0);
+      const uint32_t dst = ring + st * SH::kTileBytes;
+#pragma unroll
+      for (int i = 0; i < KT / RPI; ++i) {
+        const int r = i * RPI + lane / CH;
+        const int row = __shfl_sync(0xffffffffu, slot, r);
+        const int64_t off = (int64_t)max(row, 0) * row_ch;
+        const uint32_t to = dst + dec8_at<HD>(r, ch);
+        cp_async16(to, k_src + off, row >= 0);
+        cp_async16(to + KT * HD, v_src + off, row >= 0);
+      }
+    };
+    look_up();
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+      if (i < n_tiles) {
+        issue(i);
+        if (i + 1 < n_tiles) {
+          advance();
+          look_up();
+        }
+      }
+      cp_commit();
+    }
+
+    uint32_t qf[HD / 16][4];
+    float o[HD / 8][4], m[2], n[2], l[2], c[2];  // o[2 j], o[2 j + 1]: even and odd d of chunk j; c: a row's factor
+    auto begin = [&]() {                   // a sequence's first tile here
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = (lane >> 2) + 8 * x;
+        const uint2* src = reinterpret_cast<const uint2*>(a.q + ((int64_t)cu.b * a.n_q + head0 + r) * HD) + (lane & 3);
+        uint2 raw[HD / 16];
+        uint32_t top = 0;
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          raw[ks] = r < n_heads ? src[4 * ks] : make_uint2(0, 0);
+          top = max(max(top, (raw[ks].x << 16) & 0x7fffffffu), max(raw[ks].x & 0x7fffffffu, raw[ks].y & 0x7fffffffu));
+          top = max(top, (raw[ks].y << 16) & 0x7fffffffu);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e, e the exponent of the largest magnitude (within what float32 can scale by)
+        const int e = min(max((int)(top >> 23) - 127, -126), 126);
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+        c[x] = a.scale_log2 * __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          qf[ks][x] = pack_h2(__uint_as_float(raw[ks].x << 16) * f, __uint_as_float(raw[ks].x & 0xffff0000u) * f);
+          qf[ks][2 + x] = pack_h2(__uint_as_float(raw[ks].y << 16) * f, __uint_as_float(raw[ks].y & 0xffff0000u) * f);
+        }
+        m[x] = n[x] = -INFINITY;
+        l[x] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    };
+    bool first = cu.tile == 0;  // of the sequence: else the segment continues one of the range before
+    auto end = [&]() {          // its last tile here: the partial result
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        const int r = (lane >> 2) + 8 * x;
+        if (r < n_heads) {
+          const int64_t row = (int64_t)(first ? cu.b : a.batch + range) * a.n_q + head0 + r;
+          const float ref = m[x] + __log2f(l[x]), f = l[x] == 0.f ? 0.f : ex2(n[x] - ref);
+          if ((lane & 3) == 0) a.part_ml[row] = l[x] == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ref, 1.f);
+          float4* dst = reinterpret_cast<float4*>(a.part_o + row * HD) + (lane & 3);
+#pragma unroll
+          for (int j = 0; j < HD / 16; ++j)
+            dst[4 * j] = make_float4(f * o[2 * j][2 * x], f * o[2 * j + 1][2 * x], f * o[2 * j][2 * x + 1],
+                                     f * o[2 * j + 1][2 * x + 1]);
+        }
+      }
+    };
+    begin();
+    uint32_t st = 0;
+#pragma unroll 1
+    for (int t = 0; t < n_tiles; ++t) {
+      cp_wait<ST - 2>();
+      __syncwarp();  // this tile is here, and every lane is done with the one before
+      if (t + ST - 1 < n_tiles) {
+        issue(st == 0 ? ST - 1 : st - 1);
+        if (t + ST < n_tiles) {
+          advance();
+          look_up();
+        }
+      }
+      cp_commit();
+      {
+        const float ka = clamp_scale(s_scale[warp][st][0][lane]), vb = clamp_scale(s_scale[warp][st][1][lane]);
+        const bool in = (s_in[warp][st] >> lane) & 1;
+        s_key[warp][lane] = make_float4(ka, in ? 0.f : -INFINITY, __log2f(vb), 0.f);
+      }
+      const uint32_t kt = ring + st * SH::kTileBytes, vt = kt + KT * HD;
+      float s[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int k4 = 0; k4 < HD / 64; ++k4) {
+          uint32_t b[4];
+          ldsm4(kt + dec8_at<HD>(8 * i + (lane & 7), 4 * k4 + (lane >> 3)), b);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t b0, b1;
+            from_e4m3x4(b[x], b0, b1);
+            mma16816h(s[i], qf[4 * k4 + x], b0, b1);
+          }
+        }
+      __syncwarp();  // s_key is written
+      float4 key[NT][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) key[i][y] = s_key[warp][8 * i + 2 * (lane & 3) + y];
+      // A row's references only move where a score passes them by more than 8 powers of
+      // two; until then no lane has to know the others' maxima.
+      float top[2] = {-INFINITY, -INFINITY}, tow[2] = {-INFINITY, -INFINITY};
+      float u[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[i][x] = fmaf(s[i][x] * key[i][x & 1].x, c[x >> 1], key[i][x & 1].y);
+          u[i][x] = s[i][x] + key[i][x & 1].z;
+          top[x >> 1] = fmaxf(top[x >> 1], s[i][x]);
+          tow[x >> 1] = fmaxf(tow[x >> 1], u[i][x]);
+        }
+      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f || tow[0] > n[0] + 8.f || tow[1] > n[1] + 8.f)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float m_new = fmaxf(m[x], quad_max(top[x])), n_new = fmaxf(n[x], quad_max(tow[x]));
+          l[x] *= m_new == m[x] ? 1.f : ex2(m[x] - m_new);
+          const float f = n_new == n[x] ? 1.f : ex2(n[x] - n_new);
+          m[x] = m_new;
+          n[x] = n_new;
+#pragma unroll
+          for (int i = 0; i < HD / 8; ++i) {
+            o[i][2 * x] *= f;
+            o[i][2 * x + 1] *= f;
+          }
+        }
+      }
+      uint32_t pf[NT / 2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float off = m[x] == -INFINITY ? 0.f : -m[x], offw = n[x] == -INFINITY ? 0.f : -n[x];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          l[x] += ex2(s[i][2 * x] + off) + ex2(s[i][2 * x + 1] + off);
+          pf[i >> 1][2 * (i & 1) + x] = pack_h2(ex2(u[i][2 * x] + offw), ex2(u[i][2 * x + 1] + offw));
+        }
+      }
+      {
+        const int row = (((lane >> 3) & 1) << 3) + (lane & 7), hi = lane >> 4;
+#pragma unroll
+        for (int k2 = 0; k2 < NT / 2; ++k2)
+#pragma unroll
+          for (int j = 0; j < HD / 16; j += 2) {
+            uint32_t b[4], e0, o0, e1, o1;
+            ldsm4t(vt + dec8_at<HD>(16 * k2 + row, j + hi), b);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              from_e4m3x4(__byte_perm(b[2 * i], 0, 0x3120), e0, o0);
+              from_e4m3x4(__byte_perm(b[2 * i + 1], 0, 0x3120), e1, o1);
+              mma16816h(o[2 * (j + i)], pf[k2], e0, e1);
+              mma16816h(o[2 * (j + i) + 1], pf[k2], o0, o1);
+            }
+          }
+      }
+      st = st + 1 == ST ? 0 : st + 1;
+      // the ranges that a sequence begins and ends in, for the joining kernel
+      if (hv == 0 && lane == 0) {
+        if (cu.tile == 0) a.plan[cu.b].x = range;
+        if (cu.tile + 1 == cu.tiles) a.plan[cu.b].y = range;
+      }
+      if (++cu.tile == cu.tiles || t + 1 == n_tiles) {
+        end();
+        cu.settle(a, lane);
+        first = true;
+        if (t + 1 < n_tiles) begin();
+      }
+    }
+    cp_wait<0>();
+    __syncwarp();
+  }
+}
+
+const void* attention_decode8_kernel(int head_dim) {
+  return head_dim == 64 ? reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<64>)
+                        : reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<128>);
+}
+int attention_decode8_smem_bytes(int head_dim) {
+  return kDec8Warps * (head_dim == 64 ? Dec8Shape<64>::kWarpBytes : Dec8Shape<128>::kWarpBytes);
+}
+int attention_decode8_threads() { return 32 * kDec8Warps; }
+
+}  // namespace qkvp

@@ -441,12 +441,50 @@ struct AttnDecodeArgs {
   uint16_t* out;           // bf16 [batch, n_q, head_dim]
   float* lse;              // [batch, n_q], or null
   int32_t* dev_status;
+  // the pool in 8 bits (k_pool, v_pool are then rows of codes)
+  const float* k_scale;    // [num_pages, page_size / block, n_kv]
+  const float* v_scale;
+  int32_t block;
+  int32_t block_shift;     // log2(block), or -1
 };
+constexpr int kDec8Keys = 32;  // keys per tile of the kernel over the 8-bit pool
+const void* attention_decode8_kernel(int head_dim);
+int attention_decode8_smem_bytes(int head_dim);
+int attention_decode8_threads();
 const void* attention_decode_kernel(int head_dim);
 const void* attention_join_kernel(int head_dim);
 int attention_decode_smem_bytes(int head_dim);
 int attention_decode_threads();
 int attention_decode_warps();
+
+// New tokens' keys and values into the 8-bit pool.
+struct Write8Args {
+  const uint4* packed;
+  int64_t row_stride16;   // packed row stride, 16-byte chunks
+  const int32_t* pos;
+  const float* w_q;
+  const float* w_k;
+  const float* bias;      // in packed-row order, or null
+  float eps;
+  float inv_head_dim;
+  int64_t T;
+  int32_t n_q, n_kv, group;
+  int32_t sectioned, norm, rope_on;
+  int32_t tile;           // tokens per CTA (at most 32)
+  int32_t tab_rows;       // tokens that the cos/sin table has room for (at least tile)
+  uint4* q;
+  const int32_t* page;
+  const int32_t* offset;
+  uint8_t* k_pool;        // codes [num_pages, page_size, n_kv, head_dim]
+  uint8_t* v_pool;
+  float* k_scale;         // [num_pages, page_size / block, n_kv]
+  float* v_scale;
+  int32_t num_pages, page_size, block;
+  int32_t* dev_status;
+  RopeTable rope;
+};
+const void* pool_write8_kernel(int head_dim);
+int pool_write8_threads();
 
 // One thread whose only wait never completes (the bounded-wait self-test).
 const void* wait_selftest_kernel();

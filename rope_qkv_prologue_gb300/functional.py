@@ -522,6 +522,112 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
     return (out, lse) if save_lse else out
 
 
+def _check_pool8(k_pool, v_pool, k_scale, v_scale, device):
+    """Tokens that share a scale in the pool in 8 bits, from its tensors' shapes."""
+    if (k_pool.dtype != torch.float8_e4m3fn or v_pool.dtype != torch.float8_e4m3fn or k_pool.dim() != 4
+            or k_pool.shape != v_pool.shape or not k_pool.is_contiguous() or not v_pool.is_contiguous()):
+        raise ValueError("k_pool and v_pool must be contiguous float8_e4m3fn [num_pages, page_size, n_kv, D] tensors of "
+                         "one shape")
+    num_pages, page_size, n_kv, _ = k_pool.shape
+    if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.dim() != 3
+            or k_scale.shape != v_scale.shape or not k_scale.is_contiguous() or not v_scale.is_contiguous()
+            or k_scale.shape[0] != num_pages or k_scale.shape[2] != n_kv or k_scale.shape[1] < 1
+            or page_size % k_scale.shape[1]):
+        raise ValueError("k_scale and v_scale must be contiguous float32 [num_pages, page_size / block, n_kv] tensors of "
+                         "one shape, block a divisor of page_size")
+    if k_pool.device != device or v_pool.device != device or k_scale.device != device or v_scale.device != device:
+        raise ValueError(f"the pools and their scales must live on {device}")
+    return page_size // k_scale.shape[1]
+
+
+def prologue_pool_write8(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, k_scale, v_scale, n_q, n_kv, head_dim=64,
+                         kind="interleaved", eps=1e-6, rope_base=500000.0, nope=False, dev_status=None, stream=None,
+                         norm=True, bias=None, inv_freq=None, rope_scale=1.0, rotary_dim=None, rotary_pairs=False):
+    """prologue_pool_write into a pool in 8 bits: k_pool, v_pool float8_e4m3fn
+    [num_pages, page_size, n_kv, D] codes, k_scale, v_scale float32 [num_pages,
+    page_size / block, n_kv], a scale for each block of tokens and head; the cache
+    holds code * scale. A block whose first token is among these gets the scale
+    amax / 448; one that holds earlier tokens keeps its own, times a power of two
+    where the new values need it (the earlier codes are divided by it). The new
+    tokens of one block must follow each other in the call. The work is queued on
+    `stream` (default: the current one), as attention_forward's. Returns q."""
+    if stream is not None:
+        return _on_stream(stream, packed, prologue_pool_write8, packed, pos, w_q, w_k, page, offset, k_pool, v_pool,
+                          k_scale, v_scale, n_q, n_kv, head_dim, kind, eps, rope_base, nope, dev_status, None, norm, bias,
+                          inv_freq, rope_scale, rotary_dim, rotary_pairs)
+    L, T = _layout_of(packed, n_q, n_kv, head_dim, kind, rotary_dim)
+    dev = packed.device
+    if packed.dtype != torch.bfloat16 or not packed.is_cuda:
+        raise ValueError("packed must be a bf16 tensor on a CUDA device")
+    block = _check_pool8(k_pool, v_pool, k_scale, v_scale, dev)
+    if k_pool.shape[2] != n_kv or k_pool.shape[3] != head_dim:
+        raise ValueError(f"the pools must hold {n_kv} heads of {head_dim}")
+    for t, name in ((page, "page"), (offset, "offset")) + (() if nope else ((pos, "pos"),)):
+        _check_like(t, (T,), torch.int32, dev, name)
+    for t, name in ((w_q, "w_q"), (w_k, "w_k")) if norm else ():
+        _check_like(t, (head_dim,), torch.float32, dev, name)
+    if bias is not None:
+        _check_like(bias, ((n_q + 2 * n_kv) * head_dim,), torch.float32, dev, "bias")
+    _check_status(dev_status, dev)
+    q = torch.empty((T, n_q, head_dim), dtype=torch.bfloat16, device=dev)
+    if T == 0:
+        return q
+    C.qkv_prologue_pool_write8(L, _variant(bias, inv_freq, rope_scale, rotary_dim), T, packed, pos, w_q, w_k, eps,
+                               rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
+                               v_pool, k_scale, v_scale, k_pool.shape[0], k_pool.shape[1], block, dev_status,
+                               _current_stream(dev))
+    return q
+
+
+def attention_decode8_workspace_bytes(n_q, n_kv, head_dim, batch, page_size, max_pages):
+    """Workspace bytes attention_decode8 needs for these sizes on the current device."""
+    return C.qkv_attention_decode8_workspace(_heads(n_q, n_kv, head_dim), batch, page_size, max_pages)
+
+
+def attention_decode8(q, k_pool, v_pool, k_scale, v_scale, page_table, lengths, scale=None, save_lse=False, out=None,
+                      workspace=None, dev_status=None, stream=None):
+    """attention_decode over a pool in 8 bits, as prologue_pool_write8 fills it: q
+    [B, n_q, D] bf16; k_pool, v_pool float8_e4m3fn [num_pages, page_size, n_kv, D];
+    k_scale, v_scale float32 [num_pages, page_size / block, n_kv]; page_table int32
+    [B, max_pages] and lengths int32 [B]. Sequences that share pages name them in
+    their rows. Returns out [B, n_q, D], or (out, lse [B, n_q] float32) with
+    save_lse. `workspace` (attention_decode8_workspace_bytes bytes) and `stream` as
+    in attention_decode."""
+    if stream is not None:
+        return _on_stream(stream, q, attention_decode8, q, k_pool, v_pool, k_scale, v_scale, page_table, lengths, scale,
+                          save_lse, out, workspace, dev_status)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous() or not q.is_cuda:
+        raise ValueError("q must be a contiguous bf16 [B, n_q, D] tensor on a CUDA device")
+    dev, (B, n_q, D) = q.device, q.shape
+    block = _check_pool8(k_pool, v_pool, k_scale, v_scale, dev)
+    num_pages, page_size, n_kv, pool_dim = k_pool.shape
+    if pool_dim != D:
+        raise ValueError("the pools must have q's head_dim")
+    _check_pages(page_table, "page_table", dev, 2)
+    max_pages = page_table.shape[1]
+    if page_table.shape[0] != B or (B > 1 and page_table.stride(0) < max_pages):
+        raise ValueError("page_table must have a row per sequence, and the rows must not overlap")
+    _check_like(lengths, (B,), torch.int32, dev, "lengths")
+    _check_status(dev_status, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_like(out, q.shape, torch.bfloat16, dev, "out")
+    lse = torch.empty((B, n_q), dtype=torch.float32, device=dev) if save_lse else None
+    if B == 0:
+        return (out, lse) if save_lse else out
+    here = _current_stream(dev)  # before a size is asked for: it is the current device's
+    if workspace is None:
+        need = _decode_workspace(n_q, n_kv, D, B, page_size, max_pages, 0, dev.index)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _check_workspace(workspace, dev)
+    C.qkv_attention_decode8(_heads(n_q, n_kv, D), B, q, k_pool, v_pool, k_scale, v_scale, num_pages, page_size, block,
+                            page_table, max_pages, page_table.stride(0) if B > 1 else max_pages, lengths,
+                            0.0 if scale is None else scale, out, lse, dev_status, workspace,
+                            workspace.numel() * workspace.element_size(), here)
+    return (out, lse) if save_lse else out
+
+
 class QKVPrologue(torch.autograd.Function):
     """packed [T, row] -> (q, k, v); backward writes d(packed) in one pass.
 
