@@ -389,8 +389,17 @@ uint64_t turns_of(double inv_freq) {
 
 void rope_table(double base, int dim, const double* inv_freq, float scale, RopeTable* out) {
   if (inv_freq) {
-    std::memset(out, 0, sizeof(*out));
-    for (int i = 0; i < dim / 2; ++i) out->turns[i] = turns_of(inv_freq[i]);
+    // the last table's frequencies are kept by value: a model calls with the same ones
+    static thread_local double freq[kMaxHalf];
+    static thread_local int freq_dim = 0;
+    static thread_local RopeTable table;
+    if (dim != freq_dim || std::memcmp(freq, inv_freq, (size_t)(dim / 2) * sizeof(double)) != 0) {
+      std::memset(&table, 0, sizeof(table));
+      for (int i = 0; i < dim / 2; ++i) table.turns[i] = turns_of(inv_freq[i]);
+      std::memcpy(freq, inv_freq, (size_t)(dim / 2) * sizeof(double));
+      freq_dim = dim;
+    }
+    *out = table;
     out->scale = scale;
     return;
   }
@@ -472,6 +481,9 @@ int check_pool(int32_t num_pages, int32_t page_size) {
   return QKVP_OK;
 }
 
+uint32_t magic(uint32_t d) { return (uint32_t)((1ull << 32) / d + 1); }
+SmallDiv small_div_by(int d) { return SmallDiv{d > 1 ? magic((uint32_t)d) : 0u}; }
+
 // The 8-bit pool: blocks of tokens that share a scale divide a page.
 int check_pool8(int32_t num_pages, int32_t page_size, int32_t block) {
   QKVP_TRY(check_pool(num_pages, page_size));
@@ -485,7 +497,6 @@ struct Pool8Bytes {
         scales((size_t)num_pages * (page_size / block) * L->n_kv * sizeof(float)) {}
 };
 
-uint32_t magic(uint32_t d) { return (uint32_t)((1ull << 32) / d + 1); }
 
 // Work items of the GQA kernels: `chunks_per_thread * kThreads` consecutive
 // (token, chunk) pairs.
@@ -981,8 +992,6 @@ int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* vari
   a.n_kv = layout->n_kv;
   a.group = layout->n_q / layout->n_kv;
   a.sectioned = layout->kind == QKVP_SECTIONED;
-  a.norm = norm;
-  a.rope_on = rope;
   a.q = static_cast<uint4*>(q);
   a.page = page;
   a.offset = offset;
@@ -993,19 +1002,37 @@ int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* vari
   a.num_pages = num_pages;
   a.page_size = page_size;
   a.block = block;
+  a.block_shift = shift_of(block);
+  // A warp's rows (4 or 8) are as many query heads as that many have, the rest tokens.
+  const int log_rows = hd == 64 ? 3 : 2;
+  while (a.q_heads < log_rows && 2 << a.q_heads <= a.n_q) ++a.q_heads;
+  const int log_set = a.q_heads + pool_write8_log_rows();
+  a.q_sets = (a.n_q + (1 << log_set) - 1) >> log_set;
+  a.by_q_sets = small_div_by(a.q_sets);
+  a.by_group = small_div_by(a.group);
   a.dev_status = dev_status;
   if (rope) rope_table(rope_base, rot, vr.inv_freq, vr.scale, &a.rope);
-  // Tokens per CTA: as many as leave two CTAs per SM busy, and at most 16; a CTA's
-  // work is then divided among CTAs along y while there are too few of them.
+  // Tokens per CTA. Two CTAs are resident on an SM, and a CTA costs what its tokens do and
+  // about 2.5 more (its runs and its table): the tile with the cheapest waves. (16384 tokens,
+  // 32 over 8 heads of 128, tiles of 8, 16 and 27: see the kernel.) While there are fewer
+  // tiles than places, each is divided among CTAs along y.
   const int64_t slots = 2 * (int64_t)sms;
-  a.tile = 16;
-  while (a.tile > 1 && (T + a.tile - 1) / a.tile < slots) a.tile /= 2;
-  a.tab_rows = a.tile + std::min(block - 1, 47);
+  double best = 0.0;
+  for (int tile = 1; tile <= 32; ++tile) {
+    const int64_t waves = ((T + tile - 1) / tile + slots - 1) / slots;
+    const double cost = (double)waves * (tile + 2.5);
+    if (tile == 1 || cost < best) {
+      best = cost;
+      a.tile = tile;
+    }
+  }
+  a.tab_rows = std::min(a.tile + block - 1, 40 * 1024 / (hd * (int)sizeof(float)));
   const int64_t tiles = (T + a.tile - 1) / a.tile;
-  const int64_t units = (int64_t)a.tile * (2 * a.n_kv + (a.n_q + 15) / 16);
+  const int64_t units = (int64_t)a.tile * (2 * a.n_kv + (a.q_sets << pool_write8_log_rows())) / 4;
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, (units + 7) / 8));
-  const void* kern = pool_write8_kernel(hd);
-  const size_t smem = rope ? (size_t)a.tab_rows * hd * sizeof(float) : 0;
+  const void* kern =
+      pool_write8_kernel(hd, !rope ? kRopeNone : (rot.adjacent ? kRopeAdjacent : kRopeHalves), norm, vr.bias != nullptr);
+  const size_t smem = (size_t)pool_write8_smem_bytes(hd, rope ? a.tab_rows : 0);
   if (!allow_smem(kern, smem)) return QKVP_ERR_LAUNCH;
   return launch(kern, tiles, pool_write8_threads(), smem, static_cast<cudaStream_t>(stream), &a, (unsigned)parts);
 }

@@ -457,6 +457,11 @@ int attention_decode_smem_bytes(int head_dim);
 int attention_decode_threads();
 int attention_decode_warps();
 
+// Division of numbers below 2^16 by a fixed one: floor(2^32 / d) + 1, or 0 for d = 1.
+struct SmallDiv {
+  uint32_t magic;
+};
+
 // New tokens' keys and values into the 8-bit pool.
 struct Write8Args {
   const uint4* packed;
@@ -469,7 +474,7 @@ struct Write8Args {
   float inv_head_dim;
   int64_t T;
   int32_t n_q, n_kv, group;
-  int32_t sectioned, norm, rope_on;
+  int32_t sectioned;
   int32_t tile;           // tokens per CTA (at most 32)
   int32_t tab_rows;       // tokens that the cos/sin table has room for (at least tile)
   uint4* q;
@@ -480,11 +485,25 @@ struct Write8Args {
   float* k_scale;         // [num_pages, page_size / block, n_kv]
   float* v_scale;
   int32_t num_pages, page_size, block;
+  int32_t block_shift;    // log2(block), or -1
+  int32_t q_heads;        // log2 of the query heads in a warp's rows
+  int32_t q_sets;        // pairs of groups of so many
+  SmallDiv by_q_sets, by_group;
   int32_t* dev_status;
   RopeTable rope;
 };
-const void* pool_write8_kernel(int head_dim);
+constexpr int kRopeNone = 0, kRopeHalves = 1, kRopeAdjacent = 2;
+const void* pool_write8_kernel_d64(int rope, bool norm);
+const void* pool_write8_kernel_d64_bias(int rope, bool norm);
+const void* pool_write8_kernel_d128(int rope, bool norm);
+const void* pool_write8_kernel_d128_bias(int rope, bool norm);
+inline const void* pool_write8_kernel(int head_dim, int rope, bool norm, bool bias) {
+  if (head_dim == 64) return bias ? pool_write8_kernel_d64_bias(rope, norm) : pool_write8_kernel_d64(rope, norm);
+  return bias ? pool_write8_kernel_d128_bias(rope, norm) : pool_write8_kernel_d128(rope, norm);
+}
 int pool_write8_threads();
+int pool_write8_log_rows();
+int pool_write8_smem_bytes(int head_dim, int tab_rows);
 
 // One thread whose only wait never completes (the bounded-wait self-test).
 const void* wait_selftest_kernel();

@@ -49,8 +49,7 @@ def _variant(bias=None, inv_freq=None, rope_scale=1.0, rotary_dim=None):
         _check_dev(bias)
         if bias.dtype != torch.float32 or not bias.is_contiguous():
             raise ValueError("bias must be a contiguous float32 tensor")
-    return C.variant(inv_freq=None if inv_freq is None else [float(f) for f in inv_freq],
-                     rope_scale=0.0 if rope_scale is None else float(rope_scale), bias=bias)
+    return C.variant(inv_freq=inv_freq, rope_scale=0.0 if rope_scale is None else float(rope_scale), bias=bias)
 
 
 def _flags(nope=False, save_pre=False, norm=True, rotary_dim=None, rotary_pairs=False):
