@@ -635,7 +635,7 @@ struct DecodePlan {
 constexpr int kDecApartKeys = 128;
 
 void plan_decode(const qkvp_layout* L, int32_t batch, int32_t page_size, int32_t max_pages, int32_t prefix_len, int sms,
-                 DecodePlan* p) {
+                 int cta_warps, DecodePlan* p) {
   const int group = L->n_q / L->n_kv;
   p->box_rows = std::min(page_size & -page_size, kAttnBlock);
   p->apart = batch >= 2 && prefix_len >= kDecApartKeys && p->box_rows >= 8 && group <= kAttnBlock;
@@ -652,11 +652,11 @@ void plan_decode(const qkvp_layout* L, int32_t batch, int32_t page_size, int32_t
   }
   p->head_blocks = (group + 15) / 16;
   const int64_t heads = (int64_t)L->n_kv * p->head_blocks;
-  const int64_t warps = (int64_t)sms * attention_decode_warps();
+  const int64_t warps = (int64_t)sms * cta_warps;
   const int64_t keys = (int64_t)max_pages * page_size + (p->apart ? 0 : prefix_len);
   const int64_t parts = (int64_t)batch * ((keys + kDecMinKeys - 1) / kDecMinKeys);  // of the least length, at most
   p->ranges = (int)std::max<int64_t>(1, std::min<int64_t>(warps / heads, parts));
-  const int64_t ctas = (p->ranges * heads + attention_decode_warps() - 1) / attention_decode_warps();
+  const int64_t ctas = (p->ranges * heads + cta_warps - 1) / cta_warps;
   p->grid = (int)std::min<int64_t>(ctas, sms);
   p->rows = (int64_t)batch + p->ranges + (int64_t)p->chunks * batch;
 }
@@ -1670,7 +1670,7 @@ int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int
   int sms = 0;
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
-  plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, &p);
+  plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, attention_decode_warps(), &p);
   *bytes = decode_workspace(layout, batch, p);
   return QKVP_OK;
 }
@@ -1697,7 +1697,7 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
   int sms = 0;
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
-  plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, &p);
+  plan_decode(layout, batch, page_size, max_pages, prefix_len, sms, attention_decode_warps(), &p);
   const size_t need = decode_workspace(layout, batch, p);
   if (!workspace || workspace_bytes < need) return QKVP_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
@@ -1768,7 +1768,16 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
 
 int qkv_attention_decode8_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,
                                     size_t* bytes) {
-  return qkv_attention_decode_workspace(layout, batch, page_size, max_pages, 0, bytes);
+  QKVP_TRY(check_decode(layout, batch, page_size, max_pages, 0));
+  if (!bytes) return QKVP_ERR_NULL;
+  *bytes = 0;
+  if (batch == 0) return QKVP_OK;
+  int sms = 0;
+  QKVP_TRY(current_device(&sms));
+  DecodePlan p;
+  plan_decode(layout, batch, page_size, max_pages, 0, sms, dec8_warps(layout->head_dim), &p);
+  *bytes = decode_workspace(layout, batch, p);
+  return QKVP_OK;
 }
 
 int qkv_attention_decode8(const qkvp_layout* layout, int32_t batch, const void* q, const void* k_pool,
@@ -1792,7 +1801,7 @@ int qkv_attention_decode8(const qkvp_layout* layout, int32_t batch, const void* 
   int sms = 0;
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
-  plan_decode(layout, batch, page_size, max_pages, 0, sms, &p);
+  plan_decode(layout, batch, page_size, max_pages, 0, sms, dec8_warps(layout->head_dim), &p);
   const size_t need = decode_workspace(layout, batch, p);
   if (!workspace || workspace_bytes < need) return QKVP_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
@@ -1818,8 +1827,8 @@ int qkv_attention_decode8(const qkvp_layout* layout, int32_t batch, const void* 
   a.lengths = lengths;
   a.tile_keys = kDec8Keys;
   return launch_decode(layout, batch, p, q, page_size, max_pages, (float)((double)sc * 1.4426950408889634), out, lse,
-                       dev_status, workspace, attention_decode8_kernel(hd), attention_decode8_threads(),
-                       (size_t)attention_decode8_smem_bytes(hd), static_cast<cudaStream_t>(stream), &a);
+                       dev_status, workspace, attention_decode8_kernel(hd, layout->n_q / layout->n_kv > 8),
+                       32 * dec8_warps(hd), (size_t)attention_decode8_smem_bytes(hd), static_cast<cudaStream_t>(stream), &a);
 }
 
 int qkv_prologue_wait_selftest(void* stream) {

@@ -8,7 +8,7 @@
 // the value scale is part of the weight, and the weights have a reference of their own,
 // so their 11 significant bits are those of the largest contributions however far apart
 // the blocks' scales are. A partial result leaves as (m + log2 l, 1, 2^(n - m) O / l),
-// which joins as plain softmax's do. A key that is not attended has t = -inf.
+// which joins as plain softmax's do.
 //
 // Codes go to the matrix units (m16n8k16, f16 with fp32 accumulation) as f16, which
 // holds every e4m3 value exactly; one conversion instruction makes two values. A row of
@@ -26,24 +26,32 @@
 namespace qkvp {
 namespace {
 
-constexpr int kDec8Warps = 8;
-
 template <int HD>
 struct Dec8Shape {
   static constexpr int kKeys = kDec8Keys;
-  static constexpr int kTileBytes = 2 * kKeys * HD;         // k codes, then v codes
-  static constexpr int kStages = 24 * 1024 / kTileBytes;    // 24 KiB a warp, 192 KiB an SM
+  static constexpr int kTileBytes = 2 * kKeys * HD;  // k codes, then v codes
+  static constexpr int kStages = 3;
+  static constexpr int kWarps = dec8_warps(HD);      // 192 KiB an SM
   static constexpr int kWarpBytes = kStages * kTileBytes;
 };
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
+// The product's rows 0 .. 7 are d[0], d[1] of the lanes, its rows 8 .. 15 d[2], d[3].
+// With 8 heads or fewer the latter are padding: they take no registers between products.
 __device__ __forceinline__ void mma16816h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816h(float (&d)[2], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
+  float e, f;
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%8,%5,%8}, {%6,%7}, {%0,%1,%9,%9};"
+      : "+f"(d[0]), "+f"(d[1]), "=f"(e), "=f"(f)
+      : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   uint32_t r;
@@ -57,6 +65,9 @@ __device__ __forceinline__ float quad_max(float v) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
+// A row's references before its first key: so low that any score passes them.
+constexpr float kNoKey = -1e30f;
+
 // Place of 16-byte chunk ch of a tile's row, so that the 8 rows of a matrix of ldmatrix
 // lie in different banks: rows of 128 bytes, or of 64 (two to a line).
 template <int HD>
@@ -66,16 +77,17 @@ __device__ __forceinline__ int dec8_at(int row, int ch) {
 
 }  // namespace
 
-template <int HD>
-__global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_kernel(const AttnDecodeArgs a) {
+// X: groups of 8 query heads that a warp's products hold (1 or 2).
+template <int HD, int X>
+__global__ void __launch_bounds__(32 * dec8_warps(HD), 1) qkvp_attention_decode8_kernel(const AttnDecodeArgs a) {
   using SH = Dec8Shape<HD>;
-  constexpr int ST = SH::kStages, KT = SH::kKeys, NT = KT / 8;
+  constexpr int ST = SH::kStages, KT = SH::kKeys, NT = KT / 8, kDec8Warps = SH::kWarps;
   constexpr int CH = HD / 16, RPI = 32 / CH;  // 16-byte chunks per row, rows per copy instruction
   static_assert(KT == 32, "a lane per key");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ uint32_t s_in[kDec8Warps][ST];          // bit i: key i of the stage's tile is attended
   __shared__ float s_scale[kDec8Warps][ST][2][KT];   // its keys' scales as they are stored
-  __shared__ float4 s_key[kDec8Warps][KT];           // a, 0 (-inf: not attended), log2 b of the tile at work
+  __shared__ float2 s_key[kDec8Warps][KT];           // a, log2 b of the tile at work
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = smem_addr(smem_raw) + warp * SH::kWarpBytes;
   griddep_wait();
@@ -91,7 +103,7 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
     if (t0 >= total) break;
     const int n_tiles = (int)min(quota, total - t0);
     const int hv = w % heads, kvh = hv / a.head_blocks, hb = hv % a.head_blocks;
-    const int head0 = kvh * a.group + hb * 16, n_heads = min(16, a.group - hb * 16);
+    const int head0 = kvh * a.group + hb * 8 * X, n_heads = min(8 * X, a.group - hb * 8 * X);
     DecCursor cu = dec_begin(a, t0, lane);  // where the range begins
 
     // Loads run ST - 1 tiles ahead of the arithmetic, and the page lookup of a
@@ -106,6 +118,7 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
       ld_keys = (uint32_t)dec_own(a, ld.b);
     };
     const int ch = lane % CH, row_ch = a.n_kv * CH;
+    const uint32_t lane_to = dec8_at<HD>(lane / CH, ch);  // (its place in the rows RPI i .. of a tile, or with bit 6 turned)
     const uint4* k_src = a.k_pool + kvh * CH + ch;
     const uint4* v_src = a.v_pool + kvh * CH + ch;
     auto issue = [&](uint32_t st) {
@@ -118,10 +131,9 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
       const uint32_t dst = ring + st * SH::kTileBytes;
 #pragma unroll
       for (int i = 0; i < KT / RPI; ++i) {
-        const int r = i * RPI + lane / CH;
-        const int row = __shfl_sync(0xffffffffu, slot, r);
+        const int row = __shfl_sync(0xffffffffu, slot, i * RPI + lane / CH);
         const int64_t off = (int64_t)max(row, 0) * row_ch;
-        const uint32_t to = dst + dec8_at<HD>(r, ch);
+        const uint32_t to = dst + i * RPI * HD + ((i * RPI) & 4 ? lane_to ^ 64 : lane_to);
         cp_async16(to, k_src + off, row >= 0);
         cp_async16(to + KT * HD, v_src + off, row >= 0);
       }
@@ -139,11 +151,11 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
       cp_commit();
     }
 
-    uint32_t qf[HD / 16][4];
-    float o[HD / 8][4], m[2], n[2], l[2], c[2];  // o[2 j], o[2 j + 1]: even and odd d of chunk j; c: a row's factor
+    uint32_t qf[HD / 16][2 * X];
+    float o[HD / 8][2 * X], m[X], n[X], l[X], c[X];  // o[2 j], o[2 j + 1]: even and odd d of chunk j; c: a row's factor
     auto begin = [&]() {                   // a sequence's first tile here
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < X; ++x) {
         const int r = (lane >> 2) + 8 * x;
         const uint2* src = reinterpret_cast<const uint2*>(a.q + ((int64_t)cu.b * a.n_q + head0 + r) * HD) + (lane & 3);
         uint2 raw[HD / 16];
@@ -163,18 +175,20 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
           qf[ks][x] = pack_h2(__uint_as_float(raw[ks].x << 16) * f, __uint_as_float(raw[ks].x & 0xffff0000u) * f);
-          qf[ks][2 + x] = pack_h2(__uint_as_float(raw[ks].y << 16) * f, __uint_as_float(raw[ks].y & 0xffff0000u) * f);
+          qf[ks][X + x] = pack_h2(__uint_as_float(raw[ks].y << 16) * f, __uint_as_float(raw[ks].y & 0xffff0000u) * f);
         }
-        m[x] = n[x] = -INFINITY;
+        m[x] = n[x] = kNoKey;
         l[x] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < HD / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int i = 0; i < HD / 8; ++i)
+#pragma unroll
+        for (int x = 0; x < 2 * X; ++x) o[i][x] = 0.f;
     };
     bool first = cu.tile == 0;  // of the sequence: else the segment continues one of the range before
     auto end = [&]() {          // its last tile here: the partial result
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < X; ++x) {
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
         l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
         const int r = (lane >> 2) + 8 * x;
@@ -204,15 +218,14 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
         }
       }
       cp_commit();
-      {
-        const float ka = clamp_scale(s_scale[warp][st][0][lane]), vb = clamp_scale(s_scale[warp][st][1][lane]);
-        const bool in = (s_in[warp][st] >> lane) & 1;
-        s_key[warp][lane] = make_float4(ka, in ? 0.f : -INFINITY, __log2f(vb), 0.f);
-      }
+      const uint32_t in = s_in[warp][st];
+      s_key[warp][lane] = make_float2(clamp_scale(s_scale[warp][st][0][lane]), __log2f(clamp_scale(s_scale[warp][st][1][lane])));
       const uint32_t kt = ring + st * SH::kTileBytes, vt = kt + KT * HD;
-      float s[NT][4];
+      float s[NT][2 * X];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2 * X; ++x) s[i][x] = 0.f;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -227,30 +240,52 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
           }
         }
       __syncwarp();  // s_key is written
-      float4 key[NT][2];
+      float2 key[NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int y = 0; y < 2; ++y) key[i][y] = s_key[warp][8 * i + 2 * (lane & 3) + y];
+      float d[NT][2 * X], e[NT][2 * X];  // t - m and u - n
+      auto exponents = [&]() {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int y = 0; y < 2 * X; ++y) d[i][y] = fmaf(s[i][y], key[i][y & 1].x * c[y >> 1], -m[y >> 1]);
+        if (in != 0xffffffffu) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int y = 0; y < 2 * X; ++y)
+              if (!((in >> (8 * i + 2 * (lane & 3) + (y & 1))) & 1)) d[i][y] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int y = 0; y < 2 * X; ++y) {
+            e[i][y] = d[i][y] + (key[i][y & 1].y + (m[y >> 1] - n[y >> 1]));
+            top = max3(top, d[i][y], e[i][y]);
+          }
+        return top;
+      };
       // A row's references only move where a score passes them by more than 8 powers of
       // two; until then no lane has to know the others' maxima.
-      float top[2] = {-INFINITY, -INFINITY}, tow[2] = {-INFINITY, -INFINITY};
-      float u[NT][4];
+      if (__any_sync(0xffffffffu, exponents() > 8.f)) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+        for (int x = 0; x < X; ++x) {
+          float top = -INFINITY, tow = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          s[i][x] = fmaf(s[i][x] * key[i][x & 1].x, c[x >> 1], key[i][x & 1].y);
-          u[i][x] = s[i][x] + key[i][x & 1].z;
-          top[x >> 1] = fmaxf(top[x >> 1], s[i][x]);
-          tow[x >> 1] = fmaxf(tow[x >> 1], u[i][x]);
-        }
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f || tow[0] > n[0] + 8.f || tow[1] > n[1] + 8.f)) {
+          for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float m_new = fmaxf(m[x], quad_max(top[x])), n_new = fmaxf(n[x], quad_max(tow[x]));
-          l[x] *= m_new == m[x] ? 1.f : ex2(m[x] - m_new);
-          const float f = n_new == n[x] ? 1.f : ex2(n[x] - n_new);
+            for (int y = 0; y < 2; ++y)
+              if ((in >> (8 * i + 2 * (lane & 3) + y)) & 1) {
+                const float t = s[i][2 * x + y] * (key[i][y].x * c[x]);
+                top = fmaxf(top, t);
+                tow = fmaxf(tow, t + key[i][y].y);
+              }
+          const float m_new = fmaxf(m[x], quad_max(top)), n_new = fmaxf(n[x], quad_max(tow));
+          l[x] *= ex2(m[x] - m_new);
+          const float f = ex2(n[x] - n_new);
           m[x] = m_new;
           n[x] = n_new;
 #pragma unroll
@@ -259,17 +294,16 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
             o[i][2 * x + 1] *= f;
           }
         }
+        exponents();
       }
-      uint32_t pf[NT / 2][4];
+      uint32_t pf[NT / 2][2 * X];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float off = m[x] == -INFINITY ? 0.f : -m[x], offw = n[x] == -INFINITY ? 0.f : -n[x];
+      for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          l[x] += ex2(s[i][2 * x] + off) + ex2(s[i][2 * x + 1] + off);
-          pf[i >> 1][2 * (i & 1) + x] = pack_h2(ex2(u[i][2 * x] + offw), ex2(u[i][2 * x + 1] + offw));
+          l[x] += ex2(d[i][2 * x]) + ex2(d[i][2 * x + 1]);
+          pf[i >> 1][X * (i & 1) + x] = pack_h2(ex2(e[i][2 * x]), ex2(e[i][2 * x + 1]));
         }
-      }
       {
         const int row = (((lane >> 3) & 1) << 3) + (lane & 7), hi = lane >> 4;
 #pragma unroll
@@ -305,13 +339,16 @@ __global__ void __launch_bounds__(32 * kDec8Warps, 1) qkvp_attention_decode8_ker
   }
 }
 
-const void* attention_decode8_kernel(int head_dim) {
-  return head_dim == 64 ? reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<64>)
-                        : reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<128>);
+const void* attention_decode8_kernel(int head_dim, bool wide) {
+  if (head_dim == 64)
+    return wide ? reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<64, 2>)
+                : reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<64, 1>);
+  return wide ? reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<128, 2>)
+              : reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<128, 1>);
 }
 int attention_decode8_smem_bytes(int head_dim) {
-  return kDec8Warps * (head_dim == 64 ? Dec8Shape<64>::kWarpBytes : Dec8Shape<128>::kWarpBytes);
+  return head_dim == 64 ? Dec8Shape<64>::kWarps * Dec8Shape<64>::kWarpBytes
+                        : Dec8Shape<128>::kWarps * Dec8Shape<128>::kWarpBytes;
 }
-int attention_decode8_threads() { return 32 * kDec8Warps; }
 
 }  // namespace qkvp

@@ -448,9 +448,9 @@ struct AttnDecodeArgs {
   int32_t block_shift;     // log2(block), or -1
 };
 constexpr int kDec8Keys = 32;  // keys per tile of the kernel over the 8-bit pool
-const void* attention_decode8_kernel(int head_dim);
+QKVP_HD constexpr int dec8_warps(int head_dim) { return head_dim == 64 ? 16 : 8; }  // per CTA, of tiles of 4 and 8 KiB
+const void* attention_decode8_kernel(int head_dim, bool wide);  // wide: groups of more than 8 query heads
 int attention_decode8_smem_bytes(int head_dim);
-int attention_decode8_threads();
 const void* attention_decode_kernel(int head_dim);
 const void* attention_join_kernel(int head_dim);
 int attention_decode_smem_bytes(int head_dim);

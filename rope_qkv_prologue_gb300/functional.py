@@ -578,6 +578,11 @@ def prologue_pool_write8(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, k_
     return q
 
 
+@functools.lru_cache(maxsize=1024)
+def _decode8_workspace(n_q, n_kv, head_dim, batch, page_size, max_pages, device_index):
+    return C.qkv_attention_decode8_workspace(_heads(n_q, n_kv, head_dim), batch, page_size, max_pages)
+
+
 def attention_decode8_workspace_bytes(n_q, n_kv, head_dim, batch, page_size, max_pages):
     """Workspace bytes attention_decode8 needs for these sizes on the current device."""
     return C.qkv_attention_decode8_workspace(_heads(n_q, n_kv, head_dim), batch, page_size, max_pages)
@@ -617,7 +622,7 @@ def attention_decode8(q, k_pool, v_pool, k_scale, v_scale, page_table, lengths, 
         return (out, lse) if save_lse else out
     here = _current_stream(dev)  # before a size is asked for: it is the current device's
     if workspace is None:
-        need = _decode_workspace(n_q, n_kv, D, B, page_size, max_pages, 0, dev.index)
+        need = _decode8_workspace(n_q, n_kv, D, B, page_size, max_pages, dev.index)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     _check_workspace(workspace, dev)
     C.qkv_attention_decode8(_heads(n_q, n_kv, D), B, q, k_pool, v_pool, k_scale, v_scale, num_pages, page_size, block,
