@@ -325,12 +325,14 @@ __device__ __forceinline__ void pair_backward(const float2 (&dlo)[4], const floa
 // `adjacent`, (2i, 2i + 1); the others pass through (entries f >= half of a cos/sin
 // table are 1, 0). A unit of the head is still two of its chunks: in adjacent pairs
 // a chunk holds its own partners and the unit is (e, e + CPH/2) as ever; in halves
-// of the first half / 8 * 2 chunks it is (e, e + half / 8), and the chunks behind
-// them go two by two. So everything around the rotation stays the same, and it costs
-// nothing beside the memory traffic.
+// it is (e, e + r) for the first r = half / 8 units, and the chunks behind them go two
+// by two, (e + CPH/2, e + r): so the first chunks of a head's units, like their second
+// ones, lie in different shared-memory banks (with any other pairing of them 16384 tokens,
+// 32 over 8 heads of 128, half of the head, took 104 + 108 us instead of MEASURED).
+// Everything around the rotation stays the same.
 struct RotUnit {
   int lo;    // the unit's first chunk
-  int dist;  // its second chunk is lo + dist
+  int dist;  // its second chunk is lo + dist (it may lie before the first)
   int fa;    // table entries of its coefficients 0..3 (adjacent: of the first chunk's pairs)
   int fb;    // ... 4..7 (adjacent: of the second chunk's pairs)
 };
@@ -340,7 +342,7 @@ __device__ __forceinline__ RotUnit rot_unit(int e, const RopeTable& rope) {
   if (rope.adjacent) return RotUnit{e, PPH, 4 * e, 4 * (e + PPH)};
   const int r = rope.half >> 3;
   if (e < r) return RotUnit{e, r, 8 * e, 8 * e + 4};
-  return RotUnit{r + e, PPH - r, 8 * e, 8 * e + 4};
+  return RotUnit{PPH + e, r - PPH, 8 * e, 8 * e + 4};
 }
 
 // A unit's values rotated; back: by the negative angles. c[0..3] and c[4..7] as

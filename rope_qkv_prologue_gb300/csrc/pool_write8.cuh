@@ -500,8 +500,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qkvp_pool_write8_kernel(const 
   auto run_unit = [&](int u) {
     u -= q_units;
     const int r = __popc(__ballot_sync(0xffffffffu, lane < runs && s_before[lane + 1] <= u)), x = u - s_before[r];
-    return RunUnit{t0 + s_start[r], s_len[r], s_blk[r], s_low[r], s_page0[r], s_ts[r], (x & 1) ? (int)kRoleV : (int)kRoleK,
-                   (x >> 1) * (G::ROWS >> s_ts[r])};
+    // k of all heads, then v: neighbouring warps have the same, and each some of both
+    const int half = (s_before[r + 1] - s_before[r]) >> 1;
+    return RunUnit{t0 + s_start[r], s_len[r], s_blk[r], s_low[r], s_page0[r], s_ts[r], x >= half ? (int)kRoleV : (int)kRoleK,
+                   (x >= half ? x - half : x) * (G::ROWS >> s_ts[r])};
   };
   auto fetch_queries = [&](int u, uint32_t to) {
     const int tg = (int)quotient((uint32_t)(u * (kSets)), a.by_q_sets);
