@@ -1003,12 +1003,7 @@ int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* vari
   a.page_size = page_size;
   a.block = block;
   a.block_shift = shift_of(block);
-  // A warp's rows (4 or 8) are as many query heads as that many have, the rest tokens.
-  const int log_rows = hd == 64 ? 3 : 2;
-  while (a.q_heads < log_rows && 2 << a.q_heads <= a.n_q) ++a.q_heads;
-  const int log_set = a.q_heads + pool_write8_log_rows();
-  a.q_sets = (a.n_q + (1 << log_set) - 1) >> log_set;
-  a.by_q_sets = small_div_by(a.q_sets);
+  a.by_n_q = small_div_by(a.n_q);
   a.by_group = small_div_by(a.group);
   a.dev_status = dev_status;
   if (rope) rope_table(rope_base, rot, vr.inv_freq, vr.scale, &a.rope);
@@ -1018,7 +1013,8 @@ int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* vari
   // tiles than places, each is divided among CTAs along y.
   const int64_t slots = 2 * (int64_t)sms;
   double best = 0.0;
-  for (int tile = 1; tile <= 32; ++tile) {
+  const int most = std::min(32, 65535 / a.n_q);  // (its rows of query heads are counted in 16 bits)
+  for (int tile = 1; tile <= most; ++tile) {
     const int64_t waves = ((T + tile - 1) / tile + slots - 1) / slots;
     const double cost = (double)waves * (tile + 2.5);
     if (tile == 1 || cost < best) {
@@ -1028,7 +1024,7 @@ int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* vari
   }
   a.tab_rows = std::min(a.tile + block - 1, 40 * 1024 / (hd * (int)sizeof(float)));
   const int64_t tiles = (T + a.tile - 1) / a.tile;
-  const int64_t units = (int64_t)a.tile * (2 * a.n_kv + (a.q_sets << pool_write8_log_rows())) / 4;
+  const int64_t units = (int64_t)a.tile * (8 * a.n_kv + a.n_q) / 16;
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, (units + 7) / 8));
   const void* kern =
       pool_write8_kernel(hd, !rope ? kRopeNone : (rot.adjacent ? kRopeAdjacent : kRopeHalves), norm, vr.bias != nullptr);

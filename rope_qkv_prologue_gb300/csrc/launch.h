@@ -486,9 +486,7 @@ struct Write8Args {
   float* v_scale;
   int32_t num_pages, page_size, block;
   int32_t block_shift;    // log2(block), or -1
-  int32_t q_heads;        // log2 of the query heads in a warp's rows
-  int32_t q_sets;        // pairs of groups of so many
-  SmallDiv by_q_sets, by_group;
+  SmallDiv by_n_q, by_group;
   int32_t* dev_status;
   RopeTable rope;
 };
@@ -502,7 +500,6 @@ inline const void* pool_write8_kernel(int head_dim, int rope, bool norm, bool bi
   return bias ? pool_write8_kernel_d128_bias(rope, norm) : pool_write8_kernel_d128(rope, norm);
 }
 int pool_write8_threads();
-int pool_write8_log_rows();
 int pool_write8_smem_bytes(int head_dim, int tab_rows);
 
 // One thread whose only wait never completes (the bounded-wait self-test).

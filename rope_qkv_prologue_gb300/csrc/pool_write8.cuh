@@ -40,8 +40,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kPasses = 4;         // times the rows that a warp holds: a step
 constexpr int kStepBytes = 4096;
-constexpr int kRows = 1, kLogRows = 0;  // rows of a lane that go through the arithmetic together
-constexpr int kSets = kPasses / kRows;
 
 // A row's two chunks as they are stored, and widened.
 struct Raw {
@@ -296,33 +294,23 @@ __device__ __forceinline__ void run_step(const Write8Args& a, const RunUnit& u, 
   buf += (uint32_t)(row * (HD * 2) + 16 * ru.lo);
   const bool plain = !key && !BIAS;  // bf16 as it is
   const int i0 = (pass0 << u.ts) + tok;
-  // the values of this lane's rows of two of the chunk's passes
-  auto rows_at = [&](int p, Row (&y)[kRows]) {
-#pragma unroll
-    for (int j = 0; j < kRows; ++j)
-      widen<HD, BIAS>(a, head, read_raw(buf + min(p + j, kPasses - 1) * 1024, ru.dist), ru, y[j]);
+  auto row_at = [&](int p, Row& y) {  // the values of this lane's row of the chunk's pass
+    widen<HD, BIAS>(a, head, read_raw(buf + p * 1024, ru.dist), ru, y);
     if (key) {
       if (NORM) {
         Weights w;
         read_weights(s_w + HD, ru, w);
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) norm_row<HD>(a, w, y[j]);
+        norm_row<HD>(a, w, y);
       }
       if (ROPE) {
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          const int at = (int)(u.t0 - tab_first) + min(i0 + ((p + j) << u.ts), u.len - 1);
-          Angles g;
-          if (at < tab_rows) read_angles<HD>(s_tab + at * HD, ru, g);
-          else make_angles(a, tab_first + at, ru, g);
-          turn_row<ROPE>(g, y[j]);
-        }
+        const int at = (int)(u.t0 - tab_first) + min(i0 + (p << u.ts), u.len - 1);
+        Angles g;
+        if (at < tab_rows) read_angles<HD>(s_tab + at * HD, ru, g);
+        else make_angles(a, tab_first + at, ru, g);
+        turn_row<ROPE>(g, y);
       }
     }
-    if (st.inf || chunks > 1) {
-#pragma unroll
-      for (int j = 0; j < kRows; ++j) no_infs(y[j]);
-    }
+    if (st.inf || chunks > 1) no_infs(y);
   };
   if (step < chunks) {
     if (step == 0) {
@@ -336,12 +324,10 @@ __device__ __forceinline__ void run_step(const Write8Args& a, const RunUnit& u, 
           if (i0 + (p << u.ts) < u.len) st.top = raw_max(read_raw(buf + p * 1024, ru.dist), st.top);
       } else {
 #pragma unroll 1
-        for (int p = 0; p < n; p += kRows) {
-          Row y[kRows];
-          rows_at(p, y);
-#pragma unroll
-          for (int j = 0; j < kRows; ++j)
-            if (p + j < n && i0 + ((p + j) << u.ts) < u.len) st.top = row_max(y[j], st.top);
+        for (int p = 0; p < n; ++p) {
+          Row y;
+          row_at(p, y);
+          if (i0 + (p << u.ts) < u.len) st.top = row_max(y, st.top);
         }
       }
       if (step + 1 < chunks) return;
@@ -360,19 +346,15 @@ __device__ __forceinline__ void run_step(const Write8Args& a, const RunUnit& u, 
   const int32_t* offset = a.offset + u.t0;
   uint2* pool = reinterpret_cast<uint2*>(key ? a.k_pool : a.v_pool) + h * (HD / 8) + ru.lo;
 #pragma unroll 1
-  for (int p = 0; p < n; p += kRows) {
-    Row y[kRows];
-    int of[kRows];
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) of[j] = offset[min(i0 + ((p + j) << u.ts), u.len - 1)];
-    rows_at(p, y);
-#pragma unroll
-    for (int j = 0; j < kRows; ++j)
-      if (p + j < n && i0 + ((p + j) << u.ts) < u.len && mine) {
-        uint2* dst = pool + (int64_t)(u.page0 + of[j]) * (a.n_kv * (HD / 8));
-        dst[0] = codes8(y[j].lo, st.inv);
-        dst[ru.dist] = codes8(y[j].hi, st.inv);
-      }
+  for (int p = 0; p < n; ++p) {
+    Row y;
+    const int i = i0 + (p << u.ts), of = offset[min(i, u.len - 1)];
+    row_at(p, y);
+    if (i < u.len && mine) {
+      uint2* dst = pool + (int64_t)(u.page0 + of) * (a.n_kv * (HD / 8));
+      dst[0] = codes8(y.lo, st.inv);
+      dst[ru.dist] = codes8(y.hi, st.inv);
+    }
   }
 }
 
@@ -488,10 +470,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qkvp_pool_write8_kernel(const 
 
   const RotUnit ru = ROPE ? rot_unit<G::CPH>(lane % G::PPH, a.rope) : RotUnit{lane % G::PPH, G::PPH, 0, 4};
   const int row = lane / G::PPH;
-  // Query heads: a pass is 1 << q_heads heads of as many tokens as the warp's rows then have
-  // room for; passes go through the heads, two at a time, then the tokens.
-  const int q_tok = row >> a.q_heads, q_head = row & ((1 << a.q_heads) - 1), q_log = LOG_ROWS - a.q_heads;
-  const int q_sets = ((ntok + (1 << q_log) - 1) >> q_log) * a.q_sets, q_units = (q_sets + kSets - 1) / (kSets);
+  // The rows of query heads in their order in q, token by token: a pass takes the warp's next
+  // rows, so where they go to needs no arithmetic.
+  const int q_rows = ntok * a.n_q, q_units = (q_rows + kPasses * G::ROWS - 1) / (kPasses * G::ROWS);
   const uint32_t buffers = smem_addr(smem) + warp * 2 * kStepBytes;
   const uint32_t lane_at = (uint32_t)(row * (HD * 2) + 16 * ru.lo);
   const uint4* q_src = a.packed + t0 * a.row_stride16 + ru.lo;
@@ -506,21 +487,14 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qkvp_pool_write8_kernel(const 
                    (x >= half ? x - half : x) * (G::ROWS >> s_ts[r])};
   };
   auto fetch_queries = [&](int u, uint32_t to) {
-    const int tg = (int)quotient((uint32_t)(u * (kSets)), a.by_q_sets);
-    int h = ((u * (kSets) - tg * a.q_sets) << (a.q_heads + kLogRows)) + q_head, tok = (tg << q_log) + q_tok;
-    const uint4* x = q_src + tok * a.row_stride16;
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      if (tok < ntok && h < a.n_q) {  // (rows that are not are never used)
-        const uint4* y = x + packed_head(a, kRoleQ, h) * G::CPH;
+      const int n = (u * kPasses + p) * G::ROWS + row;
+      if (n < q_rows) {  // (rows that are not are never used)
+        const int tok = (int)quotient((uint32_t)n, a.by_n_q), h = n - tok * a.n_q;
+        const uint4* y = q_src + tok * a.row_stride16 + packed_head(a, kRoleQ, h) * G::CPH;
         copy16(to + lane_at + p * 1024, y);
         copy16(to + lane_at + p * 1024 + 16 * ru.dist, y + ru.dist);
-      }
-      h += 1 << a.q_heads;
-      if (h - q_head == a.q_sets << (a.q_heads + kLogRows)) {  // the next tokens
-        h = q_head;
-        tok += 1 << q_log;
-        x += a.row_stride16 << q_log;
       }
     }
   };
@@ -571,43 +545,32 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qkvp_pool_write8_kernel(const 
     Weights w;
     if (NORM) read_weights(s_w, ru, w);
     Angles angles;
-    int angles_of = -1;  // the group of tokens whose angles these are
+    int angles_of = -1;  // the token whose angles these are
     for (; u < q_units; u += stride) {
       fetch_next(u + stride, 0);
-            int tg = (int)quotient((uint32_t)(u * (kSets)), a.by_q_sets);
-            int h0 = (u * (kSets) - tg * a.q_sets) << (a.q_heads + kLogRows);  // of the pair (uniform)
-            const int n = kRows * min(kSets, q_sets - u * (kSets));
+      int n = u * kPasses * G::ROWS + row;
+      uint4* dst = q_dst + n * G::CPH;
+      uint32_t from = here + lane_at;
 #pragma unroll 1
-            for (int p = 0; p < n; p += kRows) {
-              const int tok = (tg << q_log) + q_tok, h = h0 + q_head;
-              if (ROPE && tg != angles_of) {
-                read_angles<HD>(s_tab + min(tok, ntok - 1) * HD, ru, angles);
-                angles_of = tg;
-              }
-              Row y[kRows];
-#pragma unroll
-              for (int j = 0; j < kRows; ++j)
-                widen<HD, BIAS>(a, BIAS ? packed_head(a, kRoleQ, min(h + (j << a.q_heads), a.n_q - 1)) : 0,
-                          read_raw(here + lane_at + (p + j) * 1024, ru.dist), ru, y[j]);
-        if (NORM) {
-#pragma unroll
-          for (int j = 0; j < kRows; ++j) norm_row<HD>(a, w, y[j]);
+      for (int p = 0; p < kPasses; ++p) {
+        if (n - row >= q_rows) break;
+        const int tok = (int)quotient((uint32_t)min(n, q_rows - 1), a.by_n_q);
+        if (ROPE && tok != angles_of) {
+          read_angles<HD>(s_tab + tok * HD, ru, angles);
+          angles_of = tok;
         }
-#pragma unroll
-              for (int j = 0; j < kRows; ++j) {
-                if (ROPE) turn_row<ROPE>(angles, y[j]);
-                if (tok < ntok && h + (j << a.q_heads) < a.n_q) {
-                  uint4* dst = q_dst + (tok * a.n_q + h + (j << a.q_heads)) * G::CPH;
-                  st_keep(dst, pack_pairs(y[j].lo));
-                  st_keep(dst + ru.dist, pack_pairs(y[j].hi));
-                }
-              }
-              h0 += kRows << a.q_heads;
-              if (h0 == a.q_sets << (a.q_heads + kLogRows)) {
-                h0 = 0;
-                ++tg;
-              }
-            }
+        Row y;
+        widen<HD, BIAS>(a, BIAS ? packed_head(a, kRoleQ, min(n, q_rows - 1) - tok * a.n_q) : 0, read_raw(from, ru.dist), ru, y);
+        if (NORM) norm_row<HD>(a, w, y);
+        if (ROPE) turn_row<ROPE>(angles, y);
+        if (n < q_rows) {
+          st_keep(dst, pack_pairs(y.lo));
+          st_keep(dst + ru.dist, pack_pairs(y.hi));
+        }
+        n += G::ROWS;
+        dst += G::ROWS * G::CPH;
+        from += 1024;
+      }
       turn_over();
     }
   }

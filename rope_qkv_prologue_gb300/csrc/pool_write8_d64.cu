@@ -6,6 +6,5 @@ const void* pool_write8_kernel_d64(int rope, bool norm) { return pool_write8_pic
 int pool_write8_smem_bytes(int head_dim, int tab_rows) {
   return kWarps * 2 * kStepBytes + tab_rows * head_dim * (int)sizeof(float);
 }
-int pool_write8_log_rows() { return kLogRows; }
 int pool_write8_threads() { return 32 * kWarps; }
 }  // namespace qkvp
