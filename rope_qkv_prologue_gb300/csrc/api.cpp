@@ -1654,7 +1654,7 @@ static int launch_decode(const qkvp_layout* layout, int32_t batch, const DecodeP
   QKVP_TRY(launch(kern, p.grid, threads, smem, st, a));
   const int per = kJoinWarps / a->wph;
   const int64_t joins = (int64_t)batch * ((layout->n_q + per - 1) / per);
-  return launch(attention_join_kernel(hd), joins, 32 * kJoinWarps, 0, st, a);
+  return launch(attention_join_kernel(hd, a->wph > 1), joins, 32 * kJoinWarps, 0, st, a);
 }
 
 int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,

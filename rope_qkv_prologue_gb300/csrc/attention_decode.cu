@@ -19,7 +19,8 @@
 // Lengths are read on the device: nothing has to be planned on the host, and a
 // captured call follows lengths that grow. A sequence that lies in several parts
 // leaves a partial result (m, l, O) in each; qkvp_attention_join_kernel adds
-// them, and the shared prefix's, in a fixed order.
+// them, and the shared prefix's, in a fixed order. Its chain of dependent reads is what it
+// costs: the results are read beside the maxima that weigh them.
 //
 // Measured: 131072 keys, 32 over 8 heads of 128: 88 us, 0.89 of the copy rate (the first
 // kernel 0.94; the join is a chain of dependent reads); 256 sequences of up to 4096 keys, 64
@@ -262,11 +263,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) qkvp_attention_decode_kernel(c
   if (a.prefix_chunks) griddep_wait();
 }
 
+// A warp's joined result of one query head, V values per lane.
+template <int HD, int V>
+__device__ __forceinline__ void join_out(const AttnDecodeArgs& a, int b, int head, int lane, float top, float sum,
+                                         const float (&o)[V]) {
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((int64_t)b * a.n_q + head) * HD) + V / 2 * lane;
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) dst[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (a.lse && lane == 0) a.lse[(int64_t)b * a.n_q + head] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 // Joins the partial results of each (sequence, head): its own in the ranges it
 // lies in and the shared prefix's key ranges, in that order. kJoinWarps warps per
 // CTA, `wph` of them per head. A chain of dependent reads (lengths, maxima and
 // sums, results), so each is made by as many lanes at once as there are.
-template <int HD>
+// WIDE: several warps per head (wph > 1).
+template <int HD, bool WIDE>
 __global__ void __launch_bounds__(32 * kJoinWarps) qkvp_attention_join_kernel(const AttnDecodeArgs a) {
   constexpr int V = HD / 32;             // values per lane
   constexpr int kCap = kJoinParts / kJoinWarps;  // factors in shared memory per warp
@@ -293,6 +306,47 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qkvp_attention_join_kernel(co
     return r * a.n_q + head;
   };
   float top = -INFINITY, sum = 0.f, o[V] = {};
+  // One warp per head and few parts (most sequences of a large batch lie in one or two):
+  // lane i holds part i's factor, and the results are read beside the maxima, not behind
+  // them. The same sums in the same order as below.
+  if (!WIDE && parts <= kJoinFew) {
+    if (!on) return;
+    float v[kJoinFew][V];
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      if (i >= parts) break;
+      const float* src = a.part_o + row_of(i) * HD + V * lane;
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i][e] = src[e];
+    }
+    const float2 ml = lane < parts ? a.part_ml[row_of(lane)] : make_float2(-INFINITY, 0.f);
+    top = ml.x;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float f = lane < parts ? ex2(ml.x - (top == -INFINITY ? 0.f : top)) : 0.f;
+    sum = lane < parts ? f * ml.y : 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      if (i >= parts) break;
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = fi != 0.f ? fmaf(fi, v[i][e], o[e]) : o[e];
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    join_out<HD>(a, b, head, lane, top, sum, o);
+    return;
+  }
+  // Of many parts, a warp's first results are on their way beside the maxima too.
+  constexpr int kAhead = WIDE ? 24 : 0;
+  float ahead[WIDE ? kAhead : 1][V];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    if (!on || sub + k * wph >= parts) break;
+    const float* src = a.part_o + row_of(sub + k * wph) * HD + V * lane;
+#pragma unroll
+    for (int e = 0; e < V; ++e) ahead[k][e] = src[e];
+  }
 #pragma unroll 4
   for (int i = on ? tid : parts; i < parts; i += 32 * wph) top = fmaxf(top, a.part_ml[row_of(i)].x);
 #pragma unroll
@@ -311,7 +365,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qkvp_attention_join_kernel(co
       sum += f[i] * v.y;
     }
     __syncthreads();
-    for (int i = on ? sub : n; i < n; i += 8 * wph) {
+    if (!i0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (!on || sub + k * wph >= n) break;
+        const float fk = f[sub + k * wph];
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fk != 0.f ? fmaf(fk, ahead[k][e], o[e]) : o[e];
+      }
+    }
+    for (int i = on ? sub + (i0 ? 0 : kAhead * wph) : n; i < n; i += 8 * wph) {
       float v[8][V];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -342,21 +405,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qkvp_attention_join_kernel(co
         for (int e = 0; e < V; ++e) o[e] += s_o[warp + x][V * lane + e];
       }
   }
-  if (!on || sub != 0) return;
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((int64_t)b * a.n_q + head) * HD) + V / 2 * lane;
-#pragma unroll
-  for (int e = 0; e < V / 2; ++e) dst[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)b * a.n_q + head] = (top + log2f(sum)) * 0.6931471805599453f;
+  if (on && sub == 0) join_out<HD>(a, b, head, lane, top, sum, o);
 }
 
 const void* attention_decode_kernel(int head_dim) {
   return head_dim == 64 ? reinterpret_cast<const void*>(&qkvp_attention_decode_kernel<64>)
                         : reinterpret_cast<const void*>(&qkvp_attention_decode_kernel<128>);
 }
-const void* attention_join_kernel(int head_dim) {
-  return head_dim == 64 ? reinterpret_cast<const void*>(&qkvp_attention_join_kernel<64>)
-                        : reinterpret_cast<const void*>(&qkvp_attention_join_kernel<128>);
+const void* attention_join_kernel(int head_dim, bool wide) {
+  if (head_dim == 64)
+    return wide ? reinterpret_cast<const void*>(&qkvp_attention_join_kernel<64, true>)
+                : reinterpret_cast<const void*>(&qkvp_attention_join_kernel<64, false>);
+  return wide ? reinterpret_cast<const void*>(&qkvp_attention_join_kernel<128, true>)
+              : reinterpret_cast<const void*>(&qkvp_attention_join_kernel<128, false>);
 }
 int attention_decode_smem_bytes(int head_dim) {
   return kDecWarps * (head_dim == 64 ? DecShape<64>::kWarpBytes : DecShape<128>::kWarpBytes);

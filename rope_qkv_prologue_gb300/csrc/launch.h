@@ -414,6 +414,7 @@ int attention_bwd_threads();
 constexpr int kDecMinKeys = 64;   // keys of a part (at least)
 QKVP_HD constexpr int dec_tile_keys(int head_dim) { return head_dim == 64 ? 32 : 16; }  // keys per tile: 8 KiB
 constexpr int kJoinWarps = 8;     // warps per CTA of the kernel that joins the partial results
+constexpr int kJoinFew = 8;       // partial results that a warp joins at once
 constexpr int kJoinParts = 1024;  // partial results whose factors it holds in shared memory
 struct AttnDecodeArgs {
   int32_t n_q, n_kv, group;
@@ -452,7 +453,7 @@ QKVP_HD constexpr int dec8_warps(int head_dim) { return head_dim == 64 ? 16 : 8;
 const void* attention_decode8_kernel(int head_dim, bool wide);  // wide: groups of more than 8 query heads
 int attention_decode8_smem_bytes(int head_dim);
 const void* attention_decode_kernel(int head_dim);
-const void* attention_join_kernel(int head_dim);
+const void* attention_join_kernel(int head_dim, bool wide);  // wide: several warps per head
 int attention_decode_smem_bytes(int head_dim);
 int attention_decode_threads();
 int attention_decode_warps();
