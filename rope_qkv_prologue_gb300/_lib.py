@@ -9,6 +9,7 @@ there is no Python or CPU fallback: if the library is missing, importing this
 module raises.
 """
 
+import array
 import ctypes
 import functools
 import os
@@ -170,9 +171,9 @@ def _ret(status, func, check):
 
 
 @functools.lru_cache(maxsize=256)
-def _frequencies(values):
-    """The C array of these frequencies (the library only reads it), as a pointer."""
-    return ctypes.cast((ctypes.c_double * len(values))(*values), ctypes.POINTER(ctypes.c_double))
+def _frequencies(doubles):
+    """The C array of these frequencies' bytes (the library only reads it), as a pointer."""
+    return ctypes.cast((ctypes.c_char * len(doubles)).from_buffer_copy(doubles), ctypes.POINTER(ctypes.c_double))
 
 
 def variant(inv_freq=None, rope_scale=0.0, bias=None):
@@ -181,7 +182,7 @@ def variant(inv_freq=None, rope_scale=0.0, bias=None):
     address, float32 [(n_q + 2 n_kv) * head_dim] in packed-row order."""
     v = qkvp_variant()
     if inv_freq is not None:
-        arr = _frequencies(tuple(map(float, inv_freq)))
+        arr = _frequencies(array.array("d", inv_freq).tobytes())
         v._inv_freq_keepalive = arr
         v.inv_freq = arr
     v.rope_scale = float(rope_scale)

@@ -86,6 +86,12 @@ def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interl
     return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
 
 
+@functools.lru_cache(maxsize=1024)
+def _backward_workspace(kind, n_q, n_kv, head_dim, T, bias):
+    # (the size depends on there being a bias, not on where it is)
+    return C.qkv_prologue_bwd_workspace_size_ex(_layout(kind, n_q, n_kv, head_dim), C.variant(bias=16) if bias else None, T)
+
+
 def prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_dim=64,
                       kind="interleaved", eps=1e-6, rope_base=500000.0, nope=False, stream=None,
                       workspace=None, norm=True, bias=None, inv_freq=None, rope_scale=1.0, rotary_dim=None,
@@ -108,7 +114,7 @@ def prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_d
             if t is not None:
                 t.zero_()
         return (dpacked, dw_q, dw_k, dbias) if bias is not None else (dpacked, dw_q, dw_k)
-    need = C.qkv_prologue_bwd_workspace_size_ex(L, V, T)
+    need = _backward_workspace(kind, n_q, n_kv, head_dim, T, bias is not None)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     C.qkv_prologue_bwd_ex(L, V, T, dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, eps, rope_base,
@@ -333,7 +339,7 @@ def _check_qkv(q, k, v):
 
 
 def _check_like(t, shape, dtype, device, name):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
 
 
@@ -523,20 +529,19 @@ def attention_decode(q, k_pool, v_pool, page_table, lengths, prefix_pages=None, 
 
 def _check_pool8(k_pool, v_pool, k_scale, v_scale, device):
     """Tokens that share a scale in the pool in 8 bits, from its tensors' shapes."""
-    if (k_pool.dtype != torch.float8_e4m3fn or v_pool.dtype != torch.float8_e4m3fn or k_pool.dim() != 4
-            or k_pool.shape != v_pool.shape or not k_pool.is_contiguous() or not v_pool.is_contiguous()):
+    shape, scales = k_pool.shape, k_scale.shape
+    if (k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn or len(shape) != 4
+            or shape != v_pool.shape or not k_pool.is_contiguous() or not v_pool.is_contiguous()):
         raise ValueError("k_pool and v_pool must be contiguous float8_e4m3fn [num_pages, page_size, n_kv, D] tensors of "
                          "one shape")
-    num_pages, page_size, n_kv, _ = k_pool.shape
-    if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.dim() != 3
-            or k_scale.shape != v_scale.shape or not k_scale.is_contiguous() or not v_scale.is_contiguous()
-            or k_scale.shape[0] != num_pages or k_scale.shape[2] != n_kv or k_scale.shape[1] < 1
-            or page_size % k_scale.shape[1]):
+    if (k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or len(scales) != 3
+            or scales != v_scale.shape or not k_scale.is_contiguous() or not v_scale.is_contiguous()
+            or scales[0] != shape[0] or scales[2] != shape[2] or scales[1] < 1 or shape[1] % scales[1]):
         raise ValueError("k_scale and v_scale must be contiguous float32 [num_pages, page_size / block, n_kv] tensors of "
                          "one shape, block a divisor of page_size")
     if k_pool.device != device or v_pool.device != device or k_scale.device != device or v_scale.device != device:
         raise ValueError(f"the pools and their scales must live on {device}")
-    return page_size // k_scale.shape[1]
+    return shape[1] // scales[1]
 
 
 def prologue_pool_write8(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, k_scale, v_scale, n_q, n_kv, head_dim=64,
@@ -556,15 +561,19 @@ def prologue_pool_write8(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, k_
                           inv_freq, rope_scale, rotary_dim, rotary_pairs)
     L, T = _layout_of(packed, n_q, n_kv, head_dim, kind, rotary_dim)
     dev = packed.device
-    if packed.dtype != torch.bfloat16 or not packed.is_cuda:
+    if packed.dtype is not torch.bfloat16 or not packed.is_cuda:
         raise ValueError("packed must be a bf16 tensor on a CUDA device")
     block = _check_pool8(k_pool, v_pool, k_scale, v_scale, dev)
     if k_pool.shape[2] != n_kv or k_pool.shape[3] != head_dim:
         raise ValueError(f"the pools must hold {n_kv} heads of {head_dim}")
-    for t, name in ((page, "page"), (offset, "offset")) + (() if nope else ((pos, "pos"),)):
-        _check_like(t, (T,), torch.int32, dev, name)
-    for t, name in ((w_q, "w_q"), (w_k, "w_k")) if norm else ():
-        _check_like(t, (head_dim,), torch.float32, dev, name)
+    tokens = (T,)
+    _check_like(page, tokens, torch.int32, dev, "page")
+    _check_like(offset, tokens, torch.int32, dev, "offset")
+    if not nope:
+        _check_like(pos, tokens, torch.int32, dev, "pos")
+    if norm:
+        _check_like(w_q, (head_dim,), torch.float32, dev, "w_q")
+        _check_like(w_k, (head_dim,), torch.float32, dev, "w_k")
     if bias is not None:
         _check_like(bias, ((n_q + 2 * n_kv) * head_dim,), torch.float32, dev, "bias")
     _check_status(dev_status, dev)
