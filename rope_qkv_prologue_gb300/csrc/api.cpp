@@ -1022,7 +1022,7 @@ int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* vari
       a.tile = tile;
     }
   }
-  a.tab_rows = std::min(a.tile + block - 1, 40 * 1024 / (hd * (int)sizeof(float)));
+  a.tab_rows = (int)std::min<int64_t>((int64_t)a.tile + block - 1, 40 * 1024 / (hd * (int)sizeof(float)));
   const int64_t tiles = (T + a.tile - 1) / a.tile;
   const int64_t units = (int64_t)a.tile * (8 * a.n_kv + a.n_q) / 16;
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, (units + 7) / 8));

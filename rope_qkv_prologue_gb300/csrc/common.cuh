@@ -322,19 +322,22 @@ __device__ __forceinline__ void pair_backward(const float2 (&dlo)[4], const floa
 // ------------------------------------------------ other rotary layouts ----
 //
 // The first 2 * half values of a head are rotated, in pairs (i, i + half) or, when
-// `adjacent`, (2i, 2i + 1); the others pass through (entries f >= half of a cos/sin
-// table are 1, 0). A unit of the head is still two of its chunks: in adjacent pairs
+// `adjacent`, (2i, 2i + 1); the others pass through (not as rotations by 0: an infinity
+// times 0 would make its unit's other value NaN). A unit of the head is still two of its chunks: in adjacent pairs
 // a chunk holds its own partners and the unit is (e, e + CPH/2) as ever; in halves
 // it is (e, e + r) for the first r = half / 8 units, and the chunks behind them go two
 // by two, (e + CPH/2, e + r): so the first chunks of a head's units, like their second
 // ones, lie in different shared-memory banks (with any other pairing of them 16384 tokens,
-// 32 over 8 heads of 128, half of the head, took 104 + 108 us instead of MEASURED).
+// 32 over 8 heads of 128, half of the head, took 208 us forward and backward instead of 190).
 // Everything around the rotation stays the same.
 struct RotUnit {
   int lo;    // the unit's first chunk
   int dist;  // its second chunk is lo + dist (it may lie before the first)
   int fa;    // table entries of its coefficients 0..3 (adjacent: of the first chunk's pairs)
   int fb;    // ... 4..7 (adjacent: of the second chunk's pairs)
+  // (half is a multiple of 8: a chunk's pairs, or a unit's, are rotated together or not at all)
+  __device__ __forceinline__ bool first_turns(const RopeTable& rope) const { return fa < rope.half; }
+  __device__ __forceinline__ bool second_turns(const RopeTable& rope) const { return fb < rope.half; }
 };
 template <int CPH>
 __device__ __forceinline__ RotUnit rot_unit(int e, const RopeTable& rope) {
@@ -345,7 +348,7 @@ __device__ __forceinline__ RotUnit rot_unit(int e, const RopeTable& rope) {
   return RotUnit{PPH + e, r - PPH, 8 * e, 8 * e + 4};
 }
 
-// A unit's values rotated; back: by the negative angles. c[0..3] and c[4..7] as
+// A unit's values rotated (sign -1: by the negative angles). c[0..3] and c[4..7] as
 // pairs are the coefficients at fa and fb.
 __device__ __forceinline__ void rotate_adjacent(float2 (&y)[4], const float2 (&c)[2], const float2 (&sn)[2], float sign) {
 #pragma unroll
@@ -356,13 +359,14 @@ __device__ __forceinline__ void rotate_adjacent(float2 (&y)[4], const float2 (&c
   }
 }
 __device__ __forceinline__ void rotate_unit(float2 (&lo)[4], float2 (&hi)[4], const float2 (&c)[4], const float2 (&sn)[4],
-                                            bool adjacent, float sign) {
-  if (adjacent) {
+                                            const RopeTable& rope, const RotUnit& ru, float sign) {
+  if (rope.adjacent) {
     const float2 ca[2] = {c[0], c[1]}, cb[2] = {c[2], c[3]}, sa[2] = {sn[0], sn[1]}, sb[2] = {sn[2], sn[3]};
-    rotate_adjacent(lo, ca, sa, sign);
-    rotate_adjacent(hi, cb, sb, sign);
+    if (ru.first_turns(rope)) rotate_adjacent(lo, ca, sa, sign);
+    if (ru.second_turns(rope)) rotate_adjacent(hi, cb, sb, sign);
     return;
   }
+  if (!ru.first_turns(rope)) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 s = __fmul2_rn(sn[i], f2(sign, sign)), ns = __fmul2_rn(sn[i], f2(-sign, -sign));
@@ -414,13 +418,14 @@ struct RotLane {
     return v;
   }
   // y rotated (sign 1) or rotated back (-1), with the table row's cos and sin.
-  __device__ __forceinline__ void rotate(float2 (&y)[4], const float* s_cos, const float* s_sin, bool adjacent,
+  __device__ __forceinline__ void rotate(float2 (&y)[4], const float* s_cos, const float* s_sin, const RopeTable& rope,
                                          float sign) const {
+    const bool turns = fa < rope.half;
     const float4 c0 = *reinterpret_cast<const float4*>(s_cos + fa), c1 = *reinterpret_cast<const float4*>(s_cos + fb);
     const float4 s0 = *reinterpret_cast<const float4*>(s_sin + fa), s1 = *reinterpret_cast<const float4*>(s_sin + fb);
-    if (adjacent) {
+    if (rope.adjacent) {
       const float2 c[2] = {f2(c0.x, c0.y), f2(c0.z, c0.w)}, sn[2] = {f2(s0.x, s0.y), f2(s0.z, s0.w)};
-      rotate_adjacent(y, c, sn, sign);
+      if (turns) rotate_adjacent(y, c, sn, sign);
       return;
     }
     const float2 c[4] = {f2(c0.x, c0.y), f2(c0.z, c0.w), f2(c1.x, c1.y), f2(c1.z, c1.w)};
@@ -429,7 +434,7 @@ struct RotLane {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 yp = f2(__shfl_sync(0xffffffffu, y[i].x, partner), __shfl_sync(0xffffffffu, y[i].y, partner));
-      y[i] = __ffma2_rn(y[i], c[i], __fmul2_rn(yp, __fmul2_rn(sn[i], sg)));
+      if (turns) y[i] = __ffma2_rn(y[i], c[i], __fmul2_rn(yp, __fmul2_rn(sn[i], sg)));
     }
   }
 };

@@ -73,9 +73,8 @@ __device__ __forceinline__ void read_cos_sin(const float* s_cos, const float* s_
   for (int i = 0; i < 4; ++i) ssin[i] = __fmul2_rn(sn[i], sg);
 }
 
-// Fill the shared cos/sin table for tokens t_first .. t_first + ntok - 1 (ROT: entries
-// behind the rotated ones are 1, 0).
-template <int HALF, bool ROT = false>
+// Fill the shared cos/sin table for tokens t_first .. t_first + ntok - 1.
+template <int HALF>
 __device__ __forceinline__ void fill_rope_table(const int32_t* pos, const RopeTable& rope,
                                                 int64_t t_first, int ntok, float* s_cos,
                                                 float* s_sin) {
@@ -83,7 +82,7 @@ __device__ __forceinline__ void fill_rope_table(const int32_t* pos, const RopeTa
     const int tl = i / HALF;
     const int f = i % HALF;
     float c, s;
-    rope_cos_sin(pos[t_first + tl], rope.turns[f], ROT && f >= rope.half ? 1.f : rope.scale, &c, &s);
+    rope_cos_sin(pos[t_first + tl], rope.turns[f], rope.scale, &c, &s);
     s_cos[i] = c;
     s_sin[i] = s;
   }
@@ -134,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_fwd_kernel(const FwdArgs a) 
     }
 
     __syncthreads();  // readers of the previous item's table are done
-    if (ROPE) fill_rope_table<HALF, ROT>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
+    if (ROPE) fill_rope_table<HALF>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
     if (POOL) {
       for (int i = tid; i < ntok; i += kThreads) {
         const int32_t pg = a.page[t_first + i], of = a.offset[t_first + i];
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_fwd_kernel(const FwdArgs a) 
       for (int i = 0; i < 4; ++i) w[i] = NORM ? (role == kRoleQ ? wq[i] : wk[i]) : f2(1.f, 1.f);
       if constexpr (ROT) {
         chunk_forward<CPH, false, NORM>(x, w, a.eps, a.inv_head_dim, c, ssin, y, rot);
-        rot.rotate(y, s_cos + tl * HALF, s_sin + tl * HALF, a.rope.adjacent != 0, 1.f);
+        rot.rotate(y, s_cos + tl * HALF, s_sin + tl * HALF, a.rope, 1.f);
       } else {
         if (ROPE) read_cos_sin<HALF>(s_cos, s_sin, tl, f0, sign, c, ssin);
         chunk_forward<CPH, ROPE, NORM>(x, w, a.eps, a.inv_head_dim, c, ssin, y);
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_bwd_kernel(const BwdArgs a) 
     }
 
     __syncthreads();
-    if (ROPE) fill_rope_table<HALF, ROT>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
+    if (ROPE) fill_rope_table<HALF>(a.pos, a.rope, t_first, ntok, s_cos, s_sin);
     __syncthreads();
 
 #pragma unroll
@@ -315,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) qkvp_bwd_kernel(const BwdArgs a) 
         float2 g[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[i] = d[i];
-        rot.rotate(g, s_cos + tl * HALF, s_sin + tl * HALF, a.rope.adjacent != 0, -1.f);
+        rot.rotate(g, s_cos + tl * HALF, s_sin + tl * HALF, a.rope, -1.f);
         chunk_backward<CPH, false, NORM>(g, x, w, a.eps, a.inv_head_dim, c, ssin, dx, gx, r, rot);
       } else {
         if (ROPE) read_cos_sin<HALF>(s_cos, s_sin, tl, f0, sign, c, ssin);

@@ -82,9 +82,7 @@ constexpr int stream_max_regs(int ncw, int cps) {
 // forward and the norm-off backward do not: there the position load paces the
 // reads, and without it they go out in bursts that interleave worse with the
 // writes (forward 147 -> 162 us; Llama 3 backward 67.5 -> 70.1 us).
-// ROT: entries of the table behind the rotated ones are 1, 0.
-template <int HALF, bool ROPE, bool POOL, bool STAGE_POS = false, bool POS_AHEAD = false, bool ROT = false,
-          class LoadTile>
+template <int HALF, bool ROPE, bool POOL, bool STAGE_POS = false, bool POS_AHEAD = false, class LoadTile>
 __device__ __forceinline__ void stream_producer(unsigned char* smem, int hd, int tpt, int stages,
                                                 int stage_bytes, int64_t n_tiles, int64_t T,
                                                 const int32_t* pos, const RopeTable& rope,
@@ -133,7 +131,7 @@ __device__ __forceinline__ void stream_producer(unsigned char* smem, int hd, int
         const int tl = i / HALF, f = i - (i / HALF) * HALF;
         const int32_t pt = pos_ahead ? __shfl_sync(0xffffffffu, pos_cur, tl) : pos[t0 + tl];
         float c, sn;
-        rope_cos_sin(pt, rope.turns[f], ROT && f >= rope.half ? 1.f : rope.scale, &c, &sn);
+        rope_cos_sin(pt, rope.turns[f], rope.scale, &c, &sn);
         tab[i] = c;
         tab[tpt * HALF + i] = sn;
       }
@@ -237,7 +235,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
   if (threadIdx.x >= NCT) {
     const uint32_t row_bytes = (uint32_t)a.cpt * 16u;
     const bool dense = a.sg.dense != 0;
-    stream_producer<HALF, ROPE, POOL, false, false, ROT>(
+    stream_producer<HALF, ROPE, POOL>(
         smem, HD, tpt, stages, stage_bytes, a.sg.n_tiles, a.T, a.pos, a.rope, a.page, a.offset, a.num_pages,
         // L2 policy of the loads, measured at T = 16384: with the pre-norm save
         // normal aging is faster (149.2 -> 147.8 us), without it evict-first
@@ -331,7 +329,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_fwd_stream_kernel(co
         load_split_weights<HD>(s_w, role, ru.lo + ru.dist, whi);
       }
       pair_forward<CPH, ROPE && !ROT, NORM>(lo, hi, wlo, whi, a.eps, a.inv_head_dim, c2, s2, ylo, yhi);
-      if (ROT) rotate_unit(ylo, yhi, c2, s2, a.rope.adjacent != 0, 1.f);
+      if (ROT) rotate_unit(ylo, yhi, c2, s2, a.rope, ru, 1.f);
       if (!valid || !in_row) continue;
       // Plain contiguous forward: cache-streaming stores (measured faster on GB300
       // at every size tried); with the pre-norm save, or into a pool that
@@ -416,7 +414,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
   __syncthreads();
 
   if (threadIdx.x >= NCT) {
-    stream_producer<HALF, ROPE, false, false, NORM, ROT>(
+    stream_producer<HALF, ROPE, false, false, NORM>(
         smem, HD, tpt, stages, stage_bytes, a.sg.n_tiles, a.T, a.pos, a.rope, nullptr, nullptr, 0, 0, nullptr, a.err,
         true, [&](unsigned char* dst, int64_t t0, int ntok, uint64_t* bar, uint64_t pol) {
           const uint32_t qb = (uint32_t)qc * 16u, kb = (uint32_t)kc * 16u;
@@ -540,7 +538,7 @@ __global__ void __maxnreg__(stream_max_regs(NCW, CPS)) qkvp_bwd_stream_kernel(co
           gl2[i] = dl2[i];
           gh2[i] = dh2[i];
         }
-        rotate_unit(gl2, gh2, c2, s2, a.rope.adjacent != 0, -1.f);
+        rotate_unit(gl2, gh2, c2, s2, a.rope, ru, -1.f);
         pair_backward<CPH, false, NORM>(gl2, gh2, xl2, xh2, wlo, whi, a.eps, a.inv_head_dim, c2, s2, dxlo, dxhi,
                                         gxlo, gxhi, r);
       } else {

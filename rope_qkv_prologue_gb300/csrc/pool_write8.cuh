@@ -128,11 +128,12 @@ struct Angles {
 };
 // rotate_unit with the negatives at hand.
 template <int ROPE>
-__device__ __forceinline__ void turn_row(const Angles& g, Row& y) {
+__device__ __forceinline__ void turn_row(const Write8Args& a, const RotUnit& ru, const Angles& g, Row& y) {
   if (ROPE == kRopeAdjacent) {
-    rotate_unit(y.lo, y.hi, g.c, g.s, true, 1.f);
+    rotate_unit(y.lo, y.hi, g.c, g.s, a.rope, ru, 1.f);
     return;
   }
+  if (!ru.first_turns(a.rope)) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 p = __ffma2_rn(y.lo[i], g.c[i], __fmul2_rn(y.hi[i], g.n[i]));
@@ -155,8 +156,8 @@ __device__ __forceinline__ void make_angles(const Write8Args& a, int64_t token, 
   for (int i = 0; i < 4; ++i) {
     const int f = (i < 2 ? ru.fa : ru.fb - 4) + 2 * i;
     float2 c, s;
-    rope_cos_sin(p, a.rope.turns[f], f >= a.rope.half ? 1.f : a.rope.scale, &c.x, &s.x);
-    rope_cos_sin(p, a.rope.turns[f + 1], f + 1 >= a.rope.half ? 1.f : a.rope.scale, &c.y, &s.y);
+    rope_cos_sin(p, a.rope.turns[f], a.rope.scale, &c.x, &s.x);
+    rope_cos_sin(p, a.rope.turns[f + 1], a.rope.scale, &c.y, &s.y);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j == i) {
@@ -307,7 +308,7 @@ __device__ __forceinline__ void run_step(const Write8Args& a, const RunUnit& u, 
         Angles g;
         if (at < tab_rows) read_angles<HD>(s_tab + at * HD, ru, g);
         else make_angles(a, tab_first + at, ru, g);
-        turn_row<ROPE>(g, y);
+        turn_row<ROPE>(a, ru, g, y);
       }
     }
     if (st.inf || chunks > 1) no_infs(y);
@@ -366,7 +367,7 @@ __device__ __forceinline__ void fill_table(const Write8Args& a, float* s_tab, in
   for (int i = first * HALF + thread; i < last * HALF; i += threads) {
     const int tl = i / HALF, f = i % HALF;
     float c, s;
-    rope_cos_sin(a.pos[t0 + tl], a.rope.turns[f], f >= a.rope.half ? 1.f : a.rope.scale, &c, &s);
+    rope_cos_sin(a.pos[t0 + tl], a.rope.turns[f], a.rope.scale, &c, &s);
     s_tab[tl * HD + f] = c;
     s_tab[tl * HD + HALF + f] = s;
   }
@@ -436,6 +437,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qkvp_pool_write8_kernel(const 
         if (n < 32) break;
       }
       low = __reduce_min_sync(0xffffffffu, low);
+      __syncwarp();  // (the minima above are in s_low)
       if (lane == 0) {
         s_len[runs - 1] += end - ntok;
         s_low[runs - 1] = min(s_low[runs - 1], low);
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qkvp_pool_write8_kernel(const 
         Row y;
         widen<HD, BIAS>(a, BIAS ? packed_head(a, kRoleQ, min(n, q_rows - 1) - tok * a.n_q) : 0, read_raw(from, ru.dist), ru, y);
         if (NORM) norm_row<HD>(a, w, y);
-        if (ROPE) turn_row<ROPE>(angles, y);
+        if (ROPE) turn_row<ROPE>(a, ru, angles, y);
         if (n < q_rows) {
           st_keep(dst, pack_pairs(y.lo));
           st_keep(dst + ru.dist, pack_pairs(y.hi));

@@ -39,10 +39,13 @@ def _check_dev(*ts):
             raise ValueError("all tensors must live on a CUDA device")
 
 
-def _variant(bias=None, inv_freq=None, rope_scale=1.0, rotary_dim=None):
-    """The qkvp_variant of the GQAttention options, or None for the plain call."""
+def _variant(bias=None, inv_freq=None, rope_scale=1.0, dim=0, rotary_dim=None):
+    """The qkvp_variant of the GQAttention options, or None for the plain call. dim: the
+    head's; the library reads a frequency for each of its pairs."""
     if rotary_dim is not None and inv_freq is not None and len(inv_freq) != rotary_dim // 2:
         raise ValueError(f"inv_freq has {len(inv_freq)} frequencies, expected rotary_dim / 2 = {rotary_dim // 2}")
+    if rotary_dim is None and inv_freq is not None and len(inv_freq) < dim // 2:
+        raise ValueError(f"inv_freq has {len(inv_freq)} frequencies, expected {dim // 2}")
     if bias is None and inv_freq is None and rope_scale in (None, 0.0, 1.0):
         return None
     if bias is not None:
@@ -81,7 +84,7 @@ def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interl
     k_pre = torch.empty_like(k) if save_pre else None
     if T == 0:  # an empty tensor has no address to pass
         return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
-    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale, rotary_dim), T, packed, pos, w_q, w_k, eps, rope_base,
+    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps, rope_base,
                           _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
     return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
 
@@ -104,7 +107,7 @@ def prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_d
     T = dq.shape[0]
     L = _layout(kind, n_q, n_kv, head_dim, rotary_dim)
     dev = dq.device
-    V = _variant(bias, inv_freq, rope_scale, rotary_dim)
+    V = _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim)
     dpacked = torch.empty(T, (n_q + 2 * n_kv) * head_dim, dtype=torch.bfloat16, device=dev)
     dw_q = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dw_k = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
@@ -133,7 +136,7 @@ def prologue_pool_write(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, n_q
     q = torch.empty(T, n_q, head_dim, dtype=torch.bfloat16, device=packed.device)
     if T == 0:
         return q
-    C.qkv_prologue_pool_write_ex(L, _variant(bias, inv_freq, rope_scale, rotary_dim), T, packed, pos, w_q, w_k, eps,
+    C.qkv_prologue_pool_write_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
                                  rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
                                  v_pool,
                                  k_pool.shape[0], k_pool.shape[1], dev_status, stream)
@@ -147,7 +150,7 @@ def latent_rows(rows, pos, w, eps=1e-6, rope_base=10000.0, norm_dim=512, rope_di
     T = rows.shape[0]
     L = C.layout("latent", norm_dim=norm_dim, rope_dim=rope_dim)
     out = torch.empty(T, norm_dim + rope_dim, dtype=torch.bfloat16, device=rows.device)
-    C.qkv_prologue_fwd_ex(L, _variant(None, inv_freq, rope_scale), T, rows, pos, None, w, eps, rope_base,
+    C.qkv_prologue_fwd_ex(L, _variant(None, inv_freq, rope_scale, rope_dim), T, rows, pos, None, w, eps, rope_base,
                           _flags(nope), None, out, None, None, None, stream)
     return out
 
@@ -158,7 +161,7 @@ def latent_pool_write(rows, pos, w, page, offset, pool, eps=1e-6, rope_base=1000
     _check_dev(rows, pos, w, page, offset, pool)
     T = rows.shape[0]
     L = C.layout("latent", norm_dim=norm_dim, rope_dim=rope_dim)
-    C.qkv_prologue_pool_write_ex(L, _variant(None, inv_freq, rope_scale), T, rows, pos, None, w, eps, rope_base,
+    C.qkv_prologue_pool_write_ex(L, _variant(None, inv_freq, rope_scale, rope_dim), T, rows, pos, None, w, eps, rope_base,
                                  _flags(nope), None, page, offset, pool, None, pool.shape[0], pool.shape[1],
                                  dev_status, stream)
 
@@ -580,7 +583,7 @@ def prologue_pool_write8(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, k_
     q = torch.empty((T, n_q, head_dim), dtype=torch.bfloat16, device=dev)
     if T == 0:
         return q
-    C.qkv_prologue_pool_write8(L, _variant(bias, inv_freq, rope_scale, rotary_dim), T, packed, pos, w_q, w_k, eps,
+    C.qkv_prologue_pool_write8(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
                                rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
                                v_pool, k_scale, v_scale, k_pool.shape[0], k_pool.shape[1], block, dev_status,
                                _current_stream(dev))

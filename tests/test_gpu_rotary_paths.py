@@ -150,3 +150,86 @@ def test_layers_on_streams(lib, cuda):
         ref = A.attention_decode(f64(last), pick(keys), pick(values))
         bound = 2.0 ** -8 * np.abs(ref["out"]) + (2.0 ** -11 + 2.0 ** -10) * 1.01 * ref["out_abs"]
         assert np.all(np.abs(f64(out) - ref["out"]) <= bound)
+
+
+def _spoil(x, at, value):
+    """x [T, heads, D] with `value` at the places of `at`."""
+    y = x.clone()
+    for i in at:
+        y[i] = value
+    return y
+
+
+# token, head, value behind the rotated 32
+SPOTS = [(0, 0, 40), (2, 1, 63), (5, 1, 32), (6, 0, 55)]
+
+
+@pytest.mark.parametrize("generic", [False, True])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_what_is_not_rotated_keeps_to_itself(lib, cuda, value, pairs, generic):
+    """Without the norm an infinity or NaN in a value that is not rotated is that value's
+    alone: every other output has the bits that it has without it, forward and back."""
+    C = lib
+    n_q, n_kv, D, rot, T = 2, 2, 64, 32, 7
+    g = workloads._gen(41)
+    x = torch.randn(T, n_q + 2 * n_kv, D, generator=g).bfloat16()
+    pos = torch.arange(T, dtype=torch.int32, device=cuda) * 37
+    bf = dict(dtype=torch.bfloat16, device=cuda)
+    L = C.layout("sectioned", n_q, n_kv, D, rope_dim=rot)
+    flags = C.QKVP_ROPE_PART | C.QKVP_NORM_OFF | (C.QKVP_ROPE_PAIRS if pairs else 0) | (C.QKVP_FORCE_GENERIC if generic else 0)
+
+    def forward(x):
+        q, k, v = (torch.empty(T, n, D, **bf) for n in (n_q, n_kv, n_kv))
+        C.qkv_prologue_fwd(L, T, x.to(cuda), pos, None, None, 1e-6, 1e4, flags, q, k, v)
+        return torch.cat([q, k, v], 1).cpu()
+
+    def pool_write(x):
+        q = torch.empty(T, n_q, D, **bf)
+        pools = [torch.zeros(1, T, n_kv, D, **bf) for _ in range(2)]
+        page, offset = (torch.tensor(y, dtype=torch.int32, device=cuda) for y in ([0] * T, list(range(T))))
+        C.qkv_prologue_pool_write(L, T, x.to(cuda), pos, None, None, 1e-6, 1e4, flags, q, page, offset, *pools, 1, T)
+        return torch.cat([q, pools[0][0], pools[1][0]], 1).cpu()
+
+    def backward(x):
+        d = [y.contiguous().to(cuda) for y in x.split([n_q, n_kv, n_kv], 1)]
+        dp = torch.empty(T, n_q + 2 * n_kv, D, **bf)
+        need = C.qkv_prologue_bwd_workspace_size(L, T)
+        C.qkv_prologue_bwd(L, T, *d, None, None, pos, None, None, 1e-6, 1e4, flags, dp, None, None,
+                           torch.empty(max(need, 16), dtype=torch.uint8, device=cuda), need)
+        return dp.cpu()
+
+    at = [(t, h, e) for t, h, e in SPOTS] + [(t, n_q + h, e) for t, h, e in SPOTS]
+    for call in (forward, pool_write, backward):
+        clean, spoilt = call(_spoil(x, at, 0.0)), call(_spoil(x, at, value))
+        for i in at:
+            got = float(spoilt[i])
+            assert got != got if value != value else got == value, (call.__name__, i, got)
+        assert np.array_equal(u16(_spoil(spoilt, at, 0.0)), u16(_spoil(clean, at, 0.0))), call.__name__
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_the_8_bit_pool_takes_what_is_not_rotated_alone(lib, cuda, value, pairs):
+    n_q, n_kv, D, T = 2, 2, 64, 7
+    x = torch.randn(T, n_q + 2 * n_kv, D, generator=workloads._gen(42)).bfloat16()
+    pos = torch.arange(T, dtype=torch.int32, device=cuda) * 37
+    page, offset = (torch.tensor(y, dtype=torch.int32, device=cuda) for y in ([1] * T, list(range(T))))
+
+    def write(x):
+        pool = Pool(2, 8, 8, n_kv, D, cuda, codes=0)
+        q = lib.functional.prologue_pool_write8(x.to(cuda), pos, None, None, page, offset, *pool.args, n_q, n_kv, D, "sectioned",
+                                                rope_base=1e4, norm=False, rotary_dim=32, rotary_pairs=pairs)
+        codes, scales = pool.read()
+        return q.cpu(), codes, scales
+
+    at = [(t, h, e) for t, h, e in SPOTS] + [(t, n_q + h, e) for t, h, e in SPOTS]
+    (q0, codes0, scales0), (q1, codes1, scales1) = write(_spoil(x, at, 0.0)), write(_spoil(x, at, value))
+    assert np.array_equal(u16(_spoil(q1, SPOTS, 0.0)), u16(_spoil(q0, SPOTS, 0.0)))
+    for a, b in zip(scales0, scales1):
+        assert np.array_equal(a, b)
+    k = codes1[0]
+    for t, h, e in SPOTS:
+        assert k[1, t, h, e] & 127 == 127 and codes0[0][1, t, h, e] & 127 == 0
+        k[1, t, h, e] = codes0[0][1, t, h, e]
+    assert np.array_equal(k, codes0[0]) and np.array_equal(codes1[1], codes0[1])

@@ -138,3 +138,12 @@ def test_oracle_is_not_the_old_one_by_another_name():
     for i in range(4):
         for j in range(i):
             assert not np.array_equal(to_bf16_rne(got[i]), to_bf16_rne(got[j]))
+
+
+def test_too_few_frequencies_are_refused(lib):
+    F = lib.functional
+    for dim, rot in ((64, None), (128, None), (64, 32), (128, 128)):
+        n = (rot or dim) // 2
+        assert F._variant(inv_freq=[0.5] * n, dim=dim, rotary_dim=rot) is not None
+        with pytest.raises(ValueError, match="frequencies"):
+            F._variant(inv_freq=[0.5] * (n - 1), dim=dim, rotary_dim=rot)
