@@ -12,12 +12,21 @@
 //
 // Codes go to the matrix units (m16n8k16, f16 with fp32 accumulation) as f16, which
 // holds every e4m3 value exactly; one conversion instruction makes two values. A row of
-// q is scaled by a power of two that brings its largest magnitude into [1, 2). The order
-// of d in S = Q K^T is free: a lane's four consecutive codes are the two operand
-// registers of one step, so ldmatrix on bytes needs no shuffling. For O = W V the
-// transposing ldmatrix moves pairs of codes (d, d + 1) of two keys; a byte permutation
-// makes the pairs of keys of d and of d + 1, and even and odd d go to accumulators of
-// their own.
+// q is scaled by a power of two that brings its largest magnitude into [1, 2). The heads
+// are the products' 8 columns (S^T = K Q^T, O^T = V^T W^T): keys and values fill the 16
+// rows, where heads as rows left half of them empty in groups of up to 8, at 32 products
+// and 570 instructions a tile of 32 keys and 64 values instead of 16 and 440. The order of
+// d in K Q^T is free: a lane's four consecutive codes are two operand registers of one step, so ldmatrix
+// on bytes needs no shuffling. For V^T W^T the transposing ldmatrix moves pairs of codes
+// (d, d + 1) of two keys; a byte permutation makes the pairs of keys of d and of d + 1,
+// which are rows g and g + 8. The weights turn from keys by heads to heads by keys with a
+// matrix move per 8 keys.
+//
+// Bound by the codes' bytes in long batches, where both kernels take (32 over 8 heads of
+// 128, up to 32768 keys) 229 us for 48 sequences, 6.74 TB/s or 0.99 of a plain copy's rate
+// (heads as rows: 253 us). 256 sequences of up to 4096 keys, 64 over 8 heads of 64: 116 us,
+// 5.10 TB/s (132 us): 48 % of the issue slots, and the join is a tenth. One sequence of
+// 131072 keys: 55 us (58 us), a dozen of them the start, the last tiles and the join.
 #include <cuda_fp16.h>
 
 #include "attention_decode.cuh"
@@ -38,20 +47,18 @@ struct Dec8Shape {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
-// The product's rows 0 .. 7 are d[0], d[1] of the lanes, its rows 8 .. 15 d[2], d[3].
-// With 8 heads or fewer the latter are padding: they take no registers between products.
-__device__ __forceinline__ void mma16816h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816h(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma16816h(float (&d)[2], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
-  float e, f;
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%8,%5,%8}, {%6,%7}, {%0,%1,%9,%9};"
-      : "+f"(d[0]), "+f"(d[1]), "=f"(e), "=f"(f)
-      : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0), "f"(0.f));
+// An 8 x 8 matrix of 16-bit values over the warp, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   uint32_t r;
@@ -59,13 +66,14 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return r;
 }
 
-// Maximum over the four lanes of a row.
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// Maximum over the eight lanes of a head.
+__device__ __forceinline__ float head_max(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
-// A row's references before its first key: so low that any score passes them.
+// A head's references before its first key: so low that any score passes them.
 constexpr float kNoKey = -1e30f;
 
 // Place of 16-byte chunk ch of a tile's row, so that the 8 rows of a matrix of ldmatrix
@@ -151,9 +159,11 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD), 1) qkvp_attention_decode8
       cp_commit();
     }
 
+    // A lane has the heads 8 x + 2 (lane % 4) + y of products, and of each the keys lane / 4 + 8 i
+    // of scores and the values 16 j + 2 (lane / 4), + 1 of results: o[j][x][y], o[j][x][2 + y].
     uint32_t qf[HD / 16][2 * X];
-    float o[HD / 8][2 * X], m[X], n[X], l[X], c[X];  // o[2 j], o[2 j + 1]: even and odd d of chunk j; c: a row's factor
-    auto begin = [&]() {                   // a sequence's first tile here
+    float o[HD / 16][X][4], m[X][2], n[X][2], l[X][2], c[X][2];  // c: a head's factor
+    auto begin = [&]() {                                        // a sequence's first tile here
 #pragma unroll
       for (int x = 0; x < X; ++x) {
         const int r = (lane >> 2) + 8 * x;
@@ -171,38 +181,45 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD), 1) qkvp_attention_decode8
         // 2^-e, e the exponent of the largest magnitude (within what float32 can scale by)
         const int e = min(max((int)(top >> 23) - 127, -126), 126);
         const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-        c[x] = a.scale_log2 * __uint_as_float((uint32_t)(e + 127) << 23);
+        const float factor = a.scale_log2 * __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          c[x][y] = __shfl_sync(0xffffffffu, factor, 8 * (lane & 3) + 4 * y);
+          m[x][y] = n[x][y] = kNoKey;
+          l[x][y] = 0.f;
+        }
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
           qf[ks][x] = pack_h2(__uint_as_float(raw[ks].x << 16) * f, __uint_as_float(raw[ks].x & 0xffff0000u) * f);
           qf[ks][X + x] = pack_h2(__uint_as_float(raw[ks].y << 16) * f, __uint_as_float(raw[ks].y & 0xffff0000u) * f);
         }
-        m[x] = n[x] = kNoKey;
-        l[x] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < HD / 8; ++i)
+      for (int j = 0; j < HD / 16; ++j)
 #pragma unroll
-        for (int x = 0; x < 2 * X; ++x) o[i][x] = 0.f;
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[j][x][y] = 0.f;
     };
     bool first = cu.tile == 0;  // of the sequence: else the segment continues one of the range before
     auto end = [&]() {          // its last tile here: the partial result
 #pragma unroll
-      for (int x = 0; x < X; ++x) {
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-        const int r = (lane >> 2) + 8 * x;
-        if (r < n_heads) {
-          const int64_t row = (int64_t)(first ? cu.b : a.batch + range) * a.n_q + head0 + r;
-          const float ref = m[x] + __log2f(l[x]), f = l[x] == 0.f ? 0.f : ex2(n[x] - ref);
-          if ((lane & 3) == 0) a.part_ml[row] = l[x] == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ref, 1.f);
-          float4* dst = reinterpret_cast<float4*>(a.part_o + row * HD) + (lane & 3);
+      for (int x = 0; x < X; ++x)
 #pragma unroll
-          for (int j = 0; j < HD / 16; ++j)
-            dst[4 * j] = make_float4(f * o[2 * j][2 * x], f * o[2 * j + 1][2 * x], f * o[2 * j][2 * x + 1],
-                                     f * o[2 * j + 1][2 * x + 1]);
+        for (int y = 0; y < 2; ++y) {
+          float sum = l[x][y];
+#pragma unroll
+          for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+          const int h = 8 * x + 2 * (lane & 3) + y;
+          if (h < n_heads) {
+            const int64_t row = (int64_t)(first ? cu.b : a.batch + range) * a.n_q + head0 + h;
+            const float ref = m[x][y] + __log2f(sum), f = sum == 0.f ? 0.f : ex2(n[x][y] - ref);
+            if ((lane >> 2) == 0) a.part_ml[row] = sum == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ref, 1.f);
+            float2* dst = reinterpret_cast<float2*>(a.part_o + row * HD) + (lane >> 2);
+#pragma unroll
+            for (int j = 0; j < HD / 16; ++j) dst[8 * j] = make_float2(f * o[j][x][y], f * o[j][x][2 + y]);
+          }
         }
-      }
     };
     begin();
     uint32_t st = 0;
@@ -221,88 +238,98 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD), 1) qkvp_attention_decode8
       const uint32_t in = s_in[warp][st];
       s_key[warp][lane] = make_float2(clamp_scale(s_scale[warp][st][0][lane]), __log2f(clamp_scale(s_scale[warp][st][1][lane])));
       const uint32_t kt = ring + st * SH::kTileBytes, vt = kt + KT * HD;
-      float s[NT][2 * X];
+      float s[NT / 2][X][4];  // [y]: key lane / 4 of 16; [2 + y]: 8 behind it
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < NT / 2; ++i)
 #pragma unroll
-        for (int x = 0; x < 2 * X; ++x) s[i][x] = 0.f;
+        for (int x = 0; x < X; ++x)
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+          for (int y = 0; y < 4; ++y) s[i][x][y] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i)
 #pragma unroll
         for (int k4 = 0; k4 < HD / 64; ++k4) {
-          uint32_t b[4];
-          ldsm4(kt + dec8_at<HD>(8 * i + (lane & 7), 4 * k4 + (lane >> 3)), b);
+          uint32_t b[2][4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t b0, b1;
-            from_e4m3x4(b[x], b0, b1);
-            mma16816h(s[i], qf[4 * k4 + x], b0, b1);
+          for (int v = 0; v < 2; ++v)
+            ldsm4(kt + dec8_at<HD>(16 * i + 8 * v + (lane & 7), 4 * k4 + (lane >> 3)), b[v]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t a0, a1, a2, a3;
+            from_e4m3x4(b[0][k], a0, a2);
+            from_e4m3x4(b[1][k], a1, a3);
+#pragma unroll
+            for (int x = 0; x < X; ++x) mma16816h(s[i][x], a0, a1, a2, a3, qf[4 * k4 + k][x], qf[4 * k4 + k][X + x]);
           }
         }
       __syncwarp();  // s_key is written
-      float2 key[NT][2];
+      float2 key[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) key[i][y] = s_key[warp][8 * i + 2 * (lane & 3) + y];
-      float d[NT][2 * X], e[NT][2 * X];  // t - m and u - n
+      for (int i = 0; i < NT; ++i) key[i] = s_key[warp][8 * i + (lane >> 2)];
+      float d[NT][X][2], e[NT][X][2];  // t - m and u - n
       auto exponents = [&]() {
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int y = 0; y < 2 * X; ++y) d[i][y] = fmaf(s[i][y], key[i][y & 1].x * c[y >> 1], -m[y >> 1]);
+          for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) d[i][x][y] = fmaf(s[i >> 1][x][2 * (i & 1) + y], key[i].x * c[x][y], -m[x][y]);
         if (in != 0xffffffffu) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
+            if (!((in >> (8 * i + (lane >> 2))) & 1)) {
 #pragma unroll
-            for (int y = 0; y < 2 * X; ++y)
-              if (!((in >> (8 * i + 2 * (lane & 3) + (y & 1))) & 1)) d[i][y] = -INFINITY;
+              for (int x = 0; x < X; ++x) d[i][x][0] = d[i][x][1] = -INFINITY;
+            }
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int y = 0; y < 2 * X; ++y) {
-            e[i][y] = d[i][y] + (key[i][y & 1].y + (m[y >> 1] - n[y >> 1]));
-            top = max3(top, d[i][y], e[i][y]);
-          }
+          for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              e[i][x][y] = d[i][x][y] + (key[i].y + (m[x][y] - n[x][y]));
+              top = max3(top, d[i][x][y], e[i][x][y]);
+            }
         return top;
       };
-      // A row's references only move where a score passes them by more than 8 powers of
+      // A head's references only move where a score passes them by more than 8 powers of
       // two; until then no lane has to know the others' maxima.
       if (__any_sync(0xffffffffu, exponents() > 8.f)) {
 #pragma unroll
-        for (int x = 0; x < X; ++x) {
-          float top = -INFINITY, tow = -INFINITY;
+        for (int x = 0; x < X; ++x)
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int y = 0; y < 2; ++y) {
+            float top = -INFINITY, tow = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-              if ((in >> (8 * i + 2 * (lane & 3) + y)) & 1) {
-                const float t = s[i][2 * x + y] * (key[i][y].x * c[x]);
+            for (int i = 0; i < NT; ++i)
+              if ((in >> (8 * i + (lane >> 2))) & 1) {
+                const float t = s[i >> 1][x][2 * (i & 1) + y] * (key[i].x * c[x][y]);
                 top = fmaxf(top, t);
-                tow = fmaxf(tow, t + key[i][y].y);
+                tow = fmaxf(tow, t + key[i].y);
               }
-          const float m_new = fmaxf(m[x], quad_max(top)), n_new = fmaxf(n[x], quad_max(tow));
-          l[x] *= ex2(m[x] - m_new);
-          const float f = ex2(n[x] - n_new);
-          m[x] = m_new;
-          n[x] = n_new;
+            const float m_new = fmaxf(m[x][y], head_max(top)), n_new = fmaxf(n[x][y], head_max(tow));
+            l[x][y] *= ex2(m[x][y] - m_new);
+            const float f = ex2(n[x][y] - n_new);
+            m[x][y] = m_new;
+            n[x][y] = n_new;
 #pragma unroll
-          for (int i = 0; i < HD / 8; ++i) {
-            o[i][2 * x] *= f;
-            o[i][2 * x + 1] *= f;
+            for (int j = 0; j < HD / 16; ++j) {
+              o[j][x][y] *= f;
+              o[j][x][2 + y] *= f;
+            }
           }
-        }
         exponents();
       }
-      uint32_t pf[NT / 2][2 * X];
+      uint32_t pf[NT][X];  // the weights as the second product's operand: a head's keys
 #pragma unroll
-      for (int x = 0; x < X; ++x)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          l[x] += ex2(d[i][2 * x]) + ex2(d[i][2 * x + 1]);
-          pf[i >> 1][X * (i & 1) + x] = pack_h2(ex2(e[i][2 * x]), ex2(e[i][2 * x + 1]));
+        for (int x = 0; x < X; ++x) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) l[x][y] += ex2(d[i][x][y]);
+          pf[i][x] = transposed(pack_h2(ex2(e[i][x][0]), ex2(e[i][x][1])));
         }
       {
         const int row = (((lane >> 3) & 1) << 3) + (lane & 7), hi = lane >> 4;
@@ -316,8 +343,8 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD), 1) qkvp_attention_decode8
             for (int i = 0; i < 2; ++i) {
               from_e4m3x4(__byte_perm(b[2 * i], 0, 0x3120), e0, o0);
               from_e4m3x4(__byte_perm(b[2 * i + 1], 0, 0x3120), e1, o1);
-              mma16816h(o[2 * (j + i)], pf[k2], e0, e1);
-              mma16816h(o[2 * (j + i) + 1], pf[k2], o0, o1);
+#pragma unroll
+              for (int x = 0; x < X; ++x) mma16816h(o[j + i][x], e0, o0, e1, o1, pf[2 * k2][x], pf[2 * k2 + 1][x]);
             }
           }
       }
