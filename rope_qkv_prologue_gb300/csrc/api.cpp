@@ -1762,6 +1762,11 @@ int qkv_attention_decode(const qkvp_layout* layout, int32_t batch, const void* q
                        (size_t)attention_decode_smem_bytes(hd), st, &a);
 }
 
+// The 8-bit pool's kernel holds 8 query heads of a group in its products, or 16 (with two
+// passes of 8 over a group of 16 instead, 48 sequences of up to 32768 keys of 128 take 206
+// us instead of 143).
+static bool wide_group(const qkvp_layout* layout) { return layout->n_q / layout->n_kv > 8; }
+
 int qkv_attention_decode8_workspace(const qkvp_layout* layout, int32_t batch, int32_t page_size, int32_t max_pages,
                                     size_t* bytes) {
   QKVP_TRY(check_decode(layout, batch, page_size, max_pages, 0));
@@ -1771,7 +1776,7 @@ int qkv_attention_decode8_workspace(const qkvp_layout* layout, int32_t batch, in
   int sms = 0;
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
-  plan_decode(layout, batch, page_size, max_pages, 0, sms, dec8_warps(layout->head_dim), &p);
+  plan_decode(layout, batch, page_size, max_pages, 0, sms, dec8_warps(layout->head_dim, wide_group(layout)), &p);
   *bytes = decode_workspace(layout, batch, p);
   return QKVP_OK;
 }
@@ -1797,11 +1802,12 @@ int qkv_attention_decode8(const qkvp_layout* layout, int32_t batch, const void* 
   int sms = 0;
   QKVP_TRY(current_device(&sms));
   DecodePlan p;
-  plan_decode(layout, batch, page_size, max_pages, 0, sms, dec8_warps(layout->head_dim), &p);
+  plan_decode(layout, batch, page_size, max_pages, 0, sms, dec8_warps(layout->head_dim, wide_group(layout)), &p);
   const size_t need = decode_workspace(layout, batch, p);
   if (!workspace || workspace_bytes < need) return QKVP_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QKVP_ERR_ALIGN;
   const int hd = layout->head_dim;
+  const bool wide = wide_group(layout);
   const size_t q_bytes = (size_t)batch * layout->n_q * hd * 2;
   const size_t lse_bytes = lse ? (size_t)batch * layout->n_q * sizeof(float) : 0;
   const Pool8Bytes pb(layout, num_pages, page_size, block);
@@ -1823,8 +1829,9 @@ int qkv_attention_decode8(const qkvp_layout* layout, int32_t batch, const void* 
   a.lengths = lengths;
   a.tile_keys = kDec8Keys;
   return launch_decode(layout, batch, p, q, page_size, max_pages, (float)((double)sc * 1.4426950408889634), out, lse,
-                       dev_status, workspace, attention_decode8_kernel(hd, layout->n_q / layout->n_kv > 8),
-                       32 * dec8_warps(hd), (size_t)attention_decode8_smem_bytes(hd), static_cast<cudaStream_t>(stream), &a);
+                       dev_status, workspace, attention_decode8_kernel(hd, wide),
+                       32 * dec8_warps(hd, wide), (size_t)attention_decode8_smem_bytes(hd, wide),
+                       static_cast<cudaStream_t>(stream), &a);
 }
 
 int qkv_prologue_wait_selftest(void* stream) {

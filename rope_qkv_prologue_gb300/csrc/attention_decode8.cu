@@ -35,12 +35,12 @@
 namespace qkvp {
 namespace {
 
-template <int HD>
+template <int HD, int X>
 struct Dec8Shape {
   static constexpr int kKeys = kDec8Keys;
   static constexpr int kTileBytes = 2 * kKeys * HD;  // k codes, then v codes
   static constexpr int kStages = 3;
-  static constexpr int kWarps = dec8_warps(HD);      // 192 KiB an SM
+  static constexpr int kWarps = dec8_warps(HD, X == 2);  // at most 192 KiB an SM
   static constexpr int kWarpBytes = kStages * kTileBytes;
 };
 
@@ -87,8 +87,8 @@ __device__ __forceinline__ int dec8_at(int row, int ch) {
 
 // X: groups of 8 query heads that a warp's products hold (1 or 2).
 template <int HD, int X>
-__global__ void __launch_bounds__(32 * dec8_warps(HD), 1) qkvp_attention_decode8_kernel(const AttnDecodeArgs a) {
-  using SH = Dec8Shape<HD>;
+__global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention_decode8_kernel(const AttnDecodeArgs a) {
+  using SH = Dec8Shape<HD, X>;
   constexpr int ST = SH::kStages, KT = SH::kKeys, NT = KT / 8, kDec8Warps = SH::kWarps;
   constexpr int CH = HD / 16, RPI = 32 / CH;  // 16-byte chunks per row, rows per copy instruction
   static_assert(KT == 32, "a lane per key");
@@ -373,9 +373,8 @@ const void* attention_decode8_kernel(int head_dim, bool wide) {
   return wide ? reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<128, 2>)
               : reinterpret_cast<const void*>(&qkvp_attention_decode8_kernel<128, 1>);
 }
-int attention_decode8_smem_bytes(int head_dim) {
-  return head_dim == 64 ? Dec8Shape<64>::kWarps * Dec8Shape<64>::kWarpBytes
-                        : Dec8Shape<128>::kWarps * Dec8Shape<128>::kWarpBytes;
+int attention_decode8_smem_bytes(int head_dim, bool wide) {
+  return dec8_warps(head_dim, wide) * (head_dim == 64 ? Dec8Shape<64, 1>::kWarpBytes : Dec8Shape<128, 1>::kWarpBytes);
 }
 
 }  // namespace qkvp

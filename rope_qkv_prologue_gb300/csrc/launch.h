@@ -449,9 +449,12 @@ struct AttnDecodeArgs {
   int32_t block_shift;     // log2(block), or -1
 };
 constexpr int kDec8Keys = 32;  // keys per tile of the kernel over the 8-bit pool
-QKVP_HD constexpr int dec8_warps(int head_dim) { return head_dim == 64 ? 16 : 8; }  // per CTA, of tiles of 4 and 8 KiB
-const void* attention_decode8_kernel(int head_dim, bool wide);  // wide: groups of more than 8 query heads
-int attention_decode8_smem_bytes(int head_dim);
+// Warps per CTA, of tiles of 4 and 8 KiB. wide: groups of more than 8 query heads, whose
+// results take 168 registers at head_dim 64 (256 sequences of up to 4096 keys, 64 over 4
+// heads of 64: 87 us with 12 warps; 130 with 16, which spill; 95 with 8).
+QKVP_HD constexpr int dec8_warps(int head_dim, bool wide) { return head_dim == 64 ? (wide ? 12 : 16) : 8; }
+const void* attention_decode8_kernel(int head_dim, bool wide);
+int attention_decode8_smem_bytes(int head_dim, bool wide);
 const void* attention_decode_kernel(int head_dim);
 const void* attention_join_kernel(int head_dim, bool wide);  // wide: several warps per head
 int attention_decode_smem_bytes(int head_dim);
