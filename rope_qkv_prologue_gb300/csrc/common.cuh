@@ -323,9 +323,9 @@ __device__ __forceinline__ void pair_backward(const float2 (&dlo)[4], const floa
 //
 // The first 2 * half values of a head are rotated, in pairs (i, i + half) or, when
 // `adjacent`, (2i, 2i + 1); the others pass through (not as rotations by 0: an infinity
-// times 0 would make its unit's other value NaN). A unit of the head is still two of its chunks: in adjacent pairs
-// a chunk holds its own partners and the unit is (e, e + CPH/2) as ever; in halves
-// it is (e, e + r) for the first r = half / 8 units, and the chunks behind them go two
+// times 0 would make its unit's other value NaN). A unit of the head is still two of its
+// chunks: in adjacent pairs a chunk holds its own partners and the unit is (e, e + CPH/2)
+// as ever; in halves it is (e, e + r) for the first r = half / 8 units, and the chunks behind them go two
 // by two, (e + CPH/2, e + r): so the first chunks of a head's units, like their second
 // ones, lie in different shared-memory banks (with any other pairing of them 16384 tokens,
 // 32 over 8 heads of 128, half of the head, took 208 us forward and backward instead of 190).
