@@ -616,7 +616,8 @@ QKVP_API int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t b
  * The products take the codes as they are (exact in 16 bits); q is scaled by a
  * power of two of its row and rounded to 11 significant bits at most (exact within
  * 2^-14 of the row's largest value), the softmax weights times the values' scales
- * to 11; sums, maxima and scales are fp32. Scales outside [2^-100, 2^120] are taken
+ * to 11 (those 2^-25 and more below the largest to fewer; 2^-36 below it they are
+ * lost); sums, maxima and scales are fp32. Scales outside [2^-100, 2^120] are taken
  * as the nearest bound. Slots that no sequence names are never used.
  *
  * layout, batch, q, page_table, max_pages, table_stride, lengths, scale, out,

@@ -2,12 +2,14 @@
 // keys: the walk, the split and the join are those of attention_decode.cu.
 //
 // With codes K, V and scales a_j, b_j of key j's blocks (float32),
-//     t_j = c a_j q . K_j,   l = sum_j 2^(t_j - m),             m >= max t_j - 8,
-//     u_j = t_j + log2(b_j), O = sum_j 2^(u_j - n) V_j,         n >= max u_j - 8,
+//     t_j = c a_j q . K_j,   l = sum_j 2^(t_j - m),         max t_j - 15 <= m <= max t_j - 11,
+//     u_j = t_j + log2(b_j), O = sum_j 2^(u_j - n) V_j,     max u_j - 15 <= n <= max u_j - 11,
 //     out = 2^(n - m) O / l:
 // the value scale is part of the weight, and the weights have a reference of their own,
 // so their 11 significant bits are those of the largest contributions however far apart
-// the blocks' scales are. A partial result leaves as (m + log2 l, 1, 2^(n - m) O / l),
+// the blocks' scales are. The largest weight is 2^11 to 2^15, near the end of f16's range:
+// one loses bits only 2^-25 below it, and vanishes 2^-36 below it (with weights of at most 1
+// a key that takes nearly all the weight, its value near 0, left nothing of the others). A partial result leaves as (m + log2 l, 1, 2^(n - m) O / l),
 // which joins as plain softmax's do.
 //
 // Codes go to the matrix units (m16n8k16, f16 with fp32 accumulation) as f16, which
@@ -23,9 +25,9 @@
 // matrix move per 8 keys.
 //
 // Bound by the codes' bytes in long batches, where both kernels take (32 over 8 heads of
-// 128, up to 32768 keys) 229 us for 48 sequences, 6.74 TB/s or 0.99 of a plain copy's rate
-// (heads as rows: 253 us). 256 sequences of up to 4096 keys, 64 over 8 heads of 64: 116 us,
-// 5.10 TB/s (132 us): 48 % of the issue slots, and the join is a tenth. One sequence of
+// 128, up to 32768 keys) 230 us for 48 sequences, 6.71 TB/s or 0.99 of a plain copy's rate
+// (heads as rows: 253 us). 256 sequences of up to 4096 keys, 64 over 8 heads of 64: 117 us,
+// 5.04 TB/s (132 us): 48 % of the issue slots, and the join is a tenth. One sequence of
 // 131072 keys: 55 us (58 us), a dozen of them the start, the last tiles and the join.
 #include <cuda_fp16.h>
 
@@ -75,6 +77,9 @@ __device__ __forceinline__ float head_max(float v) {
 
 // A head's references before its first key: so low that any score passes them.
 constexpr float kNoKey = -1e30f;
+// Powers of two by which the largest score lies above a head's reference: when that is set,
+// and where it has to move.
+constexpr float kAbove = 11.f, kAboveMost = 15.f;
 
 // Place of 16-byte chunk ch of a tile's row, so that the 8 rows of a matrix of ldmatrix
 // lie in different banks: rows of 128 bytes, or of 64 (two to a line).
@@ -213,11 +218,13 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
           const int h = 8 * x + 2 * (lane & 3) + y;
           if (h < n_heads) {
             const int64_t row = (int64_t)(first ? cu.b : a.batch + range) * a.n_q + head0 + h;
-            const float ref = m[x][y] + __log2f(sum), f = sum == 0.f ? 0.f : ex2(n[x][y] - ref);
+            const float ref = m[x][y] + __log2f(sum);
+            // (two factors: their product may be too small for a float where the result is not)
+            const float f = sum == 0.f ? 0.f : __frcp_rn(sum), e = ex2(n[x][y] - m[x][y]);
             if ((lane >> 2) == 0) a.part_ml[row] = sum == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ref, 1.f);
             float2* dst = reinterpret_cast<float2*>(a.part_o + row * HD) + (lane >> 2);
 #pragma unroll
-            for (int j = 0; j < HD / 16; ++j) dst[8 * j] = make_float2(f * o[j][x][y], f * o[j][x][2 + y]);
+            for (int j = 0; j < HD / 16; ++j) dst[8 * j] = make_float2(f * o[j][x][y] * e, f * o[j][x][2 + y] * e);
           }
         }
     };
@@ -294,9 +301,9 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
             }
         return top;
       };
-      // A head's references only move where a score passes them by more than 8 powers of
-      // two; until then no lane has to know the others' maxima.
-      if (__any_sync(0xffffffffu, exponents() > 8.f)) {
+      // A head's references only move where a score passes them by too much; until then no
+      // lane has to know the others' maxima.
+      if (__any_sync(0xffffffffu, exponents() > kAboveMost)) {
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
                 top = fmaxf(top, t);
                 tow = fmaxf(tow, t + key[i].y);
               }
-            const float m_new = fmaxf(m[x][y], head_max(top)), n_new = fmaxf(n[x][y], head_max(tow));
+            const float m_new = fmaxf(m[x][y], head_max(top) - kAbove), n_new = fmaxf(n[x][y], head_max(tow) - kAbove);
             l[x][y] *= ex2(m[x][y] - m_new);
             const float f = ex2(n[x][y] - n_new);
             m[x][y] = m_new;

@@ -128,6 +128,44 @@ def test_sharp_scores(lib, cuda):
     check(lib, cuda, Batch(8, 2, 128, 64, 64, [700, 40, 3], 9, spread=0.5), scale=0.5, what="scale")
 
 
+@pytest.mark.parametrize("D, group", [(64, 1), (64, 12), (128, 8)])
+@pytest.mark.parametrize("power", [20, 26, 30])
+def test_a_key_that_takes_the_weight_and_gives_nothing(lib, cuda, D, group, power):
+    # the first key's weight is 2^power times the others', its value 0: the result is theirs.
+    # 16 bits hold weights to 2^-25 of the reference, which lies 2^11 or more below the largest.
+    b = Batch(group, 1, D, 16, 16, [60], 30 + power)
+    for s in b.scale:
+        s[np.isfinite(s)] = 1.0
+    at = b.table[0, 0]
+    used = b.codes[0] != 127
+    b.codes[0][used] = 0
+    b.codes[0][at, 0, 0, 0] = E8.to_e4m3(np.float64(power))
+    b.codes[1][at, 0] = 0
+    b.q.zero_()
+    b.q[:, :, 0] = 1
+    n = np.arange(60)
+    rows = b.table[0, n // 16], n % 16
+    b.keys, b.values = [E8.VALUES[b.codes[0][rows]]], [E8.VALUES[b.codes[1][rows]]]
+    scale = float(np.log(2.0))
+    ref = b.want(scale)
+    assert np.abs(ref["out"]).max() > 2.0 ** -power
+    lost = 2.0 ** -36 * np.abs(b.values[0]).sum(0)[None]  # (the largest weight is at most 1)
+    assert_within(f64(b.run(lib, cuda, scale=scale)), ref["out"], bound(ref) + lost, f"2^{power}")
+
+
+def test_the_smallest_scales(lib, cuda):
+    # every value below 2^-91, many equal weights: no factor on the way falls out of float32
+    b = Batch(4, 2, 64, 16, 8, [3000, 70], 61)
+    b.q.zero_()
+    for s in b.scale[1:]:
+        s[np.isfinite(s)] = 2.0 ** -100
+    b.values = [E8.VALUES[b.codes[1][b.table[i, np.arange(n) // 16], np.arange(n) % 16]] * 2.0 ** -100
+                for i, n in enumerate(b.lengths)]
+    ref = b.want()
+    got = f64(b.run(lib, cuda))
+    assert_within(got * 2.0 ** 100, ref["out"] * 2.0 ** 100, bound(ref) * 2.0 ** 100, "2^-100")
+
+
 def test_large_and_small_queries(lib, cuda):
     # a row's power of two: queries of 2^-100 .. 2^100 with a scale that undoes it
     for e in (-120, -60, -1, 0, 1, 60, 100):
