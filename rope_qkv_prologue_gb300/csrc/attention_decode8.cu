@@ -9,8 +9,8 @@
 // so their 11 significant bits are those of the largest contributions however far apart
 // the blocks' scales are. The largest weight is 2^11 to 2^15, near the end of f16's range:
 // one loses bits only 2^-25 below it, and vanishes 2^-36 below it (with weights of at most 1
-// a key that takes nearly all the weight, its value near 0, left nothing of the others). A partial result leaves as (m + log2 l, 1, 2^(n - m) O / l),
-// which joins as plain softmax's do.
+// a key that takes nearly all the weight, its value near 0, left nothing of the others). A
+// partial result leaves as (m + log2 l, 1, 2^(n - m) O / l), which joins as plain softmax's do.
 //
 // Codes go to the matrix units (m16n8k16, f16 with fp32 accumulation) as f16, which
 // holds every e4m3 value exactly; one conversion instruction makes two values. A row of
@@ -18,11 +18,11 @@
 // are the products' 8 columns (S^T = K Q^T, O^T = V^T W^T): keys and values fill the 16
 // rows, where heads as rows left half of them empty in groups of up to 8, at 32 products
 // and 570 instructions a tile of 32 keys and 64 values instead of 16 and 440. The order of
-// d in K Q^T is free: a lane's four consecutive codes are two operand registers of one step, so ldmatrix
-// on bytes needs no shuffling. For V^T W^T the transposing ldmatrix moves pairs of codes
-// (d, d + 1) of two keys; a byte permutation makes the pairs of keys of d and of d + 1,
-// which are rows g and g + 8. The weights turn from keys by heads to heads by keys with a
-// matrix move per 8 keys.
+// d in K Q^T is free: a lane's four consecutive codes are two operand registers of one
+// step, so ldmatrix on bytes needs no shuffling. For V^T W^T the transposing ldmatrix moves
+// pairs of codes (d, d + 1) of two keys; a byte permutation makes the pairs of keys of d and
+// of d + 1, which are rows g and g + 8. The weights turn from keys by heads to heads by keys
+// with a matrix move per 8 keys.
 //
 // Bound by the codes' bytes in long batches, where both kernels take (32 over 8 heads of
 // 128, up to 32768 keys) 230 us for 48 sequences, 6.71 TB/s or 0.99 of a plain copy's rate
@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
       }
       cp_commit();
       const uint32_t in = s_in[warp][st];
-      s_key[warp][lane] = make_float2(clamp_scale(s_scale[warp][st][0][lane]), __log2f(clamp_scale(s_scale[warp][st][1][lane])));
+      s_key[warp][lane] =
+          make_float2(clamp_scale(s_scale[warp][st][0][lane]), __log2f(clamp_scale(s_scale[warp][st][1][lane])));
       const uint32_t kt = ring + st * SH::kTileBytes, vt = kt + KT * HD;
       float s[NT / 2][X][4];  // [y]: key lane / 4 of 16; [2 + y]: 8 behind it
 #pragma unroll

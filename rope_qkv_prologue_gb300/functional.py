@@ -84,8 +84,8 @@ def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interl
     k_pre = torch.empty_like(k) if save_pre else None
     if T == 0:  # an empty tensor has no address to pass
         return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
-    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps, rope_base,
-                          _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
+    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
+                          rope_base, _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
     return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
 
 
@@ -138,8 +138,7 @@ def prologue_pool_write(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, n_q
         return q
     C.qkv_prologue_pool_write_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
                                  rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
-                                 v_pool,
-                                 k_pool.shape[0], k_pool.shape[1], dev_status, stream)
+                                 v_pool, k_pool.shape[0], k_pool.shape[1], dev_status, stream)
     return q
 
 
