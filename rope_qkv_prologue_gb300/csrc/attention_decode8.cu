@@ -4,13 +4,16 @@
 // With codes K, V and scales a_j, b_j of key j's blocks (float32),
 //     t_j = c a_j q . K_j,   l = sum_j 2^(t_j - m),         max t_j - 15 <= m <= max t_j - 11,
 //     u_j = t_j + log2(b_j), O = sum_j 2^(u_j - n) V_j,     max u_j - 15 <= n <= max u_j - 11,
-//     out = 2^(n - m) O / l:
+//     out = 2^r O / l,       r = n - m
+// (m to the nearest float32, up to 2^16 more; r is what is kept, for scores so large that n and
+// m differ by less than their last bits):
 // the value scale is part of the weight, and the weights have a reference of their own,
 // so their 11 significant bits are those of the largest contributions however far apart
 // the blocks' scales are. The largest weight is 2^11 to 2^15, near the end of f16's range:
 // one loses bits only 2^-25 below it, and vanishes 2^-36 below it (with weights of at most 1
 // a key that takes nearly all the weight, its value near 0, left nothing of the others). A
-// partial result leaves as (m + log2 l, 1, 2^(n - m) O / l), which joins as plain softmax's do.
+// partial result leaves as (z, 2^w, 2^w 2^r O / l), z = m + log2 l rounded and w what its
+// rounding left, which joins as plain softmax's do.
 //
 // Codes go to the matrix units (m16n8k16, f16 with fp32 accumulation) as f16, which
 // holds every e4m3 value exactly; one conversion instruction makes two values. A row of
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
     // A lane has the heads 8 x + 2 (lane % 4) + y of products, and of each the keys lane / 4 + 8 i
     // of scores and the values 16 j + 2 (lane / 4), + 1 of results: o[j][x][y], o[j][x][2 + y].
     uint32_t qf[HD / 16][2 * X];
-    float o[HD / 16][X][4], m[X][2], n[X][2], l[X][2], c[X][2];  // c: a head's factor
+    float o[HD / 16][X][4], m[X][2], rel[X][2], l[X][2], c[X][2];  // rel: n - m; c: a head's factor
     auto begin = [&]() {                                        // a sequence's first tile here
 #pragma unroll
       for (int x = 0; x < X; ++x) {
@@ -190,8 +193,8 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           c[x][y] = __shfl_sync(0xffffffffu, factor, 8 * (lane & 3) + 4 * y);
-          m[x][y] = n[x][y] = kNoKey;
-          l[x][y] = 0.f;
+          m[x][y] = kNoKey;
+          rel[x][y] = l[x][y] = 0.f;
         }
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
@@ -218,10 +221,11 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
           const int h = 8 * x + 2 * (lane & 3) + y;
           if (h < n_heads) {
             const int64_t row = (int64_t)(first ? cu.b : a.batch + range) * a.n_q + head0 + h;
-            const float ref = m[x][y] + __log2f(sum);
+            // what ref's rounding takes from log2 l, or adds to it, goes into the sum and the result
+            const float ls = __log2f(sum), ref = m[x][y] + ls, rest = ex2((m[x][y] - ref) + ls);
             // (two factors: their product may be too small for a float where the result is not)
-            const float f = sum == 0.f ? 0.f : __frcp_rn(sum), e = ex2(n[x][y] - m[x][y]);
-            if ((lane >> 2) == 0) a.part_ml[row] = sum == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ref, 1.f);
+            const float f = sum == 0.f ? 0.f : __fdividef(rest, sum), e = ex2(rel[x][y]);
+            if ((lane >> 2) == 0) a.part_ml[row] = sum == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ref, rest);
             float2* dst = reinterpret_cast<float2*>(a.part_o + row * HD) + (lane >> 2);
 #pragma unroll
             for (int j = 0; j < HD / 16; ++j) dst[8 * j] = make_float2(f * o[j][x][y] * e, f * o[j][x][2 + y] * e);
@@ -275,14 +279,21 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
 #pragma unroll
       for (int i = 0; i < NT; ++i) key[i] = s_key[warp][8 * i + (lane >> 2)];
       float d[NT][X][2], e[NT][X][2];  // t - m and u - n
+      // t is rounded before m is taken from it: m is a rounded score less a little, and with the
+      // unrounded one the difference would hold what its rounding left, 2^3 and more for
+      // scores from 2^27 on.
       auto exponents = [&]() {
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int x = 0; x < X; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) d[i][x][y] = fmaf(s[i >> 1][x][2 * (i & 1) + y], key[i].x * c[x][y], -m[x][y]);
+          for (int x = 0; x < X; ++x) {
+            const float* si = &s[i >> 1][x][2 * (i & 1)];
+            const float2 t = __fmul2_rn(f2(si[0], si[1]), __fmul2_rn(f2(key[i].x, key[i].x), f2(c[x][0], c[x][1])));
+            const float2 dd = __fadd2_rn(t, f2(-m[x][0], -m[x][1]));
+            d[i][x][0] = dd.x;
+            d[i][x][1] = dd.y;
+          }
         if (in != 0xffffffffu) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
           for (int x = 0; x < X; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              e[i][x][y] = d[i][x][y] + (key[i].y + (m[x][y] - n[x][y]));
+              e[i][x][y] = d[i][x][y] + (key[i].y - rel[x][y]);
               top = max3(top, d[i][x][y], e[i][x][y]);
             }
         return top;
@@ -305,23 +316,27 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
       // A head's references only move where a score passes them by too much; until then no
       // lane has to know the others' maxima.
       if (__any_sync(0xffffffffu, exponents() > kAboveMost)) {
+        auto score = [&](int i, int x, int y) {
+          return __fmul_rn(s[i >> 1][x][2 * (i & 1) + y], __fmul_rn(key[i].x, c[x][y]));
+        };
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float top = -INFINITY, tow = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-              if ((in >> (8 * i + (lane >> 2))) & 1) {
-                const float t = s[i >> 1][x][2 * (i & 1) + y] * (key[i].x * c[x][y]);
-                top = fmaxf(top, t);
-                tow = fmaxf(tow, t + key[i].y);
-              }
-            const float m_new = fmaxf(m[x][y], head_max(top) - kAbove), n_new = fmaxf(n[x][y], head_max(tow) - kAbove);
-            l[x][y] *= ex2(m[x][y] - m_new);
-            const float f = ex2(n[x][y] - n_new);
+              if ((in >> (8 * i + (lane >> 2))) & 1) top = fmaxf(top, score(i, x, y));
+            const float m_new = fmaxf(m[x][y], head_max(top) - kAbove), down = m[x][y] - m_new;
+            float tow = -INFINITY;  // of u - m
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+              if ((in >> (8 * i + (lane >> 2))) & 1) tow = fmaxf(tow, (score(i, x, y) - m_new) + key[i].y);
+            const float rel_new = fmaxf(rel[x][y] + down, head_max(tow) - kAbove);
+            l[x][y] *= ex2(down);
+            const float f = ex2(rel[x][y] + down - rel_new);
             m[x][y] = m_new;
-            n[x][y] = n_new;
+            rel[x][y] = rel_new;
 #pragma unroll
             for (int j = 0; j < HD / 16; ++j) {
               o[j][x][y] *= f;
