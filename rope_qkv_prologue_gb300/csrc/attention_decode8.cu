@@ -78,7 +78,12 @@ __device__ __forceinline__ float head_max(float v) {
   return v;
 }
 
-// A head's references before its first key: so low that any score passes them.
+// The largest factor of a product q . K. With q in 16 bits (128 values below 2^16) and codes
+// below 2^9 such a product is below 2^32, so scores stay below 2^99 and no infinities meet. A
+// larger factor is taken as this one: what is lost is the order among keys whose scores are all
+// 2^34 and more (the least product that is not 0 is 2^-33).
+constexpr float kFactorMost = 0x1p67f;
+// A head's reference before its first key: so low that any score passes it.
 constexpr float kNoKey = -1e30f;
 // Powers of two by which the largest score lies above a head's reference: when that is set,
 // and where it has to move.
@@ -282,18 +287,20 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
       // t is rounded before m is taken from it: m is a rounded score less a little, and with the
       // unrounded one the difference would hold what its rounding left, 2^3 and more for
       // scores from 2^27 on.
-      auto exponents = [&]() {
+      // (bound: factors may lie above their bound)
+      auto factor = [&](int i, int x, int y, bool bound) {
+        const float f = key[i].x * c[x][y];
+        return bound ? fminf(f, kFactorMost) : f;
+      };
+      auto exponents = [&](bool bound) {
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int x = 0; x < X; ++x) {
-            const float* si = &s[i >> 1][x][2 * (i & 1)];
-            const float2 t = __fmul2_rn(f2(si[0], si[1]), __fmul2_rn(f2(key[i].x, key[i].x), f2(c[x][0], c[x][1])));
-            const float2 dd = __fadd2_rn(t, f2(-m[x][0], -m[x][1]));
-            d[i][x][0] = dd.x;
-            d[i][x][1] = dd.y;
-          }
+          for (int x = 0; x < X; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)  // (packed, the two operations become one)
+              d[i][x][y] = __fsub_rn(__fmul_rn(s[i >> 1][x][2 * (i & 1) + y], factor(i, x, y, bound)), m[x][y]);
         if (in != 0xffffffffu) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
@@ -314,11 +321,14 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
         return top;
       };
       // A head's references only move where a score passes them by too much; until then no
-      // lane has to know the others' maxima.
-      if (__any_sync(0xffffffffu, exponents() > kAboveMost)) {
-        auto score = [&](int i, int x, int y) {
-          return __fmul_rn(s[i >> 1][x][2 * (i & 1) + y], __fmul_rn(key[i].x, c[x][y]));
-        };
+      // lane has to know the others' maxima. (Factors above their bound come this way too.)
+      float a_most = key[0].x, c_most = c[0][0];
+#pragma unroll
+      for (int i = 1; i < NT; ++i) a_most = fmaxf(a_most, key[i].x);
+#pragma unroll
+      for (int x = 0; x < X; ++x) c_most = max3(c_most, c[x][0], c[x][1]);
+      if (__any_sync(0xffffffffu, exponents(false) > kAboveMost || a_most * c_most > kFactorMost)) {
+        auto score = [&](int i, int x, int y) { return __fmul_rn(s[i >> 1][x][2 * (i & 1) + y], factor(i, x, y, true)); };
 #pragma unroll
         for (int x = 0; x < X; ++x)
 #pragma unroll
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
               o[j][x][2 + y] *= f;
             }
           }
-        exponents();
+        exponents(true);
       }
       uint32_t pf[NT][X];  // the weights as the second product's operand: a head's keys
 #pragma unroll

@@ -58,3 +58,31 @@ def test_scores_far_beyond_the_weights_exponents(lib, cuda, D, group, power):
         assert_within(f64(out), ref["out"], bound(ref), what)
         ref["s_abs"] = np.full_like(ref["lse"], 2.0 ** power)
         assert_lse(lse.cpu().numpy(), ref, 700, D, what)
+
+
+@pytest.mark.parametrize("D, group", [(64, 4), (64, 12), (128, 8)])
+@pytest.mark.parametrize("bad", [float("inf"), 3e38, 2.0 ** 121, 2.0 ** 100])
+def test_key_scales_at_and_beyond_the_largest(lib, cuda, D, group, bad):
+    """Blocks of such a scale among ordinary ones, ordinary queries: the block's largest
+    score takes all the weight where it is positive, the other blocks share it where none
+    is. Scores beyond float32 are no infinities that cancel."""
+    b = Batch(group, 1, D, 16, 8, [100, 33, 8], 41, spread=0.5)
+    for row, n in zip(b.table, b.lengths):
+        b.scale[0][row[0], 0] = bad
+        if n > 90:
+            b.scale[0][row[5], 1] = bad
+    refill(b)
+    ref = b.want()
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    out = b.run(lib, cuda, dev_status=status)
+    assert_within(f64(out), ref["out"], bound(ref), f"{bad}")
+    assert int(status) == 0
+
+
+def test_a_key_of_zeros_beyond_the_largest_score(lib, cuda):
+    # a query and a scale whose product is no float32, and a key of zeros: its score is 0
+    b = Batch(4, 1, 64, 16, 16, [16], 42)
+    refill(b, codes=lambda i, shape: None if i else np.zeros(shape, np.uint8), scale=lambda i, shape: np.full(shape, 1.0 if i else 2.0 ** 120))
+    b.q = (b.q.double() * 2.0 ** 100).to(torch.bfloat16)
+    ref = b.want()
+    assert_within(f64(b.run(lib, cuda)), ref["out"], bound(ref), "zeros")
