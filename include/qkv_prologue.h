@@ -253,7 +253,8 @@ QKVP_API int qkv_prologue_pool_scatter(const qkvp_layout* layout, int64_t T, con
  * A new code is x / s rounded to nearest even (within one rounding of 1 / s in
  * float32), so its error is at most 2^-4 |x|, or 2^-10 s where that is more. NaN
  * and infinities become NaN and do not enter amax. Scales of k_scale and v_scale
- * outside [2^-100, 2^120] are taken as the nearest bound (NaN: 2^-100).
+ * outside [2^-100, 2^121] are taken as the nearest bound (NaN: 2^-100); the call
+ * writes none outside.
  *
  * T, packed, pos, w_q, w_k, eps, rope_base, q, page, offset, dev_status: as
  * qkv_prologue_pool_write; variant as in the _ex calls (NULL: none).
@@ -617,8 +618,10 @@ QKVP_API int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t b
  * power of two of its row and rounded to 11 significant bits at most (exact within
  * 2^-14 of the row's largest value), the softmax weights times the values' scales
  * to 11 (those 2^-25 and more below the largest to fewer; 2^-36 below it they are
- * lost); sums, maxima and scales are fp32. Scales outside [2^-100, 2^120] are taken
- * as the nearest bound. Slots that no sequence names are never used.
+ * lost); sums, maxima and scales are fp32. Scales outside [2^-100, 2^121] are taken
+ * as the nearest bound. k_scale times the row's power of two times scale log2(e) is
+ * taken as 2^67 where it is more, so that finite inputs make finite scores; that only
+ * changes the order among keys that all score 2^34 and more. Slots that no sequence names are never used.
  *
  * layout, batch, q, page_table, max_pages, table_stride, lengths, scale, out,
  * lse, dev_status, stream: as qkv_attention_decode. k_pool, v_pool, k_scale,

@@ -5,7 +5,7 @@ leaves. One block and head at a time; shares no code with the kernels.
 
 import numpy as np
 
-LEAST, MOST = 2.0 ** -100, 2.0 ** 120
+LEAST, MOST = 2.0 ** -100, 2.0 ** 121
 
 
 def e4m3_values():

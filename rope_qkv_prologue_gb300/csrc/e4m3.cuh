@@ -6,9 +6,11 @@
 namespace qkvp {
 
 constexpr float kE4m3Max = 448.f;
-// Scales lie between these; one outside is taken as the nearest (a NaN as the least).
-constexpr float kScaleLeast = 7.888609052210118e-31f;  // 2^-100
-constexpr float kScaleMost = 1.329227995784916e36f;    // 2^120
+// Scales lie between these; one outside is taken as the nearest (a NaN as the least). A block
+// that grows by powers of two to hold values of up to 2^128 has a scale below 2^129 / 448,
+// 1.15 2^120: below the bound, so that every scale that is written is read as it is.
+constexpr float kScaleLeast = 0x1p-100f;
+constexpr float kScaleMost = 0x1p121f;
 
 __device__ __forceinline__ float clamp_scale(float s) { return fminf(fmaxf(s, kScaleLeast), kScaleMost); }
 

@@ -86,3 +86,55 @@ def test_a_key_of_zeros_beyond_the_largest_score(lib, cuda):
     b.q = (b.q.double() * 2.0 ** 100).to(torch.bfloat16)
     ref = b.want()
     assert_within(f64(b.run(lib, cuda)), ref["out"], bound(ref), "zeros")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), 3e38, 2.0 ** 121, 2.0 ** 120])
+def test_value_scales_at_and_beyond_the_largest(lib, cuda, bad):
+    # codes of at most 32, so that the results are finite in bf16
+    b = Batch(8, 2, 64, 16, 8, [100, 33, 8], 43)
+    g = np.random.default_rng(44)
+    refill(b, codes=lambda i, shape: E8.to_e4m3(np.clip(g.standard_normal(shape) * 8, -32, 32)) if i else None)
+    for row in b.table:
+        b.scale[1][row[0], 0] = bad
+    refill(b)
+    ref = b.want()
+    down = 2.0 ** -100
+    assert_within(f64(b.run(lib, cuda)) * down, ref["out"] * down, bound(ref) * down, f"{bad}")
+
+
+def test_a_scale_that_grows_past_2_to_120_is_read_back(lib, cuda):
+    """A block with the scale 1.1 2^119 gets a value of 3.35e38: the least power of two
+    that holds it makes 1.1 2^120. What is written has to be what is read, and what a later
+    token finds."""
+    F, n_q, n_kv, D = lib.functional, 2, 1, 64
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda)  # noqa: E731
+    pools = [torch.full((1, 16, n_kv, D), 0x60, dtype=torch.uint8, device=cuda).view(F8) for _ in range(2)]  # 32
+    scales = [torch.full((1, 2, n_kv), 1.1 * 2.0 ** 119, device=cuda) for _ in range(2)]
+    first = float(scales[0][0, 0, 0])
+    held = 32.0 * first
+
+    def append(value, at):
+        rows = torch.zeros(1, (n_q + 2 * n_kv) * D, dtype=torch.bfloat16, device=cuda)
+        rows[:, n_q * D:] = value
+        F.prologue_pool_write8(rows, None, None, None, i32(0), i32(at), *pools, *scales, n_q, n_kv, D, "sectioned",
+                               norm=False, nope=True)
+
+    def read(at):
+        """The value at a place: attention to it alone, as if its block began there."""
+        one = [torch.full((1, 16, n_kv, D), 127, dtype=torch.uint8, device=cuda).view(F8) for _ in range(2)]
+        for p, o in zip(pools, one):
+            o.view(torch.uint8)[0, 0] = p.view(torch.uint8)[0, at]
+        q = torch.zeros(1, n_q, D, dtype=torch.bfloat16, device=cuda)
+        return f64(F.attention_decode8(q, *one, *scales, i32(0)[None], i32(1)))
+
+    big = float(torch.tensor(3.35e38).to(torch.bfloat16))
+    append(big, 3)
+    for s in scales:
+        assert float(s[0, 0, 0]) == 2.0 * first and float(s[0, 1, 0]) == first
+    assert np.all(np.abs(read(3) - big) <= (2.0 ** -4 + 2.0 ** -8) * big)
+    assert np.all(np.abs(read(0) - held) <= 2.0 ** -8 * held)
+    append(1.0, 4)  # no reason to grow, and none to shrink
+    for s in scales:
+        assert float(s[0, 0, 0]) == 2.0 * first
+    assert np.all(np.abs(read(3) - big) <= (2.0 ** -4 + 2.0 ** -8) * big)
+    assert np.all(np.abs(read(0) - held) <= 2.0 ** -8 * held)
