@@ -615,8 +615,8 @@ QKVP_API int qkv_attention_decode_workspace(const qkvp_layout* layout, int32_t b
  * [page, i] being code * scale of that slot and of its block i / block:
  *     out[b, h] = sum_t softmax_t(scale q[b, h] . k_t[g]) v_t[g].
  * The products take the codes as they are (exact in 16 bits); q is scaled by a
- * power of two of its row and rounded to 11 significant bits at most (exact within
- * 2^-14 of the row's largest value), the softmax weights times the values' scales
+ * power of two of its row and rounded to 16 bits (exact down to 2^-32 of the row's
+ * largest value; below 2^-40 of it nothing is left), the softmax weights times the values' scales
  * to 11 (those 2^-25 and more below the largest to fewer; 2^-36 below it they are
  * lost); sums, maxima and scales are fp32. Scales outside [2^-100, 2^121] are taken
  * as the nearest bound. k_scale times the row's power of two times scale log2(e) is

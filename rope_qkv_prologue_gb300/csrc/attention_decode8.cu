@@ -17,7 +17,9 @@
 //
 // Codes go to the matrix units (m16n8k16, f16 with fp32 accumulation) as f16, which
 // holds every e4m3 value exactly; one conversion instruction makes two values. A row of
-// q is scaled by a power of two that brings its largest magnitude into [1, 2). The heads
+// q is scaled by a power of two that brings its largest magnitude into [2^15, 2^16), the end of
+// f16's range, so that values down to 2^-32 of it keep all their bits (a channel far above the
+// others may meet keys that have nothing in it). The heads
 // are the products' 8 columns (S^T = K Q^T, O^T = V^T W^T): keys and values fill the 16
 // rows, where heads as rows left half of them empty in groups of up to 8, at 32 products
 // and 570 instructions a tile of 32 keys and 64 values instead of 16 and 440. The order of
@@ -191,8 +193,9 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^-e, e the exponent of the largest magnitude (within what float32 can scale by)
-        const int e = min(max((int)(top >> 23) - 127, -126), 126);
+        // 2^-e, which brings the largest magnitude into [2^15, 2^16) (within what float32 can
+        // scale by: a row below 2^-111 stays below that, with all its bits)
+        const int e = min(max((int)(top >> 23) - 127 - 15, -126), 112);
         const float f = __uint_as_float((uint32_t)(127 - e) << 23);
         const float factor = a.scale_log2 * __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll

@@ -138,3 +138,25 @@ def test_a_scale_that_grows_past_2_to_120_is_read_back(lib, cuda):
         assert float(s[0, 0, 0]) == 2.0 * first
     assert np.all(np.abs(read(3) - big) <= (2.0 ** -4 + 2.0 ** -8) * big)
     assert np.all(np.abs(read(0) - held) <= 2.0 ** -8 * held)
+
+
+@pytest.mark.parametrize("D, group", [(64, 4), (64, 12), (128, 8)])
+@pytest.mark.parametrize("power", [12, 16, 20, 25, 30])
+def test_a_query_value_far_above_the_others(lib, cuda, D, group, power):
+    """A channel of the query 2^power times the others, which no key has anything in: the
+    scores are those of the others. They are of 1/2 to 2 in magnitude (scaled by the
+    channel), so that every one lies within 2^-32 of the row's largest."""
+    b = Batch(group, 1, D, 16, 8, [100, 33, 3], 50 + power)
+    g = np.random.default_rng(power)
+    q = np.exp2(g.uniform(-1, 1, b.q.shape)) * g.choice((-1, 1), b.q.shape)
+    q[..., 5] = -1.5 * 2.0 ** power
+    b.q = torch.from_numpy(q).to(torch.bfloat16)
+    b.codes[0][..., 5] = np.where(b.codes[0][..., 5] == 127, 127, 0)
+    refill(b)
+    ref = b.want()
+    out, lse = b.run(lib, cuda, save_lse=True)
+    assert_within(f64(out), ref["out"], bound(ref), f"2^{power}")
+    assert_lse(lse.cpu().numpy(), ref, 100, D, f"2^{power}")
+    b.q = (b.q.double() * 2.0 ** -126).to(torch.bfloat16)  # down to the least normal numbers
+    want = A.attention_decode(f64(b.q), b.keys, b.values, 2.0 ** 123)
+    assert_within(f64(b.run(lib, cuda, scale=2.0 ** 123)), want["out"], bound(want), f"2^{power - 126}")
