@@ -250,8 +250,8 @@ QKVP_API int qkv_prologue_pool_scatter(const qkvp_layout* layout, int64_t T, con
  *     above it are not): s = s_old 2^k with the least k >= 0 for which amax <=
  *     448 s (compared by exponent and significand), and the held codes are
  *     divided by 2^k (rounded to nearest even).
- * A new code is x / s rounded to nearest even (within one rounding of 1 / s in
- * float32), so its error is at most 2^-4 |x|, or 2^-10 s where that is more. NaN
+ * A new code is x / s rounded to float32, then to e4m3, ties to even, so its error
+ * is at most 2^-4 |x|, or 2^-10 s where that is more. NaN
  * and infinities become NaN and do not enter amax. Scales of k_scale and v_scale
  * outside [2^-100, 2^121] are taken as the nearest bound (NaN: 2^-100); the call
  * writes none outside.
