@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <atomic>
 #include <mutex>
@@ -100,8 +101,9 @@ int blocks_per_sm(const void* kernel, int threads, size_t smem) {
   return n;
 }
 
-// Opt a kernel in to `smem` bytes of dynamic shared memory (once per device
-// and kernel; the attribute only ever grows).
+// Opt a kernel in to `smem` bytes of dynamic shared memory: one entry per device and
+// kernel, for the most that was asked for. The attribute only ever grows, so that a call
+// from another thread between this one and its launch takes nothing away from it.
 bool allow_smem(const void* kernel, size_t smem) {
   if (smem <= 48 * 1024) return true;
   struct Entry {
@@ -110,18 +112,26 @@ bool allow_smem(const void* kernel, size_t smem) {
     size_t bytes;
   };
   static std::mutex mu;
-  static Entry cache[256];
-  static int n = 0;
+  static Entry* cache = nullptr;
+  static int n = 0, room = 0;
   int dev = -1;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n; ++i)
-    if (cache[i].dev == dev && cache[i].kernel == kernel && cache[i].bytes >= smem) return true;
+  int i = 0;
+  while (i < n && (cache[i].dev != dev || cache[i].kernel != kernel)) ++i;
+  if (i < n && cache[i].bytes >= smem) return true;
+  if (i == room) {
+    void* more = std::realloc(cache, (size_t)(room + 256) * sizeof(Entry));
+    if (!more) return false;
+    cache = static_cast<Entry*>(more);
+    room += 256;
+  }
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  if (n < 256) cache[n++] = Entry{dev, kernel, smem};
+  cache[i] = Entry{dev, kernel, smem};
+  n = std::max(n, i + 1);
   return true;
 }
 
