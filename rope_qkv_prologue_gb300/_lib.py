@@ -176,13 +176,20 @@ def _frequencies(doubles):
     return ctypes.cast((ctypes.c_char * len(doubles)).from_buffer_copy(doubles), ctypes.POINTER(ctypes.c_double))
 
 
+def _doubles(values):
+    try:
+        return array.array("d", values)
+    except TypeError:  # numbers as texts
+        return array.array("d", [float(f) for f in values])
+
+
 def variant(inv_freq=None, rope_scale=0.0, bias=None):
     """A qkvp_variant (the GQAttention variant options). inv_freq: a sequence of
     head_dim / 2 floats (kept alive with the struct); bias: a device tensor or
     address, float32 [(n_q + 2 n_kv) * head_dim] in packed-row order."""
     v = qkvp_variant()
     if inv_freq is not None:
-        arr = _frequencies(array.array("d", inv_freq).tobytes())
+        arr = _frequencies(_doubles(inv_freq).tobytes())
         v._inv_freq_keepalive = arr
         v.inv_freq = arr
     v.rope_scale = float(rope_scale)

@@ -39,9 +39,15 @@ def _check_dev(*ts):
             raise ValueError("all tensors must live on a CUDA device")
 
 
+def _frequencies(inv_freq):
+    """inv_freq as something with a length: an iterator's numbers can be taken once."""
+    return inv_freq if inv_freq is None or hasattr(inv_freq, "__len__") else [*inv_freq]
+
+
 def _variant(bias=None, inv_freq=None, rope_scale=1.0, dim=0, rotary_dim=None):
     """The qkvp_variant of the GQAttention options, or None for the plain call. dim: the
     head's; the library reads a frequency for each of its pairs."""
+    inv_freq = _frequencies(inv_freq)
     if rotary_dim is not None and inv_freq is not None and len(inv_freq) != rotary_dim // 2:
         raise ValueError(f"inv_freq has {len(inv_freq)} frequencies, expected rotary_dim / 2 = {rotary_dim // 2}")
     if rotary_dim is None and inv_freq is not None and len(inv_freq) < dim // 2:
@@ -682,6 +688,7 @@ class GQAttentionPrologue(torch.autograd.Function):
     @staticmethod
     def forward(ctx, packed, pos, w_q, w_k, bias, n_q, n_kv, head_dim, kind, eps, rope_base, nope, norm,
                 inv_freq, rope_scale, rotary_dim=None, rotary_pairs=False):
+        inv_freq = _frequencies(inv_freq)  # (the backward takes them too)
         out = prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim, kind, eps, rope_base, nope,
                                save_pre=norm, norm=norm, bias=bias, inv_freq=inv_freq, rope_scale=rope_scale,
                                rotary_dim=rotary_dim, rotary_pairs=rotary_pairs)
