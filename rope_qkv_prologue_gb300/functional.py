@@ -66,6 +66,14 @@ def _flags(nope=False, save_pre=False, norm=True, rotary_dim=None, rotary_pairs=
             | (0 if rotary_dim is None else C.QKVP_ROPE_PART) | (C.QKVP_ROPE_PAIRS if rotary_pairs else 0))
 
 
+def _call(function, T, *args):
+    """function(*args) of T tokens. Of none the library checks its arguments and touches no
+    row; an empty tensor has no address, so any stands in for it."""
+    if T == 0:
+        args = [16 if isinstance(a, torch.Tensor) and a.numel() == 0 else a for a in args]
+    return function(*args)
+
+
 def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interleaved", eps=1e-6,
                      rope_base=500000.0, nope=False, save_pre=False, stream=None, norm=True, bias=None,
                      inv_freq=None, rope_scale=1.0, rotary_dim=None, rotary_pairs=False):
@@ -88,10 +96,8 @@ def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interl
     v = torch.empty(T, n_kv, head_dim, dtype=torch.bfloat16, device=dev)
     q_pre = torch.empty_like(q) if save_pre else None
     k_pre = torch.empty_like(k) if save_pre else None
-    if T == 0:  # an empty tensor has no address to pass
-        return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
-    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
-                          rope_base, _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
+    _call(C.qkv_prologue_fwd_ex, T, L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q,
+          w_k, eps, rope_base, _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
     return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
 
 
@@ -118,17 +124,11 @@ def prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_d
     dw_q = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dw_k = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dbias = torch.empty((n_q + 2 * n_kv) * head_dim, dtype=torch.float32, device=dev) if bias is not None else None
-    if T == 0:
-        for t in (dw_q, dw_k, dbias):
-            if t is not None:
-                t.zero_()
-        return (dpacked, dw_q, dw_k, dbias) if bias is not None else (dpacked, dw_q, dw_k)
     need = _backward_workspace(kind, n_q, n_kv, head_dim, T, bias is not None)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    C.qkv_prologue_bwd_ex(L, V, T, dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, eps, rope_base,
-                          _flags(nope, False, norm, rotary_dim, rotary_pairs), dpacked, dw_q, dw_k, dbias, workspace,
-                          need, stream)
+    _call(C.qkv_prologue_bwd_ex, T, L, V, T, dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, eps, rope_base,
+          _flags(nope, False, norm, rotary_dim, rotary_pairs), dpacked, dw_q, dw_k, dbias, workspace, need, stream)
     return (dpacked, dw_q, dw_k, dbias) if bias is not None else (dpacked, dw_q, dw_k)
 
 
@@ -140,11 +140,9 @@ def prologue_pool_write(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, n_q
     _check_dev(packed, pos, w_q, w_k, page, offset, k_pool, v_pool)
     L, T = _layout_of(packed, n_q, n_kv, head_dim, kind, rotary_dim)
     q = torch.empty(T, n_q, head_dim, dtype=torch.bfloat16, device=packed.device)
-    if T == 0:
-        return q
-    C.qkv_prologue_pool_write_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
-                                 rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
-                                 v_pool, k_pool.shape[0], k_pool.shape[1], dev_status, stream)
+    _call(C.qkv_prologue_pool_write_ex, T, L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos,
+          w_q, w_k, eps, rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool, v_pool,
+          k_pool.shape[0], k_pool.shape[1], dev_status, stream)
     return q
 
 
@@ -586,12 +584,9 @@ def prologue_pool_write8(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, k_
         _check_like(bias, ((n_q + 2 * n_kv) * head_dim,), torch.float32, dev, "bias")
     _check_status(dev_status, dev)
     q = torch.empty((T, n_q, head_dim), dtype=torch.bfloat16, device=dev)
-    if T == 0:
-        return q
-    C.qkv_prologue_pool_write8(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
-                               rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
-                               v_pool, k_scale, v_scale, k_pool.shape[0], k_pool.shape[1], block, dev_status,
-                               _current_stream(dev))
+    _call(C.qkv_prologue_pool_write8, T, L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos,
+          w_q, w_k, eps, rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool, v_pool,
+          k_scale, v_scale, k_pool.shape[0], k_pool.shape[1], block, dev_status, _current_stream(dev))
     return q
 
 
