@@ -102,8 +102,8 @@ def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interl
 
 
 @functools.lru_cache(maxsize=1024)
-def _backward_workspace(kind, n_q, n_kv, head_dim, T, bias):
-    # (the size depends on there being a bias, not on where it is)
+def _backward_workspace(kind, n_q, n_kv, head_dim, T, bias, device_index):
+    # (the size is the current device's, and depends on there being a bias, not on where it is)
     return C.qkv_prologue_bwd_workspace_size_ex(_layout(kind, n_q, n_kv, head_dim), C.variant(bias=16) if bias else None, T)
 
 
@@ -124,7 +124,7 @@ def prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_d
     dw_q = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dw_k = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dbias = torch.empty((n_q + 2 * n_kv) * head_dim, dtype=torch.float32, device=dev) if bias is not None else None
-    need = _backward_workspace(kind, n_q, n_kv, head_dim, T, bias is not None)
+    need = _backward_workspace(kind, n_q, n_kv, head_dim, T, bias is not None, torch.cuda.current_device())
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     _call(C.qkv_prologue_bwd_ex, T, L, V, T, dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, eps, rope_base,
