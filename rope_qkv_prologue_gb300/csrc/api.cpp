@@ -1017,25 +1017,44 @@ int qkv_prologue_pool_write8(const qkvp_layout* layout, const qkvp_variant* vari
   a.by_group = small_div_by(a.group);
   a.dev_status = dev_status;
   if (rope) rope_table(rope_base, rot, vr.inv_freq, vr.scale, &a.rope);
-  // Tokens per CTA. Two CTAs are resident on an SM, and a CTA costs what its tokens do and
-  // about 2.5 more (its runs and its table): the tile with the cheapest waves. (16384 tokens,
-  // 32 over 8 heads of 128, tiles of 8, 16 and 27: see the kernel.) While there are fewer
-  // tiles than places, each is divided among CTAs along y.
-  const int64_t slots = 2 * (int64_t)sms;
-  double best = 0.0;
-  const int most = std::min(32, 65535 / a.n_q);  // (its rows of query heads are counted in 16 bits)
-  for (int tile = 1; tile <= most; ++tile) {
-    const int64_t waves = ((T + tile - 1) / tile + slots - 1) / slots;
-    const double cost = (double)waves * (tile + 2.5);
-    if (tile == 1 || cost < best) {
-      best = cost;
-      a.tile = tile;
+  // Tokens per CTA along x, and CTAs that share them along y. A block's new tokens of one head
+  // are one warp's work, k or v, however many they are, so a prompt's blocks are 2 n_kv units
+  // each, in the CTAs of the tile that they begin in: `share` CTAs have a warp for each. (All
+  // figures: 32 over 8 heads of 128, one prompt in blocks of 16 / 64 tokens, then single tokens
+  // of as many sequences; the rule, and behind the bar one CTA per tile.)
+  //  * What one wave of shared tiles holds takes that. 256 tokens 12 / 39, 8.2 | 18 / 41, 8.2 us;
+  //    512 tokens 14 / 39, 9.7 | 18 / 59, 8.9; 2048 tokens 18 / 43, 18 | 22 / 63, 18. (Larger tiles
+  //    on half as many CTAs: prompts in blocks of 64 a tenth faster, single tokens a tenth slower.)
+  //  * Of more tokens, blocks that are no shorter than a tile can be leave most CTAs without k
+  //    and v: the largest tiles, shared. Blocks of 32 / 64: 4096 tokens 31 / 45 | 41 / 68, 16384
+  //    97 / 110 | 96 / 124. (Single tokens of 4096 sequences 37 | 33.)
+  //  * Else a CTA costs what its tokens do and about 2.5 more (its runs and its table): the tile
+  //    with the cheapest waves. Blocks of 16: 16384 tokens in tiles of 16, 27 (the rule's) and 32
+  //    82, 86 and 86; 4096 tokens in tiles of 14 (the rule's), 16 and 32: 27, 27 and 32.
+  const int64_t slots = 2 * (int64_t)sms;           // two CTAs an SM
+  const int most = std::min(32, 65535 / a.n_q);     // (its rows of query heads are counted in 16 bits)
+  const int share = std::min(4, (a.n_kv + 3) / 4);  // (of 8 warps)
+  int64_t parts = 1;
+  if (T <= 7 * slots) {
+    a.tile = (int)std::min<int64_t>(most, std::max<int64_t>(share, (share * T + slots - 1) / slots));
+    const int64_t tiles = (T + a.tile - 1) / a.tile, units = (int64_t)a.tile * (8 * a.n_kv + a.n_q) / 16;
+    parts = std::max<int64_t>(share, std::min<int64_t>(slots / tiles, (units + 7) / 8));
+  } else if (block >= 32) {
+    a.tile = most;
+    parts = share;
+  } else {
+    double best = 0.0;
+    for (int tile = 1; tile <= most; ++tile) {
+      const int64_t waves = ((T + tile - 1) / tile + slots - 1) / slots;
+      const double cost = (double)waves * (tile + 2.5);
+      if (tile == 1 || cost < best) {
+        best = cost;
+        a.tile = tile;
+      }
     }
   }
   a.tab_rows = (int)std::min<int64_t>((int64_t)a.tile + block - 1, 40 * 1024 / (hd * (int)sizeof(float)));
   const int64_t tiles = (T + a.tile - 1) / a.tile;
-  const int64_t units = (int64_t)a.tile * (8 * a.n_kv + a.n_q) / 16;
-  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, (units + 7) / 8));
   const void* kern =
       pool_write8_kernel(hd, !rope ? kRopeNone : (rot.adjacent ? kRopeAdjacent : kRopeHalves), norm, vr.bias != nullptr);
   const size_t smem = (size_t)pool_write8_smem_bytes(hd, rope ? a.tab_rows : 0);
