@@ -160,3 +160,37 @@ def test_a_query_value_far_above_the_others(lib, cuda, D, group, power):
     b.q = (b.q.double() * 2.0 ** -126).to(torch.bfloat16)  # down to the least normal numbers
     want = A.attention_decode(f64(b.q), b.keys, b.values, 2.0 ** 123)
     assert_within(f64(b.run(lib, cuda, scale=2.0 ** 123)), want["out"], bound(want), f"2^{power - 126}")
+
+
+@pytest.mark.parametrize("spread", [5.0, 20.0])
+def test_key_scales_far_apart(lib, cuda, spread):
+    # blocks whose key scales lie apart by up to e^(2 spread), queries that keep the largest
+    # scores moderate: several keys of the large blocks share the weight with all the small ones
+    b = Batch(8, 2, 64, 16, 8, [200, 33, 1, 40], 45, spread=spread)
+    scale = 0.125 * 8 * np.exp(-spread)
+    ref = b.want(scale)
+    scores = max(np.abs(k[:, h // 4] @ f64(b.q)[i, h]).max() * scale for i, k in enumerate(b.keys) for h in range(8))
+    assert 1 < scores < 64
+    out, lse = b.run(lib, cuda, save_lse=True, scale=float(scale))
+    assert_within(f64(out), ref["out"], bound(ref), f"{spread}")
+    assert_lse(lse.cpu().numpy(), ref, 200, 64, f"{spread}")
+
+
+def test_a_length_beyond_the_table_attends_what_the_table_names(lib, cuda):
+    b = Batch(8, 2, 64, 16, 8, [40, 96, 7], 46)
+    b.table = b.table[:, :6]
+    b.lengths[0] = 1 << 30
+    b.table[0, 3:] = (-1, 1 << 20, 1 << 30)  # no pages of the pool: nothing there is attended
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    # (the oracle's keys of row 0: its three pages, the last of which holds 8 tokens and NaN codes behind them)
+    b.codes[0][b.table[0, 2], 8:], b.codes[1][b.table[0, 2], 8:] = 0, E8.to_e4m3(np.float64(3.0))
+    for s in b.scale:
+        s[b.table[0, 2], 1] = 0.5
+    keys, values = np.zeros((48, 2, 64)), np.full((48, 2, 64), 1.5)
+    keys[:40], values[:40] = b.keys[0], b.values[0]
+    b.keys[0], b.values[0] = keys, values
+    ref = b.want()
+    out, lse = b.run(lib, cuda, save_lse=True, dev_status=status)
+    assert_within(f64(out), ref["out"], bound(ref), "rows")
+    assert_lse(lse.cpu().numpy(), ref, 96, 64, "rows")
+    assert int(status) == lib.QKVP_DEV_BAD_LENGTH | lib.QKVP_DEV_BAD_PAGE
