@@ -451,7 +451,9 @@ struct AttnDecodeArgs {
 constexpr int kDec8Keys = 32;  // keys per tile of the kernel over the 8-bit pool
 // Warps per CTA, of tiles of 4 and 8 KiB. wide: groups of more than 8 query heads, whose
 // results take 168 registers at head_dim 64 (256 sequences of up to 4096 keys, 64 over 4
-// heads of 64: 87 us with 12 warps; 130 with 16, which spill; 95 with 8).
+// heads of 64: 87 us with 12 warps; 130 with 16, which spill; 95 with 8). At head_dim 128 three
+// tiles of 8 warps fill the shared memory (48 sequences of up to 32768 keys, 64 over 4 heads: 144
+// us; 12 warps with two tiles each 228, 32 over 8 heads 236 instead of 229).
 QKVP_HD constexpr int dec8_warps(int head_dim, bool wide) { return head_dim == 64 ? (wide ? 12 : 16) : 8; }
 const void* attention_decode8_kernel(int head_dim, bool wide);
 int attention_decode8_smem_bytes(int head_dim, bool wide);

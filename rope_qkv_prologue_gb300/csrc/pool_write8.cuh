@@ -11,8 +11,9 @@
 // error is half a step of e4m3, 2^-4 of the value (2^-10 s below 2^-6 s): with a
 // floating code the scale has to keep the values in range, not to centre them.
 //
-// Work. A CTA takes `tile` tokens. The tokens of one block that follow each other are a
-// run; the CTA whose tile has a run's first token does the whole run. A row of a head is
+// Work. A CTA, or several along y that divide its units, takes `tile` tokens. The tokens of one
+// block that follow each other are a run; the CTAs whose tile has a run's first token do the
+// whole run, k or v of a head in one warp (of short runs, of a few heads). A row of a head is
 // CPH / 2 lanes, two chunks of 8 values each (the units of rot_unit), so a warp holds 4 or 8
 // rows at once: of a run that many tokens of one head, of a shorter run several heads too (a
 // decode step's runs are single tokens). A warp works in steps of four times that, 4 KiB of

@@ -47,12 +47,14 @@ def _frequencies(inv_freq):
 def _variant(bias=None, inv_freq=None, rope_scale=1.0, dim=0, rotary_dim=None):
     """The qkvp_variant of the GQAttention options, or None for the plain call. dim: the
     head's; the library reads a frequency for each of its pairs."""
-    inv_freq = _frequencies(inv_freq)
-    if rotary_dim is not None and inv_freq is not None and len(inv_freq) != rotary_dim // 2:
-        raise ValueError(f"inv_freq has {len(inv_freq)} frequencies, expected rotary_dim / 2 = {rotary_dim // 2}")
-    if rotary_dim is None and inv_freq is not None and len(inv_freq) < dim // 2:
-        raise ValueError(f"inv_freq has {len(inv_freq)} frequencies, expected {dim // 2}")
-    if bias is None and inv_freq is None and rope_scale in (None, 0.0, 1.0):
+    if inv_freq is not None:
+        inv_freq = _frequencies(inv_freq)
+        n = len(inv_freq)
+        if rotary_dim is not None and n != rotary_dim // 2:
+            raise ValueError(f"inv_freq has {n} frequencies, expected rotary_dim / 2 = {rotary_dim // 2}")
+        if rotary_dim is None and n < dim // 2:
+            raise ValueError(f"inv_freq has {n} frequencies, expected {dim // 2}")
+    elif bias is None and rope_scale in (None, 0.0, 1.0):
         return None
     if bias is not None:
         _check_dev(bias)
@@ -66,12 +68,10 @@ def _flags(nope=False, save_pre=False, norm=True, rotary_dim=None, rotary_pairs=
             | (0 if rotary_dim is None else C.QKVP_ROPE_PART) | (C.QKVP_ROPE_PAIRS if rotary_pairs else 0))
 
 
-def _call(function, T, *args):
-    """function(*args) of T tokens. Of none the library checks its arguments and touches no
-    row; an empty tensor has no address, so any stands in for it."""
-    if T == 0:
-        args = [16 if isinstance(a, torch.Tensor) and a.numel() == 0 else a for a in args]
-    return function(*args)
+def _addresses(*tensors):
+    """The tensors of a call of no tokens: the library checks its arguments and touches no
+    row, but an empty tensor has no address to pass, so any stands in for it."""
+    return (t if t is None or t.numel() else 16 for t in tensors)
 
 
 def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interleaved", eps=1e-6,
@@ -96,9 +96,12 @@ def prologue_forward(packed, pos, w_q, w_k, n_q, n_kv, head_dim=64, kind="interl
     v = torch.empty(T, n_kv, head_dim, dtype=torch.bfloat16, device=dev)
     q_pre = torch.empty_like(q) if save_pre else None
     k_pre = torch.empty_like(k) if save_pre else None
-    _call(C.qkv_prologue_fwd_ex, T, L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q,
-          w_k, eps, rope_base, _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
-    return (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
+    out = (q, k, v, q_pre, k_pre) if save_pre else (q, k, v)
+    if T == 0:
+        packed, pos, q, k, v, q_pre, k_pre = _addresses(packed, pos, q, k, v, q_pre, k_pre)
+    C.qkv_prologue_fwd_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
+                          rope_base, _flags(nope, save_pre, norm, rotary_dim, rotary_pairs), q, k, v, q_pre, k_pre, stream)
+    return out
 
 
 @functools.lru_cache(maxsize=1024)
@@ -124,12 +127,16 @@ def prologue_backward(dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, n_q, n_kv, head_d
     dw_q = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dw_k = torch.empty(head_dim, dtype=torch.float32, device=dev) if norm else None
     dbias = torch.empty((n_q + 2 * n_kv) * head_dim, dtype=torch.float32, device=dev) if bias is not None else None
-    need = _backward_workspace(kind, n_q, n_kv, head_dim, T, bias is not None, torch.cuda.current_device())
+    need = _backward_workspace(kind, n_q, n_kv, head_dim, T, bias is not None, torch._C._cuda_getDevice())
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _call(C.qkv_prologue_bwd_ex, T, L, V, T, dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, eps, rope_base,
-          _flags(nope, False, norm, rotary_dim, rotary_pairs), dpacked, dw_q, dw_k, dbias, workspace, need, stream)
-    return (dpacked, dw_q, dw_k, dbias) if bias is not None else (dpacked, dw_q, dw_k)
+    out = (dpacked, dw_q, dw_k, dbias) if bias is not None else (dpacked, dw_q, dw_k)
+    if T == 0:
+        dq, dk, dv, q_pre, k_pre, pos, dpacked = _addresses(dq, dk, dv, q_pre, k_pre, pos, dpacked)
+    C.qkv_prologue_bwd_ex(L, V, T, dq, dk, dv, q_pre, k_pre, pos, w_q, w_k, eps, rope_base,
+                          _flags(nope, False, norm, rotary_dim, rotary_pairs), dpacked, dw_q, dw_k, dbias, workspace,
+                          need, stream)
+    return out
 
 
 def prologue_pool_write(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, n_q, n_kv, head_dim=64,
@@ -140,10 +147,13 @@ def prologue_pool_write(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, n_q
     _check_dev(packed, pos, w_q, w_k, page, offset, k_pool, v_pool)
     L, T = _layout_of(packed, n_q, n_kv, head_dim, kind, rotary_dim)
     q = torch.empty(T, n_q, head_dim, dtype=torch.bfloat16, device=packed.device)
-    _call(C.qkv_prologue_pool_write_ex, T, L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos,
-          w_q, w_k, eps, rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool, v_pool,
-          k_pool.shape[0], k_pool.shape[1], dev_status, stream)
-    return q
+    out = q
+    if T == 0:
+        packed, pos, q, page, offset = _addresses(packed, pos, q, page, offset)
+    C.qkv_prologue_pool_write_ex(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
+                                 rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
+                                 v_pool, k_pool.shape[0], k_pool.shape[1], dev_status, stream)
+    return out
 
 
 def latent_rows(rows, pos, w, eps=1e-6, rope_base=10000.0, norm_dim=512, rope_dim=64, nope=False,
@@ -584,10 +594,14 @@ def prologue_pool_write8(packed, pos, w_q, w_k, page, offset, k_pool, v_pool, k_
         _check_like(bias, ((n_q + 2 * n_kv) * head_dim,), torch.float32, dev, "bias")
     _check_status(dev_status, dev)
     q = torch.empty((T, n_q, head_dim), dtype=torch.bfloat16, device=dev)
-    _call(C.qkv_prologue_pool_write8, T, L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos,
-          w_q, w_k, eps, rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool, v_pool,
-          k_scale, v_scale, k_pool.shape[0], k_pool.shape[1], block, dev_status, _current_stream(dev))
-    return q
+    out = q
+    if T == 0:
+        packed, pos, q, page, offset = _addresses(packed, pos, q, page, offset)
+    C.qkv_prologue_pool_write8(L, _variant(bias, inv_freq, rope_scale, head_dim, rotary_dim), T, packed, pos, w_q, w_k, eps,
+                               rope_base, _flags(nope, False, norm, rotary_dim, rotary_pairs), q, page, offset, k_pool,
+                               v_pool, k_scale, v_scale, k_pool.shape[0], k_pool.shape[1], block, dev_status,
+                               _current_stream(dev))
+    return out
 
 
 @functools.lru_cache(maxsize=1024)
