@@ -31,8 +31,9 @@
 //
 // Bound by the codes' bytes in long batches, where both kernels take (32 over 8 heads of
 // 128, up to 32768 keys) 230 us for 48 sequences, 6.71 TB/s or 0.99 of a plain copy's rate
-// (heads as rows: 253 us). 256 sequences of up to 4096 keys, 64 over 8 heads of 64: 117 us,
-// 5.04 TB/s (132 us): 48 % of the issue slots, and the join is a tenth. One sequence of
+// (heads as rows: 253 us). 256 sequences of up to 4096 keys, 64 over 8 heads of 64: 115 to 119
+// us, 5.05 TB/s (132 us): 55 % of the issue slots, and the join is a tenth. Over 4 heads 89 us
+// (X = 2: twice the softmax arithmetic a byte, 56 % of the slots of 12 warps). One sequence of
 // 131072 keys: 55 us (58 us), a dozen of them the start, the last tiles and the join.
 #include <cuda_fp16.h>
 

@@ -27,10 +27,11 @@
 // registers); tokens of a run beyond the table's end get theirs computed by the lanes that
 // use them.
 //
-// Bound by instructions: 16384 tokens, 32 over 8 heads of 128, blocks of 16, take 82 us, 4.5
-// TB/s or 0.66 of a plain copy's rate, with 53 % of the issue slots used by the 16 warps that
+// Bound by instructions: 16384 tokens, 32 over 8 heads of 128, blocks of 16, take 83 to 86 us,
+// 4.4 TB/s or 0.64 of a plain copy's rate, with 54 % of the issue slots used by the 16 warps that
 // 119 to 124 registers leave room for. 4001 tokens behind 100 held ones (64 over 8 heads of 64, blocks
-// of 8, bias): 28 us in one wave of CTAs. 256 single tokens (128 over 16 heads of 64): 8 us,
+// of 8, bias): 30 us in one wave of CTAs. In longer blocks what a warp's run takes: 4096 tokens of
+// the first heads 27 us in blocks of 16, 46 of 64, 218 of 256. 256 single tokens (128 over 16 heads of 64): 8 us,
 // the chain of reads of one CTA.
 #pragma once
 
