@@ -5,8 +5,8 @@
 //     t_j = c a_j q . K_j,   l = sum_j 2^(t_j - m),         max t_j - 15 <= m <= max t_j - 11,
 //     u_j = t_j + log2(b_j), O = sum_j 2^(u_j - n) V_j,     max u_j - 15 <= n <= max u_j - 11,
 //     out = 2^r O / l,       r = n - m
-// (m to the nearest float32, up to 2^16 more; r is what is kept, for scores so large that n and
-// m differ by less than their last bits):
+// (m is a float32, whose steps from 2^27 on are 16 and more: t_j - m is then 0 or 16. r is what
+// is kept, since such an m and n may differ by less than a step):
 // the value scale is part of the weight, and the weights have a reference of their own,
 // so their 11 significant bits are those of the largest contributions however far apart
 // the blocks' scales are. The largest weight is 2^11 to 2^15, near the end of f16's range:
@@ -290,8 +290,7 @@ __global__ void __launch_bounds__(32 * dec8_warps(HD, X == 2), 1) qkvp_attention
       float d[NT][X][2], e[NT][X][2];  // t - m and u - n
       // t is rounded before m is taken from it: m is a rounded score less a little, and with the
       // unrounded one the difference would hold what its rounding left, 2^3 and more for
-      // scores from 2^27 on.
-      // (bound: factors may lie above their bound)
+      // scores from 2^27 on. bound: whether factors may lie above theirs.
       auto factor = [&](int i, int x, int y, bool bound) {
         const float f = key[i].x * c[x][y];
         return bound ? fminf(f, kFactorMost) : f;
